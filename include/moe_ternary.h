@@ -206,6 +206,95 @@ int32_t moe_draft_head(const uint16_t* hidden, const uint16_t* emb, int64_t n_to
                        const uint16_t* w1, const uint16_t* b1, const uint16_t* w2, const uint16_t* b2,
                        uint16_t* y, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* Element types of the operators below. */
+enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
+
+/* Device: quantize a bf16 or fp16 matrix to 8-bit floating point (e4m3: 4
+ * exponent and 3 mantissa bits, largest value 448) with one fp32 scale per block
+ * of 128 columns and block_rows rows: 1 for activations, 128 for weights (the
+ * last row block may be shorter).  For a block whose largest magnitude is m,
+ * floored at 1e-30,
+ *   scale = m / 448,  code = e4m3(v * (448 / m)), nearest even; value = code * scale.
+ * Every step is one correctly rounded fp32 operation, so the result is a pure
+ * function of the input bits.  A block with a NaN gets a NaN scale, one with an
+ * infinity an infinite scale.
+ *   type    MOE_BF16 or MOE_F16
+ *   x       device [rows x cols], 16-byte aligned, cols % 128 == 0
+ *   q       device e4m3 [rows x cols], 16-byte aligned
+ *   scales  device fp32 [ceil(rows / block_rows) x cols / 128]
+ * The buffers must not overlap.  Ordered on `stream`; nothing is allocated.
+ * rows = 0 is a no-op.  Errors: MOE_E_FORMAT (type), MOE_E_ARG (NULL, block_rows,
+ * misaligned, overlapping), MOE_E_SHAPE (also above 2^40 values), MOE_E_DEVICE. */
+int32_t moe_fp8_quantize(int32_t type, const uint16_t* x, int64_t rows, int32_t cols, int32_t block_rows, uint8_t* q,
+                         float* scales, void* stream);
+
+/* Device: root-mean-square norm of each row, with the residual's addition, as
+ * bf16 (the block's x) and / or as e4m3 with scales (moe_fp8_linear's a):
+ *   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * weight
+ *   x, residual  device bf16 [n_tokens x d]; residual NULL for h = x
+ *   weight       device fp32 [d] (the releases keep their norms in F32)
+ *   sum          device bf16 [n_tokens x d], h rounded, or NULL; needs a residual
+ *   y            device bf16 [n_tokens x d], or NULL
+ *   q, scales    device e4m3 [n_tokens x d] and fp32 [n_tokens x d / 128], the
+ *                1 x 128 blocks of moe_fp8_quantize, or both NULL
+ * At least one of y and q.  h, the mean and y are fp32; sum, y and q are each
+ * rounded once from them (q is not taken from the rounded y).  sum and y may be
+ * x or residual themselves (an in-place update of the residual stream); no other
+ * overlap is allowed.  d is a multiple of 128, at most 32768; every buffer but
+ * scales is 16-byte aligned.  n_tokens = 0 is a no-op.  Ordered on `stream`;
+ * nothing is allocated.  Errors: MOE_E_SHAPE, MOE_E_ARG, MOE_E_DEVICE. */
+int32_t moe_rms_norm(const uint16_t* x, const uint16_t* residual, int64_t n_tokens, int32_t d, const float* weight,
+                     float eps, uint16_t* sum, uint16_t* y, uint8_t* q, float* scales, void* stream);
+
+/* Device: matrix product of e4m3 operands with a scale for each block of 128:
+ *   y[t, n] = sum_g a_scales[t, g] w_scales[n / 128, g] sum_{k in group g} a[t, k] w[n, k]
+ *   a         device e4m3 [m x K], a_scales fp32 [m x K / 128]
+ *   w         device e4m3 [n x K], w_scales fp32 [ceil(n / 128) x K / 128]
+ *   y_type    MOE_BF16 or MOE_F32
+ *   y         device [m x n], row stride ldy >= n elements; the columns behind
+ *             n are left as they are
+ * Each group is one fp32 sum on the matrix cores, scaled and added in fp32; y is
+ * rounded once.  m and n are arbitrary, K is a multiple of 128.  a and w are
+ * 16-byte aligned; y must not overlap an input.  m = 0 or n = 0 is a no-op.
+ * Results depend on the shapes and the input bits alone.  Ordered on `stream`;
+ * nothing is allocated.  Errors: MOE_E_FORMAT (y_type), MOE_E_SHAPE, MOE_E_ARG,
+ * MOE_E_DEVICE. */
+int32_t moe_fp8_linear(const uint8_t* a, const float* a_scales, int64_t m, const uint8_t* w, const float* w_scales,
+                       int64_t n, int32_t K, int32_t y_type, void* y, int64_t ldy, void* stream);
+
+/* Device: one token per row of logits, from given random numbers.  The row's
+ * tokens are ordered by falling logit, equal logits by rising index, and token i
+ * weighs w_i = exp((l_i - l_max) / temperature).  In turn,
+ *   top_k  keeps the first k (k <= 0 or k >= vocab: all);
+ *   top_p  keeps the shortest prefix with at least top_p of the mass left by
+ *          top_k, at least one token (top_p >= 1 or NaN: all);
+ *   min_p  keeps the tokens with w_i >= min_p (<= 0 or NaN: all), and always
+ *          those with the largest logit;
+ * and the answer is the first token whose cumulative weight exceeds u times the
+ * mass left (u in [0, 1); a u of 1 or more gives the last token with mass, one
+ * below 0 or NaN the first).  A temperature that is not positive takes the first
+ * token of the order.  A NaN logit counts as -inf; a row of -inf gives token -1
+ * and probability 0; logits of +inf share the mass.
+ *   type         MOE_F32, MOE_BF16 or MOE_F16
+ *   logits       device [batch x vocab], row stride ld >= vocab elements
+ *   temperature, top_p, min_p  device fp32 [batch], top_k int32 [batch]; each may
+ *                be NULL (1, all, all, all)
+ *   u            device fp32 [batch]
+ *   tokens       device int32 [batch]
+ *   probs        device fp32 [batch], the token's share of the mass left, or NULL
+ *   workspace    >= moe_sample_workspace_bytes(batch, vocab), 256-byte aligned
+ *                (NULL if that is 0)
+ * Weights are fp64 and sums 64-bit integers in units of 2^-42 of l_max's weight,
+ * so no result depends on an order of additions; a token of less than half a unit
+ * has no mass.  vocab is at most 2^21.  batch = 0 is a no-op.  Ordered on
+ * `stream`; nothing is allocated.  Errors: MOE_E_FORMAT (type), MOE_E_SHAPE,
+ * MOE_E_ARG, MOE_E_SPACE, MOE_E_DEVICE. */
+int64_t moe_sample_workspace_bytes(int64_t batch, int32_t vocab);
+int32_t moe_sample(int32_t type, const void* logits, int64_t batch, int32_t vocab, int64_t ld,
+                   const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                   const float* u, int32_t* tokens, float* probs, void* workspace, int64_t workspace_bytes,
+                   void* stream);
+
 /* Host: reorder the blocks of a [rows x cols] container (rows % 16 == 0,
  * cols % 128 == 0) between the row-major order moe_pack writes and the
  * tile-major order the expert kernels read.  With G = cols / 128, block

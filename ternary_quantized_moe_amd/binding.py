@@ -27,6 +27,7 @@ EXPORTS = [
     "moe_block_bytes", "moe_packed_bytes", "moe_pack", "moe_unpack", "moe_unpack_device",
     "moe_quantize_device", "moe_ple_gather_q4_0", "moe_ternary_forward_q", "moe_draft_head_workspace_bytes",
     "moe_draft_head", "moe_lowrank_workspace_bytes", "moe_lowrank_apply",
+    "moe_fp8_quantize", "moe_rms_norm", "moe_fp8_linear", "moe_sample_workspace_bytes", "moe_sample",
     "moe_workspace_bytes_factored", "moe_ternary_forward_factored",
     "moe_tile_container", "moe_untile_container", "moe_workspace_bytes", "moe_ternary_forward", "moe_route_workspace_bytes", "moe_route",
     "moe_route_workspace_bytes_factored", "moe_route_factored", "moe_ternary_forward_noalloc",
@@ -82,6 +83,11 @@ def lib():
             "moe_draft_head": (i32, [vp, vp, i64, i32, i32, vp, vp, vp, vp, vp, vp, i64, vp]),
             "moe_lowrank_workspace_bytes": (i64, [i64, i32, i32]),
             "moe_lowrank_apply": (i32, [vp, vp, i64, i32, vp, vp, vp, vp, i32, vp, vp, i64, vp]),
+            "moe_fp8_quantize": (i32, [i32, vp, i64, i32, i32, vp, vp, vp]),
+            "moe_rms_norm": (i32, [vp, vp, i64, i32, vp, ctypes.c_float, vp, vp, vp, vp, vp]),
+            "moe_fp8_linear": (i32, [vp, vp, i64, vp, vp, i64, i32, i32, vp, i64, vp]),
+            "moe_sample_workspace_bytes": (i64, [i64, i32]),
+            "moe_sample": (i32, [i32, vp, i64, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]),
             "moe_workspace_bytes_factored": (i64, [ctypes.POINTER(ExpertBanksC), i64, i32, i32, i32]),
             "moe_ternary_forward_factored": (i32, [vp, i64, vp, vp, vp, i32, ctypes.POINTER(ExpertBanksC), vp, vp,
                                                    i32, i32, vp, vp, i64, vp]),
@@ -401,6 +407,167 @@ def lowrank_apply(x, y_in, a, b, rank: int, a_q=None, b_q=None, y=None, workspac
     _check(lib().moe_lowrank_apply(_dev_ptr(x), _dev_ptr(y_in), T, d, _dev_ptr(a), _dev_ptr(a_q), _dev_ptr(b),
                                    _dev_ptr(b_q), rank, _dev_ptr(y), wp, wn, _stream(stream)))
     return y
+
+
+def _operand(name, t, device, dtypes, shape, strided=False):
+    """Checks one device tensor of the calls below: on the current device, of one
+    of these types, of this shape (a size of None is any) and contiguous
+    (strided: each row is)."""
+    if not t.is_cuda or t.device != device:
+        raise MoeError(-1, f"{name} is on {t.device}, not on {device}")
+    if t.dtype not in dtypes:
+        raise MoeError(-2, f"{name} has type {t.dtype}")
+    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
+        raise MoeError(-3, f"{name} has shape {tuple(t.shape)}, {tuple(shape)} wanted")
+    if strided:
+        if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+            raise MoeError(-1, f"the rows of {name} are not contiguous")
+    elif not t.is_contiguous():
+        raise MoeError(-1, f"{name} is not contiguous")
+
+
+def _row_stride(t):
+    """Row stride of a 2-d tensor with contiguous rows (a single row's is its length)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _device_of(t):
+    """The tensor's device, which has to be the current one."""
+    import torch
+    if not t.is_cuda:
+        raise MoeError(-1, f"a device tensor is wanted, got one on {t.device}")
+    if t.device.index != torch.cuda.current_device():
+        raise MoeError(-1, f"the tensor is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+BF16, F16, F32 = 0, 1, 2
+
+
+def fp8_quantize(x, block_rows: int, q=None, scales=None, stream=None):
+    """bf16 (torch.bfloat16 or int16 bits) or fp16 matrix [rows, cols] -> e4m3 codes
+    and fp32 scales [ceil(rows / block_rows), cols / 128]: block_rows 1 for
+    activations, 128 for weights."""
+    import torch
+    dev = _device_of(x)
+    _operand("x", x, dev, (torch.bfloat16, torch.int16, torch.float16), (None, None))
+    rows, cols = x.shape
+    if block_rows < 1 or cols % 128:
+        _check(lib().moe_fp8_quantize(BF16, None, rows, cols, block_rows, None, None, None))
+    size = (-(-rows // block_rows), cols // 128)
+    if q is None:
+        q = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        _operand("q", q, dev, (torch.float8_e4m3fn, torch.uint8), (rows, cols))
+    if scales is None:
+        scales = torch.empty(size, dtype=torch.float32, device=dev)
+    else:
+        _operand("scales", scales, dev, (torch.float32,), size)
+    _check(lib().moe_fp8_quantize(F16 if x.dtype == torch.float16 else BF16, x.data_ptr(), rows, cols, block_rows,
+                                  q.data_ptr(), scales.data_ptr(), _stream(stream)))
+    return q, scales
+
+
+def rms_norm(x, weight, eps: float, residual=None, bf16: bool = True, fp8: bool = False, sum=None, y=None, q=None,
+             scales=None, stream=None):
+    """RMS norm of x (+ residual), bf16 [T, d] (torch.bfloat16 or int16 bits), with
+    fp32 weight [d].  Returns a dict: "sum" (x + residual, with a residual only),
+    "y" (bf16=True), "q" and "scales" (fp8=True: e4m3 with one scale per 128).
+    sum, y, q, scales: buffers for them; sum and y may be x or residual."""
+    import torch
+    dev = _device_of(x)
+    half = (torch.bfloat16, torch.int16)
+    _operand("x", x, dev, half, (None, None))
+    T, d = x.shape
+    _operand("weight", weight, dev, (torch.float32,), (d,))
+    out = {}
+    if residual is not None:
+        _operand("residual", residual, dev, half, (T, d))
+        if sum is None:
+            sum = torch.empty_like(x)
+        else:
+            _operand("sum", sum, dev, half, (T, d))
+        out["sum"] = sum
+    if bf16:
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _operand("y", y, dev, half, (T, d))
+        out["y"] = y
+    elif y is not None:
+        raise MoeError(-1, "y is given, but bf16 is off")
+    if fp8:
+        if q is None:
+            q = torch.empty((T, d), dtype=torch.float8_e4m3fn, device=dev)
+        else:
+            _operand("q", q, dev, (torch.float8_e4m3fn, torch.uint8), (T, d))
+        if scales is None:
+            scales = torch.empty((T, d // 128), dtype=torch.float32, device=dev)
+        else:
+            _operand("scales", scales, dev, (torch.float32,), (T, d // 128))
+        out["q"], out["scales"] = q, scales
+    elif q is not None or scales is not None:
+        raise MoeError(-1, "q or scales is given, but fp8 is off")
+    _check(lib().moe_rms_norm(x.data_ptr(), _dev_ptr(residual), T, d, weight.data_ptr(), eps, _dev_ptr(sum),
+                              _dev_ptr(y), _dev_ptr(q), _dev_ptr(scales), _stream(stream)))
+    return out
+
+
+def fp8_linear(a, a_scales, w, w_scales, y=None, out_dtype=None, stream=None):
+    """a [m, K] times w [n, K] transposed, both e4m3 (torch.float8_e4m3fn or uint8
+    codes) with the scales of fp8_quantize (block_rows 1 and 128) -> y [m, n],
+    torch.bfloat16 (default) or torch.float32.  A given y may be padded: its rows
+    are contiguous and its row stride is at least n."""
+    import torch
+    dev = _device_of(a)
+    codes = (torch.float8_e4m3fn, torch.uint8)
+    _operand("a", a, dev, codes, (None, None))
+    m, K = a.shape
+    _operand("w", w, dev, codes, (None, K))
+    n = w.shape[0]
+    _operand("a_scales", a_scales, dev, (torch.float32,), (m, K // 128))
+    _operand("w_scales", w_scales, dev, (torch.float32,), (-(-n // 128), K // 128))
+    if y is None:
+        y = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
+    elif out_dtype is not None and out_dtype != y.dtype:
+        raise MoeError(-2, f"y has type {y.dtype}, {out_dtype} wanted")
+    _operand("y", y, dev, (torch.bfloat16, torch.float32), (m, n), strided=True)
+    _check(lib().moe_fp8_linear(a.data_ptr(), a_scales.data_ptr(), m, w.data_ptr(), w_scales.data_ptr(), n, K,
+                                F32 if y.dtype == torch.float32 else BF16, y.data_ptr(), _row_stride(y),
+                                _stream(stream)))
+    return y
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, tokens=None, probs=None, workspace=None,
+           stream=None):
+    """One token per row of logits [batch, vocab] (fp32, bf16 or fp16; rows may be
+    padded) from uniform numbers u [batch]; temperature, top_p, min_p: fp32 [batch]
+    or None, top_k: int32 [batch] or None.  Returns (tokens int32, probs fp32)."""
+    import torch
+    dev = _device_of(logits)
+    f32 = (torch.float32,)
+    _operand("logits", logits, dev, (torch.float32, torch.bfloat16, torch.float16), (None, None), strided=True)
+    B, V = logits.shape
+    for name, t, types in (("u", u, f32), ("temperature", temperature, f32), ("top_k", top_k, (torch.int32,)),
+                           ("top_p", top_p, f32), ("min_p", min_p, f32), ("tokens", tokens, (torch.int32,)),
+                           ("probs", probs, f32)):
+        if t is not None:
+            _operand(name, t, dev, types, (B,))
+    if tokens is None:
+        tokens = torch.empty(B, dtype=torch.int32, device=dev)
+    if probs is None:
+        probs = torch.empty(B, dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = lib().moe_sample_workspace_bytes(B, V)
+        if need < 0:
+            raise MoeError(-3, f"invalid sampler shape batch={B} vocab={V}")
+        workspace = alloc_workspace(need, dev)
+    wp, wn = _aligned(workspace)
+    kind = F32 if logits.dtype == torch.float32 else BF16 if logits.dtype == torch.bfloat16 else F16
+    _check(lib().moe_sample(kind, logits.data_ptr(), B, V, _row_stride(logits), _dev_ptr(temperature), _dev_ptr(top_k),
+                            _dev_ptr(top_p), _dev_ptr(min_p), _dev_ptr(u), tokens.data_ptr(), probs.data_ptr(), wp, wn,
+                            _stream(stream)))
+    return tokens, probs
 
 
 def _route_outputs(T, n_experts, top_k, dev):

@@ -13,6 +13,7 @@
 #include <string>
 
 #include "moe_ternary.h"
+#include "fp8_internal.h"
 #include "host_error.h"
 #include "moe_internal.h"
 #include "router_delta.h"
@@ -350,6 +351,124 @@ int32_t moe_draft_head(const uint16_t* hidden, const uint16_t* emb, int64_t T, i
   moe::HeadArgs a{hidden, emb, T, h, m, w1, b1, w2, b2, y};
   hipError_t e = moe::launch_head(a, (char*)ws, (hipStream_t)stream, g_stage_events);
   if (e != hipSuccess) return device_fail(e, "moe_draft_head launch");
+  return ok();
+}
+
+// ------------------------------------------------- norm, 8-bit product, sampler
+// Whether two byte ranges share a byte (a NULL range has none).
+static bool overlaps(const void* p, int64_t n, const void* q, int64_t m) {
+  if (!p || !q) return false;
+  const char *a = (const char*)p, *b = (const char*)q;
+  return a < b + m && b < a + n;
+}
+// Whether an output may sit on an input: on all of it or on none of it.
+static bool same_or_apart(const void* out, const void* in, int64_t n) { return out == in || !overlaps(out, n, in, n); }
+
+int32_t moe_fp8_quantize(int32_t type, const uint16_t* x, int64_t rows, int32_t cols, int32_t block_rows, uint8_t* q,
+                         float* scales, void* stream) {
+  if (type != MOE_BF16 && type != MOE_F16) return fail(MOE_E_FORMAT, "type %d is neither MOE_BF16 nor MOE_F16", (int)type);
+  if (block_rows != 1 && block_rows != 128)
+    return fail(MOE_E_ARG, "block_rows %d is neither 1 nor 128", (int)block_rows);
+  if (cols <= 0 || cols % 128) return fail(MOE_E_SHAPE, "cols %d is not a positive multiple of 128", (int)cols);
+  if (rows < 0) return fail(MOE_E_SHAPE, "negative row count %lld", (long long)rows);
+  if (rows > ((int64_t)1 << 40) / cols)
+    return fail(MOE_E_SHAPE, "%lld x %d values exceed one launch (2^40)", (long long)rows, (int)cols);
+  if (rows == 0) return ok();
+  if (!x || !q || !scales) return fail(MOE_E_ARG, "NULL pointer");
+  if ((uintptr_t)x % 16 || (uintptr_t)q % 16 || (uintptr_t)scales % 4)
+    return fail(MOE_E_ARG, "x and q must be 16-byte and scales 4-byte aligned");
+  const int64_t n = rows * cols, ns = (rows + block_rows - 1) / block_rows * (cols / 128) * 4;
+  if (overlaps(x, 2 * n, q, n) || overlaps(x, 2 * n, scales, ns) || overlaps(q, n, scales, ns))
+    return fail(MOE_E_ARG, "x, q and scales must not overlap");
+  const hipError_t e = moe::launch_fp8_quantize(type == MOE_F16, x, rows, cols, block_rows, q, scales, (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_fp8_quantize launch");
+  return ok();
+}
+
+int32_t moe_rms_norm(const uint16_t* x, const uint16_t* residual, int64_t T, int32_t d, const float* weight, float eps,
+                     uint16_t* sum, uint16_t* y, uint8_t* q, float* scales, void* stream) {
+  if (d <= 0 || d % 128 || d > moe::kNormMaxD)
+    return fail(MOE_E_SHAPE, "d %d is not a positive multiple of 128 up to %d", (int)d, moe::kNormMaxD);
+  if (T < 0 || T > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "token count %lld outside [0, 2^31)", (long long)T);
+  if (!(eps >= 0.f) || std::isinf(eps)) return fail(MOE_E_ARG, "eps must be finite and not negative");
+  if (T == 0) return ok();
+  if (!y && !q) return fail(MOE_E_ARG, "give y, q or both");
+  if ((q == nullptr) != (scales == nullptr)) return fail(MOE_E_ARG, "give q and scales together");
+  if (sum && !residual) return fail(MOE_E_ARG, "sum needs a residual");
+  if (!x || !weight) return fail(MOE_E_ARG, "NULL pointer");
+  if ((uintptr_t)x % 16 || (uintptr_t)residual % 16 || (uintptr_t)weight % 16 || (uintptr_t)sum % 16 ||
+      (uintptr_t)y % 16 || (uintptr_t)q % 16 || (uintptr_t)scales % 4)
+    return fail(MOE_E_ARG, "scales must be 4-byte and every other buffer 16-byte aligned");
+  const int64_t n = T * d, n2 = 2 * n, ns = n / 128 * 4;
+  if (!same_or_apart(sum, x, n2) || !same_or_apart(sum, residual, n2) || !same_or_apart(y, x, n2) ||
+      !same_or_apart(y, residual, n2))
+    return fail(MOE_E_ARG, "sum and y may be x or residual, but not part of them");
+  const struct { const void* p; int64_t n; } out[] = {{sum, n2}, {y, n2}, {q, n}, {scales, ns}},
+                                             in[] = {{x, n2}, {residual, n2}, {weight, 4 * (int64_t)d}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return fail(MOE_E_ARG, "the outputs overlap");
+    for (int j = i < 2 ? 2 : 0; j < 3; ++j)
+      if (overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return fail(MOE_E_ARG, "an output overlaps an input");
+  }
+  const hipError_t e = moe::launch_rms_norm({x, residual, T, d, weight, eps, sum, y, q, scales}, (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_rms_norm launch");
+  return ok();
+}
+
+int32_t moe_fp8_linear(const uint8_t* a, const float* a_scales, int64_t M, const uint8_t* w, const float* w_scales,
+                       int64_t N, int32_t K, int32_t y_type, void* y, int64_t ldy, void* stream) {
+  if (y_type != MOE_BF16 && y_type != MOE_F32)
+    return fail(MOE_E_FORMAT, "output type %d is neither MOE_BF16 nor MOE_F32", (int)y_type);
+  if (K <= 0 || K % 128) return fail(MOE_E_SHAPE, "K %d is not a positive multiple of 128", (int)K);
+  if (M < 0 || N < 0 || M > (1 << 30) || N > (1 << 30))
+    return fail(MOE_E_SHAPE, "M %lld and N %lld must lie in [0, 2^30]", (long long)M, (long long)N);
+  if (ldy < N) return fail(MOE_E_SHAPE, "row stride %lld below N %lld", (long long)ldy, (long long)N);
+  if (M == 0 || N == 0) return ok();
+  if (!a || !a_scales || !w || !w_scales || !y) return fail(MOE_E_ARG, "NULL pointer");
+  const int64_t ysize = y_type == MOE_F32 ? 4 : 2;
+  if ((uintptr_t)a % 16 || (uintptr_t)w % 16 || (uintptr_t)a_scales % 4 || (uintptr_t)w_scales % 4 || (uintptr_t)y % ysize)
+    return fail(MOE_E_ARG, "a and w must be 16-byte, scales 4-byte and y element aligned");
+  if (ldy > ((int64_t)1 << 60) / M) return fail(MOE_E_SHAPE, "row stride %lld too large", (long long)ldy);
+  const int64_t yn = ((M - 1) * ldy + N) * ysize, groups = K / 128;
+  if (overlaps(y, yn, a, M * K) || overlaps(y, yn, w, N * K) || overlaps(y, yn, a_scales, M * groups * 4) ||
+      overlaps(y, yn, w_scales, (N + 127) / 128 * groups * 4))
+    return fail(MOE_E_ARG, "y overlaps an input");
+  const hipError_t e = moe::launch_fp8_linear({a, a_scales, M, w, w_scales, N, K, y_type == MOE_F32, y, ldy},
+                                              (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_fp8_linear launch");
+  return ok();
+}
+
+int64_t moe_sample_workspace_bytes(int64_t batch, int32_t vocab) {
+  if (batch < 0 || batch > 0x7FFFFFFFll || vocab <= 0 || vocab > moe::kSampleMaxVocab) return -1;
+  return moe::sample_workspace_bytes(batch, vocab);
+}
+
+int32_t moe_sample(int32_t type, const void* logits, int64_t batch, int32_t vocab, int64_t ld, const float* temperature,
+                   const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,
+                   float* probs, void* ws, int64_t ws_bytes, void* stream) {
+  if (type != MOE_F32 && type != MOE_BF16 && type != MOE_F16)
+    return fail(MOE_E_FORMAT, "unknown logit type %d", (int)type);
+  if (vocab <= 0 || vocab > moe::kSampleMaxVocab)
+    return fail(MOE_E_SHAPE, "vocabulary %d outside [1, %lld]", (int)vocab, (long long)moe::kSampleMaxVocab);
+  if (batch < 0 || batch > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "batch %lld outside [0, 2^31)", (long long)batch);
+  if (ld < vocab || ld > ((int64_t)1 << 31))
+    return fail(MOE_E_SHAPE, "row stride %lld below the vocabulary or above 2^31", (long long)ld);
+  if (batch == 0) return ok();
+  if (!logits || !u || !tokens) return fail(MOE_E_ARG, "NULL pointer");
+  const int64_t need = moe::sample_workspace_bytes(batch, vocab);
+  if (need && !ws) return fail(MOE_E_ARG, "NULL workspace");
+  if ((uintptr_t)ws % kAlign) return fail(MOE_E_ARG, "workspace must be 256-byte aligned");
+  if ((uintptr_t)logits % (type == MOE_F32 ? 4 : 2) || (uintptr_t)temperature % 4 || (uintptr_t)top_k % 4 ||
+      (uintptr_t)top_p % 4 || (uintptr_t)min_p % 4 || (uintptr_t)u % 4 || (uintptr_t)tokens % 4 || (uintptr_t)probs % 4)
+    return fail(MOE_E_ARG, "logits must be element and every other array 4-byte aligned");
+  if (ws_bytes < need)
+    return fail(MOE_E_SPACE, "workspace holds %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
+  const moe::SampleType t = type == MOE_F32 ? moe::kSampleF32 : type == MOE_BF16 ? moe::kSampleBf16 : moe::kSampleF16;
+  const hipError_t e = moe::launch_sample(
+      t, {logits, batch, vocab, ld, temperature, top_k, top_p, min_p, u, tokens, probs}, ws, (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_sample launch");
   return ok();
 }
 
