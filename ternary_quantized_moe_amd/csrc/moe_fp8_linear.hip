@@ -27,6 +27,7 @@ namespace moe {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // D = A(16 x 128) B(128 x 16), fp32, both operands e4m3.  Lane l supplies row
 // l % 16 of A and column l % 16 of B; the order of K inside the group is free
@@ -74,6 +75,23 @@ __device__ __forceinline__ f32x4 group_product(const Frag<true>& w, const Frag<t
   return s;
 }
 
+// Four neighbouring results of one token; `quads`: rows of y keep n's alignment.
+template <bool F32>
+__device__ __forceinline__ void store4(const F8LinearArgs& p, int64_t t, int64_t n, f32x4 v, bool quads) {
+  const int64_t at = t * p.ldy + n;
+  if (quads && n + 4 <= p.N) {
+    if (F32) *(f32x4*)((float*)p.y + at) = v;
+    else *(u32x2*)((uint16_t*)p.y + at) = u32x2{f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w)};
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (n + j >= p.N) break;
+      if (F32) ((float*)p.y)[at + j] = v[j];
+      else ((uint16_t*)p.y)[at + j] = (uint16_t)f32_to_bf16(v[j]);
+    }
+  }
+}
+
 constexpr int kLinThreads = 256;
 
 // 64 rows of w (16 a wave) and 64 tokens per block.
@@ -106,26 +124,318 @@ __global__ __launch_bounds__(kLinThreads) void fp8_linear_kernel(F8LinearArgs p)
       for (int j = 0; j < 4; ++j) acc[i][j] += s[j] * f;
     }
   }
+  const bool quads = (p.ldy % 4 == 0) && ((uintptr_t)p.y % (F32 ? 16 : 8) == 0);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t t = m0 + 16 * i + c, n = n0 + 4 * q;
     if (t >= p.M) continue;
+    store4<F32>(p, t, n, acc[i], quads);
+  }
+}
+
+
+// ------------------------------------------------------------------ tiled kernel
+// A block computes BN rows of w times BM tokens, a wave WTN x WTM of them as 32 x
+// 32 matrix-core tiles.  One group of every row of the block, BN + BM rows of 128
+// bytes, is staged in LDS by loads that go there directly; two buffers, so the
+// next group arrives while this one is multiplied.
+//
+// A staging load writes 64 consecutive pieces of 16 bytes, eight rows, in lane
+// order, so the swizzle that keeps the reads off each other's banks is in the
+// lane's source address: piece p of row r is kept at place p ^ f(r) of the row,
+// f(r) = r % 8 ^ r / 8 % 2, which is distinct over eight consecutive rows and over
+// the even and the odd rows of sixteen.
+__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+
+__device__ __forceinline__ f32x16 mfma_f8_32(i32x8 a, i32x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 half_product(const Frag<false>& w, const Frag<false>& a, f32x16 c) {
+  return mfma_f8_32(w.v, a.v, c);
+}
+__device__ __forceinline__ f32x16 half_product(const Frag<true>& w, const Frag<true>& a, f32x16 c) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (n + j >= p.N) continue;
-      if (F32) ((float*)p.y)[t * p.ldy + n + j] = acc[i][j];
-      else ((uint16_t*)p.y)[t * p.ldy + n + j] = (uint16_t)f32_to_bf16(acc[i][j]);
+  for (int i = 0; i < 4; ++i) c = mfma32(w.v[i], a.v[i], c);
+  return c;
+}
+
+// A number that the compiler no longer knows: what is computed from it is not kept
+// over a loop.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Lane l's 32 bytes of half h of a staged row: pieces 4 h + 2 (l / 32) and the
+// next.  `at`: the place of half 0's first piece; the others differ from it in one
+// or two address bits.
+__device__ __forceinline__ int staged_at(int row, int q) { return row * kF8Group + 16 * ((2 * q) ^ swizzle(row)); }
+template <bool F32>
+__device__ __forceinline__ Frag<F32> staged_frag(const uint8_t* buf, int at, int h) {
+  const u32x4 lo = *(const u32x4*)(buf + (at ^ 64 * h)), hi = *(const u32x4*)(buf + (at ^ (64 * h + 16)));
+  Frag<F32> r;
+  r.set(i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w});
+  return r;
+}
+
+// A buffer descriptor over the bytes from p on (the lanes' offsets stay inside),
+// or over none (bytes = 0): loads through that one touch no memory.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int bytes = -1) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, bytes, 0x00027000);
+}
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t src, uint32_t lane_off, int off, uint8_t* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16, (int)lane_off, off, 0, 0);
+}
+
+template <int BN, int BM, int WTN, int WTM, bool F32>
+struct Tile {
+  static constexpr int kWavesN = BN / WTN, kWaves = kWavesN * (BM / WTM), kThreads = 64 * kWaves;
+  static constexpr int TN = WTN / 32, TM = WTM / 32;
+  static constexpr int kLoads = (BN + BM) / 8 / kWaves;  // staging loads of a wave per group
+  static constexpr int kBufBytes = (BN + BM) * kF8Group;
+
+  f32x16 acc[TN][TM], t[2];
+  Frag<F32> fa[TM][2], fw[2][2];
+  float s[TM], raw[TM];  // the pending products' scales; the tokens' scales of the next group to begin
+  const uint8_t *w, *a;
+  int lane, wave, wn, wm, K, groups, last_n, last_m;
+  int at_w, at_a;  // the lane's places in the wave's first 32 rows of w and of a (a tile's rows keep the swizzle)
+
+  // A wave's loads: eight rows each, kWaves chunks apart (a multiple of 16 rows:
+  // one swizzle for all).  Rows past the matrix repeat its last row; their results
+  // are not stored.  Past the last group nothing is loaded, without a branch: one
+  // would let the compiler move the additions behind it past it, and keep every
+  // product.  The lanes' offsets are made anew each time: kept, they would take
+  // eight registers that the products need.
+  __device__ __forceinline__ void stage(uint8_t* buf, int g) const {
+    const int tid = opaque(threadIdx.x), row0 = tid >> 3, piece = 16 * ((tid & 7) ^ swizzle(row0));
+    const int bytes = __builtin_amdgcn_readfirstlane((g - groups) >> 31);
+    const __amdgpu_buffer_rsrc_t from_w = buffer_of(w, bytes), from_a = buffer_of(a, bytes);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const bool of_w = i * kWaves < BN / 8;
+      const int row = min(row0 + (i * kWaves * 8 - (of_w ? 0 : BN)), of_w ? last_n : last_m);
+      load_to_lds(of_w ? from_w : from_a, __umul24(row, K) + piece, g * kF8Group, buf + (wave + i * kWaves) * 1024);
     }
   }
+
+  __device__ __forceinline__ void scale_add(int i, int j, const f32x16& t, float s) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[i][j][e] += t[e] * s;
+  }
+
+  __device__ __forceinline__ void read_w(const uint8_t* buf, int i, Frag<F32> (&f)[2]) const {
+    const int at = opaque(at_w);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) f[h] = staged_frag<F32>(buf + 32 * kF8Group * i, at, h);
+  }
+  __device__ __forceinline__ void read_a(const uint8_t* buf, int j) {
+    const int at = opaque(at_a);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) fa[j][h] = staged_frag<F32>(buf + (BN + 32 * j) * kF8Group, at, h);
+  }
+
+  // The wave's results through LDS: token rows of WTN results, pieces of 16 bytes
+  // kept at place p ^ token % pieces so that neither side meets in a bank, then 16
+  // bytes a lane, whole rows a wave.
+  __device__ __forceinline__ void store(const F8LinearArgs& p, uint8_t* buf, int64_t m, int64_t n) const {
+    constexpr int SIZE = F32 ? 4 : 2, PER = 16 / SIZE, PIECES = WTN / PER;
+    static_assert(WTM * WTN * SIZE * (kWaves / 2) <= kBufBytes, "the waves' shares fit");
+    uint8_t* mine = buf + (wave % (kWaves / 2)) * (WTM * WTN * SIZE);
+    const int c = lane & 31, q = lane >> 5;
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      const int token = 32 * j + c;
+#pragma unroll
+      for (int i = 0; i < TN; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int at = 32 * i + 8 * e + 4 * q, piece = (at / PER) ^ (token % PIECES);
+          const f32x4 v = {acc[i][j][4 * e], acc[i][j][4 * e + 1], acc[i][j][4 * e + 2], acc[i][j][4 * e + 3]};
+          uint8_t* to = mine + token * (WTN * SIZE) + 16 * piece + (at % PER) * SIZE;
+          if (F32) *(f32x4*)to = v;
+          else *(u32x2*)to = u32x2{f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w)};
+        }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    const bool whole = p.ldy % PER == 0 && (uintptr_t)p.y % 16 == 0;
+    const int piece = lane % PIECES;
+    const int64_t col = n + piece * PER;
+#pragma unroll
+    for (int k = 0; k < WTM * PIECES / 64; ++k) {
+      const int token = lane / PIECES + k * (64 / PIECES);
+      const u32x4 v = *(const u32x4*)(mine + token * (WTN * SIZE) + 16 * (piece ^ (token % PIECES)));
+      if (m + token >= p.M) continue;
+      uint8_t* to = (uint8_t*)p.y + ((m + token) * p.ldy + col) * SIZE;
+      if (whole && col + PER <= p.N) {
+        *(u32x4*)to = v;
+      } else {
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+          if (col + x >= p.N) break;
+          if (F32) ((uint32_t*)to)[x] = v[x];
+          else ((uint16_t*)to)[x] = (uint16_t)(v[x / 2] >> (16 * (x & 1)));
+        }
+      }
+    }
+  }
+
+  // Group g, whose bytes are in `now`, its tokens' operands and the first of w's
+  // already read.  A 32 x 32 tile's product is scaled and added while the matrix
+  // core works on the next one.  When the last row of tiles has begun, every read
+  // of `now` has been made and the next group's bytes have arrived in `then`: the
+  // block meets at the one barrier, `now` takes the loads of group g + 2, a whole
+  // group ahead, and the next group's first operands are read behind the last
+  // tiles' products.  The scheduling barriers keep the compiler from issuing all
+  // products first, whose results would not fit the registers.
+  template <int PARITY, class Meet>
+  __device__ __forceinline__ void step(const uint8_t* now, const uint8_t* then, float sw, Meet meet) {
+    constexpr int N = TN * TM;
+  
+
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int i = n / TM, j = n % TM, at = PARITY * N + n, slot = (PARITY * TN + i) & 1;
+      if (j == 0 && i + 1 < TN) read_w(now, i + 1, fw[slot ^ 1]);
+      f32x16& mine = t[at & 1];
+      mine = half_product(fw[slot][0], fa[j][0], f32x16{});
+      mine = half_product(fw[slot][1], fa[j][1], mine);
+      __builtin_amdgcn_sched_barrier(0);
+      const f32x16& done = t[(at & 1) ^ 1];
+      if (n) {
+        scale_add((n - 1) / TM, (n - 1) % TM, done, s[(n - 1) % TM]);
+      } else {  // the last product of the group before, by its own scale
+        scale_add(TN - 1, TM - 1, done, s[TM - 1]);
+#pragma unroll
+        for (int k = 0; k < TM; ++k) s[k] = raw[k] * sw;
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (n == N - TM) {
+        meet();
+        read_w(then, 0, fw[slot ^ 1]);
+      }
+      if (i == TN - 1) read_a(then, j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+};
+
+template <int BN, int BM, int WTN, int WTM, bool F32>
+__global__ __launch_bounds__(64 * (BN / WTN) * (BM / WTM), 2) void fp8_tile_kernel(F8LinearArgs p, int tiles_n) {
+  typedef Tile<BN, BM, WTN, WTM, F32> T;
+  static_assert((BN / 8) % T::kWaves == 0 && (BM / 8) % T::kWaves == 0 && T::kWaves % 2 == 0,
+                "a wave's staging loads split evenly, 16 rows or a multiple apart");
+  __shared__ __attribute__((aligned(1024))) uint8_t buf0[T::kBufBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t buf1[T::kBufBytes];
+  // consecutive blocks go to the eight XCDs in turn: each XCD takes a contiguous
+  // run of tiles, whose rows of w and a meet in its L2
+  const int tiles = gridDim.x, per = (tiles + 7) / 8, rest = tiles % 8 ? tiles % 8 : 8;
+  const int xcd = blockIdx.x % 8, at = blockIdx.x / 8;
+  const int tile = xcd < rest ? xcd * per + at : rest * per + (xcd - rest) * (per - 1) + at;
+  // ... and goes through it in bands of eight tiles of tokens: the 32 tiles that an
+  // XCD works on at a time are 8 x 4, 12 tiles' rows for its L2 to fetch
+  const int tiles_m = tiles / tiles_n, band = tile / (8 * tiles_n), in_band = tile - band * 8 * tiles_n;
+  const int height = min(8, tiles_m - 8 * band);
+  const int64_t m0 = (int64_t)(8 * band + in_band % height) * BM, n0 = (int64_t)(in_band / height) * BN;
+  const int groups = p.K / kF8Group;
+  const int last_n = (int)min((int64_t)BN, p.N - n0) - 1, last_m = (int)min((int64_t)BM, p.M - m0) - 1;
+
+  T t;
+  t.lane = threadIdx.x & 63;
+  t.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  t.wn = t.wave % T::kWavesN;
+  t.wm = t.wave / T::kWavesN;
+  t.w = p.w + n0 * p.K;
+  t.a = p.a + m0 * p.K;
+  t.at_w = staged_at(t.wn * WTN + (t.lane & 31), t.lane >> 5);
+  t.at_a = staged_at(t.wm * WTM + (t.lane & 31), t.lane >> 5);
+  t.K = p.K;
+  t.groups = groups;
+  t.last_n = last_n;
+  t.last_m = last_m;
+#pragma unroll
+  for (int i = 0; i < T::TN; ++i)
+#pragma unroll
+    for (int j = 0; j < T::TM; ++j) t.acc[i][j] = f32x16{};
+
+  const __amdgpu_buffer_rsrc_t sa = buffer_of(p.a_scales + m0 * groups);
+  // constant address space: the wave's scales of w come through scalar loads
+  const auto sw = (const __attribute__((address_space(4))) float*)(p.w_scales +
+                                                                   min(n0 + t.wn * WTN, p.N - 1) / kF8Group * groups);
+  auto read_scales = [&](int g) {
+    const int token = t.wm * WTM + (opaque(threadIdx.x) & 31);
+#pragma unroll
+    for (int j = 0; j < T::TM; ++j)
+      t.raw[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                               sa, 4 * __umul24(min(token + 32 * j, last_m), groups), 4 * g, 0));
+  };
+  read_scales(0);
+  t.stage(buf0, 0);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < T::TM; ++j) {
+    t.read_a(buf0, j);
+    t.s[j] = 0.f;
+  }
+  t.read_w(buf0, 0, t.fw[0]);
+  t.t[1] = f32x16{};  // no product is pending before the first
+  t.stage(buf1, 1);
+  auto meet = [&](uint8_t* now, int g) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    read_scales(min(g + 1, groups - 1));
+    t.stage(now, g + 2);
+  };
+  int g = 0;
+  for (; g + 2 <= groups; g += 2) {
+    t.template step<0>(buf0, buf1, sw[g], [&] { meet(buf0, g); });
+    t.template step<1>(buf1, buf0, sw[g + 1], [&] { meet(buf1, g + 1); });
+  }
+  if (g < groups) t.template step<0>(buf0, buf1, sw[g], [&] { meet(buf0, g); });
+  // the last product is pending in t[1], after an odd number of single-tile groups in t[0]
+  if (T::TN * T::TM % 2 && g < groups) t.scale_add(T::TN - 1, T::TM - 1, t.t[0], t.s[T::TM - 1]);
+  else t.scale_add(T::TN - 1, T::TM - 1, t.t[1], t.s[T::TM - 1]);
+  // no staging load is on its way any more: each wave turns its results round in
+  // its share of the buffers and writes whole lines of y
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  t.store(p, t.wave < T::kWaves / 2 ? buf0 : buf1, m0 + t.wm * WTM, n0 + t.wn * WTN);
+}
+
+template <int BN, int BM, int WTN, int WTM, bool F32>
+hipError_t launch_tiles(const F8LinearArgs& a, hipStream_t stream) {
+  const int64_t tiles_n = (a.N + BN - 1) / BN, tiles = tiles_n * ((a.M + BM - 1) / BM);
+  fp8_tile_kernel<BN, BM, WTN, WTM, F32>
+      <<<(unsigned)tiles, Tile<BN, BM, WTN, WTM, F32>::kThreads, 0, stream>>>(a, (int)tiles_n);
+  return hipGetLastError();
+}
+
+template <bool F32>
+hipError_t launch(const F8LinearArgs& a, hipStream_t stream) {
+  if (a.M <= 64) {
+    const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64));
+    fp8_linear_kernel<F32><<<grid, kLinThreads, 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  // the largest tile that still gives every CU one
+  const int64_t cus = 256;
+  auto tiles = [&](int64_t n, int64_t m) { return ((a.N + n - 1) / n) * ((a.M + m - 1) / m); };
+  if (!F32 && tiles(256, 256) >= cus) return launch_tiles<256, 256, 128, 64, false>(a, stream);
+  if (tiles(128, 128) >= cus) return launch_tiles<128, 128, 64, 64, F32>(a, stream);
+  return launch_tiles<64, 64, 32, 32, F32>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_fp8_linear(const F8LinearArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64));
-  auto kernel = a.f32 ? fp8_linear_kernel<true> : fp8_linear_kernel<false>;
-  kernel<<<grid, kLinThreads, 0, stream>>>(a);
-  return hipGetLastError();
+  return a.f32 ? launch<true>(a, stream) : launch<false>(a, stream);
 }
 
 }  // namespace moe
