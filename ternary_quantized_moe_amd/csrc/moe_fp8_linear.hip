@@ -196,6 +196,7 @@ struct Tile {
   static constexpr int kWavesN = BN / WTN, kWaves = kWavesN * (BM / WTM), kThreads = 64 * kWaves;
   static constexpr int TN = WTN / 32, TM = WTM / 32;
   static constexpr int kLoads = (BN + BM) / 8 / kWaves;  // staging loads of a wave per group
+  static constexpr int kPerTile = TN * TM > 1 ? 2 * kLoads / (TN * TM) : kLoads;  // ... and behind a tile's product
   static constexpr int kBufBytes = (BN + BM) * kF8Group;
 
   f32x16 acc[TN][TM], t[2];
@@ -211,12 +212,13 @@ struct Tile {
   // would let the compiler move the additions behind it past it, and keep every
   // product.  The lanes' offsets are made anew each time: kept, they would take
   // eight registers that the products need.
-  __device__ __forceinline__ void stage(uint8_t* buf, int g) const {
+  __device__ __forceinline__ void stage(uint8_t* buf, int g, int first = 0, int last = kLoads) const {
     const int tid = opaque(threadIdx.x), row0 = tid >> 3, piece = 16 * ((tid & 7) ^ swizzle(row0));
     const int bytes = __builtin_amdgcn_readfirstlane((g - groups) >> 31);
     const __amdgpu_buffer_rsrc_t from_w = buffer_of(w, bytes), from_a = buffer_of(a, bytes);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
+      if (i < first || i >= last) continue;
       const bool of_w = i * kWaves < BN / 8;
       const int row = min(row0 + (i * kWaves * 8 - (of_w ? 0 : BN)), of_w ? last_n : last_m);
       load_to_lds(of_w ? from_w : from_a, __umul24(row, K) + piece, g * kF8Group, buf + (wave + i * kWaves) * 1024);
@@ -290,12 +292,14 @@ struct Tile {
   // already read.  A 32 x 32 tile's product is scaled and added while the matrix
   // core works on the next one.  When the last row of tiles has begun, every read
   // of `now` has been made and the next group's bytes have arrived in `then`: the
-  // block meets at the one barrier, `now` takes the loads of group g + 2, a whole
-  // group ahead, and the next group's first operands are read behind the last
-  // tiles' products.  The scheduling barriers keep the compiler from issuing all
-  // products first, whose results would not fit the registers.
+  // block meets at the one barrier and `now` takes the loads of group g + 2, a few
+  // behind each of the next tiles' products, half a group's worth of them (all at
+  // once they cost 10%: they stand in the way of the reads).  The next group's
+  // first operands are read behind the last tiles' products.  The scheduling
+  // barriers keep the compiler from issuing all products first, whose results
+  // would not fit the registers.
   template <int PARITY, class Meet>
-  __device__ __forceinline__ void step(const uint8_t* now, const uint8_t* then, float sw, Meet meet) {
+  __device__ __forceinline__ void step(uint8_t* now, uint8_t* then, int g, float sw, Meet meet) {
     constexpr int N = TN * TM;
   
 
@@ -317,10 +321,12 @@ struct Tile {
       }
       __builtin_amdgcn_sched_barrier(0);
       if (n == N - TM) {
-        meet();
+        meet(g);
         read_w(then, 0, fw[slot ^ 1]);
       }
       if (i == TN - 1) read_a(then, j);
+      const int k = (n + TM) % N * kPerTile;  // the loads go on into the next group's first tiles
+      if (k < kLoads) stage(i == TN - 1 ? now : then, i == TN - 1 ? g + 2 : g + 1, k, k + kPerTile);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -386,19 +392,18 @@ __global__ __launch_bounds__(64 * (BN / WTN) * (BM / WTM), 2) void fp8_tile_kern
   }
   t.read_w(buf0, 0, t.fw[0]);
   t.t[1] = f32x16{};  // no product is pending before the first
-  t.stage(buf1, 1);
-  auto meet = [&](uint8_t* now, int g) {
+  t.stage(buf1, 1, 0, T::TM * T::kPerTile);  // the first of group 1's loads; step 0 goes on with them
+  auto meet = [&](int g) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
     read_scales(min(g + 1, groups - 1));
-    t.stage(now, g + 2);
   };
   int g = 0;
   for (; g + 2 <= groups; g += 2) {
-    t.template step<0>(buf0, buf1, sw[g], [&] { meet(buf0, g); });
-    t.template step<1>(buf1, buf0, sw[g + 1], [&] { meet(buf1, g + 1); });
+    t.template step<0>(buf0, buf1, g, sw[g], meet);
+    t.template step<1>(buf1, buf0, g + 1, sw[g + 1], meet);
   }
-  if (g < groups) t.template step<0>(buf0, buf1, sw[g], [&] { meet(buf0, g); });
+  if (g < groups) t.template step<0>(buf0, buf1, g, sw[g], meet);
   // the last product is pending in t[1], after an odd number of single-tile groups in t[0]
   if (T::TN * T::TM % 2 && g < groups) t.scale_add(T::TN - 1, T::TM - 1, t.t[0], t.s[T::TM - 1]);
   else t.scale_add(T::TN - 1, T::TM - 1, t.t[1], t.s[T::TM - 1]);
