@@ -75,64 +75,103 @@ __device__ __forceinline__ f32x4 group_product(const Frag<true>& w, const Frag<t
   return s;
 }
 
-// Four neighbouring results of one token; `quads`: rows of y keep n's alignment.
-template <bool F32>
-__device__ __forceinline__ void store4(const F8LinearArgs& p, int64_t t, int64_t n, f32x4 v, bool quads) {
-  const int64_t at = t * p.ldy + n;
-  if (quads && n + 4 <= p.N) {
-    if (F32) *(f32x4*)((float*)p.y + at) = v;
-    else *(u32x2*)((uint16_t*)p.y + at) = u32x2{f32x2_to_bf16x2(v.x, v.y), f32x2_to_bf16x2(v.z, v.w)};
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (n + j >= p.N) break;
-      if (F32) ((float*)p.y)[at + j] = v[j];
-      else ((uint16_t*)p.y)[at + j] = (uint16_t)f32_to_bf16(v[j]);
-    }
-  }
-}
+// ------------------------------------------------------------------ streaming kernel
+// Up to 64 tokens: w is the traffic and is read once, straight into registers.  A
+// block takes 16 RT rows of w and every token, its eight waves the groups of K in
+// turn, so each wave has few, independent loads to wait for and 16 rows are enough
+// work for a block (4096 rows fill the card).  A wave keeps two of its groups on
+// the way.  The waves' sums meet in LDS and are added in wave order.
+constexpr int kStreamWaves = 8;
 
-constexpr int kLinThreads = 256;
-
-// 64 rows of w (16 a wave) and 64 tokens per block.
-template <bool F32>
-__global__ __launch_bounds__(kLinThreads) void fp8_linear_kernel(F8LinearArgs p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, q = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * 64 + 16 * wave, m0 = (int64_t)blockIdx.y * 64;
-  if (n0 >= p.N) return;
+template <int MT, int RT, bool F32>
+__global__ __launch_bounds__(64 * kStreamWaves) void fp8_stream_kernel(F8LinearArgs p) {
+  __shared__ float part[kStreamWaves][MT * RT][16][17];  // [wave][tile][token][row], a row of 16 padded by one
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15,
+            q = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
   const int groups = p.K / kF8Group;
-  const uint8_t* w = p.w + min(n0 + c, p.N - 1) * p.K;
-  const float* sw = p.w_scales + n0 / kF8Group * groups;
-  const uint8_t* a[4];
-  const float* sa[4];
+  const uint8_t* w[RT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = min(m0 + 16 * i + c, p.M - 1);
+  for (int r = 0; r < RT; ++r) w[r] = p.w + min(n0 + 16 * r + c, p.N - 1) * p.K;
+  const float* sw = p.w_scales + n0 / kF8Group * groups;
+  const uint8_t* a[MT];
+  const float* sa[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t t = min((int64_t)(16 * i + c), p.M - 1);
     a[i] = p.a + t * p.K;
     sa[i] = p.a_scales + t * groups;
   }
-  f32x4 acc[4] = {};
-  for (int g = 0; g < groups; ++g) {
-    Frag<F32> wf, af;
-    wf.set(load_frag(w + g * kF8Group, q));
+  struct Loads {
+    i32x8 w[RT], a[MT];
+    float sa[MT], sw;
+  } ring[2];
+  auto load = [&](Loads& l, int g) {
+    g = min(g, groups - 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      af.set(load_frag(a[i] + g * kF8Group, q));
-      const f32x4 s = group_product(wf, af);
-      const float f = sa[i][g] * sw[g];
+    for (int r = 0; r < RT; ++r) l.w[r] = load_frag(w[r] + (int64_t)g * kF8Group, q);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] += s[j] * f;
+    for (int i = 0; i < MT; ++i) {
+      l.a[i] = load_frag(a[i] + (int64_t)g * kF8Group, q);
+      l.sa[i] = sa[i][g];
+    }
+    l.sw = sw[g];
+  };
+  f32x4 acc[RT][MT] = {};
+  auto multiply = [&](const Loads& l) {
+    Frag<F32> fw[RT], fa;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) fw[r].set(l.w[r]);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      fa.set(l.a[i]);
+      const float f = l.sa[i] * l.sw;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const f32x4 s = group_product(fw[r], fa);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[r][i][j] += s[j] * f;
+      }
+    }
+  };
+  if (wave < groups) {
+    load(ring[0], wave);
+    load(ring[1], wave + kStreamWaves);
+    for (int g = wave; g < groups; g += 2 * kStreamWaves) {
+      multiply(ring[0]);
+      load(ring[0], g + 2 * kStreamWaves);
+      if (g + kStreamWaves < groups) multiply(ring[1]);
+      load(ring[1], g + 3 * kStreamWaves);
     }
   }
-  const bool quads = (p.ldy % 4 == 0) && ((uintptr_t)p.y % (F32 ? 16 : 8) == 0);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = m0 + 16 * i + c, n = n0 + 4 * q;
-    if (t >= p.M) continue;
-    store4<F32>(p, t, n, acc[i], quads);
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[wave][r * MT + i][c][4 * q + j] = acc[r][i][j];
+  __syncthreads();
+  for (int k = threadIdx.x; k < MT * RT * 256; k += 64 * kStreamWaves) {
+    const int tile = k >> 8, row = k & 15, col = (k >> 4) & 15;
+    const int64_t t = 16 * (tile % MT) + col, n = n0 + 16 * (tile / MT) + row;
+    float y = part[0][tile][col][row];
+#pragma unroll
+    for (int v = 1; v < kStreamWaves; ++v) y += part[v][tile][col][row];
+    if (t < p.M && n < p.N) {
+      if (F32) ((float*)p.y)[t * p.ldy + n] = y;
+      else ((uint16_t*)p.y)[t * p.ldy + n] = (uint16_t)f32_to_bf16(y);
+    }
   }
 }
 
+template <int MT, bool F32>
+hipError_t launch_stream(const F8LinearArgs& a, hipStream_t stream) {
+  const int64_t tiles = (a.N + 15) / 16;
+  const int rt = tiles >= 2048 ? 2 : 1;
+  auto kernel = rt == 2 ? fp8_stream_kernel<MT, 2, F32> : fp8_stream_kernel<MT, 1, F32>;
+  kernel<<<(unsigned)((tiles + rt - 1) / rt), 64 * kStreamWaves, 0, stream>>>(a);
+  return hipGetLastError();
+}
 
 // ------------------------------------------------------------------ tiled kernel
 // A block computes BN rows of w times BM tokens, a wave WTN x WTM of them as 32 x
@@ -191,7 +230,7 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t src, uint32_t
   __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16, (int)lane_off, off, 0, 0);
 }
 
-template <int BN, int BM, int WTN, int WTM, bool F32>
+template <int BN, int BM, int WTN, int WTM, int NB, bool F32>
 struct Tile {
   static constexpr int kWavesN = BN / WTN, kWaves = kWavesN * (BM / WTM), kThreads = 64 * kWaves;
   static constexpr int TN = WTN / 32, TM = WTM / 32;
@@ -201,7 +240,7 @@ struct Tile {
 
   f32x16 acc[TN][TM], t[2];
   Frag<F32> fa[TM][2], fw[2][2];
-  float s[TM], raw[TM];  // the pending products' scales; the tokens' scales of the next group to begin
+  float s[TM], raw[NB][TM];  // the pending products' scales; the tokens' scales of the groups in the buffers
   const uint8_t *w, *a;
   int lane, wave, wn, wm, K, groups, last_n, last_m;
   int at_w, at_a;  // the lane's places in the wave's first 32 rows of w and of a (a tile's rows keep the swizzle)
@@ -292,20 +331,20 @@ struct Tile {
   // already read.  A 32 x 32 tile's product is scaled and added while the matrix
   // core works on the next one.  When the last row of tiles has begun, every read
   // of `now` has been made and the next group's bytes have arrived in `then`: the
-  // block meets at the one barrier and `now` takes the loads of group g + 2, a few
+  // block meets at the one barrier and `now` takes the loads of group g + NB, a few
   // behind each of the next tiles' products, half a group's worth of them (all at
-  // once they cost 10%: they stand in the way of the reads).  The next group's
-  // first operands are read behind the last tiles' products.  The scheduling
-  // barriers keep the compiler from issuing all products first, whose results
-  // would not fit the registers.
-  template <int PARITY, class Meet>
-  __device__ __forceinline__ void step(uint8_t* now, uint8_t* then, int g, float sw, Meet meet) {
+  // once they cost 10%: they stand in the way of the reads); `last` takes the rest
+  // of those that the group before began.  The next group's first operands are
+  // read behind the last tiles' products.  The scheduling barriers keep the
+  // compiler from issuing all products first, whose results would not fit the
+  // registers.
+  template <int SLOT, class Meet, class Scales>
+  __device__ __forceinline__ void step(uint8_t* now, uint8_t* then, uint8_t* last, int g, float sw, Meet meet,
+                                       Scales read_scales) {
     constexpr int N = TN * TM;
-  
-
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const int i = n / TM, j = n % TM, at = PARITY * N + n, slot = (PARITY * TN + i) & 1;
+      const int i = n / TM, j = n % TM, at = SLOT * N + n, slot = (SLOT * TN + i) & 1;
       if (j == 0 && i + 1 < TN) read_w(now, i + 1, fw[slot ^ 1]);
       f32x16& mine = t[at & 1];
       mine = half_product(fw[slot][0], fa[j][0], f32x16{});
@@ -317,28 +356,40 @@ struct Tile {
       } else {  // the last product of the group before, by its own scale
         scale_add(TN - 1, TM - 1, done, s[TM - 1]);
 #pragma unroll
-        for (int k = 0; k < TM; ++k) s[k] = raw[k] * sw;
+        for (int k = 0; k < TM; ++k) s[k] = raw[SLOT][k] * sw;
       }
       __builtin_amdgcn_sched_barrier(0);
       if (n == N - TM) {
-        meet(g);
+        meet();
         read_w(then, 0, fw[slot ^ 1]);
+        read_scales(raw[SLOT], g + NB);
       }
       if (i == TN - 1) read_a(then, j);
       const int k = (n + TM) % N * kPerTile;  // the loads go on into the next group's first tiles
-      if (k < kLoads) stage(i == TN - 1 ? now : then, i == TN - 1 ? g + 2 : g + 1, k, k + kPerTile);
+      if (k < kLoads) stage(i == TN - 1 ? now : last, i == TN - 1 ? g + NB : g + NB - 1, k, k + kPerTile);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 };
 
-template <int BN, int BM, int WTN, int WTM, bool F32>
+// The block meets when every wave has at most N loads on their way and its LDS
+// operations are done.  (__syncthreads() would wait for every staging load.)
+template <int N>
+__device__ __forceinline__ void meet_with_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <int BN, int BM, int WTN, int WTM, int NB, bool F32>
 __global__ __launch_bounds__(64 * (BN / WTN) * (BM / WTM), 2) void fp8_tile_kernel(F8LinearArgs p, int tiles_n) {
-  typedef Tile<BN, BM, WTN, WTM, F32> T;
+  typedef Tile<BN, BM, WTN, WTM, NB, F32> T;
   static_assert((BN / 8) % T::kWaves == 0 && (BM / 8) % T::kWaves == 0 && T::kWaves % 2 == 0,
                 "a wave's staging loads split evenly, 16 rows or a multiple apart");
+  static_assert(NB == 2 || NB == 4, "an even number of buffers, as step() counts them");
+  // separate arrays: the compiler sees that a read does not wait for the loads of another buffer
   __shared__ __attribute__((aligned(1024))) uint8_t buf0[T::kBufBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t buf1[T::kBufBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t buf2[NB == 4 ? T::kBufBytes : 1024];
+  __shared__ __attribute__((aligned(1024))) uint8_t buf3[NB == 4 ? T::kBufBytes : 1024];
   // consecutive blocks go to the eight XCDs in turn: each XCD takes a contiguous
   // run of tiles, whose rows of w and a meet in its L2
   const int tiles = gridDim.x, per = (tiles + 7) / 8, rest = tiles % 8 ? tiles % 8 : 8;
@@ -374,17 +425,21 @@ __global__ __launch_bounds__(64 * (BN / WTN) * (BM / WTM), 2) void fp8_tile_kern
   // constant address space: the wave's scales of w come through scalar loads
   const auto sw = (const __attribute__((address_space(4))) float*)(p.w_scales +
                                                                    min(n0 + t.wn * WTN, p.N - 1) / kF8Group * groups);
-  auto read_scales = [&](int g) {
+  auto read_scales = [&](float (&to)[T::TM], int g) {
     const int token = t.wm * WTM + (opaque(threadIdx.x) & 31);
 #pragma unroll
     for (int j = 0; j < T::TM; ++j)
-      t.raw[j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                               sa, 4 * __umul24(min(token + 32 * j, last_m), groups), 4 * g, 0));
+      to[j] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(sa, 4 * __umul24(min(token + 32 * j, last_m), groups),
+                                                      4 * min(g, groups - 1), 0));
   };
-  read_scales(0);
-  t.stage(buf0, 0);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
+  // groups 0 .. NB - 1 begin; of the last one as much as step 0 does not go on with
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    read_scales(t.raw[i], i);
+    t.stage(i == 0 ? buf0 : i == 1 ? buf1 : i == 2 ? buf2 : buf3, i, 0, i < NB - 1 ? T::kLoads : T::TM * T::kPerTile);
+  }
+  meet_with_loads<(NB - 2) * T::kLoads>();
 #pragma unroll
   for (int j = 0; j < T::TM; ++j) {
     t.read_a(buf0, j);
@@ -392,49 +447,48 @@ __global__ __launch_bounds__(64 * (BN / WTN) * (BM / WTM), 2) void fp8_tile_kern
   }
   t.read_w(buf0, 0, t.fw[0]);
   t.t[1] = f32x16{};  // no product is pending before the first
-  t.stage(buf1, 1, 0, T::TM * T::kPerTile);  // the first of group 1's loads; step 0 goes on with them
-  auto meet = [&](int g) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    read_scales(min(g + 1, groups - 1));
-  };
+  // the loads of the NB - 2 groups after the next may go on
+  auto meet = [&] { meet_with_loads<(NB - 2) * T::kLoads>(); };
   int g = 0;
-  for (; g + 2 <= groups; g += 2) {
-    t.template step<0>(buf0, buf1, g, sw[g], meet);
-    t.template step<1>(buf1, buf0, g + 1, sw[g + 1], meet);
+  for (; g + NB <= groups; g += NB) {
+    t.template step<0>(buf0, buf1, NB == 2 ? buf1 : buf3, g, sw[g], meet, read_scales);
+    t.template step<1>(buf1, NB == 2 ? buf0 : buf2, buf0, g + 1, sw[g + 1], meet, read_scales);
+    if (NB == 4) {
+      t.template step<2 % NB>(buf2, buf3, buf1, g + 2, sw[g + 2], meet, read_scales);
+      t.template step<3 % NB>(buf3, buf0, buf2, g + 3, sw[g + 3], meet, read_scales);
+    }
   }
-  if (g < groups) t.template step<0>(buf0, buf1, g, sw[g], meet);
+  if (g < groups) t.template step<0>(buf0, buf1, NB == 2 ? buf1 : buf3, g, sw[g], meet, read_scales);
+  if (NB == 4 && g + 1 < groups) t.template step<1>(buf1, buf2, buf0, g + 1, sw[g + 1], meet, read_scales);
+  if (NB == 4 && g + 2 < groups) t.template step<2 % NB>(buf2, buf3, buf1, g + 2, sw[g + 2], meet, read_scales);
   // the last product is pending in t[1], after an odd number of single-tile groups in t[0]
-  if (T::TN * T::TM % 2 && g < groups) t.scale_add(T::TN - 1, T::TM - 1, t.t[0], t.s[T::TM - 1]);
+  if (T::TN * T::TM % 2 && groups % 2) t.scale_add(T::TN - 1, T::TM - 1, t.t[0], t.s[T::TM - 1]);
   else t.scale_add(T::TN - 1, T::TM - 1, t.t[1], t.s[T::TM - 1]);
   // no staging load is on its way any more: each wave turns its results round in
   // its share of the buffers and writes whole lines of y
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
+  meet_with_loads<0>();
   t.store(p, t.wave < T::kWaves / 2 ? buf0 : buf1, m0 + t.wm * WTM, n0 + t.wn * WTN);
 }
 
-template <int BN, int BM, int WTN, int WTM, bool F32>
+template <int BN, int BM, int WTN, int WTM, int NB, bool F32>
 hipError_t launch_tiles(const F8LinearArgs& a, hipStream_t stream) {
   const int64_t tiles_n = (a.N + BN - 1) / BN, tiles = tiles_n * ((a.M + BM - 1) / BM);
-  fp8_tile_kernel<BN, BM, WTN, WTM, F32>
-      <<<(unsigned)tiles, Tile<BN, BM, WTN, WTM, F32>::kThreads, 0, stream>>>(a, (int)tiles_n);
+  fp8_tile_kernel<BN, BM, WTN, WTM, NB, F32>
+      <<<(unsigned)tiles, Tile<BN, BM, WTN, WTM, NB, F32>::kThreads, 0, stream>>>(a, (int)tiles_n);
   return hipGetLastError();
 }
 
 template <bool F32>
 hipError_t launch(const F8LinearArgs& a, hipStream_t stream) {
-  if (a.M <= 64) {
-    const dim3 grid((unsigned)((a.N + 63) / 64), (unsigned)((a.M + 63) / 64));
-    fp8_linear_kernel<F32><<<grid, kLinThreads, 0, stream>>>(a);
-    return hipGetLastError();
-  }
+  if (a.M <= 16) return launch_stream<1, F32>(a, stream);
+  if (a.M <= 32) return launch_stream<2, F32>(a, stream);
+  if (a.M <= 64) return launch_stream<4, F32>(a, stream);
   // the largest tile that still gives every CU one
   const int64_t cus = 256;
   auto tiles = [&](int64_t n, int64_t m) { return ((a.N + n - 1) / n) * ((a.M + m - 1) / m); };
-  if (!F32 && tiles(256, 256) >= cus) return launch_tiles<256, 256, 128, 64, false>(a, stream);
-  if (tiles(128, 128) >= cus) return launch_tiles<128, 128, 64, 64, F32>(a, stream);
-  return launch_tiles<64, 64, 32, 32, F32>(a, stream);
+  if (!F32 && tiles(256, 256) >= cus) return launch_tiles<256, 256, 128, 64, 2, false>(a, stream);
+  if (tiles(128, 128) >= cus) return launch_tiles<128, 128, 64, 64, 2, F32>(a, stream);
+  return launch_tiles<64, 64, 32, 32, 4, F32>(a, stream);
 }
 
 }  // namespace
