@@ -36,12 +36,6 @@ __device__ __forceinline__ f32x4 mfma_f8_16(i32x8 a, i32x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);
 }
 
-// Lane quarter q's 32 bytes of one group: bytes 16 q .. + 15 and 64 + 16 q .. + 15.
-__device__ __forceinline__ i32x8 load_frag(const uint8_t* row, int q) {
-  const u32x4 lo = *(const u32x4*)(row + 16 * q), hi = *(const u32x4*)(row + 64 + 16 * q);
-  return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
-}
-
 // Four e4m3 codes -> four bf16 (exact).
 __device__ __forceinline__ u32x2 widen_f8x4(int v) {
   return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false)),
@@ -73,104 +67,6 @@ __device__ __forceinline__ f32x4 group_product(const Frag<true>& w, const Frag<t
 #pragma unroll
   for (int i = 0; i < 4; ++i) s = mfma16(w.v[i], a.v[i], s);
   return s;
-}
-
-// ------------------------------------------------------------------ streaming kernel
-// Up to 64 tokens: w is the traffic and is read once, straight into registers.  A
-// block takes 16 RT rows of w and every token, its eight waves the groups of K in
-// turn, so each wave has few, independent loads to wait for and 16 rows are enough
-// work for a block (4096 rows fill the card).  A wave keeps two of its groups on
-// the way.  The waves' sums meet in LDS and are added in wave order.
-constexpr int kStreamWaves = 8;
-
-template <int MT, int RT, bool F32>
-__global__ __launch_bounds__(64 * kStreamWaves) void fp8_stream_kernel(F8LinearArgs p) {
-  __shared__ float part[kStreamWaves][MT * RT][16][17];  // [wave][tile][token][row], a row of 16 padded by one
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15,
-            q = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT);
-  const int groups = p.K / kF8Group;
-  const uint8_t* w[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) w[r] = p.w + min(n0 + 16 * r + c, p.N - 1) * p.K;
-  const float* sw = p.w_scales + n0 / kF8Group * groups;
-  const uint8_t* a[MT];
-  const float* sa[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const int64_t t = min((int64_t)(16 * i + c), p.M - 1);
-    a[i] = p.a + t * p.K;
-    sa[i] = p.a_scales + t * groups;
-  }
-  struct Loads {
-    i32x8 w[RT], a[MT];
-    float sa[MT], sw;
-  } ring[2];
-  auto load = [&](Loads& l, int g) {
-    g = min(g, groups - 1);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) l.w[r] = load_frag(w[r] + (int64_t)g * kF8Group, q);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      l.a[i] = load_frag(a[i] + (int64_t)g * kF8Group, q);
-      l.sa[i] = sa[i][g];
-    }
-    l.sw = sw[g];
-  };
-  f32x4 acc[RT][MT] = {};
-  auto multiply = [&](const Loads& l) {
-    Frag<F32> fw[RT], fa;
-#pragma unroll
-    for (int r = 0; r < RT; ++r) fw[r].set(l.w[r]);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      fa.set(l.a[i]);
-      const float f = l.sa[i] * l.sw;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const f32x4 s = group_product(fw[r], fa);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[r][i][j] += s[j] * f;
-      }
-    }
-  };
-  if (wave < groups) {
-    load(ring[0], wave);
-    load(ring[1], wave + kStreamWaves);
-    for (int g = wave; g < groups; g += 2 * kStreamWaves) {
-      multiply(ring[0]);
-      load(ring[0], g + 2 * kStreamWaves);
-      if (g + kStreamWaves < groups) multiply(ring[1]);
-      load(ring[1], g + 3 * kStreamWaves);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) part[wave][r * MT + i][c][4 * q + j] = acc[r][i][j];
-  __syncthreads();
-  for (int k = threadIdx.x; k < MT * RT * 256; k += 64 * kStreamWaves) {
-    const int tile = k >> 8, row = k & 15, col = (k >> 4) & 15;
-    const int64_t t = 16 * (tile % MT) + col, n = n0 + 16 * (tile / MT) + row;
-    float y = part[0][tile][col][row];
-#pragma unroll
-    for (int v = 1; v < kStreamWaves; ++v) y += part[v][tile][col][row];
-    if (t < p.M && n < p.N) {
-      if (F32) ((float*)p.y)[t * p.ldy + n] = y;
-      else ((uint16_t*)p.y)[t * p.ldy + n] = (uint16_t)f32_to_bf16(y);
-    }
-  }
-}
-
-template <int MT, bool F32>
-hipError_t launch_stream(const F8LinearArgs& a, hipStream_t stream) {
-  const int64_t tiles = (a.N + 15) / 16;
-  const int rt = tiles >= 2048 ? 2 : 1;
-  auto kernel = rt == 2 ? fp8_stream_kernel<MT, 2, F32> : fp8_stream_kernel<MT, 1, F32>;
-  kernel<<<(unsigned)((tiles + rt - 1) / rt), 64 * kStreamWaves, 0, stream>>>(a);
-  return hipGetLastError();
 }
 
 // ------------------------------------------------------------------ tiled kernel
@@ -478,17 +374,151 @@ hipError_t launch_tiles(const F8LinearArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// ------------------------------------------------------------------ split kernel
+// Few tokens and few rows of w: too few tiles to fill the card, and K the only
+// axis left to share out.  A block takes 16 RT rows of w and 16 MT tokens, its
+// eight waves the groups of K in turn.  Each wave stages its own groups in LDS
+// (loads of whole lines: straight into registers a load would touch 16 rows, and
+// ran at half the rate), two at a time, and waits for nobody; the waves' sums meet
+// in LDS at the end and are added in wave order.
+constexpr int kSplitWaves = 8;
+
+template <int RT, int MT, bool F32>
+__global__ __launch_bounds__(64 * kSplitWaves) void fp8_split_kernel(F8LinearArgs p) {
+  constexpr int ROWS = 16 * (RT + MT), LOADS = ROWS / 8, BYTES = kSplitWaves * ROWS * kF8Group;
+  typedef float Part[RT * MT][16][17];  // [tile][token][row], a row of 16 padded by one
+  static_assert(sizeof(Part) * kSplitWaves <= BYTES, "the sums fit a buffer");
+  __shared__ __attribute__((aligned(1024))) uint8_t buf0[BYTES];
+  __shared__ __attribute__((aligned(1024))) uint8_t buf1[BYTES];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c = lane & 15,
+            q = lane >> 4;
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * RT), m0 = (int64_t)blockIdx.y * (16 * MT);
+  const int groups = p.K / kF8Group;
+  const int last_n = (int)min((int64_t)16 * RT, p.N - n0) - 1, last_m = (int)min((int64_t)16 * MT, p.M - m0) - 1;
+  uint32_t off[LOADS];
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) {  // rows past the matrix repeat its last row; their results are not stored
+    const int row = 8 * i + (lane >> 3);
+    off[i] = __umul24(i < 2 * RT ? min(row, last_n) : min(row - 16 * RT, last_m), p.K) +
+             16 * ((lane & 7) ^ swizzle(row));
+  }
+  const __amdgpu_buffer_rsrc_t scales = buffer_of(p.a_scales + m0 * groups);
+  const auto sw = (const __attribute__((address_space(4))) float*)(p.w_scales + n0 / kF8Group * groups);
+  float s0[MT], s1[MT];
+  auto load = [&](uint8_t* buf, float (&s)[MT], int g) {  // past the last group nothing is loaded
+    const int at = min(g, groups - 1), bytes = __builtin_amdgcn_readfirstlane((g - groups) >> 31);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      s[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                           scales, 4 * __umul24(min(16 * i + c, last_m), groups), 4 * at, 0));
+    const __amdgpu_buffer_rsrc_t from_w = buffer_of(p.w + n0 * p.K, bytes), from_a = buffer_of(p.a + m0 * p.K, bytes);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i)
+      load_to_lds(i < 2 * RT ? from_w : from_a, off[i], at * kF8Group, buf + (wave * ROWS + 8 * i) * kF8Group);
+  };
+  f32x4 acc[RT][MT] = {};
+  auto multiply = [&](const uint8_t* buf, const float (&s)[MT], int g) {
+    const float of_w = sw[g];
+    // lane quarter q's 32 bytes of a row: pieces 2 q and the next
+    const uint8_t* at = buf + wave * ROWS * kF8Group + c * kF8Group;
+    const int first = 16 * ((2 * q) ^ swizzle(c));
+    auto frag = [&](int tile) {
+      const u32x4 lo = *(const u32x4*)(at + tile * 16 * kF8Group + first),
+                  hi = *(const u32x4*)(at + tile * 16 * kF8Group + (first ^ 16));
+      Frag<F32> f;
+      f.set(i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w});
+      return f;
+    };
+    Frag<F32> fw[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) fw[r] = frag(r);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const Frag<F32> fa = frag(RT + i);
+      const float f = s[i] * of_w;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const f32x4 t = group_product(fw[r], fa);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[r][i][j] += t[j] * f;
+      }
+    }
+  };
+  // this wave's loads of one buffer have arrived (those of the other may go on);
+  // its reads of a buffer are done before new loads write there
+  auto arrived = [] { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory"); };
+  auto read = [] { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
+  load(buf0, s0, wave);
+  load(buf1, s1, wave + kSplitWaves);
+  for (int g = wave; g < groups; g += 2 * kSplitWaves) {
+    arrived();
+    multiply(buf0, s0, g);
+    read();
+    load(buf0, s0, g + 2 * kSplitWaves);
+    arrived();
+    if (g + kSplitWaves < groups) multiply(buf1, s1, g + kSplitWaves);
+    read();
+    load(buf1, s1, g + 3 * kSplitWaves);
+  }
+  meet_with_loads<0>();
+  Part* part = (Part*)buf0;
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) part[wave][r * MT + i][c][4 * q + j] = acc[r][i][j];
+  __syncthreads();
+  for (int k = threadIdx.x; k < MT * RT * 256; k += 64 * kSplitWaves) {
+    const int tile = k >> 8, row = k & 15, col = (k >> 4) & 15;
+    const int64_t t = m0 + 16 * (tile % MT) + col, n = n0 + 16 * (tile / MT) + row;
+    float y = part[0][tile][col][row];
+#pragma unroll
+    for (int v = 1; v < kSplitWaves; ++v) y += part[v][tile][col][row];
+    if (t < p.M && n < p.N) {
+      if (F32) ((float*)p.y)[t * p.ldy + n] = y;
+      else ((uint16_t*)p.y)[t * p.ldy + n] = (uint16_t)f32_to_bf16(y);
+    }
+  }
+}
+
+template <int RT, int MT, bool F32>
+hipError_t launch_split(const F8LinearArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.N + 16 * RT - 1) / (16 * RT)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+  fp8_split_kernel<RT, MT, F32><<<grid, 64 * kSplitWaves, 0, stream>>>(a);
+  return hipGetLastError();
+}
+
+// The largest tile of which there are enough for three quarters of the 256 CUs,
+// whose token side is not half empty: a larger tile reads less per product, but
+// each takes its time alone.  Microseconds for 4096 x 4096 x 4096, 1024 x 4096 x
+// 4096, 512 x 4096 x 4096 and 333 x 2561 x 4096 tokens x rows x K to bf16:
+//   256 x 256   73   -    -    -       (fp32 results do not fit the registers)
+//   128 x 128   94   26   22   23
+//   128 x 64    -    36   19   19
+//    64 x 64    -    39   21   14
+// Four buffers where a CU has one block (1024 tokens: 26 us, two: 29), two where
+// a second block fills the gaps (2048 x 4096 x 2048: 25.5 us, four: 28).  Where even
+// the small tiles are too few, the split kernel with the largest block that there
+// are 256 of (64 x 1024 x 8192: 6.9 us, 64 x 32 tiles 19; 64 x 8192 x 4096: 16, tiles 12).
 template <bool F32>
 hipError_t launch(const F8LinearArgs& a, hipStream_t stream) {
-  if (a.M <= 16) return launch_stream<1, F32>(a, stream);
-  if (a.M <= 32) return launch_stream<2, F32>(a, stream);
-  if (a.M <= 64) return launch_stream<4, F32>(a, stream);
-  // the largest tile that still gives every CU one
-  const int64_t cus = 256;
-  auto tiles = [&](int64_t n, int64_t m) { return ((a.N + n - 1) / n) * ((a.M + m - 1) / m); };
-  if (!F32 && tiles(256, 256) >= cus) return launch_tiles<256, 256, 128, 64, 2, false>(a, stream);
-  if (tiles(128, 128) >= cus) return launch_tiles<128, 128, 64, 64, 2, F32>(a, stream);
-  return launch_tiles<64, 64, 32, 32, 4, F32>(a, stream);
+  constexpr int64_t CUS = 256;
+  auto blocks = [&](int64_t n, int64_t m) { return ((a.N + n - 1) / n) * ((a.M + m - 1) / m); };
+  auto fills = [&](int64_t n, int64_t m) { return m < 2 * a.M && 4 * blocks(n, m) >= 3 * CUS; };
+  if (!F32 && fills(256, 256)) return launch_tiles<256, 256, 128, 64, 2, false>(a, stream);
+  if (fills(128, 128))
+    return blocks(128, 128) <= CUS ? launch_tiles<128, 128, 64, 32, 4, F32>(a, stream)
+                                   : launch_tiles<128, 128, 64, 32, 2, F32>(a, stream);
+  if (fills(128, 64))
+    return blocks(128, 64) <= CUS ? launch_tiles<128, 64, 64, 32, 4, F32>(a, stream)
+                                  : launch_tiles<128, 64, 64, 32, 2, F32>(a, stream);
+  if (fills(64, 64)) return launch_tiles<64, 64, 32, 32, 4, F32>(a, stream);
+  if (a.M <= 32 && fills(128, 32)) return launch_tiles<128, 32, 32, 32, 4, F32>(a, stream);
+  if (fills(64, 32)) return launch_tiles<64, 32, 32, 32, 4, F32>(a, stream);
+  if (a.M > 16 && blocks(32, 32) >= CUS) return launch_split<2, 2, F32>(a, stream);
+  if (blocks(32, 16) >= CUS) return launch_split<2, 1, F32>(a, stream);
+  return launch_split<1, 1, F32>(a, stream);
 }
 
 }  // namespace
