@@ -507,11 +507,13 @@ hipError_t launch(const F8LinearArgs& a, hipStream_t stream) {
   auto blocks = [&](int64_t n, int64_t m) { return ((a.N + n - 1) / n) * ((a.M + m - 1) / m); };
   auto fills = [&](int64_t n, int64_t m) { return m < 2 * a.M && 4 * blocks(n, m) >= 3 * CUS; };
   if (!F32 && fills(256, 256)) return launch_tiles<256, 256, 128, 64, 2, false>(a, stream);
+  if (F32 && fills(128, 128) && blocks(128, 128) > CUS)  // larger wave tiles: fewer operands to widen
+    return launch_tiles<128, 128, 64, 64, 2, true>(a, stream);
   if (fills(128, 128))
     return blocks(128, 128) <= CUS ? launch_tiles<128, 128, 64, 32, 4, F32>(a, stream)
                                    : launch_tiles<128, 128, 64, 32, 2, F32>(a, stream);
   if (fills(128, 64))
-    return blocks(128, 64) <= CUS ? launch_tiles<128, 64, 64, 32, 4, F32>(a, stream)
+    return blocks(128, 64) <= CUS ? launch_tiles<128, 64, 32, 32, 4, F32>(a, stream)
                                   : launch_tiles<128, 64, 64, 32, 2, F32>(a, stream);
   if (fills(64, 64)) return launch_tiles<64, 64, 32, 32, 4, F32>(a, stream);
   if (a.M <= 32 && fills(128, 32)) return launch_tiles<128, 32, 32, 32, 4, F32>(a, stream);
