@@ -286,7 +286,7 @@ int32_t moe_fp8_linear(const uint8_t* a, const float* a_scales, int64_t m, const
  *                (NULL if that is 0)
  * Weights are fp64 and sums 64-bit integers in units of 2^-42 of l_max's weight,
  * so no result depends on an order of additions; a token of less than half a unit
- * has no mass.  vocab is at most 2^21.  batch = 0 is a no-op.  Ordered on
+ * has no mass.  vocab is at most 2^21, batch 2^22.  batch = 0 is a no-op.  Ordered on
  * `stream`; nothing is allocated.  Errors: MOE_E_FORMAT (type), MOE_E_SHAPE,
  * MOE_E_ARG, MOE_E_SPACE, MOE_E_DEVICE. */
 int64_t moe_sample_workspace_bytes(int64_t batch, int32_t vocab);

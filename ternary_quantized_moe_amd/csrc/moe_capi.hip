@@ -441,7 +441,7 @@ int32_t moe_fp8_linear(const uint8_t* a, const float* a_scales, int64_t M, const
 }
 
 int64_t moe_sample_workspace_bytes(int64_t batch, int32_t vocab) {
-  if (batch < 0 || batch > 0x7FFFFFFFll || vocab <= 0 || vocab > moe::kSampleMaxVocab) return -1;
+  if (batch < 0 || batch > moe::kSampleMaxBatch || vocab <= 0 || vocab > moe::kSampleMaxVocab) return -1;
   return moe::sample_workspace_bytes(batch, vocab);
 }
 
@@ -452,7 +452,8 @@ int32_t moe_sample(int32_t type, const void* logits, int64_t batch, int32_t voca
     return fail(MOE_E_FORMAT, "unknown logit type %d", (int)type);
   if (vocab <= 0 || vocab > moe::kSampleMaxVocab)
     return fail(MOE_E_SHAPE, "vocabulary %d outside [1, %lld]", (int)vocab, (long long)moe::kSampleMaxVocab);
-  if (batch < 0 || batch > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "batch %lld outside [0, 2^31)", (long long)batch);
+  if (batch < 0 || batch > moe::kSampleMaxBatch)
+    return fail(MOE_E_SHAPE, "batch %lld outside [0, %lld]", (long long)batch, (long long)moe::kSampleMaxBatch);
   if (ld < vocab || ld > ((int64_t)1 << 31))
     return fail(MOE_E_SHAPE, "row stride %lld below the vocabulary or above 2^31", (long long)ld);
   if (batch == 0) return ok();

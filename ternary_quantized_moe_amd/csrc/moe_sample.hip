@@ -267,39 +267,552 @@ struct Row {
   }
 };
 
+// The whole row by radix descents alone: right for every row, and taken where the
+// histogram below does not hold the answer.
 template <int TYPE>
-__global__ __launch_bounds__(kSampThreads) void sample_kernel(SampleArgs a) {
-  __shared__ Shared s;
+__device__ void solve_by_radix(Row<TYPE>& row, Weigher& w, int k, double p, double mp, double u, int& token,
+                               double& prob) {
+  Prefix keep{0, row.V - 1, 0.0};
+  if (k > 0 && k < row.V) keep = row.template find<true>(w, keep, (uint64_t)k);
+  if (p < 1.0) {
+    const uint64_t all = row.total(w, keep);
+    const double x = ceil(p * (double)all);
+    keep = row.template find<false>(w, keep, x >= 1.0 ? (uint64_t)x : 1);
+  }
+  if (mp > 0.0) keep.floor = mp;
+  const uint64_t all = row.total(w, keep);
+  const double x = floor(u * (double)all) + 1.0;
+  const uint64_t target = x >= (double)all ? all : x >= 1.0 ? (uint64_t)x : 1;
+  const Prefix at = row.template find<false>(w, keep, target);
+  token = at.last;
+  prob = w.weight(at.key) / ((double)all / kMassUnit);
+}
+
+// ------------------------------------------------------------------ histograms
+// One read of the logits: blocks take a chunk of a row each, keep it in registers
+// for its largest value, and count it into 512 bins of 1 / 16 nat below that, on a
+// grid that all chunks of the row share (bin edges are multiples of 1 / 16 of l / T).
+// A bin holds a count and a mass: the weight of a token relative to its bin's upper
+// edge lies in (e^-1/16, 1] and is rounded to 35 bits, so a chunk's sums are exact
+// in whatever order they come, count and mass in one 64-bit number.  32 nats below
+// the chunk's largest value a token has no mass (2^-46 of it).
+constexpr int kBins = 512;
+constexpr double kPerNat = 16.0, kBinUnit = 34359738368.0;  // 2^35
+constexpr int kCountShift = 50;                            // 2^13 tokens of at most 2^35 below it
+constexpr int kScanThreads = 256;
+constexpr double kFarthestBin = 1099511627776.0;           // 2^40: beyond, the grid is not exact enough
+
+struct ChunkHead {
+  uint64_t top;  // largest key, then the complement of its lowest index
+  double edge;   // number of the top bin, floor(16 l / T)
+};
+
+// l / T on the grid: the bin number, and the weight in units of 2^-35 relative to
+// the bin's upper edge.
+struct Grid {
+  double per;  // 16 / T
+  __device__ __forceinline__ double bin(float l) const { return floor((double)l * per); }
+  __device__ __forceinline__ uint64_t unit(float l, double bin) const {
+    // e^x on [-1/16, 0] by its series: the first term left out is 6e-15 of it
+    const double x = fma((double)l, per, -(bin + 1.0)) * (1.0 / kPerNat);
+    double e = 1.0 / 5040;
+    e = fma(e, x, 1.0 / 720);
+    e = fma(e, x, 1.0 / 120);
+    e = fma(e, x, 1.0 / 24);
+    e = fma(e, x, 1.0 / 6);
+    e = fma(e, x, 0.5);
+    e = fma(e, x, 1.0);
+    e = fma(e, x, 1.0);
+    // adding 2^52 leaves the rounded integer in the low bits
+    return (uint64_t)__double_as_longlong(fma(e, kBinUnit, 4503599627370496.0)) & ((1ull << 52) - 1);
+  }
+};
+
+__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v = max_u64(v, __shfl_xor(v, o, 64));
+  return v;
+}
+
+// VE neighbouring logits of a row from index i on; past the row -inf.
+template <int TYPE>
+struct Vec {
+  static constexpr int VE = TYPE == kSampleF32 ? 4 : 8;
+  float v[VE];
+  __device__ __forceinline__ void load(const void* row, int i, int V) {
+    typedef typename Logit<TYPE>::T T;
+    const T* p = (const T*)row + i;
+    if (i + VE <= V) {
+      if (TYPE == kSampleF32) {
+        const u32x4_a4 w = *(const u32x4_a4*)p;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) v[k] = __uint_as_float(w[k & 3]);
+      } else {  // rows of 16-bit logits are only 2-byte aligned
+        typedef u32x4 __attribute__((aligned(2))) u32x4_a2;
+        const u32x4 w = *(const u32x4_a2*)p;
+#pragma unroll
+        for (int k = 0; k < VE; ++k) v[k] = Logit<TYPE>::f32((T)(w[(k / 2) & 3] >> (16 * (k & 1))));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < VE; ++k) v[k] = i + k < V ? Logit<TYPE>::f32(p[k]) : -__builtin_inff();
+    }
+  }
+};
+
+template <int TYPE, int PT>
+__global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a, int chunks, ChunkHead* heads,
+                                                                   uint64_t* hists) {
+  constexpr int VE = Vec<TYPE>::VE, N = PT / VE;
+  __shared__ uint64_t hist[kBins];
+  __shared__ uint64_t tops[kScanThreads / 64];
+  const int64_t b = blockIdx.x / chunks;
+  const int chunk = (int)(blockIdx.x - b * chunks), base = chunk * (kScanThreads * PT);
+  const void* row = (const typename Logit<TYPE>::T*)a.logits + b * a.ld;
+  Vec<TYPE> x[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) x[j].load(row, base + (j * kScanThreads + (int)threadIdx.x) * VE, a.V);
+  const float t = a.temperature ? a.temperature[b] : 1.0f;
+  const int k = a.top_k ? a.top_k[b] : 0;
+  uint64_t top = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const int i = base + (j * kScanThreads + (int)threadIdx.x) * VE + e;
+      if (i < a.V) top = max_u64(top, (uint64_t)key_of(x[j].v[e]) << 32 | (uint32_t)~i);
+    }
+  top = wave_max(top);
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+#pragma unroll
+  for (int i = 0; i < kBins; i += kScanThreads) hist[i + threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kScanThreads / 64; ++w) top = max_u64(top, tops[w]);
+  const Grid grid{kPerNat / (double)t};
+  const double edge = grid.bin(logit_of((uint32_t)(top >> 32)));
+  if (threadIdx.x == 0) heads[blockIdx.x] = ChunkHead{top, edge};
+  // the first token needs no histogram; a grid too far out is not exact
+  if (!(t > 0.f) || k == 1 || !(fabs(edge) <= kFarthestBin)) return;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float l = x[j].v[e];
+      const double bin = grid.bin(l), d = edge - bin;
+      if (d < (double)kBins)  // not for -inf and NaN
+        atomicAdd((unsigned long long*)&hist[(int)d], (unsigned long long)(grid.unit(l, bin) + (1ull << kCountShift)));
+    }
+  __syncthreads();
+  uint64_t* out = hists + (int64_t)blockIdx.x * kBins;
+#pragma unroll
+  for (int i = 0; i < kBins; i += kScanThreads) out[i + threadIdx.x] = hist[i + threadIdx.x];
+}
+
+// ------------------------------------------------------------------ the choice
+// One block per row: the chunks' histograms added up say in which bin of the order
+// each filter ends and the answer lies.  Mostly the tokens down to the last bin that
+// can matter are few: they are collected, sorted by counting how many come before
+// each, and the filters are read off their running sums.  Otherwise each border
+// bin's tokens are collected alone and the place among them is found by bins of
+// their order (logit, then index).  What does not fit that either (a bin of more
+// tokens than the list holds) goes through the radix descents over the whole row.
+constexpr int kList = 8192;   // tokens collected at a time
+constexpr int kSorted = 1024;
+
+struct Pick {
+  union {
+    Shared radix;
+    struct {
+      uint64_t order[kList];  // complement of the key, then the index: rising in the order of tokens
+      uint64_t hist[kRadix];
+    } s;
+    struct {
+      uint64_t order[kList];
+      uint64_t sorted[kSorted];
+      double mass[kSorted];
+    } few;
+  };
+  uint32_t count[kBins];  // tokens in the bins up to and with this one
+  double mass[kBins];     // and their mass, relative to the largest weight
+  uint64_t wave_u64[kSampWaves], wave_min[kSampWaves];
+  double wave_f64[kSampWaves];
+  uint32_t wave_u32[kSampWaves];
+  uint64_t before;
+  int n, found;
+};
+
+__device__ __forceinline__ double scan_f64(double v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const double t = __shfl_up(v, o, 64);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+
+template <int TYPE>
+struct Picker {
+  const void* row;
+  int V, chunks, chunk_len;
+  const ChunkHead* heads;
+  const uint64_t* hists;
+  Pick& s;
+  Grid grid;
+  double edge, top;  // the row's top bin, its largest l / T
+
+  // Weight of a bin's unit: e^(upper edge - top) 2^-35.
+  __device__ __forceinline__ double unit_of(int bin) const {
+    return exp((edge - (double)bin + 1.0) / kPerNat - top) / kBinUnit;
+  }
+  __device__ __forceinline__ double weight(float l) const { return exp((double)l * grid.per / kPerNat - top); }
+
+  // The row's running counts and masses from the chunks' histograms.
+  __device__ void merge() {
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    uint64_t m = 0;
+    uint32_t c = 0;
+    if (t < kBins) {
+      for (int i = 0; i < chunks; ++i) {
+        const double d = edge - heads[i].edge;  // uniform; chunks whose top bin is out of reach have no histogram
+        if (!(d < (double)kBins)) continue;
+        const int at = t - (int)d;
+        if (at >= 0) {
+          const uint64_t h = hists[(int64_t)i * kBins + at];
+          m += h & ((1ull << kCountShift) - 1);
+          c += (uint32_t)(h >> kCountShift);
+        }
+      }
+    }
+    uint32_t ci = scan_u32(c, lane);
+    double mi = scan_f64(t < kBins ? (double)m * unit_of(t) : 0.0, lane);
+    if (lane == 63) {
+      s.wave_u32[wave] = ci;
+      s.wave_f64[wave] = mi;
+    }
+    __syncthreads();
+    for (int i = 0; i < wave; ++i) {
+      ci += s.wave_u32[i];
+      mi += s.wave_f64[i];
+    }
+    if (t < kBins) {
+      s.count[t] = ci;
+      s.mass[t] = mi;
+    }
+    __syncthreads();
+  }
+
+  // First bin whose running count reaches k (kBins if none does), or whose running
+  // mass reaches `target` (`over`: exceeds it; the last bin with mass if none does).
+  __device__ int bin_of_count(uint32_t k) {
+    if (threadIdx.x == 0) s.found = kBins;
+    __syncthreads();
+    const int t = threadIdx.x;
+    if (t < kBins && s.count[t] >= k && (t == 0 || s.count[t - 1] < k)) s.found = t;
+    __syncthreads();
+    const int f = s.found;
+    __syncthreads();
+    return f;
+  }
+  __device__ int bin_of_mass(double target, bool over) {
+    if (threadIdx.x == 0) s.found = kBins - 1;
+    __syncthreads();
+    const int t = threadIdx.x;
+    auto reached = [&](int i) { return over ? s.mass[i] > target : s.mass[i] >= target; };
+    if (t < kBins && s.count[t] > (t ? s.count[t - 1] : 0) &&
+        (reached(t) || s.count[t] == s.count[kBins - 1]))
+      atomicMin(&s.found, t);
+    __syncthreads();
+    const int f = s.found;
+    __syncthreads();
+    return f;
+  }
+
+  // Collects the tokens of bins lo .. hi; false if they do not fit the list.
+  __device__ bool collect(int lo, int hi) {
+    constexpr int VE = Vec<TYPE>::VE;
+    if (threadIdx.x == 0) s.n = 0;
+    __syncthreads();
+    const int vecs = chunk_len / VE;
+    for (int i = 0; i < chunks; ++i) {
+      const double d = edge - heads[i].edge;
+      if (!(d <= (double)hi)) continue;
+      if (lo == hi && hists[(int64_t)i * kBins + hi - (int)d] >> kCountShift == 0) continue;
+      for (int j = threadIdx.x; j < vecs; j += kSampThreads) {
+        const int at = i * chunk_len + j * VE;
+        if (at >= V) break;
+        Vec<TYPE> x;
+        x.load(row, at, V);
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const double b = edge - grid.bin(x.v[e]);
+          if (b >= (double)lo && b <= (double)hi) {
+            const int n = atomicAdd(&s.n, 1);
+            if (n < kList) s.s.order[n] = (uint64_t)~key_of(x.v[e]) << 32 | (uint32_t)(at + e);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    const int n = s.n;
+    __syncthreads();
+    return n <= kList;
+  }
+
+  __device__ __forceinline__ uint64_t unit_at(uint64_t order) const {
+    const float l = logit_of(~(uint32_t)(order >> 32));
+    return grid.unit(l, grid.bin(l));
+  }
+
+  // Among the collected tokens, the one with which the count (COUNT) or the units
+  // of mass first reach `target` (>= 1, at most the whole).  Bins of the remaining
+  // tokens' order, 2048 over the span between their first and last, until one
+  // token is left.
+  template <bool COUNT>
+  __device__ uint64_t select(uint64_t target) {
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, n = s.n;
+    uint64_t lo = 0, hi = ~0ull, before = 0;
+    for (;;) {
+      uint64_t mn = ~0ull, mx = 0;
+      for (int i = t; i < n; i += kSampThreads) {
+        const uint64_t o = s.s.order[i];
+        if (o >= lo && o <= hi) {
+          mn = ~max_u64(~mn, ~o);
+          mx = max_u64(mx, o);
+        }
+      }
+      mn = ~wave_max(~mn);
+      mx = wave_max(mx);
+      if (lane == 0) {
+        s.wave_u64[wave] = mx;
+        s.wave_min[wave] = mn;
+      }
+      for (int i = t; i < kRadix; i += kSampThreads) s.s.hist[i] = 0;
+      __syncthreads();
+      for (int w = 0; w < kSampWaves; ++w) {
+        mx = max_u64(mx, s.wave_u64[w]);
+        mn = ~max_u64(~mn, ~s.wave_min[w]);
+      }
+      __syncthreads();
+      if (mn >= mx) return mn;
+      const int shift = max(0, 53 - __clzll(mn ^ mx));  // at most 2048 bins
+      for (int i = t; i < n; i += kSampThreads) {
+        const uint64_t o = s.s.order[i];
+        if (o >= lo && o <= hi)
+          atomicAdd((unsigned long long*)&s.s.hist[(o >> shift) - (mn >> shift)],
+                    (unsigned long long)(COUNT ? 1 : unit_at(o)));
+      }
+      __syncthreads();
+      const uint64_t m0 = s.s.hist[2 * t], m1 = s.s.hist[2 * t + 1];
+      uint64_t mi = scan_u64(m0 + m1, lane);
+      if (lane == 63) s.wave_u64[wave] = mi;
+      if (t == 0) s.found = 0;
+      __syncthreads();
+      for (int w = 0; w < wave; ++w) mi += s.wave_u64[w];
+      const uint64_t e0 = before + mi - m0 - m1, e1 = e0 + m0;
+      if (e0 < target && e1 >= target) {
+        s.found = 2 * t;
+        s.before = e0;
+      }
+      if (e1 < target && e1 + m1 >= target) {
+        s.found = 2 * t + 1;
+        s.before = e1;
+      }
+      __syncthreads();
+      before = s.before;
+      lo = ((mn >> shift) + (uint64_t)s.found) << shift;
+      hi = lo | ((1ull << shift) - 1);
+      lo = max_u64(lo, mn);
+      if (shift == 0) return lo;
+    }
+  }
+
+  // Units of mass of the collected tokens up to `last` in the order with weight >= floor.
+  __device__ uint64_t units(uint64_t last, double floor) {
+    uint64_t m = 0;
+    for (int i = threadIdx.x; i < s.n; i += kSampThreads) {
+      const uint64_t o = s.s.order[i];
+      if (o <= last && weight(logit_of(~(uint32_t)(o >> 32))) >= floor) m += unit_at(o);
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) m += __shfl_xor(m, o, 64);
+    if ((threadIdx.x & 63) == 0) s.wave_u64[threadIdx.x >> 6] = m;
+    __syncthreads();
+    m = 0;
+    for (int w = 0; w < kSampWaves; ++w) m += s.wave_u64[w];
+    __syncthreads();
+    return m;
+  }
+
+  // The collected tokens, at most kSorted, are all that can matter: sorted, with
+  // running masses; cut and choose.  `all`: the mass that top_p is a share of, where
+  // top-k has not cut it (else the first k tokens').
+  __device__ void few(int k, double p, double mp, double u, double all, int& token, double& prob) {
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, n = s.n;
+    uint64_t mine = ~0ull;
+    double w = 0.0;
+    int rank = 0;
+    if (t < n) {
+      mine = s.s.order[t];
+      for (int i = 0; i < n; ++i) rank += s.s.order[i] < mine;
+    }
+    __syncthreads();
+    if (t < n) s.few.sorted[rank] = mine;
+    __syncthreads();
+    const bool cut = k > 0 && k < V;
+    const int most = cut ? min(k, n) : n;
+    if (t < most) {
+      mine = s.few.sorted[t];
+      const float l = logit_of(~(uint32_t)(mine >> 32));
+      const double b = grid.bin(l);
+      w = (double)grid.unit(l, b) * unit_of((int)(edge - b));
+    }
+    double c = scan_f64(w, lane);
+    if (lane == 63) s.wave_f64[wave] = c;
+    if (t == 0) s.n = 0;
+    __syncthreads();
+    for (int i = 0; i < wave; ++i) c += s.wave_f64[i];
+    s.few.mass[t] = c;
+    __syncthreads();
+    if (cut) all = s.few.mass[most - 1];
+    // kept: a prefix; its length is the number of threads whose token is in it
+    bool kept = t < most;
+    if (p < 1.0 && t > 0 && kept) kept = s.few.mass[t - 1] < p * all;
+    if (mp > 0.0 && kept) kept = t == 0 || weight(logit_of(~(uint32_t)(mine >> 32))) >= mp ||
+                                 (mine >> 32) == (s.few.sorted[0] >> 32);
+    if (kept) atomicMax(&s.n, t + 1);
+    __syncthreads();
+    const int len = s.n;
+    const double left = s.few.mass[len - 1], target = u * left;
+    __syncthreads();
+    if (t == 0) s.n = len - 1;
+    __syncthreads();
+    // the last token with mass stands in for a u of 1 or more
+    if (t < len && (s.few.mass[t] > target || !(u >= 0.0) || s.few.mass[t] == left)) atomicMin(&s.n, t);
+    __syncthreads();
+    const int at = s.n;
+    token = (int)(uint32_t)s.few.sorted[at];
+    prob = weight(logit_of(~(uint32_t)(s.few.sorted[at] >> 32))) / left;
+  }
+
+  // Border by border; false if a border's tokens do not fit the list.
+  __device__ bool many(int k, double p, double mp, double u, int& token, double& prob) {
+    uint64_t last = ~0ull;  // the last token kept, in the order
+    int end = kBins - 1;    // and its bin
+    double kept = s.mass[kBins - 1];
+    if (k > 0 && k < V) {
+      const int b = bin_of_count((uint32_t)k);
+      if (b < kBins) {  // else the tokens beyond the bins have no mass
+        if (!collect(b, b)) return false;
+        last = select<true>((uint64_t)k - (b ? s.count[b - 1] : 0));
+        end = b;
+        kept = (b ? s.mass[b - 1] : 0.0) + (double)units(last, 0.0) * unit_of(b);
+      }
+    }
+    // the place in the order where the mass reaches (or exceeds) a target below `kept`
+    auto place = [&](double target, bool over, int& b, uint64_t& at) {
+      b = min(bin_of_mass(target, over), end);
+      if (!collect(b, b)) return false;
+      const double in = (target - (b ? s.mass[b - 1] : 0.0)) / unit_of(b);
+      const double need = over ? floor(in) + 1.0 : ceil(in);
+      const uint64_t whole = units(b == end ? last : ~0ull, 0.0);
+      at = select<false>(need >= (double)whole ? whole : need >= 1.0 ? (uint64_t)need : 1);
+      return true;
+    };
+    if (p < 1.0) {
+      int b;
+      if (!place(p > 0.0 ? p * kept : 0.0, false, b, last)) return false;
+      end = b;
+      kept = (b ? s.mass[b - 1] : 0.0) + (double)units(last, 0.0) * unit_of(b);
+    }
+    if (mp > 0.0) {
+      // the bin that weight mp falls into, and the one below: the rounding of its
+      // logarithm may put it into the wrong one of two
+      const double mpc = mp < 1.0 ? mp : 1.0;
+      const double at = edge - floor((log(mpc) + top) * kPerNat);
+      const int near = (int)fmin(at, (double)kBins);
+      bool found = false;
+      for (int b = max(0, near - 1); b <= near + 1 && b <= end && !found; ++b) {
+        if (!collect(b, b)) return false;
+        const uint64_t in_prefix = units(b == end ? last : ~0ull, 0.0),
+                       heavy = units(b == end ? last : ~0ull, mpc);
+        if (heavy < in_prefix) {  // this bin holds the border: it is the last one, or the one before it
+          found = true;
+          kept = (b ? s.mass[b - 1] : 0.0) + (double)heavy * unit_of(b);
+          last = heavy ? select<false>(heavy) : ~0ull;
+          end = heavy ? b : b - 1;
+        }
+      }
+      if (!found && end > near + 1) {  // no token near the border: the bins beyond it go whole
+        end = near + 1;
+        last = ~0ull;
+        kept = s.mass[end];
+      }
+    }
+    int b;
+    uint64_t at;
+    if (!(u >= 0.0)) u = 0.0;
+    if (u >= 1.0) {  // the last token with mass
+      if (!place(kept, false, b, at)) return false;
+    } else if (!place(u * kept, true, b, at)) {
+      return false;
+    }
+    token = (int)(uint32_t)at;
+    prob = weight(logit_of(~(uint32_t)(at >> 32))) / kept;
+    return true;
+  }
+};
+
+template <int TYPE>
+__global__ __launch_bounds__(kSampThreads) void sample_pick_kernel(SampleArgs a, int chunks, int chunk_len,
+                                                                   const ChunkHead* heads, const uint64_t* hists) {
+  __shared__ Pick s;
   typedef Logit<TYPE> L;
   const int64_t b = blockIdx.x;
-  Row<TYPE> row{(const typename L::T*)a.logits + b * a.ld, a.V, s};
-  Weigher w;
-  int token;
-  row.top(w.top_key, token);
-  w.top = (double)logit_of(w.top_key);
-  w.t = a.temperature ? (double)a.temperature[b] : 1.0;
+  heads += b * chunks;
+  uint64_t best = 0;
+  for (int i = threadIdx.x; i < chunks; i += kSampThreads) best = max_u64(best, heads[i].top);
+  best = wave_max(best);
+  if ((threadIdx.x & 63) == 0) s.wave_u64[threadIdx.x >> 6] = best;
+  __syncthreads();
+  for (int w = 0; w < kSampWaves; ++w) best = max_u64(best, s.wave_u64[w]);
+  __syncthreads();
+  const float t = a.temperature ? a.temperature[b] : 1.0f;
+  const int k = a.top_k ? a.top_k[b] : 0;
+  const uint32_t top_key = (uint32_t)(best >> 32);
+  int token = (int)~(uint32_t)best;
   double prob = 1.0;
-  if (w.top_key == kKeyNegInf) {
+  if (top_key == kKeyNegInf) {
     token = -1;
     prob = 0.0;
-  } else if (w.t > 0.0) {
-    Prefix keep{0, a.V - 1, 0.0};
-    const int k = a.top_k ? a.top_k[b] : 0;
-    if (k > 0 && k < a.V) keep = row.template find<true>(w, keep, (uint64_t)k);
-    const double p = a.top_p ? (double)a.top_p[b] : 1.0;
-    if (p < 1.0) {
-      const uint64_t all = row.total(w, keep);
-      const double x = ceil(p * (double)all);
-      keep = row.template find<false>(w, keep, x >= 1.0 ? (uint64_t)x : 1);
+  } else if (t > 0.f && k != 1) {
+    const double p = a.top_p ? (double)a.top_p[b] : 1.0, mp = a.min_p ? (double)a.min_p[b] : 0.0, u = (double)a.u[b];
+    const float top = logit_of(top_key);
+    Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, chunks, chunk_len, heads,
+                      hists + b * chunks * kBins, s, Grid{kPerNat / (double)t}, 0.0, 0.0};
+    pick.edge = pick.grid.bin(top);
+    pick.top = (double)top * pick.grid.per / kPerNat;
+    bool done = false;
+    if (fabs(pick.edge) <= kFarthestBin) {
+      pick.merge();
+      // the last bin that can matter
+      int hi = kBins - 1;
+      if (k > 0 && k < a.V) hi = min(hi, pick.bin_of_count((uint32_t)k));
+      else if (p < 1.0) hi = pick.bin_of_mass(p > 0.0 ? p * s.mass[kBins - 1] : 0.0, false);
+      if (s.count[hi] <= kSorted) {
+        done = pick.collect(0, hi);
+        if (done) pick.few(k, p, mp, u, s.mass[kBins - 1], token, prob);
+      } else {
+        done = pick.many(k, p, mp, u, token, prob);
+      }
+      __syncthreads();
     }
-    const double mp = a.min_p ? (double)a.min_p[b] : 0.0;
-    if (mp > 0.0) keep.floor = mp;
-    const uint64_t all = row.total(w, keep);
-    const double x = floor((double)a.u[b] * (double)all) + 1.0;
-    const uint64_t target = x >= (double)all ? all : x >= 1.0 ? (uint64_t)x : 1;
-    const Prefix at = row.template find<false>(w, keep, target);
-    token = at.last;
-    prob = w.weight(at.key) / ((double)all / kMassUnit);
+    if (!done) {
+      Row<TYPE> row{(const typename L::T*)a.logits + b * a.ld, a.V, s.radix};
+      Weigher w{(double)top, (double)t, top_key};
+      solve_by_radix(row, w, k, p, mp, u, token, prob);
+    }
   }
   if (threadIdx.x == 0) {
     a.tokens[b] = token;
@@ -307,20 +820,40 @@ __global__ __launch_bounds__(kSampThreads) void sample_kernel(SampleArgs a) {
   }
 }
 
+// Logits per thread of a scan block: as many as leave 512 blocks, so that the card
+// is full, and at least 8: shorter chunks cost more in adding up their histograms.
+int scan_pt(int64_t B, int V) {
+  int pt = 32;
+  while (pt > 8 && B * ((V + kScanThreads * pt - 1) / (kScanThreads * pt)) < 512) pt /= 2;
+  return pt;
+}
+int chunks_of(int V, int pt) { return (V + kScanThreads * pt - 1) / (kScanThreads * pt); }
+
+template <int TYPE>
+hipError_t launch_type(const SampleArgs& a, void* ws, hipStream_t stream) {
+  const int pt = scan_pt(a.B, a.V), chunks = chunks_of(a.V, pt);
+  ChunkHead* heads = (ChunkHead*)ws;
+  uint64_t* hists = (uint64_t*)((char*)ws + (a.B * chunks * (int64_t)sizeof(ChunkHead) + 255) / 256 * 256);
+  auto scan = pt == 8 ? sample_scan_kernel<TYPE, 8> : pt == 16 ? sample_scan_kernel<TYPE, 16>
+                                                               : sample_scan_kernel<TYPE, 32>;
+  scan<<<(unsigned)(a.B * chunks), kScanThreads, 0, stream>>>(a, chunks, heads, hists);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  sample_pick_kernel<TYPE><<<(unsigned)a.B, kSampThreads, 0, stream>>>(a, chunks, kScanThreads * pt, heads, hists);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 int64_t sample_workspace_bytes(int64_t B, int V) {
-  (void)B;
-  (void)V;
-  return 0;
+  const int64_t chunks = B * chunks_of(V, scan_pt(B, V));
+  return (chunks * (int64_t)sizeof(ChunkHead) + 255) / 256 * 256 + chunks * kBins * 8;
 }
 
 hipError_t launch_sample(SampleType type, const SampleArgs& a, void* ws, hipStream_t stream) {
-  (void)ws;
-  auto kernel = type == kSampleF32 ? sample_kernel<kSampleF32> : type == kSampleBf16 ? sample_kernel<kSampleBf16>
-                                                                                     : sample_kernel<kSampleF16>;
-  kernel<<<(unsigned)a.B, kSampThreads, 0, stream>>>(a);
-  return hipGetLastError();
+  return type == kSampleF32 ? launch_type<kSampleF32>(a, ws, stream)
+         : type == kSampleBf16 ? launch_type<kSampleBf16>(a, ws, stream)
+                               : launch_type<kSampleF16>(a, ws, stream);
 }
 
 }  // namespace moe
