@@ -291,32 +291,36 @@ __device__ void solve_by_radix(Row<TYPE>& row, Weigher& w, int k, double p, doub
 // ------------------------------------------------------------------ histograms
 // One read of the logits: blocks take a chunk of a row each, keep it in registers
 // for its largest value, and count it into 512 bins of 1 / 16 nat below that, on a
-// grid that all chunks of the row share (bin edges are multiples of 1 / 16 of l / T).
-// A bin holds a count and a mass: the weight of a token relative to its bin's upper
-// edge lies in (e^-1/16, 1] and is rounded to 35 bits, so a chunk's sums are exact
-// in whatever order they come, count and mass in one 64-bit number.  32 nats below
-// the chunk's largest value a token has no mass (2^-46 of it).
+// grid that all chunks of the row share: bin floor(16 l / T), in fp32 (a rounding
+// moves a bin's edge, the same way for everyone).  A bin holds a count and a mass:
+// the weight of a token relative to the bin's upper edge, in fp64, lies in
+// (e^-1/16, 1] but for that rounding and becomes an integer of 35 bits, so a
+// chunk's sums are exact in whatever order they come, count and mass in one 64-bit
+// number.  32 nats below the chunk's largest value a token has no mass (2^-46 of it).
 constexpr int kBins = 512;
 constexpr double kPerNat = 16.0, kBinUnit = 34359738368.0;  // 2^35
-constexpr int kCountShift = 50;                            // 2^13 tokens of at most 2^35 below it
+constexpr int kCountShift = 50;                            // 2^13 tokens of about 2^35 below it
 constexpr int kScanThreads = 256;
-constexpr double kFarthestBin = 1099511627776.0;           // 2^40: beyond, the grid is not exact enough
+constexpr float kFarthestBin = 4194304.f;                  // 2^22: bin numbers are exact in fp32 up to it
 
 struct ChunkHead {
   uint64_t top;  // largest key, then the complement of its lowest index
-  double edge;   // number of the top bin, floor(16 l / T)
+  float edge;    // number of the top bin
+  float pad;
 };
 
 // l / T on the grid: the bin number, and the weight in units of 2^-35 relative to
 // the bin's upper edge.
 struct Grid {
   double per;  // 16 / T
-  __device__ __forceinline__ double bin(float l) const { return floor((double)l * per); }
-  __device__ __forceinline__ uint64_t unit(float l, double bin) const {
-    // e^x on [-1/16, 0] by its series: the first term left out is 6e-15 of it
-    const double x = fma((double)l, per, -(bin + 1.0)) * (1.0 / kPerNat);
-    double e = 1.0 / 5040;
-    e = fma(e, x, 1.0 / 720);
+  float perf;
+  __device__ __forceinline__ explicit Grid(float t) : per(kPerNat / (double)t), perf((float)per) {}
+  __device__ __forceinline__ float place(float l) const { return l * perf; }
+  __device__ __forceinline__ float bin(float l) const { return floorf(place(l)); }
+  __device__ __forceinline__ uint64_t unit(float l, float bin) const {
+    // e^x on [-1/16, 0] by its series: the first term left out is 2^-40 of it
+    const double x = fma((double)l, per, -((double)bin + 1.0)) * (1.0 / kPerNat);
+    double e = 1.0 / 720;
     e = fma(e, x, 1.0 / 120);
     e = fma(e, x, 1.0 / 24);
     e = fma(e, x, 1.0 / 6);
@@ -390,18 +394,18 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kScanThreads / 64; ++w) top = max_u64(top, tops[w]);
-  const Grid grid{kPerNat / (double)t};
-  const double edge = grid.bin(logit_of((uint32_t)(top >> 32)));
-  if (threadIdx.x == 0) heads[blockIdx.x] = ChunkHead{top, edge};
+  const Grid grid(t);
+  const float edge = grid.bin(logit_of((uint32_t)(top >> 32)));
+  if (threadIdx.x == 0) heads[blockIdx.x] = ChunkHead{top, edge, 0.f};
   // the first token needs no histogram; a grid too far out is not exact
-  if (!(t > 0.f) || k == 1 || !(fabs(edge) <= kFarthestBin)) return;
+  if (!(t > 0.f) || k == 1 || !(fabsf(edge) <= kFarthestBin)) return;
 #pragma unroll
   for (int j = 0; j < N; ++j)
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
       const float l = x[j].v[e];
-      const double bin = grid.bin(l), d = edge - bin;
-      if (d < (double)kBins)  // not for -inf and NaN
+      const float bin = grid.bin(l), d = edge - bin;
+      if (d < (float)kBins)  // not for -inf and NaN
         atomicAdd((unsigned long long*)&hist[(int)d], (unsigned long long)(grid.unit(l, bin) + (1ull << kCountShift)));
     }
   __syncthreads();
@@ -412,14 +416,16 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
 
 // ------------------------------------------------------------------ the choice
 // One block per row: the chunks' histograms added up say in which bin of the order
-// each filter ends and the answer lies.  Mostly the tokens down to the last bin that
-// can matter are few: they are collected, sorted by counting how many come before
-// each, and the filters are read off their running sums.  Otherwise each border
-// bin's tokens are collected alone and the place among them is found by bins of
-// their order (logit, then index).  What does not fit that either (a bin of more
-// tokens than the list holds) goes through the radix descents over the whole row.
-constexpr int kList = 8192;   // tokens collected at a time
-constexpr int kSorted = 1024;
+// each filter ends and the answer lies.  Where the bins down to the last one that
+// can matter hold at most 8192 tokens, those are collected in one more read of the
+// row (as far as its chunks have any); otherwise each border bin's tokens are, one
+// read each.  A place within a bin is found among its tokens: each counts what
+// stands before it, at most 256 of them; a fuller bin is first divided by the order
+// of its tokens (logit, then index), 2048 ways.  A border bin of more tokens than
+// the list holds goes through the radix descents over the whole row.
+constexpr int kList = 8192;  // tokens collected at a time
+constexpr int kFew = 256;
+constexpr int kMaxChunks = (int)(kSampleMaxVocab / (kScanThreads * 32));
 
 struct Pick {
   union {
@@ -428,19 +434,20 @@ struct Pick {
       uint64_t order[kList];  // complement of the key, then the index: rising in the order of tokens
       uint64_t hist[kRadix];
     } s;
-    struct {
-      uint64_t order[kList];
-      uint64_t sorted[kSorted];
-      double mass[kSorted];
-    } few;
   };
+  uint64_t few[kFew], few_mass[kFew];
   uint32_t count[kBins];  // tokens in the bins up to and with this one
   double mass[kBins];     // and their mass, relative to the largest weight
+  double unit[kBins];     // weight of a bin's unit of mass
+  uint64_t units[kBins];  // a bin's units
   uint64_t wave_u64[kSampWaves], wave_min[kSampWaves];
   double wave_f64[kSampWaves];
   uint32_t wave_u32[kSampWaves];
-  uint64_t before;
-  int n, found;
+  short dist[kMaxChunks];    // bins between the row's top and a chunk's, kBins for a chunk out of reach
+  uint8_t wanted[kMaxChunks];
+  uint64_t before, answer;
+  uint32_t bin_count;
+  int n, found, n_few;
 };
 
 __device__ __forceinline__ double scan_f64(double v, int lane) {
@@ -460,33 +467,45 @@ struct Picker {
   const uint64_t* hists;
   Pick& s;
   Grid grid;
-  double edge, top;  // the row's top bin, its largest l / T
+  float edge;  // the row's top bin
+  double top;  // its largest l / T
+  bool whole;  // the list holds every token that can matter
 
-  // Weight of a bin's unit: e^(upper edge - top) 2^-35.
-  __device__ __forceinline__ double unit_of(int bin) const {
-    return exp((edge - (double)bin + 1.0) / kPerNat - top) / kBinUnit;
-  }
   __device__ __forceinline__ double weight(float l) const { return exp((double)l * grid.per / kPerNat - top); }
 
   // The row's running counts and masses from the chunks' histograms.
   __device__ void merge() {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    for (int i = t; i < chunks; i += kSampThreads) {
+      const float e = heads[i].edge, d = edge - e;  // a chunk too far out has no histogram
+      s.dist[i] = (short)(fabsf(e) <= kFarthestBin && d < (float)kBins ? (int)d : kBins);
+    }
+    __syncthreads();
+    // half of the threads take every other chunk
+    const int bin = t & (kBins - 1);
     uint64_t m = 0;
     uint32_t c = 0;
-    if (t < kBins) {
-      for (int i = 0; i < chunks; ++i) {
-        const double d = edge - heads[i].edge;  // uniform; chunks whose top bin is out of reach have no histogram
-        if (!(d < (double)kBins)) continue;
-        const int at = t - (int)d;
-        if (at >= 0) {
-          const uint64_t h = hists[(int64_t)i * kBins + at];
-          m += h & ((1ull << kCountShift) - 1);
-          c += (uint32_t)(h >> kCountShift);
-        }
-      }
+#pragma unroll 8
+    for (int i = t / kBins; i < chunks; i += kSampThreads / kBins) {
+      const int at = bin - s.dist[i];
+      const uint64_t h = at >= 0 ? hists[(int64_t)i * kBins + at] : 0;
+      m += h & ((1ull << kCountShift) - 1);
+      c += (uint32_t)(h >> kCountShift);
     }
-    uint32_t ci = scan_u32(c, lane);
-    double mi = scan_f64(t < kBins ? (double)m * unit_of(t) : 0.0, lane);
+    if (t >= kBins) {
+      s.s.hist[bin] = m;
+      s.count[bin] = c;
+    } else {
+      // e^(upper edge - top) 2^-35
+      s.unit[t] = exp(((double)edge - (double)t + 1.0) / kPerNat - top) / kBinUnit;
+    }
+    __syncthreads();
+    if (t < kBins) {
+      m += s.s.hist[t];
+      c += s.count[t];
+    }
+    uint32_t ci = scan_u32(t < kBins ? c : 0, lane);
+    double mi = scan_f64(t < kBins ? (double)m * s.unit[t] : 0.0, lane);
     if (lane == 63) {
       s.wave_u32[wave] = ci;
       s.wave_f64[wave] = mi;
@@ -499,85 +518,103 @@ struct Picker {
     if (t < kBins) {
       s.count[t] = ci;
       s.mass[t] = mi;
+      s.units[t] = m;
     }
+    if (t == 0) s.found = kBins;
     __syncthreads();
   }
+  __device__ __forceinline__ uint32_t count_before(int b) const { return b ? s.count[b - 1] : 0; }
+  __device__ __forceinline__ double mass_before(int b) const { return b ? s.mass[b - 1] : 0.0; }
 
   // First bin whose running count reaches k (kBins if none does), or whose running
   // mass reaches `target` (`over`: exceeds it; the last bin with mass if none does).
-  __device__ int bin_of_count(uint32_t k) {
-    if (threadIdx.x == 0) s.found = kBins;
-    __syncthreads();
-    const int t = threadIdx.x;
-    if (t < kBins && s.count[t] >= k && (t == 0 || s.count[t - 1] < k)) s.found = t;
+  // s.found is kBins between calls.
+  __device__ int found_bin() {
     __syncthreads();
     const int f = s.found;
     __syncthreads();
+    if (threadIdx.x == 0) s.found = kBins;
     return f;
+  }
+  __device__ int bin_of_count(uint32_t k) {
+    const int t = threadIdx.x;
+    if (t < kBins && s.count[t] >= k && count_before(t) < k) s.found = t;
+    return found_bin();
   }
   __device__ int bin_of_mass(double target, bool over) {
-    if (threadIdx.x == 0) s.found = kBins - 1;
-    __syncthreads();
     const int t = threadIdx.x;
-    auto reached = [&](int i) { return over ? s.mass[i] > target : s.mass[i] >= target; };
-    if (t < kBins && s.count[t] > (t ? s.count[t - 1] : 0) &&
-        (reached(t) || s.count[t] == s.count[kBins - 1]))
+    if (t < kBins && s.count[t] > count_before(t) &&
+        ((over ? s.mass[t] > target : s.mass[t] >= target) || s.count[t] == s.count[kBins - 1]))
       atomicMin(&s.found, t);
-    __syncthreads();
-    const int f = s.found;
-    __syncthreads();
-    return f;
+    return found_bin();
   }
 
-  // Collects the tokens of bins lo .. hi; false if they do not fit the list.
+  // Collects the tokens of bins lo .. hi, reading the chunks that have some; false
+  // if they do not fit the list.
   __device__ bool collect(int lo, int hi) {
-    constexpr int VE = Vec<TYPE>::VE;
+    constexpr int VE = Vec<TYPE>::VE, AHEAD = 32 / VE;
     if (threadIdx.x == 0) s.n = 0;
+    for (int i = threadIdx.x; i < chunks; i += kSampThreads) {
+      const int d = s.dist[i];
+      s.wanted[i] = d <= hi && (lo < hi || hists[(int64_t)i * kBins + hi - d] >> kCountShift != 0);
+    }
     __syncthreads();
-    const int vecs = chunk_len / VE;
-    for (int i = 0; i < chunks; ++i) {
-      const double d = edge - heads[i].edge;
-      if (!(d <= (double)hi)) continue;
-      if (lo == hi && hists[(int64_t)i * kBins + hi - (int)d] >> kCountShift == 0) continue;
-      for (int j = threadIdx.x; j < vecs; j += kSampThreads) {
-        const int at = i * chunk_len + j * VE;
-        if (at >= V) break;
-        Vec<TYPE> x;
-        x.load(row, at, V);
+    // bin numbers edge - hi .. edge - lo, as bounds of places on the grid
+    const float from = edge - (float)hi, to = edge - (float)lo + 1.f;
+    const int shift = 31 - __clz(chunk_len), vecs = (V + VE - 1) / VE, lane = threadIdx.x & 63;
+    for (int j0 = threadIdx.x; j0 - lane < vecs; j0 += AHEAD * kSampThreads) {  // waves stay together
+      Vec<TYPE> x[AHEAD];
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        const int at = (j0 + a * kSampThreads) * VE;
+        if (at < V && s.wanted[at >> shift]) {
+          x[a].load(row, at, V);
+        } else {
+#pragma unroll
+          for (int e = 0; e < VE; ++e) x[a].v[e] = __builtin_nanf("");
+        }
+      }
+#pragma unroll
+      for (int a = 0; a < AHEAD; ++a) {
+        const int at = (j0 + a * kSampThreads) * VE;
 #pragma unroll
         for (int e = 0; e < VE; ++e) {
-          const double b = edge - grid.bin(x.v[e]);
-          if (b >= (double)lo && b <= (double)hi) {
-            const int n = atomicAdd(&s.n, 1);
-            if (n < kList) s.s.order[n] = (uint64_t)~key_of(x.v[e]) << 32 | (uint32_t)(at + e);
+          const float z = grid.place(x[a].v[e]);
+          const bool hit = z >= from && z < to;
+          const uint64_t votes = __ballot(hit);
+          if (votes) {
+            int n = 0;
+            if (lane == 0) n = atomicAdd(&s.n, __popcll(votes));
+            n = __builtin_amdgcn_readfirstlane(n) + __popcll(votes & ((1ull << lane) - 1));
+            if (hit && n < kList) s.s.order[n] = (uint64_t)~key_of(x[a].v[e]) << 32 | (uint32_t)(at + e);
           }
         }
       }
     }
     __syncthreads();
-    const int n = s.n;
-    __syncthreads();
-    return n <= kList;
+    return s.n <= kList;
   }
 
+  static __device__ __forceinline__ float logit_at(uint64_t order) { return logit_of(~(uint32_t)(order >> 32)); }
+  __device__ __forceinline__ int bin_at(uint64_t order) const { return (int)(edge - grid.bin(logit_at(order))); }
   __device__ __forceinline__ uint64_t unit_at(uint64_t order) const {
-    const float l = logit_of(~(uint32_t)(order >> 32));
+    const float l = logit_at(order);
     return grid.unit(l, grid.bin(l));
   }
 
-  // Among the collected tokens, the one with which the count (COUNT) or the units
-  // of mass first reach `target` (>= 1, at most the whole).  Bins of the remaining
-  // tokens' order, 2048 over the span between their first and last, until one
-  // token is left.
+  // The token of bin b with which the bin's count (COUNT) or its units of mass first
+  // reach `target` (from 1 to the whole); `cum` receives the units up to and with it.
   template <bool COUNT>
-  __device__ uint64_t select(uint64_t target) {
+  __device__ uint64_t select(int b, uint64_t target, uint64_t& cum) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, n = s.n;
-    uint64_t lo = 0, hi = ~0ull, before = 0;
-    for (;;) {
+    uint64_t lo = 0, hi = ~0ull, before = 0, before_units = 0;
+    uint32_t left = s.count[b] - count_before(b);
+    bool in_bin = !whole;  // the list holds this bin alone, or [lo, hi] has been narrowed to it
+    while (left > (uint32_t)kFew) {
       uint64_t mn = ~0ull, mx = 0;
       for (int i = t; i < n; i += kSampThreads) {
         const uint64_t o = s.s.order[i];
-        if (o >= lo && o <= hi) {
+        if (o >= lo && o <= hi && (in_bin || bin_at(o) == b)) {
           mn = ~max_u64(~mn, ~o);
           mx = max_u64(mx, o);
         }
@@ -595,45 +632,86 @@ struct Picker {
         mn = ~max_u64(~mn, ~s.wave_min[w]);
       }
       __syncthreads();
-      if (mn >= mx) return mn;
-      const int shift = max(0, 53 - __clzll(mn ^ mx));  // at most 2048 bins
+      in_bin = true;  // a bin's tokens are neighbours in the order
+      lo = mn;
+      hi = mx;
+      const int shift = max(0, 53 - __clzll(mn ^ mx));  // at most 2048 parts
+      // counts above, units of at most 2^13 tokens below
       for (int i = t; i < n; i += kSampThreads) {
         const uint64_t o = s.s.order[i];
         if (o >= lo && o <= hi)
           atomicAdd((unsigned long long*)&s.s.hist[(o >> shift) - (mn >> shift)],
-                    (unsigned long long)(COUNT ? 1 : unit_at(o)));
+                    (unsigned long long)((1ull << kCountShift) + unit_at(o)));
       }
       __syncthreads();
+      constexpr uint64_t UNITS = (1ull << kCountShift) - 1;
       const uint64_t m0 = s.s.hist[2 * t], m1 = s.s.hist[2 * t + 1];
       uint64_t mi = scan_u64(m0 + m1, lane);
       if (lane == 63) s.wave_u64[wave] = mi;
-      if (t == 0) s.found = 0;
       __syncthreads();
       for (int w = 0; w < wave; ++w) mi += s.wave_u64[w];
-      const uint64_t e0 = before + mi - m0 - m1, e1 = e0 + m0;
-      if (e0 < target && e1 >= target) {
-        s.found = 2 * t;
-        s.before = e0;
-      }
-      if (e1 < target && e1 + m1 >= target) {
-        s.found = 2 * t + 1;
-        s.before = e1;
-      }
+      const uint64_t e0 = mi - m0 - m1, e1 = e0 + m0;
+      auto at = [&](uint64_t v) { return COUNT ? before + (v >> kCountShift) : before + (v & UNITS); };
+      auto take = [&](int part, uint64_t e, uint64_t m) {
+        if (at(e) < target && at(e + m) >= target) {
+          s.found = part;
+          s.before = e;
+          s.bin_count = (uint32_t)(m >> kCountShift);
+        }
+      };
+      take(2 * t, e0, m0);
+      take(2 * t + 1, e1, m1);
       __syncthreads();
-      before = s.before;
-      lo = ((mn >> shift) + (uint64_t)s.found) << shift;
-      hi = lo | ((1ull << shift) - 1);
-      lo = max_u64(lo, mn);
-      if (shift == 0) return lo;
+      const uint64_t part = (mn >> shift) + (uint64_t)s.found, e = s.before;
+      left = s.bin_count;
+      before = at(e);
+      before_units += e & UNITS;
+      lo = max_u64(lo, part << shift);
+      hi = ~max_u64(~hi, ~((part << shift) | ((1ull << shift) - 1)));
+      __syncthreads();
+      if (t == 0) s.found = kBins;
+      if (shift == 0) left = 1;
     }
+    // at most kFew are left: each counts what stands before it
+    if (t == 0) s.n_few = 0;
+    __syncthreads();
+    for (int i = t; i < n; i += kSampThreads) {
+      const uint64_t o = s.s.order[i];
+      if (o >= lo && o <= hi && (in_bin || bin_at(o) == b)) {
+        const int k = atomicAdd(&s.n_few, 1);
+        s.few[k] = o;
+        s.few_mass[k] = unit_at(o);
+      }
+    }
+    __syncthreads();
+    if (t < s.n_few) {
+      const uint64_t o = s.few[t], m = s.few_mass[t];
+      uint64_t c = 0;
+      uint64_t r = 0;
+      for (int i = 0; i < s.n_few; ++i) {
+        const bool first = s.few[i] < o;
+        r += first ? 1 : 0;
+        c += first ? s.few_mass[i] : 0;
+      }
+      const uint64_t was = before + (COUNT ? r : c), is = was + (COUNT ? 1 : m);
+      if (was < target && is >= target) {
+        s.answer = o;
+        s.before = before_units + c + m;
+      }
+    }
+    __syncthreads();
+    cum = s.before;
+    const uint64_t o = s.answer;
+    __syncthreads();
+    return o;
   }
 
-  // Units of mass of the collected tokens up to `last` in the order with weight >= floor.
-  __device__ uint64_t units(uint64_t last, double floor) {
+  // Units of mass of bin b's tokens up to `last` in the order with weight >= floor.
+  __device__ uint64_t heavy_units(int b, uint64_t last, double floor) {
     uint64_t m = 0;
     for (int i = threadIdx.x; i < s.n; i += kSampThreads) {
       const uint64_t o = s.s.order[i];
-      if (o <= last && weight(logit_of(~(uint32_t)(o >> 32))) >= floor) m += unit_at(o);
+      if (o <= last && bin_at(o) == b && weight(logit_at(o)) >= floor) m += unit_at(o);
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) m += __shfl_xor(m, o, 64);
@@ -645,121 +723,77 @@ struct Picker {
     return m;
   }
 
-  // The collected tokens, at most kSorted, are all that can matter: sorted, with
-  // running masses; cut and choose.  `all`: the mass that top_p is a share of, where
-  // top-k has not cut it (else the first k tokens').
-  __device__ void few(int k, double p, double mp, double u, double all, int& token, double& prob) {
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, n = s.n;
-    uint64_t mine = ~0ull;
-    double w = 0.0;
-    int rank = 0;
-    if (t < n) {
-      mine = s.s.order[t];
-      for (int i = 0; i < n; ++i) rank += s.s.order[i] < mine;
-    }
-    __syncthreads();
-    if (t < n) s.few.sorted[rank] = mine;
-    __syncthreads();
-    const bool cut = k > 0 && k < V;
-    const int most = cut ? min(k, n) : n;
-    if (t < most) {
-      mine = s.few.sorted[t];
-      const float l = logit_of(~(uint32_t)(mine >> 32));
-      const double b = grid.bin(l);
-      w = (double)grid.unit(l, b) * unit_of((int)(edge - b));
-    }
-    double c = scan_f64(w, lane);
-    if (lane == 63) s.wave_f64[wave] = c;
-    if (t == 0) s.n = 0;
-    __syncthreads();
-    for (int i = 0; i < wave; ++i) c += s.wave_f64[i];
-    s.few.mass[t] = c;
-    __syncthreads();
-    if (cut) all = s.few.mass[most - 1];
-    // kept: a prefix; its length is the number of threads whose token is in it
-    bool kept = t < most;
-    if (p < 1.0 && t > 0 && kept) kept = s.few.mass[t - 1] < p * all;
-    if (mp > 0.0 && kept) kept = t == 0 || weight(logit_of(~(uint32_t)(mine >> 32))) >= mp ||
-                                 (mine >> 32) == (s.few.sorted[0] >> 32);
-    if (kept) atomicMax(&s.n, t + 1);
-    __syncthreads();
-    const int len = s.n;
-    const double left = s.few.mass[len - 1], target = u * left;
-    __syncthreads();
-    if (t == 0) s.n = len - 1;
-    __syncthreads();
-    // the last token with mass stands in for a u of 1 or more
-    if (t < len && (s.few.mass[t] > target || !(u >= 0.0) || s.few.mass[t] == left)) atomicMin(&s.n, t);
-    __syncthreads();
-    const int at = s.n;
-    token = (int)(uint32_t)s.few.sorted[at];
-    prob = weight(logit_of(~(uint32_t)(s.few.sorted[at] >> 32))) / left;
-  }
-
-  // Border by border; false if a border's tokens do not fit the list.
-  __device__ bool many(int k, double p, double mp, double u, int& token, double& prob) {
-    uint64_t last = ~0ull;  // the last token kept, in the order
-    int end = kBins - 1;    // and its bin
+  // The filters and the choice; false if a border's tokens do not fit the list.
+  __device__ bool choose(int k, double p, double mp, double u, int& token, double& prob) {
+    // what is kept: the bins before `end`, and of bin `end` the tokens up to `last`,
+    // which hold `part` of its units; `kept` is the mass of it all
+    uint64_t last = ~0ull, part = 0;
+    int end = kBins;
     double kept = s.mass[kBins - 1];
-    if (k > 0 && k < V) {
-      const int b = bin_of_count((uint32_t)k);
-      if (b < kBins) {  // else the tokens beyond the bins have no mass
-        if (!collect(b, b)) return false;
-        last = select<true>((uint64_t)k - (b ? s.count[b - 1] : 0));
-        end = b;
-        kept = (b ? s.mass[b - 1] : 0.0) + (double)units(last, 0.0) * unit_of(b);
-      }
+    const bool cut = k > 0 && k < V;
+    int b = kBins;
+    if (cut) b = bin_of_count((uint32_t)k);
+    // the last bin that can matter
+    int hi = min(b, kBins - 1);
+    if (!cut && p < 1.0) hi = bin_of_mass(p > 0.0 ? p * kept : 0.0, false);
+    whole = s.count[hi] <= (uint32_t)kList;
+    if (whole) collect(0, hi);
+    auto border = [&](int bin) { return whole || collect(bin, bin); };
+    if (b < kBins) {  // else the tokens beyond the bins have no mass
+      if (!border(b)) return false;
+      last = select<true>(b, (uint64_t)k - count_before(b), part);
+      end = b;
+      kept = mass_before(b) + (double)part * s.unit[b];
     }
-    // the place in the order where the mass reaches (or exceeds) a target below `kept`
-    auto place = [&](double target, bool over, int& b, uint64_t& at) {
-      b = min(bin_of_mass(target, over), end);
-      if (!collect(b, b)) return false;
-      const double in = (target - (b ? s.mass[b - 1] : 0.0)) / unit_of(b);
-      const double need = over ? floor(in) + 1.0 : ceil(in);
-      const uint64_t whole = units(b == end ? last : ~0ull, 0.0);
-      at = select<false>(need >= (double)whole ? whole : need >= 1.0 ? (uint64_t)need : 1);
+    // the place in the order where the mass reaches (exceeds) a target, at most `kept`
+    auto place = [&](double target, bool over, int& bin, uint64_t& at, uint64_t& cum) {
+      bin = min(bin_of_mass(target, over), end);
+      if (!border(bin)) return false;
+      const double in = (target - mass_before(bin)) / s.unit[bin], need = over ? floor(in) + 1.0 : ceil(in);
+      const uint64_t all = bin == end ? part : s.units[bin];
+      at = select<false>(bin, need >= (double)all ? all : need >= 1.0 ? (uint64_t)need : 1, cum);
       return true;
     };
     if (p < 1.0) {
-      int b;
-      if (!place(p > 0.0 ? p * kept : 0.0, false, b, last)) return false;
-      end = b;
-      kept = (b ? s.mass[b - 1] : 0.0) + (double)units(last, 0.0) * unit_of(b);
+      int bin;
+      uint64_t at, cum;
+      if (!place(p > 0.0 ? p * kept : 0.0, false, bin, at, cum)) return false;
+      end = bin;
+      last = at;
+      part = cum;
+      kept = mass_before(end) + (double)part * s.unit[end];
     }
     if (mp > 0.0) {
-      // the bin that weight mp falls into, and the one below: the rounding of its
-      // logarithm may put it into the wrong one of two
-      const double mpc = mp < 1.0 ? mp : 1.0;
-      const double at = edge - floor((log(mpc) + top) * kPerNat);
-      const int near = (int)fmin(at, (double)kBins);
+      // the bin that weight mp falls into; rounding may put it into a neighbour
+      const double floor_w = mp < 1.0 ? mp : 1.0;
+      const int near = (int)fmin(fmax((double)edge - floor((log(floor_w) + top) * kPerNat), 0.0), (double)kBins);
       bool found = false;
-      for (int b = max(0, near - 1); b <= near + 1 && b <= end && !found; ++b) {
-        if (!collect(b, b)) return false;
-        const uint64_t in_prefix = units(b == end ? last : ~0ull, 0.0),
-                       heavy = units(b == end ? last : ~0ull, mpc);
-        if (heavy < in_prefix) {  // this bin holds the border: it is the last one, or the one before it
+      for (int bin = max(0, near - 1); bin <= near + 1 && bin <= end && bin < kBins && !found; ++bin) {
+        if (s.count[bin] == count_before(bin)) continue;
+        if (!border(bin)) return false;
+        const uint64_t whole_units = bin == end ? part : s.units[bin],
+                       heavy = heavy_units(bin, bin == end ? last : ~0ull, floor_w);
+        if (heavy < whole_units) {  // this bin holds the border
           found = true;
-          kept = (b ? s.mass[b - 1] : 0.0) + (double)heavy * unit_of(b);
-          last = heavy ? select<false>(heavy) : ~0ull;
-          end = heavy ? b : b - 1;
+          end = bin;
+          part = heavy;
+          kept = mass_before(bin) + (double)heavy * s.unit[bin];
+          if (heavy) last = select<false>(bin, heavy, part);
         }
       }
-      if (!found && end > near + 1) {  // no token near the border: the bins beyond it go whole
-        end = near + 1;
-        last = ~0ull;
-        kept = s.mass[end];
+      if (!found && end > near + 1) {  // no token near the border: nothing beyond it stays
+        end = min(near + 2, kBins);
+        part = 0;
+        kept = s.mass[end - 1];
       }
     }
-    int b;
-    uint64_t at;
+    int bin;
+    uint64_t at, cum;
     if (!(u >= 0.0)) u = 0.0;
-    if (u >= 1.0) {  // the last token with mass
-      if (!place(kept, false, b, at)) return false;
-    } else if (!place(u * kept, true, b, at)) {
-      return false;
-    }
+    // the last token with mass stands in for a u of 1 or more
+    if (!(u < 1.0 ? place(u * kept, true, bin, at, cum) : place(kept, false, bin, at, cum))) return false;
     token = (int)(uint32_t)at;
-    prob = weight(logit_of(~(uint32_t)(at >> 32))) / kept;
+    prob = weight(logit_at(at)) / kept;
     return true;
   }
 };
@@ -771,6 +805,10 @@ __global__ __launch_bounds__(kSampThreads) void sample_pick_kernel(SampleArgs a,
   typedef Logit<TYPE> L;
   const int64_t b = blockIdx.x;
   heads += b * chunks;
+  // everything the row is told, read at once
+  const float t = a.temperature ? a.temperature[b] : 1.0f, pf = a.top_p ? a.top_p[b] : 1.0f,
+              mpf = a.min_p ? a.min_p[b] : 0.0f, uf = a.u[b];
+  const int k = a.top_k ? a.top_k[b] : 0;
   uint64_t best = 0;
   for (int i = threadIdx.x; i < chunks; i += kSampThreads) best = max_u64(best, heads[i].top);
   best = wave_max(best);
@@ -778,8 +816,6 @@ __global__ __launch_bounds__(kSampThreads) void sample_pick_kernel(SampleArgs a,
   __syncthreads();
   for (int w = 0; w < kSampWaves; ++w) best = max_u64(best, s.wave_u64[w]);
   __syncthreads();
-  const float t = a.temperature ? a.temperature[b] : 1.0f;
-  const int k = a.top_k ? a.top_k[b] : 0;
   const uint32_t top_key = (uint32_t)(best >> 32);
   int token = (int)~(uint32_t)best;
   double prob = 1.0;
@@ -787,25 +823,16 @@ __global__ __launch_bounds__(kSampThreads) void sample_pick_kernel(SampleArgs a,
     token = -1;
     prob = 0.0;
   } else if (t > 0.f && k != 1) {
-    const double p = a.top_p ? (double)a.top_p[b] : 1.0, mp = a.min_p ? (double)a.min_p[b] : 0.0, u = (double)a.u[b];
+    const double p = (double)pf, mp = (double)mpf, u = (double)uf;
     const float top = logit_of(top_key);
     Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, chunks, chunk_len, heads,
-                      hists + b * chunks * kBins, s, Grid{kPerNat / (double)t}, 0.0, 0.0};
+                      hists + b * chunks * kBins, s, Grid(t), 0.f, 0.0, false};
     pick.edge = pick.grid.bin(top);
     pick.top = (double)top * pick.grid.per / kPerNat;
     bool done = false;
-    if (fabs(pick.edge) <= kFarthestBin) {
+    if (fabsf(pick.edge) <= kFarthestBin) {
       pick.merge();
-      // the last bin that can matter
-      int hi = kBins - 1;
-      if (k > 0 && k < a.V) hi = min(hi, pick.bin_of_count((uint32_t)k));
-      else if (p < 1.0) hi = pick.bin_of_mass(p > 0.0 ? p * s.mass[kBins - 1] : 0.0, false);
-      if (s.count[hi] <= kSorted) {
-        done = pick.collect(0, hi);
-        if (done) pick.few(k, p, mp, u, s.mass[kBins - 1], token, prob);
-      } else {
-        done = pick.many(k, p, mp, u, token, prob);
-      }
+      done = pick.choose(k, p, mp, u, token, prob);
       __syncthreads();
     }
     if (!done) {
