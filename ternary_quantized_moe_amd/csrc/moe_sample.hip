@@ -297,6 +297,9 @@ __device__ void solve_by_radix(Row<TYPE>& row, Weigher& w, int k, double p, doub
 // (e^-1/16, 1] but for that rounding and becomes an integer of 35 bits, so a
 // chunk's sums are exact in whatever order they come, count and mass in one 64-bit
 // number.  32 nats below the chunk's largest value a token has no mass (2^-46 of it).
+// The chunk's tokens are also written down by bin (their places in the chunk, in no
+// order within a bin), so that whoever wants a bin's tokens need not search the row;
+// with a top-k only as many bins as hold the chunk's own first k.
 constexpr int kBins = 512;
 constexpr double kPerNat = 16.0, kBinUnit = 34359738368.0;  // 2^35
 constexpr int kCountShift = 50;                            // 2^13 tokens of about 2^35 below it
@@ -365,18 +368,31 @@ struct Vec {
   }
 };
 
+// The workspace: one of each per chunk.
+struct Chunks {
+  int n, len;       // chunks of a row, tokens in a chunk
+  ChunkHead* heads;
+  uint64_t* hists;  // [kBins] count and units of each bin below the chunk's top one
+  uint16_t* begins; // [kBins] where a bin's tokens begin among the chunk's
+  uint16_t* tokens; // [len] places in the chunk, by bin
+};
+
 template <int TYPE, int PT>
-__global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a, int chunks, ChunkHead* heads,
-                                                                   uint64_t* hists) {
-  constexpr int VE = Vec<TYPE>::VE, N = PT / VE;
+__global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a, Chunks ws) {
+  constexpr int VE = Vec<TYPE>::VE, N = PT / VE, LEN = kScanThreads * PT, WAVES = kScanThreads / 64;
+  static_assert(kBins == 2 * kScanThreads, "two bins a thread");
   __shared__ uint64_t hist[kBins];
-  __shared__ uint64_t tops[kScanThreads / 64];
-  const int64_t b = blockIdx.x / chunks;
-  const int chunk = (int)(blockIdx.x - b * chunks), base = chunk * (kScanThreads * PT);
+  __shared__ uint32_t cursor[kBins];
+  __shared__ uint64_t tops[WAVES];
+  __shared__ uint32_t counts[WAVES];
+  __shared__ int end_bin, end_count;
+  __shared__ __attribute__((aligned(16))) uint16_t places[LEN];
+  const int64_t b = blockIdx.x / ws.n;
+  const int chunk = (int)(blockIdx.x - b * ws.n), base = chunk * LEN, tid = threadIdx.x, lane = tid & 63;
   const void* row = (const typename Logit<TYPE>::T*)a.logits + b * a.ld;
   Vec<TYPE> x[N];
 #pragma unroll
-  for (int j = 0; j < N; ++j) x[j].load(row, base + (j * kScanThreads + (int)threadIdx.x) * VE, a.V);
+  for (int j = 0; j < N; ++j) x[j].load(row, base + (j * kScanThreads + tid) * VE, a.V);
   const float t = a.temperature ? a.temperature[b] : 1.0f;
   const int k = a.top_k ? a.top_k[b] : 0;
   uint64_t top = 0;
@@ -384,19 +400,19 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   for (int j = 0; j < N; ++j)
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const int i = base + (j * kScanThreads + (int)threadIdx.x) * VE + e;
+      const int i = base + (j * kScanThreads + tid) * VE + e;
       if (i < a.V) top = max_u64(top, (uint64_t)key_of(x[j].v[e]) << 32 | (uint32_t)~i);
     }
   top = wave_max(top);
-  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-#pragma unroll
-  for (int i = 0; i < kBins; i += kScanThreads) hist[i + threadIdx.x] = 0;
+  if (lane == 0) tops[tid >> 6] = top;
+  hist[tid] = 0;
+  hist[tid + kScanThreads] = 0;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kScanThreads / 64; ++w) top = max_u64(top, tops[w]);
+  for (int w = 0; w < WAVES; ++w) top = max_u64(top, tops[w]);
   const Grid grid(t);
   const float edge = grid.bin(logit_of((uint32_t)(top >> 32)));
-  if (threadIdx.x == 0) heads[blockIdx.x] = ChunkHead{top, edge, 0.f};
+  if (tid == 0) ws.heads[blockIdx.x] = ChunkHead{top, edge, 0.f};
   // the first token needs no histogram; a grid too far out is not exact
   if (!(t > 0.f) || k == 1 || !(fabsf(edge) <= kFarthestBin)) return;
 #pragma unroll
@@ -409,21 +425,54 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
         atomicAdd((unsigned long long*)&hist[(int)d], (unsigned long long)(grid.unit(l, bin) + (1ull << kCountShift)));
     }
   __syncthreads();
-  uint64_t* out = hists + (int64_t)blockIdx.x * kBins;
+  const uint64_t h0 = hist[2 * tid], h1 = hist[2 * tid + 1];
+  const uint32_t c0 = (uint32_t)(h0 >> kCountShift), c1 = (uint32_t)(h1 >> kCountShift);
+  uint32_t ci = scan_u32(c0 + c1, lane);
+  if (lane == 63) counts[tid >> 6] = ci;
+  if (tid == 0) end_bin = kBins;
+  __syncthreads();
+  for (int w = 0; w < tid >> 6; ++w) ci += counts[w];
+  const uint32_t b1 = ci - c1, b0 = b1 - c0;
+  cursor[2 * tid] = b0;
+  cursor[2 * tid + 1] = b1;
+  if (tid == kScanThreads - 1) end_count = (int)ci;
+  __syncthreads();
+  if (k > 0) {  // past the chunk's own first k nothing is the row's
+    const uint32_t n = (uint32_t)k;
+    if (b0 < n && b1 >= n) {
+      end_bin = 2 * tid + 1;
+      end_count = (int)b1;
+    }
+    if (b1 < n && ci >= n) {
+      end_bin = 2 * tid + 2;
+      end_count = (int)ci;
+    }
+  }
+  const int64_t at = (int64_t)blockIdx.x * kBins + 2 * tid;
+  *(u32x4*)(ws.hists + at) = u32x4{(uint32_t)h0, (uint32_t)(h0 >> 32), (uint32_t)h1, (uint32_t)(h1 >> 32)};
+  *(uint32_t*)(ws.begins + at) = b0 | b1 << 16;
+  __syncthreads();
+  const float limit = (float)end_bin;
 #pragma unroll
-  for (int i = 0; i < kBins; i += kScanThreads) out[i + threadIdx.x] = hist[i + threadIdx.x];
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const float d = edge - grid.bin(x[j].v[e]);
+      if (d < limit) places[atomicAdd(&cursor[(int)d], 1u)] = (uint16_t)((j * kScanThreads + tid) * VE + e);
+    }
+  __syncthreads();
+  u32x4* out = (u32x4*)(ws.tokens + (int64_t)blockIdx.x * LEN);
+  for (int i = tid; i < (end_count + 7) / 8; i += kScanThreads) out[i] = ((const u32x4*)places)[i];
 }
 
 // ------------------------------------------------------------------ the choice
 // One block per row: the chunks' histograms added up say in which bin of the order
-// each filter ends and the answer lies.  Where the bins down to the last one that
-// can matter hold at most 8192 tokens, those are collected in one more read of the
-// row (as far as its chunks have any); otherwise each border bin's tokens are, one
-// read each.  A place within a bin is found among its tokens: each counts what
+// each filter ends and the answer lies; a border bin's tokens are fetched from the
+// chunks' lists.  A place within a bin is found among its tokens: each counts what
 // stands before it, at most 256 of them; a fuller bin is first divided by the order
-// of its tokens (logit, then index), 2048 ways.  A border bin of more tokens than
-// the list holds goes through the radix descents over the whole row.
-constexpr int kList = 8192;  // tokens collected at a time
+// of its tokens (logit, then index), 2048 ways.  A border bin of more than 8192
+// tokens goes through the radix descents over the whole row.
+constexpr int kList = 8192;  // tokens fetched at a time
 constexpr int kFew = 256;
 constexpr int kMaxChunks = (int)(kSampleMaxVocab / (kScanThreads * 32));
 
@@ -444,7 +493,6 @@ struct Pick {
   double wave_f64[kSampWaves];
   uint32_t wave_u32[kSampWaves];
   short dist[kMaxChunks];    // bins between the row's top and a chunk's, kBins for a chunk out of reach
-  uint8_t wanted[kMaxChunks];
   uint64_t before, answer;
   uint32_t bin_count;
   int n, found, n_few;
@@ -462,22 +510,21 @@ __device__ __forceinline__ double scan_f64(double v, int lane) {
 template <int TYPE>
 struct Picker {
   const void* row;
-  int V, chunks, chunk_len;
-  const ChunkHead* heads;
-  const uint64_t* hists;
+  int V;
+  const Chunks& ws;  // this row's
   Pick& s;
   Grid grid;
   float edge;  // the row's top bin
   double top;  // its largest l / T
-  bool whole;  // the list holds every token that can matter
+  int held;    // the bin whose tokens are in the list
 
   __device__ __forceinline__ double weight(float l) const { return exp((double)l * grid.per / kPerNat - top); }
 
   // The row's running counts and masses from the chunks' histograms.
   __device__ void merge() {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    for (int i = t; i < chunks; i += kSampThreads) {
-      const float e = heads[i].edge, d = edge - e;  // a chunk too far out has no histogram
+    for (int i = t; i < ws.n; i += kSampThreads) {
+      const float e = ws.heads[i].edge, d = edge - e;  // a chunk too far out has no histogram
       s.dist[i] = (short)(fabsf(e) <= kFarthestBin && d < (float)kBins ? (int)d : kBins);
     }
     __syncthreads();
@@ -486,9 +533,9 @@ struct Picker {
     uint64_t m = 0;
     uint32_t c = 0;
 #pragma unroll 8
-    for (int i = t / kBins; i < chunks; i += kSampThreads / kBins) {
+    for (int i = t / kBins; i < ws.n; i += kSampThreads / kBins) {
       const int at = bin - s.dist[i];
-      const uint64_t h = at >= 0 ? hists[(int64_t)i * kBins + at] : 0;
+      const uint64_t h = at >= 0 ? ws.hists[(int64_t)i * kBins + at] : 0;
       m += h & ((1ull << kCountShift) - 1);
       c += (uint32_t)(h >> kCountShift);
     }
@@ -543,78 +590,60 @@ struct Picker {
   }
   __device__ int bin_of_mass(double target, bool over) {
     const int t = threadIdx.x;
+    auto reached = [&](int i) { return over ? s.mass[i] > target : s.mass[i] >= target; };
     if (t < kBins && s.count[t] > count_before(t) &&
-        ((over ? s.mass[t] > target : s.mass[t] >= target) || s.count[t] == s.count[kBins - 1]))
-      atomicMin(&s.found, t);
+        (reached(t) ? t == 0 || !reached(t - 1) : s.count[t] == s.count[kBins - 1]))
+      s.found = t;
     return found_bin();
   }
 
-  // Collects the tokens of bins lo .. hi, reading the chunks that have some; false
-  // if they do not fit the list.
-  __device__ bool collect(int lo, int hi) {
-    constexpr int VE = Vec<TYPE>::VE, AHEAD = 32 / VE;
+  // Fetches bin b's tokens: 16 lanes a chunk.  False if they do not fit the list.
+  __device__ bool fetch(int b) {
+    if (held == b) return true;
+    if (s.count[b] - count_before(b) > (uint32_t)kList) return false;
+    held = b;
     if (threadIdx.x == 0) s.n = 0;
-    for (int i = threadIdx.x; i < chunks; i += kSampThreads) {
+    __syncthreads();
+    const int lane = threadIdx.x & 15;
+    for (int i = threadIdx.x >> 4; i < ws.n; i += kSampThreads / 16) {
       const int d = s.dist[i];
-      s.wanted[i] = d <= hi && (lo < hi || hists[(int64_t)i * kBins + hi - d] >> kCountShift != 0);
-    }
-    __syncthreads();
-    // bin numbers edge - hi .. edge - lo, as bounds of places on the grid
-    const float from = edge - (float)hi, to = edge - (float)lo + 1.f;
-    const int shift = 31 - __clz(chunk_len), vecs = (V + VE - 1) / VE, lane = threadIdx.x & 63;
-    for (int j0 = threadIdx.x; j0 - lane < vecs; j0 += AHEAD * kSampThreads) {  // waves stay together
-      Vec<TYPE> x[AHEAD];
-#pragma unroll
-      for (int a = 0; a < AHEAD; ++a) {
-        const int at = (j0 + a * kSampThreads) * VE;
-        if (at < V && s.wanted[at >> shift]) {
-          x[a].load(row, at, V);
-        } else {
-#pragma unroll
-          for (int e = 0; e < VE; ++e) x[a].v[e] = __builtin_nanf("");
-        }
-      }
-#pragma unroll
-      for (int a = 0; a < AHEAD; ++a) {
-        const int at = (j0 + a * kSampThreads) * VE;
-#pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const float z = grid.place(x[a].v[e]);
-          const bool hit = z >= from && z < to;
-          const uint64_t votes = __ballot(hit);
-          if (votes) {
-            int n = 0;
-            if (lane == 0) n = atomicAdd(&s.n, __popcll(votes));
-            n = __builtin_amdgcn_readfirstlane(n) + __popcll(votes & ((1ull << lane) - 1));
-            if (hit && n < kList) s.s.order[n] = (uint64_t)~key_of(x[a].v[e]) << 32 | (uint32_t)(at + e);
-          }
-        }
+      if (d > b) continue;
+      const int64_t at = (int64_t)i * kBins + b - d;
+      const int n = (int)(ws.hists[at] >> kCountShift);
+      const uint16_t* from = ws.tokens + (int64_t)i * ws.len + ws.begins[at];
+      if (n == 0) continue;
+      int to = 0;
+      if (lane == 0) to = atomicAdd(&s.n, n);
+      to = __shfl(to, threadIdx.x & 48, 64);
+      for (int j = lane; j < n; j += 16) {
+        const int token = i * ws.len + from[j];
+        s.s.order[to + j] = (uint64_t)~key_of(Logit<TYPE>::f32(((const typename Logit<TYPE>::T*)row)[token])) << 32 |
+                            (uint32_t)token;
       }
     }
     __syncthreads();
-    return s.n <= kList;
+    return true;
   }
 
   static __device__ __forceinline__ float logit_at(uint64_t order) { return logit_of(~(uint32_t)(order >> 32)); }
-  __device__ __forceinline__ int bin_at(uint64_t order) const { return (int)(edge - grid.bin(logit_at(order))); }
   __device__ __forceinline__ uint64_t unit_at(uint64_t order) const {
     const float l = logit_at(order);
     return grid.unit(l, grid.bin(l));
   }
 
-  // The token of bin b with which the bin's count (COUNT) or its units of mass first
-  // reach `target` (from 1 to the whole); `cum` receives the units up to and with it.
+  // The token of the fetched bin with which its count (COUNT) or its units of mass
+  // first reach `target` (from 1 to the whole); `cum` receives the units up to and
+  // with it.
   template <bool COUNT>
-  __device__ uint64_t select(int b, uint64_t target, uint64_t& cum) {
+  __device__ uint64_t select(uint64_t target, uint64_t& cum) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6, n = s.n;
     uint64_t lo = 0, hi = ~0ull, before = 0, before_units = 0;
-    uint32_t left = s.count[b] - count_before(b);
-    bool in_bin = !whole;  // the list holds this bin alone, or [lo, hi] has been narrowed to it
+    uint32_t left = (uint32_t)n;
     while (left > (uint32_t)kFew) {
       uint64_t mn = ~0ull, mx = 0;
       for (int i = t; i < n; i += kSampThreads) {
         const uint64_t o = s.s.order[i];
-        if (o >= lo && o <= hi && (in_bin || bin_at(o) == b)) {
+        if (o >= lo && o <= hi) {
           mn = ~max_u64(~mn, ~o);
           mx = max_u64(mx, o);
         }
@@ -632,7 +661,6 @@ struct Picker {
         mn = ~max_u64(~mn, ~s.wave_min[w]);
       }
       __syncthreads();
-      in_bin = true;  // a bin's tokens are neighbours in the order
       lo = mn;
       hi = mx;
       const int shift = max(0, 53 - __clzll(mn ^ mx));  // at most 2048 parts
@@ -677,7 +705,7 @@ struct Picker {
     __syncthreads();
     for (int i = t; i < n; i += kSampThreads) {
       const uint64_t o = s.s.order[i];
-      if (o >= lo && o <= hi && (in_bin || bin_at(o) == b)) {
+      if (o >= lo && o <= hi) {
         const int k = atomicAdd(&s.n_few, 1);
         s.few[k] = o;
         s.few_mass[k] = unit_at(o);
@@ -706,12 +734,12 @@ struct Picker {
     return o;
   }
 
-  // Units of mass of bin b's tokens up to `last` in the order with weight >= floor.
-  __device__ uint64_t heavy_units(int b, uint64_t last, double floor) {
+  // Units of mass of the fetched tokens up to `last` in the order with weight >= floor.
+  __device__ uint64_t heavy_units(uint64_t last, double floor) {
     uint64_t m = 0;
     for (int i = threadIdx.x; i < s.n; i += kSampThreads) {
       const uint64_t o = s.s.order[i];
-      if (o <= last && bin_at(o) == b && weight(logit_at(o)) >= floor) m += unit_at(o);
+      if (o <= last && weight(logit_at(o)) >= floor) m += unit_at(o);
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) m += __shfl_xor(m, o, 64);
@@ -730,28 +758,22 @@ struct Picker {
     uint64_t last = ~0ull, part = 0;
     int end = kBins;
     double kept = s.mass[kBins - 1];
-    const bool cut = k > 0 && k < V;
-    int b = kBins;
-    if (cut) b = bin_of_count((uint32_t)k);
-    // the last bin that can matter
-    int hi = min(b, kBins - 1);
-    if (!cut && p < 1.0) hi = bin_of_mass(p > 0.0 ? p * kept : 0.0, false);
-    whole = s.count[hi] <= (uint32_t)kList;
-    if (whole) collect(0, hi);
-    auto border = [&](int bin) { return whole || collect(bin, bin); };
-    if (b < kBins) {  // else the tokens beyond the bins have no mass
-      if (!border(b)) return false;
-      last = select<true>(b, (uint64_t)k - count_before(b), part);
-      end = b;
-      kept = mass_before(b) + (double)part * s.unit[b];
+    if (k > 0 && k < V) {
+      const int b = bin_of_count((uint32_t)k);
+      if (b < kBins) {  // else the tokens beyond the bins have no mass
+        if (!fetch(b)) return false;
+        last = select<true>((uint64_t)k - count_before(b), part);
+        end = b;
+        kept = mass_before(b) + (double)part * s.unit[b];
+      }
     }
     // the place in the order where the mass reaches (exceeds) a target, at most `kept`
     auto place = [&](double target, bool over, int& bin, uint64_t& at, uint64_t& cum) {
       bin = min(bin_of_mass(target, over), end);
-      if (!border(bin)) return false;
+      if (!fetch(bin)) return false;
       const double in = (target - mass_before(bin)) / s.unit[bin], need = over ? floor(in) + 1.0 : ceil(in);
       const uint64_t all = bin == end ? part : s.units[bin];
-      at = select<false>(bin, need >= (double)all ? all : need >= 1.0 ? (uint64_t)need : 1, cum);
+      at = select<false>(need >= (double)all ? all : need >= 1.0 ? (uint64_t)need : 1, cum);
       return true;
     };
     if (p < 1.0) {
@@ -770,15 +792,15 @@ struct Picker {
       bool found = false;
       for (int bin = max(0, near - 1); bin <= near + 1 && bin <= end && bin < kBins && !found; ++bin) {
         if (s.count[bin] == count_before(bin)) continue;
-        if (!border(bin)) return false;
+        if (!fetch(bin)) return false;
         const uint64_t whole_units = bin == end ? part : s.units[bin],
-                       heavy = heavy_units(bin, bin == end ? last : ~0ull, floor_w);
+                       heavy = heavy_units(bin == end ? last : ~0ull, floor_w);
         if (heavy < whole_units) {  // this bin holds the border
           found = true;
           end = bin;
           part = heavy;
           kept = mass_before(bin) + (double)heavy * s.unit[bin];
-          if (heavy) last = select<false>(bin, heavy, part);
+          if (heavy) last = select<false>(heavy, part);
         }
       }
       if (!found && end > near + 1) {  // no token near the border: nothing beyond it stays
@@ -799,18 +821,20 @@ struct Picker {
 };
 
 template <int TYPE>
-__global__ __launch_bounds__(kSampThreads) void sample_pick_kernel(SampleArgs a, int chunks, int chunk_len,
-                                                                   const ChunkHead* heads, const uint64_t* hists) {
+__global__ __launch_bounds__(kSampThreads) void sample_pick_kernel(SampleArgs a, Chunks ws) {
   __shared__ Pick s;
   typedef Logit<TYPE> L;
   const int64_t b = blockIdx.x;
-  heads += b * chunks;
+  ws.heads += b * ws.n;
+  ws.hists += b * ws.n * kBins;
+  ws.begins += b * ws.n * kBins;
+  ws.tokens += b * ws.n * ws.len;
   // everything the row is told, read at once
   const float t = a.temperature ? a.temperature[b] : 1.0f, pf = a.top_p ? a.top_p[b] : 1.0f,
               mpf = a.min_p ? a.min_p[b] : 0.0f, uf = a.u[b];
   const int k = a.top_k ? a.top_k[b] : 0;
   uint64_t best = 0;
-  for (int i = threadIdx.x; i < chunks; i += kSampThreads) best = max_u64(best, heads[i].top);
+  for (int i = threadIdx.x; i < ws.n; i += kSampThreads) best = max_u64(best, ws.heads[i].top);
   best = wave_max(best);
   if ((threadIdx.x & 63) == 0) s.wave_u64[threadIdx.x >> 6] = best;
   __syncthreads();
@@ -825,8 +849,7 @@ __global__ __launch_bounds__(kSampThreads) void sample_pick_kernel(SampleArgs a,
   } else if (t > 0.f && k != 1) {
     const double p = (double)pf, mp = (double)mpf, u = (double)uf;
     const float top = logit_of(top_key);
-    Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, chunks, chunk_len, heads,
-                      hists + b * chunks * kBins, s, Grid(t), 0.f, 0.0, false};
+    Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, ws, s, Grid(t), 0.f, 0.0, -1};
     pick.edge = pick.grid.bin(top);
     pick.top = (double)top * pick.grid.per / kPerNat;
     bool done = false;
@@ -856,25 +879,44 @@ int scan_pt(int64_t B, int V) {
 }
 int chunks_of(int V, int pt) { return (V + kScanThreads * pt - 1) / (kScanThreads * pt); }
 
+int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
+
+// The chunks' places in a workspace, and its size.
+Chunks chunks_in(char* ws, int64_t B, int V, int64_t& bytes) {
+  Chunks c;
+  const int pt = scan_pt(B, V);
+  c.len = kScanThreads * pt;
+  c.n = chunks_of(V, pt);
+  const int64_t n = B * c.n;
+  int64_t at = 0;
+  c.heads = (ChunkHead*)(ws + at); at += up256(n * (int64_t)sizeof(ChunkHead));
+  c.hists = (uint64_t*)(ws + at); at += n * kBins * 8;
+  c.begins = (uint16_t*)(ws + at); at += n * kBins * 2;
+  c.tokens = (uint16_t*)(ws + at); at += n * c.len * 2;
+  bytes = at;
+  return c;
+}
+
 template <int TYPE>
 hipError_t launch_type(const SampleArgs& a, void* ws, hipStream_t stream) {
-  const int pt = scan_pt(a.B, a.V), chunks = chunks_of(a.V, pt);
-  ChunkHead* heads = (ChunkHead*)ws;
-  uint64_t* hists = (uint64_t*)((char*)ws + (a.B * chunks * (int64_t)sizeof(ChunkHead) + 255) / 256 * 256);
-  auto scan = pt == 8 ? sample_scan_kernel<TYPE, 8> : pt == 16 ? sample_scan_kernel<TYPE, 16>
-                                                               : sample_scan_kernel<TYPE, 32>;
-  scan<<<(unsigned)(a.B * chunks), kScanThreads, 0, stream>>>(a, chunks, heads, hists);
+  int64_t bytes;
+  const Chunks c = chunks_in((char*)ws, a.B, a.V, bytes);
+  auto scan = c.len == 8 * kScanThreads    ? sample_scan_kernel<TYPE, 8>
+              : c.len == 16 * kScanThreads ? sample_scan_kernel<TYPE, 16>
+                                           : sample_scan_kernel<TYPE, 32>;
+  scan<<<(unsigned)(a.B * c.n), kScanThreads, 0, stream>>>(a, c);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  sample_pick_kernel<TYPE><<<(unsigned)a.B, kSampThreads, 0, stream>>>(a, chunks, kScanThreads * pt, heads, hists);
+  sample_pick_kernel<TYPE><<<(unsigned)a.B, kSampThreads, 0, stream>>>(a, c);
   return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t sample_workspace_bytes(int64_t B, int V) {
-  const int64_t chunks = B * chunks_of(V, scan_pt(B, V));
-  return (chunks * (int64_t)sizeof(ChunkHead) + 255) / 256 * 256 + chunks * kBins * 8;
+  int64_t bytes;
+  chunks_in(nullptr, B, V, bytes);
+  return bytes;
 }
 
 hipError_t launch_sample(SampleType type, const SampleArgs& a, void* ws, hipStream_t stream) {
