@@ -28,7 +28,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kSampThreads = 1024;
+constexpr int kSampThreads = 512;  // two blocks a CU, as registers and LDS allow
 constexpr int kSampWaves = kSampThreads / 64;
 constexpr int kRadix = 2048;
 constexpr double kMassUnit = 4398046511104.0;  // 2^42
@@ -165,7 +165,7 @@ struct Row {
   __device__ Prefix find(const Weigher& w, const Prefix& in, uint64_t target) {
     uint32_t prefix = 0;
     uint64_t before_mass = 0;
-    uint32_t before_count = 0, ties = 0;
+    uint32_t before_count = 0;
     for (int level = 0; level < 3; ++level) {
       const int shift = level == 0 ? 21 : level == 1 ? 10 : 0;
       const uint32_t digits = level == 2 ? 1024u : 2048u;
@@ -188,11 +188,17 @@ struct Row {
         }
       }
       __syncthreads();
-      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b0 = 2 * threadIdx.x;
-      const uint32_t c0 = s.count[b0], c1 = s.count[b0 + 1];
-      const uint64_t m0 = s.mass[b0], m1 = s.mass[b0 + 1];
-      uint32_t ci = scan_u32(c0 + c1, lane);
-      uint64_t mi = scan_u64(m0 + m1, lane);
+      constexpr int PER = kRadix / kSampThreads;
+      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, b0 = PER * threadIdx.x;
+      uint32_t c = 0;
+      uint64_t m = 0;
+#pragma unroll
+      for (int h = 0; h < PER; ++h) {
+        c += s.count[b0 + h];
+        m += s.mass[b0 + h];
+      }
+      uint32_t ci = scan_u32(c, lane);
+      uint64_t mi = scan_u64(m, lane);
       if (lane == 63) {
         s.wave_count[wave] = ci;
         s.wave_mass[wave] = mi;
@@ -202,27 +208,27 @@ struct Row {
         ci += s.wave_count[i];
         mi += s.wave_mass[i];
       }
-      const uint32_t ce = before_count + ci - c0 - c1;
-      const uint64_t me = before_mass + mi - m0 - m1;
+      uint32_t cb = before_count + ci - c;
+      uint64_t mb = before_mass + mi - m;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t cb = h ? ce + c0 : ce, c = h ? c1 : c0;
-        const uint64_t mb = h ? me + m0 : me, m = h ? m1 : m0;
+      for (int h = 0; h < PER; ++h) {
+        c = s.count[b0 + h];
+        m = s.mass[b0 + h];
         if (COUNT ? (cb < target && cb + (uint64_t)c >= target) : (mb < target && mb + m >= target)) {
           s.digit = digits - 1 - (uint32_t)(b0 + h);
           s.before_count = cb;
           s.before_mass = mb;
-          s.found = (int)c;
         }
+        cb += c;
+        mb += m;
       }
       __syncthreads();
       prefix = level == 0 ? s.digit : level == 1 ? prefix << 11 | s.digit : prefix << 10 | s.digit;
       before_count = s.before_count;
       before_mass = s.before_mass;
-      ties = (uint32_t)s.found;
       __syncthreads();
     }
-    // `ties` tokens have the key `prefix`: the place is the nth of them
+    // the place is the nth of the tokens with the key `prefix`
     uint32_t nth;
     if (COUNT) {
       nth = (uint32_t)target - before_count;
@@ -230,7 +236,6 @@ struct Row {
       const uint64_t m = w.mass(prefix), need = target - before_mass;
       nth = (uint32_t)((need + m - 1) / m);
     }
-    (void)ties;
     Prefix out;
     out.key = prefix;
     out.floor = in.floor;
@@ -470,9 +475,9 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
 // each filter ends and the answer lies; a border bin's tokens are fetched from the
 // chunks' lists.  A place within a bin is found among its tokens: each counts what
 // stands before it, at most 256 of them; a fuller bin is first divided by the order
-// of its tokens (logit, then index), 2048 ways.  A border bin of more than 8192
+// of its tokens (logit, then index), 2048 ways.  A border bin of more than 4096
 // tokens goes through the radix descents over the whole row.
-constexpr int kList = 8192;  // tokens fetched at a time
+constexpr int kList = 4096;  // tokens fetched at a time
 constexpr int kFew = 256;
 constexpr int kMaxChunks = (int)(kSampleMaxVocab / (kScanThreads * 32));
 
@@ -484,7 +489,9 @@ struct Pick {
       uint64_t hist[kRadix];
     } s;
   };
-  uint64_t few[kFew], few_mass[kFew];
+  struct __attribute__((aligned(16))) Few {
+    uint64_t order, units;
+  } few[kFew];
   uint32_t count[kBins];  // tokens in the bins up to and with this one
   double mass[kBins];     // and their mass, relative to the largest weight
   double unit[kBins];     // weight of a bin's unit of mass
@@ -528,31 +535,20 @@ struct Picker {
       s.dist[i] = (short)(fabsf(e) <= kFarthestBin && d < (float)kBins ? (int)d : kBins);
     }
     __syncthreads();
-    // half of the threads take every other chunk
-    const int bin = t & (kBins - 1);
+    static_assert(kBins == kSampThreads, "a bin a thread");
     uint64_t m = 0;
     uint32_t c = 0;
 #pragma unroll 8
-    for (int i = t / kBins; i < ws.n; i += kSampThreads / kBins) {
-      const int at = bin - s.dist[i];
+    for (int i = 0; i < ws.n; ++i) {
+      const int at = t - s.dist[i];
       const uint64_t h = at >= 0 ? ws.hists[(int64_t)i * kBins + at] : 0;
       m += h & ((1ull << kCountShift) - 1);
       c += (uint32_t)(h >> kCountShift);
     }
-    if (t >= kBins) {
-      s.s.hist[bin] = m;
-      s.count[bin] = c;
-    } else {
-      // e^(upper edge - top) 2^-35
-      s.unit[t] = exp(((double)edge - (double)t + 1.0) / kPerNat - top) / kBinUnit;
-    }
-    __syncthreads();
-    if (t < kBins) {
-      m += s.s.hist[t];
-      c += s.count[t];
-    }
-    uint32_t ci = scan_u32(t < kBins ? c : 0, lane);
-    double mi = scan_f64(t < kBins ? (double)m * s.unit[t] : 0.0, lane);
+    // e^(upper edge - top) 2^-35
+    const double unit = exp(((double)edge - (double)t + 1.0) / kPerNat - top) / kBinUnit;
+    uint32_t ci = scan_u32(c, lane);
+    double mi = scan_f64((double)m * unit, lane);
     if (lane == 63) {
       s.wave_u32[wave] = ci;
       s.wave_f64[wave] = mi;
@@ -562,11 +558,10 @@ struct Picker {
       ci += s.wave_u32[i];
       mi += s.wave_f64[i];
     }
-    if (t < kBins) {
-      s.count[t] = ci;
-      s.mass[t] = mi;
-      s.units[t] = m;
-    }
+    s.count[t] = ci;
+    s.mass[t] = mi;
+    s.unit[t] = unit;
+    s.units[t] = m;
     if (t == 0) s.found = kBins;
     __syncthreads();
   }
@@ -585,13 +580,13 @@ struct Picker {
   }
   __device__ int bin_of_count(uint32_t k) {
     const int t = threadIdx.x;
-    if (t < kBins && s.count[t] >= k && count_before(t) < k) s.found = t;
+    if (s.count[t] >= k && count_before(t) < k) s.found = t;
     return found_bin();
   }
   __device__ int bin_of_mass(double target, bool over) {
     const int t = threadIdx.x;
     auto reached = [&](int i) { return over ? s.mass[i] > target : s.mass[i] >= target; };
-    if (t < kBins && s.count[t] > count_before(t) &&
+    if (s.count[t] > count_before(t) &&
         (reached(t) ? t == 0 || !reached(t - 1) : s.count[t] == s.count[kBins - 1]))
       s.found = t;
     return found_bin();
@@ -673,24 +668,29 @@ struct Picker {
       }
       __syncthreads();
       constexpr uint64_t UNITS = (1ull << kCountShift) - 1;
-      const uint64_t m0 = s.s.hist[2 * t], m1 = s.s.hist[2 * t + 1];
-      uint64_t mi = scan_u64(m0 + m1, lane);
-      if (lane == 63) s.wave_u64[wave] = mi;
+      constexpr int PER = kRadix / kSampThreads;
+      uint64_t m = 0;
+#pragma unroll
+      for (int h = 0; h < PER; ++h) m += s.s.hist[PER * t + h];
+      uint64_t e = scan_u64(m, lane);
+      if (lane == 63) s.wave_u64[wave] = e;
       __syncthreads();
-      for (int w = 0; w < wave; ++w) mi += s.wave_u64[w];
-      const uint64_t e0 = mi - m0 - m1, e1 = e0 + m0;
+      for (int w = 0; w < wave; ++w) e += s.wave_u64[w];
+      e -= m;
       auto at = [&](uint64_t v) { return COUNT ? before + (v >> kCountShift) : before + (v & UNITS); };
-      auto take = [&](int part, uint64_t e, uint64_t m) {
+#pragma unroll
+      for (int h = 0; h < PER; ++h) {
+        m = s.s.hist[PER * t + h];
         if (at(e) < target && at(e + m) >= target) {
-          s.found = part;
+          s.found = PER * t + h;
           s.before = e;
           s.bin_count = (uint32_t)(m >> kCountShift);
         }
-      };
-      take(2 * t, e0, m0);
-      take(2 * t + 1, e1, m1);
+        e += m;
+      }
       __syncthreads();
-      const uint64_t part = (mn >> shift) + (uint64_t)s.found, e = s.before;
+      const uint64_t part = (mn >> shift) + (uint64_t)s.found;
+      e = s.before;
       left = s.bin_count;
       before = at(e);
       before_units += e & UNITS;
@@ -707,19 +707,21 @@ struct Picker {
       const uint64_t o = s.s.order[i];
       if (o >= lo && o <= hi) {
         const int k = atomicAdd(&s.n_few, 1);
-        s.few[k] = o;
-        s.few_mass[k] = unit_at(o);
+        s.few[k] = Pick::Few{o, unit_at(o)};
       }
     }
     __syncthreads();
-    if (t < s.n_few) {
-      const uint64_t o = s.few[t], m = s.few_mass[t];
+    const int few = s.n_few;
+    if (t < few) {
+      const uint64_t o = s.few[t].order, m = s.few[t].units;
       uint64_t c = 0;
-      uint64_t r = 0;
-      for (int i = 0; i < s.n_few; ++i) {
-        const bool first = s.few[i] < o;
+      uint32_t r = 0;
+#pragma unroll 4
+      for (int i = 0; i < few; ++i) {
+        const Pick::Few f = s.few[i];
+        const bool first = f.order < o;
         r += first ? 1 : 0;
-        c += first ? s.few_mass[i] : 0;
+        c += first ? f.units : 0;
       }
       const uint64_t was = before + (COUNT ? r : c), is = was + (COUNT ? 1 : m);
       if (was < target && is >= target) {
@@ -821,7 +823,7 @@ struct Picker {
 };
 
 template <int TYPE>
-__global__ __launch_bounds__(kSampThreads) void sample_pick_kernel(SampleArgs a, Chunks ws) {
+__global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs a, Chunks ws) {
   __shared__ Pick s;
   typedef Logit<TYPE> L;
   const int64_t b = blockIdx.x;
@@ -870,14 +872,15 @@ __global__ __launch_bounds__(kSampThreads) void sample_pick_kernel(SampleArgs a,
   }
 }
 
-// Logits per thread of a scan block: as many as leave 512 blocks, so that the card
-// is full, and at least 8: shorter chunks cost more in adding up their histograms.
+int chunks_of(int V, int pt) { return (V + kScanThreads * pt - 1) / (kScanThreads * pt); }
+// Logits per thread of a scan block: 8 where that is enough for 1024 blocks at most
+// and 32 chunks a row (a chunk's histogram costs the row's block a read; 1 x 131072
+// with 64 chunks 26 us, with 32 24), else 16 or 32.
 int scan_pt(int64_t B, int V) {
-  int pt = 32;
-  while (pt > 8 && B * ((V + kScanThreads * pt - 1) / (kScanThreads * pt)) < 512) pt /= 2;
+  int pt = 8;
+  while (pt < 32 && (chunks_of(V, pt) > 32 || B * chunks_of(V, pt) > 1024)) pt *= 2;
   return pt;
 }
-int chunks_of(int V, int pt) { return (V + kScanThreads * pt - 1) / (kScanThreads * pt); }
 
 int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
