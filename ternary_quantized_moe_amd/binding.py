@@ -409,62 +409,96 @@ def lowrank_apply(x, y_in, a, b, rank: int, a_q=None, b_q=None, y=None, workspac
     return y
 
 
-def _operand(name, t, device, dtypes, shape, strided=False):
-    """Checks one device tensor of the calls below: on the current device, of one
-    of these types, of this shape (a size of None is any) and contiguous
-    (strided: each row is)."""
-    if not t.is_cuda or t.device != device:
-        raise MoeError(-1, f"{name} is on {t.device}, not on {device}")
+def _wrong(name, t, device, dtypes, shape):
+    """The refusal of an operand that _operand found wrong."""
+    if t.get_device() != device:
+        return MoeError(-1, f"{name} is on {t.device}, not on the current device cuda:{device}")
+    if t.dtype not in dtypes:
+        return MoeError(-2, f"{name} has type {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        return MoeError(-3, f"{name} has shape {tuple(t.shape)}, {tuple(shape)} wanted")
+    return MoeError(-1, f"{name} is not contiguous")
+
+
+def _operand(name, t, device, dtypes, shape):
+    """Pointer of a contiguous tensor of one of these types and this shape on the
+    device with this index; anything else is refused.  (One expression on the
+    good path: these calls are a few microseconds long.)"""
+    if t.get_device() == device and t.dtype in dtypes and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    raise _wrong(name, t, device, dtypes, shape)
+
+
+def _current(t, T):
+    """Index of the current device, which has to be the tensor's."""
+    d = t.get_device()
+    if d < 0:
+        raise MoeError(-1, f"a device tensor is wanted, got one on {t.device}")
+    now = T["device"]()
+    if d != now:
+        raise MoeError(-1, f"the tensor is on cuda:{d}, the current device is cuda:{now}")
+    return d
+
+
+def _rows(name, t, dtypes):
+    """(pointer, rows, columns, row stride) of a matrix with contiguous rows."""
     if t.dtype not in dtypes:
         raise MoeError(-2, f"{name} has type {t.dtype}")
-    if t.dim() != len(shape) or any(s is not None and s != n for s, n in zip(shape, t.shape)):
-        raise MoeError(-3, f"{name} has shape {tuple(t.shape)}, {tuple(shape)} wanted")
-    if strided:
-        if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
-            raise MoeError(-1, f"the rows of {name} are not contiguous")
-    elif not t.is_contiguous():
-        raise MoeError(-1, f"{name} is not contiguous")
-
-
-def _row_stride(t):
-    """Row stride of a 2-d tensor with contiguous rows (a single row's is its length)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
-
-
-def _device_of(t):
-    """The tensor's device, which has to be the current one."""
-    import torch
-    if not t.is_cuda:
-        raise MoeError(-1, f"a device tensor is wanted, got one on {t.device}")
-    if t.device.index != torch.cuda.current_device():
-        raise MoeError(-1, f"the tensor is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
+    if t.dim() != 2:
+        raise MoeError(-3, f"{name} has {t.dim()} dimensions, 2 wanted")
+    rows, cols = t.shape
+    stride, step = t.stride()
+    if cols > 1 and step != 1 and rows:
+        raise MoeError(-1, f"the rows of {name} are not contiguous")
+    return t.data_ptr(), rows, cols, stride if rows > 1 else max(cols, 1)
 
 
 BF16, F16, F32 = 0, 1, 2
+_TYPES = {}
+
+
+def _types():
+    """torch types by role, looked up once (torch is imported with the first call)."""
+    if not _TYPES:
+        import torch
+        # the C bindings where torch has them: they cost less per call
+        device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _TYPES.update(
+            device=device, stream=raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), empty=torch.empty, f8=torch.float8_e4m3fn, bf16=torch.bfloat16, f32=torch.float32, i32=torch.int32,
+            codes=(torch.float8_e4m3fn, torch.uint8), half=(torch.bfloat16, torch.int16), f32s=(torch.float32,), i32s=(torch.int32,),
+            quant={torch.bfloat16: BF16, torch.int16: BF16, torch.float16: F16},
+            out={torch.bfloat16: BF16, torch.float32: F32},
+            logits={torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32})
+    return _TYPES
 
 
 def fp8_quantize(x, block_rows: int, q=None, scales=None, stream=None):
     """bf16 (torch.bfloat16 or int16 bits) or fp16 matrix [rows, cols] -> e4m3 codes
     and fp32 scales [ceil(rows / block_rows), cols / 128]: block_rows 1 for
     activations, 128 for weights."""
-    import torch
-    dev = _device_of(x)
-    _operand("x", x, dev, (torch.bfloat16, torch.int16, torch.float16), (None, None))
-    rows, cols = x.shape
+    T = _types()
+    dev = _current(x, T)
+    xp, rows, cols, stride = _rows("x", x, T["quant"])
+    if stride != cols and rows > 1:
+        raise MoeError(-1, "x is not contiguous")
+    fn = lib().moe_fp8_quantize
     if block_rows < 1 or cols % 128:
-        _check(lib().moe_fp8_quantize(BF16, None, rows, cols, block_rows, None, None, None))
+        _check(fn(BF16, None, rows, cols, block_rows, None, None, None))
     size = (-(-rows // block_rows), cols // 128)
     if q is None:
-        q = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+        q = T["empty"]((rows, cols), dtype=T["f8"], device=x.device)
+        qp = q.data_ptr()
     else:
-        _operand("q", q, dev, (torch.float8_e4m3fn, torch.uint8), (rows, cols))
+        qp = _operand("q", q, dev, T["codes"], (rows, cols))
     if scales is None:
-        scales = torch.empty(size, dtype=torch.float32, device=dev)
+        scales = T["empty"](size, dtype=T["f32"], device=x.device)
+        sp = scales.data_ptr()
     else:
-        _operand("scales", scales, dev, (torch.float32,), size)
-    _check(lib().moe_fp8_quantize(F16 if x.dtype == torch.float16 else BF16, x.data_ptr(), rows, cols, block_rows,
-                                  q.data_ptr(), scales.data_ptr(), _stream(stream)))
+        sp = _operand("scales", scales, dev, T["f32s"], size)
+    rc = fn(T["quant"][x.dtype], xp, rows, cols, block_rows, qp, sp, T["stream"](dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc)
     return q, scales
 
 
@@ -474,42 +508,53 @@ def rms_norm(x, weight, eps: float, residual=None, bf16: bool = True, fp8: bool 
     fp32 weight [d].  Returns a dict: "sum" (x + residual, with a residual only),
     "y" (bf16=True), "q" and "scales" (fp8=True: e4m3 with one scale per 128).
     sum, y, q, scales: buffers for them; sum and y may be x or residual."""
-    import torch
-    dev = _device_of(x)
-    half = (torch.bfloat16, torch.int16)
-    _operand("x", x, dev, half, (None, None))
-    T, d = x.shape
-    _operand("weight", weight, dev, (torch.float32,), (d,))
+    T = _types()
+    dev = _current(x, T)
+    half, empty = T["half"], T["empty"]
+    xp, n, d, stride = _rows("x", x, half)
+    if stride != d and n > 1:
+        raise MoeError(-1, "x is not contiguous")
+    wp = _operand("weight", weight, dev, T["f32s"], (d,))
+    shape, device = (n, d), x.device
+    rp = sump = yp = qp = sp = None
     out = {}
     if residual is not None:
-        _operand("residual", residual, dev, half, (T, d))
+        rp = _operand("residual", residual, dev, half, shape)
         if sum is None:
-            sum = torch.empty_like(x)
+            sum = empty(shape, dtype=x.dtype, device=device)
+            sump = sum.data_ptr()
         else:
-            _operand("sum", sum, dev, half, (T, d))
+            sump = _operand("sum", sum, dev, half, shape)
         out["sum"] = sum
+    elif sum is not None:
+        raise MoeError(-1, "sum needs a residual")
     if bf16:
         if y is None:
-            y = torch.empty_like(x)
+            y = empty(shape, dtype=x.dtype, device=device)
+            yp = y.data_ptr()
         else:
-            _operand("y", y, dev, half, (T, d))
+            yp = _operand("y", y, dev, half, shape)
         out["y"] = y
     elif y is not None:
         raise MoeError(-1, "y is given, but bf16 is off")
     if fp8:
         if q is None:
-            q = torch.empty((T, d), dtype=torch.float8_e4m3fn, device=dev)
+            q = empty(shape, dtype=T["f8"], device=device)
+            qp = q.data_ptr()
         else:
-            _operand("q", q, dev, (torch.float8_e4m3fn, torch.uint8), (T, d))
+            qp = _operand("q", q, dev, T["codes"], shape)
         if scales is None:
-            scales = torch.empty((T, d // 128), dtype=torch.float32, device=dev)
+            scales = empty((n, d // 128), dtype=T["f32"], device=device)
+            sp = scales.data_ptr()
         else:
-            _operand("scales", scales, dev, (torch.float32,), (T, d // 128))
-        out["q"], out["scales"] = q, scales
+            sp = _operand("scales", scales, dev, T["f32s"], (n, d // 128))
+        out["q"] = q
+        out["scales"] = scales
     elif q is not None or scales is not None:
         raise MoeError(-1, "q or scales is given, but fp8 is off")
-    _check(lib().moe_rms_norm(x.data_ptr(), _dev_ptr(residual), T, d, weight.data_ptr(), eps, _dev_ptr(sum),
-                              _dev_ptr(y), _dev_ptr(q), _dev_ptr(scales), _stream(stream)))
+    rc = lib().moe_rms_norm(xp, rp, n, d, wp, eps, sump, yp, qp, sp, T["stream"](dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc)
     return out
 
 
@@ -518,23 +563,27 @@ def fp8_linear(a, a_scales, w, w_scales, y=None, out_dtype=None, stream=None):
     codes) with the scales of fp8_quantize (block_rows 1 and 128) -> y [m, n],
     torch.bfloat16 (default) or torch.float32.  A given y may be padded: its rows
     are contiguous and its row stride is at least n."""
-    import torch
-    dev = _device_of(a)
-    codes = (torch.float8_e4m3fn, torch.uint8)
-    _operand("a", a, dev, codes, (None, None))
-    m, K = a.shape
-    _operand("w", w, dev, codes, (None, K))
-    n = w.shape[0]
-    _operand("a_scales", a_scales, dev, (torch.float32,), (m, K // 128))
-    _operand("w_scales", w_scales, dev, (torch.float32,), (-(-n // 128), K // 128))
+    T = _types()
+    dev = _current(a, T)
+    ap, m, K, stride = _rows("a", a, T["codes"])
+    if stride != K and m > 1:
+        raise MoeError(-1, "a is not contiguous")
+    n = w.shape[0] if w.dim() == 2 else -1
+    wp = _operand("w", w, dev, T["codes"], (n, K))
+    asp = _operand("a_scales", a_scales, dev, T["f32s"], (m, K // 128))
+    wsp = _operand("w_scales", w_scales, dev, T["f32s"], (-(-n // 128), K // 128))
     if y is None:
-        y = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=dev)
+        y = T["empty"]((m, n), dtype=out_dtype or T["bf16"], device=a.device)
+    elif y.get_device() != dev:
+        raise _wrong("y", y, dev, T["out"], (m, n))
     elif out_dtype is not None and out_dtype != y.dtype:
         raise MoeError(-2, f"y has type {y.dtype}, {out_dtype} wanted")
-    _operand("y", y, dev, (torch.bfloat16, torch.float32), (m, n), strided=True)
-    _check(lib().moe_fp8_linear(a.data_ptr(), a_scales.data_ptr(), m, w.data_ptr(), w_scales.data_ptr(), n, K,
-                                F32 if y.dtype == torch.float32 else BF16, y.data_ptr(), _row_stride(y),
-                                _stream(stream)))
+    yp, ym, yn, ldy = _rows("y", y, T["out"])
+    if ym != m or yn != n:
+        raise MoeError(-3, f"y has shape {(ym, yn)}, {(m, n)} wanted")
+    rc = lib().moe_fp8_linear(ap, asp, m, wp, wsp, n, K, T["out"][y.dtype], yp, ldy, T["stream"](dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc)
     return y
 
 
@@ -543,30 +592,33 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     """One token per row of logits [batch, vocab] (fp32, bf16 or fp16; rows may be
     padded) from uniform numbers u [batch]; temperature, top_p, min_p: fp32 [batch]
     or None, top_k: int32 [batch] or None.  Returns (tokens int32, probs fp32)."""
-    import torch
-    dev = _device_of(logits)
-    f32 = (torch.float32,)
-    _operand("logits", logits, dev, (torch.float32, torch.bfloat16, torch.float16), (None, None), strided=True)
-    B, V = logits.shape
-    for name, t, types in (("u", u, f32), ("temperature", temperature, f32), ("top_k", top_k, (torch.int32,)),
-                           ("top_p", top_p, f32), ("min_p", min_p, f32), ("tokens", tokens, (torch.int32,)),
-                           ("probs", probs, f32)):
-        if t is not None:
-            _operand(name, t, dev, types, (B,))
+    T = _types()
+    dev = _current(logits, T)
+    lp, B, V, ld = _rows("logits", logits, T["logits"])
+    f32s, size = T["f32s"], (B,)
+    up = _operand("u", u, dev, f32s, size)
+    tp = None if temperature is None else _operand("temperature", temperature, dev, f32s, size)
+    kp = None if top_k is None else _operand("top_k", top_k, dev, T["i32s"], size)
+    pp = None if top_p is None else _operand("top_p", top_p, dev, f32s, size)
+    mp = None if min_p is None else _operand("min_p", min_p, dev, f32s, size)
     if tokens is None:
-        tokens = torch.empty(B, dtype=torch.int32, device=dev)
+        tokens = T["empty"](size, dtype=T["i32"], device=logits.device)
     if probs is None:
-        probs = torch.empty(B, dtype=torch.float32, device=dev)
+        probs = T["empty"](size, dtype=T["f32"], device=logits.device)
+    tokp = _operand("tokens", tokens, dev, T["i32s"], size)
+    prp = _operand("probs", probs, dev, f32s, size)
+    L = lib()
     if workspace is None:
-        need = lib().moe_sample_workspace_bytes(B, V)
+        need = L.moe_sample_workspace_bytes(B, V)
         if need < 0:
             raise MoeError(-3, f"invalid sampler shape batch={B} vocab={V}")
-        workspace = alloc_workspace(need, dev)
-    wp, wn = _aligned(workspace)
-    kind = F32 if logits.dtype == torch.float32 else BF16 if logits.dtype == torch.bfloat16 else F16
-    _check(lib().moe_sample(kind, logits.data_ptr(), B, V, _row_stride(logits), _dev_ptr(temperature), _dev_ptr(top_k),
-                            _dev_ptr(top_p), _dev_ptr(min_p), _dev_ptr(u), tokens.data_ptr(), probs.data_ptr(), wp, wn,
-                            _stream(stream)))
+        workspace = alloc_workspace(need, logits.device)
+    elif workspace.get_device() != dev:
+        raise MoeError(-1, f"the workspace is on {workspace.device}, not on the current device cuda:{dev}")
+    ws, wn = _aligned(workspace)
+    rc = L.moe_sample(T["logits"][logits.dtype], lp, B, V, ld, tp, kp, pp, mp, up, tokp, prp, ws, wn, T["stream"](dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc)
     return tokens, probs
 
 
