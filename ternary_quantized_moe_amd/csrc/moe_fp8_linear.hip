@@ -42,14 +42,16 @@ __device__ __forceinline__ u32x2 widen_f8x4(int v) {
                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true))};
 }
 
-// One lane's 32 values of a group as the matrix cores take them.
-template <bool F32>
+// One lane's 32 values of a group: as codes for the 8-bit instruction, widened, or
+// as codes that are widened with every use.
+enum { kCodes, kWide, kWidenLater };
+template <int MODE>
 struct Frag {
   i32x8 v;
   __device__ __forceinline__ void set(i32x8 codes) { v = codes; }
 };
 template <>
-struct Frag<true> {
+struct Frag<kWide> {
   u32x4 v[4];
   __device__ __forceinline__ void set(i32x8 codes) {
 #pragma unroll
@@ -59,10 +61,10 @@ struct Frag<true> {
     }
   }
 };
-__device__ __forceinline__ f32x4 group_product(const Frag<false>& w, const Frag<false>& a) {
+__device__ __forceinline__ f32x4 group_product(const Frag<kCodes>& w, const Frag<kCodes>& a) {
   return mfma_f8_16(w.v, a.v, f32x4{0.f, 0.f, 0.f, 0.f});
 }
-__device__ __forceinline__ f32x4 group_product(const Frag<true>& w, const Frag<true>& a) {
+__device__ __forceinline__ f32x4 group_product(const Frag<kWide>& w, const Frag<kWide>& a) {
   f32x4 s = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 4; ++i) s = mfma16(w.v[i], a.v[i], s);
@@ -89,13 +91,19 @@ __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                  0, 0, 0);
 }
-__device__ __forceinline__ f32x16 half_product(const Frag<false>& w, const Frag<false>& a, f32x16 c) {
+__device__ __forceinline__ f32x16 half_product(const Frag<kCodes>& w, const Frag<kCodes>& a, f32x16 c) {
   return mfma_f8_32(w.v, a.v, c);
 }
-__device__ __forceinline__ f32x16 half_product(const Frag<true>& w, const Frag<true>& a, f32x16 c) {
+__device__ __forceinline__ f32x16 half_product(const Frag<kWide>& w, const Frag<kWide>& a, f32x16 c) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) c = mfma32(w.v[i], a.v[i], c);
   return c;
+}
+__device__ __forceinline__ f32x16 half_product(const Frag<kWidenLater>& w, const Frag<kWidenLater>& a, f32x16 c) {
+  Frag<kWide> wide_w, wide_a;
+  wide_w.set(w.v);
+  wide_a.set(a.v);
+  return half_product(wide_w, wide_a, c);
 }
 
 // A number that the compiler no longer knows: what is computed from it is not kept
@@ -109,10 +117,10 @@ __device__ __forceinline__ int opaque(int v) {
 // next.  `at`: the place of half 0's first piece; the others differ from it in one
 // or two address bits.
 __device__ __forceinline__ int staged_at(int row, int q) { return row * kF8Group + 16 * ((2 * q) ^ swizzle(row)); }
-template <bool F32>
-__device__ __forceinline__ Frag<F32> staged_frag(const uint8_t* buf, int at, int h) {
+template <int MODE>
+__device__ __forceinline__ Frag<MODE> staged_frag(const uint8_t* buf, int at, int h) {
   const u32x4 lo = *(const u32x4*)(buf + (at ^ 64 * h)), hi = *(const u32x4*)(buf + (at ^ (64 * h + 16)));
-  Frag<F32> r;
+  Frag<MODE> r;
   r.set(i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w});
   return r;
 }
@@ -130,12 +138,15 @@ template <int BN, int BM, int WTN, int WTM, int NB, bool F32>
 struct Tile {
   static constexpr int kWavesN = BN / WTN, kWaves = kWavesN * (BM / WTM), kThreads = 64 * kWaves;
   static constexpr int TN = WTN / 32, TM = WTM / 32;
+  // a single tile uses its operands once: widened with the use, they are not waited for when they are read
+  // (1 x 50304 x 2048 to fp32)
+  static constexpr int kMode = !F32 ? kCodes : TN * TM == 1 ? kWidenLater : kWide;
   static constexpr int kLoads = (BN + BM) / 8 / kWaves;  // staging loads of a wave per group
   static constexpr int kPerTile = TN * TM > 1 ? 2 * kLoads / (TN * TM) : kLoads;  // ... and behind a tile's product
   static constexpr int kBufBytes = (BN + BM) * kF8Group;
 
   f32x16 acc[TN][TM], t[2];
-  Frag<F32> fa[TM][2], fw[2][2];
+  Frag<kMode> fa[TM][2], fw[2][2];
   float s[TM], raw[NB][TM];  // the pending products' scales; the tokens' scales of the groups in the buffers
   const uint8_t *w, *a;
   int lane, wave, wn, wm, K, groups, last_n, last_m;
@@ -165,15 +176,15 @@ struct Tile {
     for (int e = 0; e < 16; ++e) acc[i][j][e] += t[e] * s;
   }
 
-  __device__ __forceinline__ void read_w(const uint8_t* buf, int i, Frag<F32> (&f)[2]) const {
+  __device__ __forceinline__ void read_w(const uint8_t* buf, int i, Frag<kMode> (&f)[2]) const {
     const int at = opaque(at_w);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) f[h] = staged_frag<F32>(buf + 32 * kF8Group * i, at, h);
+    for (int h = 0; h < 2; ++h) f[h] = staged_frag<kMode>(buf + 32 * kF8Group * i, at, h);
   }
   __device__ __forceinline__ void read_a(const uint8_t* buf, int j) {
     const int at = opaque(at_a);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) fa[j][h] = staged_frag<F32>(buf + (BN + 32 * j) * kF8Group, at, h);
+    for (int h = 0; h < 2; ++h) fa[j][h] = staged_frag<kMode>(buf + (BN + 32 * j) * kF8Group, at, h);
   }
 
   // The wave's results through LDS: token rows of WTN results, pieces of 16 bytes
@@ -425,16 +436,16 @@ __global__ __launch_bounds__(64 * kSplitWaves) void fp8_split_kernel(F8LinearArg
     auto frag = [&](int tile) {
       const u32x4 lo = *(const u32x4*)(at + tile * 16 * kF8Group + first),
                   hi = *(const u32x4*)(at + tile * 16 * kF8Group + (first ^ 16));
-      Frag<F32> f;
+      Frag<F32 ? kWide : kCodes> f;
       f.set(i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w});
       return f;
     };
-    Frag<F32> fw[RT];
+    Frag<F32 ? kWide : kCodes> fw[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) fw[r] = frag(r);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      const Frag<F32> fa = frag(RT + i);
+      const Frag<F32 ? kWide : kCodes> fa = frag(RT + i);
       const float f = s[i] * of_w;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
@@ -490,8 +501,8 @@ hipError_t launch_split(const F8LinearArgs& a, hipStream_t stream) {
 }
 
 // The largest tile of which there are enough for three quarters of the 256 CUs,
-// whose token side is not half empty: a larger tile reads less per product, but
-// each takes its time alone.  Microseconds for 4096 x 4096 x 4096, 1024 x 4096 x
+// whose token side (above 32) is not half empty: a larger tile reads less per
+// product, but each takes its time alone.  Microseconds for 4096 x 4096 x 4096, 1024 x 4096 x
 // 4096, 512 x 4096 x 4096 and 333 x 2561 x 4096 tokens x rows x K to bf16:
 //   256 x 256   73   -    -    -       (fp32 results do not fit the registers)
 //   128 x 128   94   26   22   23
@@ -505,7 +516,7 @@ template <bool F32>
 hipError_t launch(const F8LinearArgs& a, hipStream_t stream) {
   constexpr int64_t CUS = 256;
   auto blocks = [&](int64_t n, int64_t m) { return ((a.N + n - 1) / n) * ((a.M + m - 1) / m); };
-  auto fills = [&](int64_t n, int64_t m) { return m < 2 * a.M && 4 * blocks(n, m) >= 3 * CUS; };
+  auto fills = [&](int64_t n, int64_t m) { return (m == 32 || m < 2 * a.M) && 4 * blocks(n, m) >= 3 * CUS; };
   if (!F32 && fills(256, 256)) return launch_tiles<256, 256, 128, 64, 2, false>(a, stream);
   if (F32 && fills(128, 128) && blocks(128, 128) > CUS)  // larger wave tiles: fewer operands to widen
     return launch_tiles<128, 128, 64, 64, 2, true>(a, stream);
@@ -516,7 +527,7 @@ hipError_t launch(const F8LinearArgs& a, hipStream_t stream) {
     return blocks(128, 64) <= CUS ? launch_tiles<128, 64, 32, 32, 4, F32>(a, stream)
                                   : launch_tiles<128, 64, 64, 32, 2, F32>(a, stream);
   if (fills(64, 64)) return launch_tiles<64, 64, 32, 32, 4, F32>(a, stream);
-  if (a.M <= 32 && fills(128, 32)) return launch_tiles<128, 32, 32, 32, 4, F32>(a, stream);
+  if (fills(128, 32)) return launch_tiles<128, 32, 32, 32, 4, F32>(a, stream);
   if (fills(64, 32)) return launch_tiles<64, 32, 32, 32, 4, F32>(a, stream);
   if (a.M > 16 && blocks(32, 32) >= CUS) return launch_split<2, 2, F32>(a, stream);
   if (blocks(32, 16) >= CUS) return launch_split<2, 1, F32>(a, stream);
