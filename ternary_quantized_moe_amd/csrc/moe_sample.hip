@@ -388,9 +388,9 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   static_assert(kBins == 2 * kScanThreads, "two bins a thread");
   __shared__ uint64_t hist[kBins];
   __shared__ uint32_t cursor[kBins];
-  __shared__ uint64_t tops[WAVES];
+  __shared__ float tops[WAVES];
   __shared__ uint32_t counts[WAVES];
-  __shared__ int end_bin, end_count;
+  __shared__ int end_bin, end_count, top_index;
   __shared__ __attribute__((aligned(16))) uint16_t places[LEN];
   const int64_t b = blockIdx.x / ws.n;
   const int chunk = (int)(blockIdx.x - b * ws.n), base = chunk * LEN, tid = threadIdx.x, lane = tid & 63;
@@ -400,36 +400,49 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   for (int j = 0; j < N; ++j) x[j].load(row, base + (j * kScanThreads + tid) * VE, a.V);
   const float t = a.temperature ? a.temperature[b] : 1.0f;
   const int k = a.top_k ? a.top_k[b] : 0;
-  uint64_t top = 0;
+  // the largest value (a NaN is passed over), then the lowest index that has it
+  float mine = -__builtin_inff();
 #pragma unroll
   for (int j = 0; j < N; ++j)
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const int i = base + (j * kScanThreads + tid) * VE + e;
-      if (i < a.V) top = max_u64(top, (uint64_t)key_of(x[j].v[e]) << 32 | (uint32_t)~i);
-    }
-  top = wave_max(top);
+    for (int e = 0; e < VE; ++e) mine = fmaxf(mine, x[j].v[e]);
+  float top = mine;
+#pragma unroll
+  for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
   if (lane == 0) tops[tid >> 6] = top;
+  if (tid == 0) top_index = 0x7FFFFFFF;
   hist[tid] = 0;
   hist[tid + kScanThreads] = 0;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) top = max_u64(top, tops[w]);
+  for (int w = 0; w < WAVES; ++w) top = fmaxf(top, tops[w]);
+  if (mine == top) {
+    int first = 0x7FFFFFFF;
+#pragma unroll
+    for (int j = N - 1; j >= 0; --j)
+#pragma unroll
+      for (int e = VE - 1; e >= 0; --e)
+        if (x[j].v[e] == top) first = base + (j * kScanThreads + tid) * VE + e;
+    atomicMin(&top_index, first);
+  }
   const Grid grid(t);
-  const float edge = grid.bin(logit_of((uint32_t)(top >> 32)));
-  if (tid == 0) ws.heads[blockIdx.x] = ChunkHead{top, edge, 0.f};
+  const float edge = grid.bin(top);
+  const bool counted = t > 0.f && k != 1 && fabsf(edge) <= kFarthestBin;
   // the first token needs no histogram; a grid too far out is not exact
-  if (!(t > 0.f) || k == 1 || !(fabsf(edge) <= kFarthestBin)) return;
+  if (counted) {
 #pragma unroll
-  for (int j = 0; j < N; ++j)
+    for (int j = 0; j < N; ++j)
 #pragma unroll
-    for (int e = 0; e < VE; ++e) {
-      const float l = x[j].v[e];
-      const float bin = grid.bin(l), d = edge - bin;
-      if (d < (float)kBins)  // not for -inf and NaN
-        atomicAdd((unsigned long long*)&hist[(int)d], (unsigned long long)(grid.unit(l, bin) + (1ull << kCountShift)));
-    }
+      for (int e = 0; e < VE; ++e) {
+        const float l = x[j].v[e];
+        const float bin = grid.bin(l), d = edge - bin;
+        if (d < (float)kBins)  // not for -inf and NaN
+          atomicAdd((unsigned long long*)&hist[(int)d], (unsigned long long)(grid.unit(l, bin) + (1ull << kCountShift)));
+      }
+  }
   __syncthreads();
+  if (tid == 0) ws.heads[blockIdx.x] = ChunkHead{(uint64_t)key_of(top) << 32 | (uint32_t)~top_index, edge, 0.f};
+  if (!counted) return;
   const uint64_t h0 = hist[2 * tid], h1 = hist[2 * tid + 1];
   const uint32_t c0 = (uint32_t)(h0 >> kCountShift), c1 = (uint32_t)(h1 >> kCountShift);
   uint32_t ci = scan_u32(c0 + c1, lane);
