@@ -211,6 +211,58 @@ def test_linear(tq, m, n, k, dtype):
     check_linear(tq.fp8_linear(*ops, out_dtype=dtype), *ops)
 
 
+# sizes at which each tile shape and the split kernel are taken, with ragged edges on every side and an
+# odd number of groups
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,n,k", [(3500, 3601, 384), (1800, 1701, 640), (2500, 2203, 128), (700, 2402, 1152),
+                                   (60, 34001, 256), (1030, 1101, 896), (20, 25003, 384), (3, 25000, 640), (30, 13001, 1152),
+                                   (1, 13000, 256), (40, 4101, 1152), (10, 8301, 2176), (5, 100, 2304)])
+def test_linear_every_shape(tq, m, n, k, dtype):
+    say(f"fp8 linear {m} x {n} x {k} {dtype}")
+    ops = operands(tq, m, n, k, seed=m + n)
+    check_linear(tq.fp8_linear(*ops, out_dtype=dtype), *ops)
+
+
+def test_linear_past_32_bits(tq):
+    """An output of more than 2^31 values, and a w of more than 2^32 bytes: rows at the far end."""
+    say("fp8 linear past 32 bits")
+    a, sa, w, sw = operands(tq, 70001, 33000, 128)
+    y = tq.fp8_linear(a, sa, w, sw)
+    far = [0, 40000, 65535, 69999, 70000]
+    check_linear(y[far], a.view(torch.uint8)[far].view(a.dtype), sa[far], w, sw)
+    del y
+    n, k = 36000, 1024 * 128
+    w = torch.randint(0, 100, (n, k), dtype=torch.uint8, device="cuda")
+    sw = torch.rand((-(-n // 128), k // 128), device="cuda")
+    a, sa = tq.fp8_quantize(randn(1, 3, k).bfloat16(), 1)
+    y = tq.fp8_linear(a, sa, w, sw, out_dtype=torch.float32)
+    check_linear(y[:, 281 * 128:], a, sa, w[281 * 128:].view(a.dtype), sw[281:])
+    del w
+    torch.cuda.empty_cache()
+
+
+def test_norm_and_quantize_past_32_bits(tq):
+    T, d = 1_100_000, 2048
+    say("norm and quantizer past 32 bits")
+    x = torch.empty((T, d), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, T, 100_000):
+        x[i:i + 100_000] = randn(i, min(100_000, T - i), d).bfloat16()
+    w = 1 + 0.1 * randn(1, d)
+    far = [0, 600_000, 1_048_576, T - 1]
+    out = tq.rms_norm(x, w, EPS, bf16=True, fp8=True)
+    check_norm({k: t[far] if t.dtype != torch.float8_e4m3fn else t.view(torch.uint8)[far].view(t.dtype)
+                for k, t in out.items()}, x[far], None, w, EPS)
+    del out
+    for rows in (1, 128):
+        q, s = tq.fp8_quantize(x, rows)
+        lo = 1_099_900 // 128 * 128
+        want_q, want_s = fp8.quantize(x[lo:].float().cpu().numpy(), rows)
+        assert np.array_equal(q.view(torch.uint8)[lo:].cpu().numpy(), want_q)
+        assert np.array_equal(s[lo // rows:].cpu().numpy(), want_s)
+        del q
+    torch.cuda.empty_cache()
+
+
 def test_linear_long_k(tq):
     ops = operands(tq, 5, 130, 128 * 150)
     check_linear(tq.fp8_linear(*ops, out_dtype=torch.float32), *ops)
@@ -229,8 +281,9 @@ def test_linear_padded_output_keeps_its_padding(tq, m):
         assert bool((buf == 7.0).all())
 
 
-def test_linear_nan_stays_in_its_row_and_column(tq):
-    a, sa, w, sw = operands(tq, 40, 260, 256)
+@pytest.mark.parametrize("m,n", [(40, 260), (700, 2402)])
+def test_linear_nan_stays_in_its_row_and_column(tq, m, n):
+    a, sa, w, sw = operands(tq, m, n, 256)
     base = tq.fp8_linear(a, sa, w, sw, out_dtype=torch.float32)
     a2, w2 = a.view(torch.uint8).clone(), w.view(torch.uint8).clone()
     a2[3, 100] = 0x7F

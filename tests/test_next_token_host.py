@@ -56,6 +56,7 @@ def test_linear_refusals():
     assert rc(type=F16) == FORMAT
     assert rc(k=100) == SHAPE and rc(k=0) == SHAPE and rc(m=-1) == SHAPE and rc(n=-1) == SHAPE
     assert rc(m=1 << 31) == SHAPE and rc(ldy=299) == SHAPE and rc(ldy=1 << 62) == SHAPE
+    assert rc(k=(1 << 22) + 128) == SHAPE and rc(m=1 << 21, n=1 << 20, ldy=1 << 20) == SHAPE
     for k in ("a", "sa", "w", "sw", "y"):
         assert rc(**{k: None}) == ARG
     assert rc(a=0x100008) == ARG and rc(w=0x300008) == ARG and rc(sa=0x200002) == ARG
@@ -72,7 +73,7 @@ def test_sample_refusals():
         return L.moe_sample(type, logits, b, v, ld, t, k, p, mp, u, tokens, probs, ws, ws_bytes, None)
     assert rc(type=3) == FORMAT
     assert rc(v=0) == SHAPE and rc(v=(1 << 21) + 1, ld=1 << 22) == SHAPE
-    assert rc(b=-1) == SHAPE and rc(b=1 << 31) == SHAPE and rc(ld=999) == SHAPE
+    assert rc(b=-1) == SHAPE and rc(b=(1 << 22) + 1) == SHAPE and rc(ld=999) == SHAPE
     assert rc(logits=None) == ARG and rc(u=None) == ARG and rc(tokens=None) == ARG
     assert rc(ws=0x400010) == ARG
     for k in ("logits", "t", "k", "p", "mp", "u", "tokens", "probs"):
