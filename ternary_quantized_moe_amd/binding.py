@@ -465,7 +465,7 @@ def _types():
         device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _TYPES.update(
-            device=device, stream=raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), empty=torch.empty, f8=torch.float8_e4m3fn, bf16=torch.bfloat16, f32=torch.float32, i32=torch.int32,
+            device=device, stream=raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), like=torch.empty_like, u8=torch.uint8, f8=torch.float8_e4m3fn, bf16=torch.bfloat16, f32=torch.float32, i32=torch.int32,
             codes=(torch.float8_e4m3fn, torch.uint8), half=(torch.bfloat16, torch.int16), f32s=(torch.float32,), i32s=(torch.int32,),
             quant={torch.bfloat16: BF16, torch.int16: BF16, torch.float16: F16},
             out={torch.bfloat16: BF16, torch.float32: F32},
@@ -487,12 +487,12 @@ def fp8_quantize(x, block_rows: int, q=None, scales=None, stream=None):
         _check(fn(BF16, None, rows, cols, block_rows, None, None, None))
     size = (-(-rows // block_rows), cols // 128)
     if q is None:
-        q = T["empty"]((rows, cols), dtype=T["f8"], device=x.device)
+        q = T["like"](x, dtype=T["f8"])
         qp = q.data_ptr()
     else:
         qp = _operand("q", q, dev, T["codes"], (rows, cols))
     if scales is None:
-        scales = T["empty"](size, dtype=T["f32"], device=x.device)
+        scales = x.new_empty(size, dtype=T["f32"])
         sp = scales.data_ptr()
     else:
         sp = _operand("scales", scales, dev, T["f32s"], size)
@@ -510,18 +510,18 @@ def rms_norm(x, weight, eps: float, residual=None, bf16: bool = True, fp8: bool 
     sum, y, q, scales: buffers for them; sum and y may be x or residual."""
     T = _types()
     dev = _current(x, T)
-    half, empty = T["half"], T["empty"]
+    half, like = T["half"], T["like"]
     xp, n, d, stride = _rows("x", x, half)
     if stride != d and n > 1:
         raise MoeError(-1, "x is not contiguous")
     wp = _operand("weight", weight, dev, T["f32s"], (d,))
-    shape, device = (n, d), x.device
+    shape = (n, d)
     rp = sump = yp = qp = sp = None
     out = {}
     if residual is not None:
         rp = _operand("residual", residual, dev, half, shape)
         if sum is None:
-            sum = empty(shape, dtype=x.dtype, device=device)
+            sum = like(x)
             sump = sum.data_ptr()
         else:
             sump = _operand("sum", sum, dev, half, shape)
@@ -530,7 +530,7 @@ def rms_norm(x, weight, eps: float, residual=None, bf16: bool = True, fp8: bool 
         raise MoeError(-1, "sum needs a residual")
     if bf16:
         if y is None:
-            y = empty(shape, dtype=x.dtype, device=device)
+            y = like(x)
             yp = y.data_ptr()
         else:
             yp = _operand("y", y, dev, half, shape)
@@ -539,12 +539,12 @@ def rms_norm(x, weight, eps: float, residual=None, bf16: bool = True, fp8: bool 
         raise MoeError(-1, "y is given, but bf16 is off")
     if fp8:
         if q is None:
-            q = empty(shape, dtype=T["f8"], device=device)
+            q = like(x, dtype=T["f8"])
             qp = q.data_ptr()
         else:
             qp = _operand("q", q, dev, T["codes"], shape)
         if scales is None:
-            scales = empty((n, d // 128), dtype=T["f32"], device=device)
+            scales = x.new_empty((n, d // 128), dtype=T["f32"])
             sp = scales.data_ptr()
         else:
             sp = _operand("scales", scales, dev, T["f32s"], (n, d // 128))
@@ -573,7 +573,7 @@ def fp8_linear(a, a_scales, w, w_scales, y=None, out_dtype=None, stream=None):
     asp = _operand("a_scales", a_scales, dev, T["f32s"], (m, K // 128))
     wsp = _operand("w_scales", w_scales, dev, T["f32s"], (-(-n // 128), K // 128))
     if y is None:
-        y = T["empty"]((m, n), dtype=out_dtype or T["bf16"], device=a.device)
+        y = a_scales.new_empty((m, n), dtype=out_dtype or T["bf16"])
     elif y.get_device() != dev:
         raise _wrong("y", y, dev, T["out"], (m, n))
     elif out_dtype is not None and out_dtype != y.dtype:
@@ -602,9 +602,9 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     pp = None if top_p is None else _operand("top_p", top_p, dev, f32s, size)
     mp = None if min_p is None else _operand("min_p", min_p, dev, f32s, size)
     if tokens is None:
-        tokens = T["empty"](size, dtype=T["i32"], device=logits.device)
+        tokens = logits.new_empty(size, dtype=T["i32"])
     if probs is None:
-        probs = T["empty"](size, dtype=T["f32"], device=logits.device)
+        probs = T["like"](u)
     tokp = _operand("tokens", tokens, dev, T["i32s"], size)
     prp = _operand("probs", probs, dev, f32s, size)
     L = lib()
@@ -612,7 +612,7 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
         need = L.moe_sample_workspace_bytes(B, V)
         if need < 0:
             raise MoeError(-3, f"invalid sampler shape batch={B} vocab={V}")
-        workspace = alloc_workspace(need, logits.device)
+        workspace = logits.new_empty(need + 256, dtype=T["u8"])
     elif workspace.get_device() != dev:
         raise MoeError(-1, f"the workspace is on {workspace.device}, not on the current device cuda:{dev}")
     ws, wn = _aligned(workspace)
