@@ -540,18 +540,20 @@ struct Picker {
 
   __device__ __forceinline__ double weight(float l) const { return exp((double)l * grid.per / kPerNat - top); }
 
-  // The row's running counts and masses from the chunks' histograms.
-  __device__ void merge() {
+  // The row's running counts and masses from the chunks' histograms; `e` is the top
+  // bin of the thread's own chunk, if it has one.
+  __device__ void merge(float e) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    for (int i = t; i < ws.n; i += kSampThreads) {
-      const float e = ws.heads[i].edge, d = edge - e;  // a chunk too far out has no histogram
-      s.dist[i] = (short)(fabsf(e) <= kFarthestBin && d < (float)kBins ? (int)d : kBins);
+    static_assert(kMaxChunks <= kSampThreads, "a thread a chunk");
+    if (t < ws.n) {
+      const float d = edge - e;  // a chunk too far out has no histogram
+      s.dist[t] = (short)(fabsf(e) <= kFarthestBin && d < (float)kBins ? (int)d : kBins);
     }
     __syncthreads();
     static_assert(kBins == kSampThreads, "a bin a thread");
     uint64_t m = 0;
     uint32_t c = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int i = 0; i < ws.n; ++i) {
       const int at = t - s.dist[i];
       const uint64_t h = at >= 0 ? ws.hists[(int64_t)i * kBins + at] : 0;
@@ -849,7 +851,12 @@ __global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs
               mpf = a.min_p ? a.min_p[b] : 0.0f, uf = a.u[b];
   const int k = a.top_k ? a.top_k[b] : 0;
   uint64_t best = 0;
-  for (int i = threadIdx.x; i < ws.n; i += kSampThreads) best = max_u64(best, ws.heads[i].top);
+  float chunk_edge = 0.f;
+  if ((int)threadIdx.x < ws.n) {
+    const ChunkHead h = ws.heads[threadIdx.x];
+    best = h.top;
+    chunk_edge = h.edge;
+  }
   best = wave_max(best);
   if ((threadIdx.x & 63) == 0) s.wave_u64[threadIdx.x >> 6] = best;
   __syncthreads();
@@ -869,7 +876,7 @@ __global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs
     pick.top = (double)top * pick.grid.per / kPerNat;
     bool done = false;
     if (fabsf(pick.edge) <= kFarthestBin) {
-      pick.merge();
+      pick.merge(chunk_edge);
       done = pick.choose(k, p, mp, u, token, prob);
       __syncthreads();
     }
