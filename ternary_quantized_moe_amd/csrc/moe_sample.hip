@@ -488,9 +488,10 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
 // each filter ends and the answer lies; a border bin's tokens are fetched from the
 // chunks' lists.  A place within a bin is found among its tokens: each counts what
 // stands before it, at most 256 of them; a fuller bin is first divided by the order
-// of its tokens (logit, then index), 2048 ways.  A border bin of more than 4096
-// tokens goes through the radix descents over the whole row.
-constexpr int kList = 4096;  // tokens fetched at a time
+// of its tokens (logit, then index), 2048 ways.  Up to 4096 tokens are kept in LDS
+// for that, more are read from the chunks' lists every time.  Only rows whose grid is
+// not exact (an infinite logit, a temperature near 0) go through the radix descents.
+constexpr int kList = 4096;  // tokens kept
 constexpr int kFew = 256;
 constexpr int kMaxChunks = (int)(kSampleMaxVocab / (kScanThreads * 32));
 
@@ -500,6 +501,7 @@ struct Pick {
     struct {
       uint64_t order[kList];  // complement of the key, then the index: rising in the order of tokens
       uint64_t hist[kRadix];
+      uint32_t parts[kRadix];
     } s;
   };
   struct __attribute__((aligned(16))) Few {
@@ -514,7 +516,7 @@ struct Pick {
   uint32_t wave_u32[kSampWaves];
   short dist[kMaxChunks];    // bins between the row's top and a chunk's, kBins for a chunk out of reach
   uint64_t before, answer;
-  uint32_t bin_count;
+  uint32_t before_count, bin_count;
   int n, found, n_few;
 };
 
@@ -536,7 +538,8 @@ struct Picker {
   Grid grid;
   float edge;  // the row's top bin
   double top;  // its largest l / T
-  int held;    // the bin whose tokens are in the list
+  int held;    // the fetched bin
+  bool kept;   // whether its tokens are in the list
 
   __device__ __forceinline__ double weight(float l) const { return exp((double)l * grid.per / kPerNat - top); }
 
@@ -607,13 +610,11 @@ struct Picker {
     return found_bin();
   }
 
-  // Fetches bin b's tokens: 16 lanes a chunk.  False if they do not fit the list.
-  __device__ bool fetch(int b) {
-    if (held == b) return true;
-    if (s.count[b] - count_before(b) > (uint32_t)kList) return false;
-    held = b;
-    if (threadIdx.x == 0) s.n = 0;
-    __syncthreads();
+  // Every token of a bin from the chunks' lists, 16 lanes a chunk: begin(n) is called
+  // with a chunk's n tokens and says the number of its first, use(number, o) with each
+  // token's place in the order.
+  template <class Begin, class Use>
+  __device__ __forceinline__ void read_tokens(int b, Begin begin, Use use) {
     const int lane = threadIdx.x & 15;
     for (int i = threadIdx.x >> 4; i < ws.n; i += kSampThreads / 16) {
       const int d = s.dist[i];
@@ -622,17 +623,43 @@ struct Picker {
       const int n = (int)(ws.hists[at] >> kCountShift);
       const uint16_t* from = ws.tokens + (int64_t)i * ws.len + ws.begins[at];
       if (n == 0) continue;
-      int to = 0;
-      if (lane == 0) to = atomicAdd(&s.n, n);
-      to = __shfl(to, threadIdx.x & 48, 64);
+      const int to = begin(n);
       for (int j = lane; j < n; j += 16) {
         const int token = i * ws.len + from[j];
-        s.s.order[to + j] = (uint64_t)~key_of(Logit<TYPE>::f32(((const typename Logit<TYPE>::T*)row)[token])) << 32 |
-                            (uint32_t)token;
+        use(to + j, (uint64_t)~key_of(Logit<TYPE>::f32(((const typename Logit<TYPE>::T*)row)[token])) << 32 |
+                        (uint32_t)token);
       }
     }
+  }
+
+  // Makes bin b the one that the functions below look at.
+  __device__ void fetch(int b) {
+    if (held == b) return;
+    held = b;
+    const int n = (int)(s.count[b] - count_before(b));
+    kept = n <= kList;
+    if (threadIdx.x == 0) s.n = kept ? 0 : n;
     __syncthreads();
-    return true;
+    if (kept) {
+      read_tokens(
+          b,
+          [&](int more) {
+            int to = 0;
+            if ((threadIdx.x & 15) == 0) to = atomicAdd(&s.n, more);
+            return __shfl(to, threadIdx.x & 48, 64);
+          },
+          [&](int at, uint64_t o) { s.s.order[at] = o; });
+      __syncthreads();
+    }
+  }
+  // Every token of the fetched bin.
+  template <class Use>
+  __device__ __forceinline__ void each(Use use) {
+    if (kept) {
+      for (int i = threadIdx.x; i < s.n; i += kSampThreads) use(s.s.order[i]);
+    } else {
+      read_tokens(held, [](int) { return 0; }, [&](int, uint64_t o) { use(o); });
+    }
   }
 
   static __device__ __forceinline__ float logit_at(uint64_t order) { return logit_of(~(uint32_t)(order >> 32)); }
@@ -646,25 +673,27 @@ struct Picker {
   // with it.
   template <bool COUNT>
   __device__ uint64_t select(uint64_t target, uint64_t& cum) {
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, n = s.n;
-    uint64_t lo = 0, hi = ~0ull, before = 0, before_units = 0;
-    uint32_t left = (uint32_t)n;
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    uint64_t lo = 0, hi = ~0ull, before_units = 0;
+    uint32_t left = (uint32_t)s.n, before_count = 0;
     while (left > (uint32_t)kFew) {
       uint64_t mn = ~0ull, mx = 0;
-      for (int i = t; i < n; i += kSampThreads) {
-        const uint64_t o = s.s.order[i];
+      each([&](uint64_t o) {
         if (o >= lo && o <= hi) {
           mn = ~max_u64(~mn, ~o);
           mx = max_u64(mx, o);
         }
-      }
+      });
       mn = ~wave_max(~mn);
       mx = wave_max(mx);
       if (lane == 0) {
         s.wave_u64[wave] = mx;
         s.wave_min[wave] = mn;
       }
-      for (int i = t; i < kRadix; i += kSampThreads) s.s.hist[i] = 0;
+      for (int i = t; i < kRadix; i += kSampThreads) {
+        s.s.hist[i] = 0;
+        s.s.parts[i] = 0;
+      }
       __syncthreads();
       for (int w = 0; w < kSampWaves; ++w) {
         mx = max_u64(mx, s.wave_u64[w]);
@@ -674,41 +703,53 @@ struct Picker {
       lo = mn;
       hi = mx;
       const int shift = max(0, 53 - __clzll(mn ^ mx));  // at most 2048 parts
-      // counts above, units of at most 2^13 tokens below
-      for (int i = t; i < n; i += kSampThreads) {
-        const uint64_t o = s.s.order[i];
-        if (o >= lo && o <= hi)
-          atomicAdd((unsigned long long*)&s.s.hist[(o >> shift) - (mn >> shift)],
-                    (unsigned long long)((1ull << kCountShift) + unit_at(o)));
-      }
+      each([&](uint64_t o) {
+        if (o >= lo && o <= hi) {
+          const int part = (int)((o >> shift) - (mn >> shift));
+          atomicAdd((unsigned long long*)&s.s.hist[part], (unsigned long long)unit_at(o));
+          atomicAdd(&s.s.parts[part], 1u);
+        }
+      });
       __syncthreads();
-      constexpr uint64_t UNITS = (1ull << kCountShift) - 1;
       constexpr int PER = kRadix / kSampThreads;
       uint64_t m = 0;
+      uint32_t c = 0;
 #pragma unroll
-      for (int h = 0; h < PER; ++h) m += s.s.hist[PER * t + h];
+      for (int h = 0; h < PER; ++h) {
+        m += s.s.hist[PER * t + h];
+        c += s.s.parts[PER * t + h];
+      }
       uint64_t e = scan_u64(m, lane);
-      if (lane == 63) s.wave_u64[wave] = e;
+      uint32_t f = scan_u32(c, lane);
+      if (lane == 63) {
+        s.wave_u64[wave] = e;
+        s.wave_u32[wave] = f;
+      }
       __syncthreads();
-      for (int w = 0; w < wave; ++w) e += s.wave_u64[w];
-      e -= m;
-      auto at = [&](uint64_t v) { return COUNT ? before + (v >> kCountShift) : before + (v & UNITS); };
+      for (int w = 0; w < wave; ++w) {
+        e += s.wave_u64[w];
+        f += s.wave_u32[w];
+      }
+      e += before_units - m;
+      f += before_count - c;
 #pragma unroll
       for (int h = 0; h < PER; ++h) {
         m = s.s.hist[PER * t + h];
-        if (at(e) < target && at(e + m) >= target) {
+        c = s.s.parts[PER * t + h];
+        if (COUNT ? (f < target && f + (uint64_t)c >= target) : (e < target && e + m >= target)) {
           s.found = PER * t + h;
           s.before = e;
-          s.bin_count = (uint32_t)(m >> kCountShift);
+          s.before_count = f;
+          s.bin_count = c;
         }
         e += m;
+        f += c;
       }
       __syncthreads();
       const uint64_t part = (mn >> shift) + (uint64_t)s.found;
-      e = s.before;
       left = s.bin_count;
-      before = at(e);
-      before_units += e & UNITS;
+      before_units = s.before;
+      before_count = s.before_count;
       lo = max_u64(lo, part << shift);
       hi = ~max_u64(~hi, ~((part << shift) | ((1ull << shift) - 1)));
       __syncthreads();
@@ -718,13 +759,9 @@ struct Picker {
     // at most kFew are left: each counts what stands before it
     if (t == 0) s.n_few = 0;
     __syncthreads();
-    for (int i = t; i < n; i += kSampThreads) {
-      const uint64_t o = s.s.order[i];
-      if (o >= lo && o <= hi) {
-        const int k = atomicAdd(&s.n_few, 1);
-        s.few[k] = Pick::Few{o, unit_at(o)};
-      }
-    }
+    each([&](uint64_t o) {
+      if (o >= lo && o <= hi) s.few[atomicAdd(&s.n_few, 1)] = Pick::Few{o, unit_at(o)};
+    });
     __syncthreads();
     const int few = s.n_few;
     if (t < few) {
@@ -738,7 +775,7 @@ struct Picker {
         r += first ? 1 : 0;
         c += first ? f.units : 0;
       }
-      const uint64_t was = before + (COUNT ? r : c), is = was + (COUNT ? 1 : m);
+      const uint64_t was = COUNT ? before_count + (uint64_t)r : before_units + c, is = was + (COUNT ? 1 : m);
       if (was < target && is >= target) {
         s.answer = o;
         s.before = before_units + c + m;
@@ -754,10 +791,9 @@ struct Picker {
   // Units of mass of the fetched tokens up to `last` in the order with weight >= floor.
   __device__ uint64_t heavy_units(uint64_t last, double floor) {
     uint64_t m = 0;
-    for (int i = threadIdx.x; i < s.n; i += kSampThreads) {
-      const uint64_t o = s.s.order[i];
+    each([&](uint64_t o) {
       if (o <= last && weight(logit_at(o)) >= floor) m += unit_at(o);
-    }
+    });
 #pragma unroll
     for (int o = 32; o; o >>= 1) m += __shfl_xor(m, o, 64);
     if ((threadIdx.x & 63) == 0) s.wave_u64[threadIdx.x >> 6] = m;
@@ -768,39 +804,38 @@ struct Picker {
     return m;
   }
 
-  // The filters and the choice; false if a border's tokens do not fit the list.
-  __device__ bool choose(int k, double p, double mp, double u, int& token, double& prob) {
+  // The filters and the choice.
+  __device__ void choose(int k, double p, double mp, double u, int& token, double& prob) {
     // what is kept: the bins before `end`, and of bin `end` the tokens up to `last`,
-    // which hold `part` of its units; `kept` is the mass of it all
+    // which hold `part` of its units; `held_mass` is the mass of it all
     uint64_t last = ~0ull, part = 0;
     int end = kBins;
-    double kept = s.mass[kBins - 1];
+    double held_mass = s.mass[kBins - 1];
     if (k > 0 && k < V) {
       const int b = bin_of_count((uint32_t)k);
       if (b < kBins) {  // else the tokens beyond the bins have no mass
-        if (!fetch(b)) return false;
+        fetch(b);
         last = select<true>((uint64_t)k - count_before(b), part);
         end = b;
-        kept = mass_before(b) + (double)part * s.unit[b];
+        held_mass = mass_before(b) + (double)part * s.unit[b];
       }
     }
-    // the place in the order where the mass reaches (exceeds) a target, at most `kept`
+    // the place in the order where the mass reaches (exceeds) a target, at most `held_mass`
     auto place = [&](double target, bool over, int& bin, uint64_t& at, uint64_t& cum) {
       bin = min(bin_of_mass(target, over), end);
-      if (!fetch(bin)) return false;
+      fetch(bin);
       const double in = (target - mass_before(bin)) / s.unit[bin], need = over ? floor(in) + 1.0 : ceil(in);
       const uint64_t all = bin == end ? part : s.units[bin];
       at = select<false>(need >= (double)all ? all : need >= 1.0 ? (uint64_t)need : 1, cum);
-      return true;
     };
     if (p < 1.0) {
       int bin;
       uint64_t at, cum;
-      if (!place(p > 0.0 ? p * kept : 0.0, false, bin, at, cum)) return false;
+      place(p > 0.0 ? p * held_mass : 0.0, false, bin, at, cum);
       end = bin;
       last = at;
       part = cum;
-      kept = mass_before(end) + (double)part * s.unit[end];
+      held_mass = mass_before(end) + (double)part * s.unit[end];
     }
     if (mp > 0.0) {
       // the bin that weight mp falls into; rounding may put it into a neighbour
@@ -809,31 +844,31 @@ struct Picker {
       bool found = false;
       for (int bin = max(0, near - 1); bin <= near + 1 && bin <= end && bin < kBins && !found; ++bin) {
         if (s.count[bin] == count_before(bin)) continue;
-        if (!fetch(bin)) return false;
+        fetch(bin);
         const uint64_t whole_units = bin == end ? part : s.units[bin],
                        heavy = heavy_units(bin == end ? last : ~0ull, floor_w);
         if (heavy < whole_units) {  // this bin holds the border
           found = true;
           end = bin;
           part = heavy;
-          kept = mass_before(bin) + (double)heavy * s.unit[bin];
+          held_mass = mass_before(bin) + (double)heavy * s.unit[bin];
           if (heavy) last = select<false>(heavy, part);
         }
       }
       if (!found && end > near + 1) {  // no token near the border: nothing beyond it stays
         end = min(near + 2, kBins);
         part = 0;
-        kept = s.mass[end - 1];
+        held_mass = s.mass[end - 1];
       }
     }
     int bin;
     uint64_t at, cum;
     if (!(u >= 0.0)) u = 0.0;
     // the last token with mass stands in for a u of 1 or more
-    if (!(u < 1.0 ? place(u * kept, true, bin, at, cum) : place(kept, false, bin, at, cum))) return false;
+    if (u < 1.0) place(u * held_mass, true, bin, at, cum);
+    else place(held_mass, false, bin, at, cum);
     token = (int)(uint32_t)at;
-    prob = weight(logit_at(at)) / kept;
-    return true;
+    prob = weight(logit_at(at)) / held_mass;
   }
 };
 
@@ -871,14 +906,14 @@ __global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs
   } else if (t > 0.f && k != 1) {
     const double p = (double)pf, mp = (double)mpf, u = (double)uf;
     const float top = logit_of(top_key);
-    Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, ws, s, Grid(t), 0.f, 0.0, -1};
+    Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, ws, s, Grid(t), 0.f, 0.0, -1, false};
     pick.edge = pick.grid.bin(top);
     pick.top = (double)top * pick.grid.per / kPerNat;
     bool done = false;
     if (fabsf(pick.edge) <= kFarthestBin) {
       pick.merge(chunk_edge);
-      done = pick.choose(k, p, mp, u, token, prob);
-      __syncthreads();
+      pick.choose(k, p, mp, u, token, prob);
+      done = true;
     }
     if (!done) {
       Row<TYPE> row{(const typename L::T*)a.logits + b * a.ld, a.V, s.radix};

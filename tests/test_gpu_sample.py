@@ -102,6 +102,15 @@ def test_flat_and_peaked(tq, spread):
     check(tq, logits_of(6, V, 1, spread=spread), np.random.default_rng(2).random(6), **settings)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_full_borders(tq, dtype):
+    """A long vocabulary so even that every border lies among thousands of near-equal logits."""
+    V = 180001
+    settings = dict(temperature=[1.3] * 7, top_k=[0, 0, 60000, 0, 90000, 0, 170000], top_p=[0.5, 1.0, 1.0, 0.99, 0.7, 0.2, 1.0],
+                    min_p=[0.0, 0.0, 0.0, 0.3, 0.2, 0.0, 0.5])
+    check(tq, logits_of(7, V, 3, dtype, spread=1.0), np.random.default_rng(5).random(7), **settings)
+
+
 def test_ties_take_the_lowest_index(tq):
     V = 5000
     logits = torch.zeros((5, V), device="cuda")
