@@ -38,16 +38,19 @@ struct Logit;
 template <>
 struct Logit<kSampleF32> {
   typedef float T;
+  static constexpr int kDead = 0;  // low bits of an ordered key that say nothing
   static __device__ __forceinline__ float f32(float v) { return v; }
 };
 template <>
 struct Logit<kSampleBf16> {
   typedef uint16_t T;
+  static constexpr int kDead = 16;
   static __device__ __forceinline__ float f32(uint16_t v) { return bf16_to_f32(v); }
 };
 template <>
 struct Logit<kSampleF16> {
   typedef uint16_t T;
+  static constexpr int kDead = 13;
   static __device__ __forceinline__ float f32(uint16_t v) { return f16_to_f32(v); }
 };
 
@@ -325,18 +328,18 @@ struct Grid {
   __device__ __forceinline__ explicit Grid(float t) : per(kPerNat / (double)t), perf((float)per) {}
   __device__ __forceinline__ float place(float l) const { return l * perf; }
   __device__ __forceinline__ float bin(float l) const { return floorf(place(l)); }
+  // COUNTED: with 2^50 on top.  The polynomial of degree 4 that meets
+  // 2^35 e^((y - 1) / 16) at the Chebyshev nodes of y in [0, 1] is off by 0.52 units
+  // at most.  Adding 2^52 leaves the rounded integer in a double's low bits.
+  template <bool COUNTED>
   __device__ __forceinline__ uint64_t unit(float l, float bin) const {
-    // e^x on [-1/16, 0] by its series: the first term left out is 2^-40 of it
-    const double x = fma((double)l, per, -((double)bin + 1.0)) * (1.0 / kPerNat);
-    double e = 1.0 / 720;
-    e = fma(e, x, 1.0 / 120);
-    e = fma(e, x, 1.0 / 24);
-    e = fma(e, x, 1.0 / 6);
-    e = fma(e, x, 0.5);
-    e = fma(e, x, 1.0);
-    e = fma(e, x, 1.0);
-    // adding 2^52 leaves the rounded integer in the low bits
-    return (uint64_t)__double_as_longlong(fma(e, kBinUnit, 4503599627370496.0)) & ((1ull << 52) - 1);
+    const double y = fma((double)l, per, -(double)bin);
+    double e = 21174.08417495729;
+    e = fma(e, y, 1312820.8186157919);
+    e = fma(e, y, 63043148.908760265);
+    e = fma(e, y, 2017374165.4019043);
+    e = fma(e, y, 32277987058.26685 + 4503599627370496.0 + (COUNTED ? 1125899906842624.0 : 0.0));
+    return (uint64_t)__double_as_longlong(e) & ~(0xFFFull << 52);
   }
 };
 
@@ -386,8 +389,8 @@ template <int TYPE, int PT>
 __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a, Chunks ws) {
   constexpr int VE = Vec<TYPE>::VE, N = PT / VE, LEN = kScanThreads * PT, WAVES = kScanThreads / 64;
   static_assert(kBins == 2 * kScanThreads, "two bins a thread");
-  __shared__ uint64_t hist[kBins];
-  __shared__ uint32_t cursor[kBins];
+  __shared__ uint64_t hist[kBins + 64];
+  __shared__ uint32_t begin[kBins];
   __shared__ float tops[WAVES];
   __shared__ uint32_t counts[WAVES];
   __shared__ int end_bin, end_count, top_index;
@@ -430,14 +433,17 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   const bool counted = t > 0.f && k != 1 && fabsf(edge) <= kFarthestBin;
   // the first token needs no histogram; a grid too far out is not exact
   if (counted) {
+    // a token's seat: its bin and its number there.  What is too far below the top
+    // has one in the bins behind, one for each lane of a wave
+    const float nowhere = (float)(kBins + lane);
 #pragma unroll
     for (int j = 0; j < N; ++j)
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        const float l = x[j].v[e];
-        const float bin = grid.bin(l), d = edge - bin;
-        if (d < (float)kBins)  // not for -inf and NaN
-          atomicAdd((unsigned long long*)&hist[(int)d], (unsigned long long)(grid.unit(l, bin) + (1ull << kCountShift)));
+        const float l = x[j].v[e], bin = grid.bin(l);
+        const uint32_t at = (uint32_t)fminf(edge - bin, nowhere);  // a NaN is passed over
+        const uint64_t was = atomicAdd((unsigned long long*)&hist[at], (unsigned long long)grid.template unit<true>(l, bin));
+        x[j].v[e] = __uint_as_float(at << 16 | (uint32_t)(was >> kCountShift));  // from here on a seat
       }
   }
   __syncthreads();
@@ -451,8 +457,8 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   __syncthreads();
   for (int w = 0; w < tid >> 6; ++w) ci += counts[w];
   const uint32_t b1 = ci - c1, b0 = b1 - c0;
-  cursor[2 * tid] = b0;
-  cursor[2 * tid + 1] = b1;
+  begin[2 * tid] = b0;
+  begin[2 * tid + 1] = b1;
   if (tid == kScanThreads - 1) end_count = (int)ci;
   __syncthreads();
   if (k > 0) {  // past the chunk's own first k nothing is the row's
@@ -470,13 +476,13 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   *(u32x4*)(ws.hists + at) = u32x4{(uint32_t)h0, (uint32_t)(h0 >> 32), (uint32_t)h1, (uint32_t)(h1 >> 32)};
   *(uint32_t*)(ws.begins + at) = b0 | b1 << 16;
   __syncthreads();
-  const float limit = (float)end_bin;
+  const uint32_t limit = (uint32_t)end_bin << 16;
 #pragma unroll
   for (int j = 0; j < N; ++j)
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const float d = edge - grid.bin(x[j].v[e]);
-      if (d < limit) places[atomicAdd(&cursor[(int)d], 1u)] = (uint16_t)((j * kScanThreads + tid) * VE + e);
+      const uint32_t seat = __float_as_uint(x[j].v[e]);
+      if (seat < limit) places[begin[seat >> 16] + (seat & 0xFFFFu)] = (uint16_t)((j * kScanThreads + tid) * VE + e);
     }
   __syncthreads();
   u32x4* out = (u32x4*)(ws.tokens + (int64_t)blockIdx.x * LEN);
@@ -499,7 +505,7 @@ struct Pick {
   union {
     Shared radix;
     struct {
-      uint64_t order[kList];  // complement of the key, then the index: rising in the order of tokens
+      uint64_t order[kList];
       uint64_t hist[kRadix];
       uint32_t parts[kRadix];
     } s;
@@ -531,6 +537,7 @@ __device__ __forceinline__ double scan_f64(double v, int lane) {
 
 template <int TYPE>
 struct Picker {
+  typedef Logit<TYPE> L;
   const void* row;
   int V;
   const Chunks& ws;  // this row's
@@ -538,8 +545,9 @@ struct Picker {
   Grid grid;
   float edge;  // the row's top bin
   double top;  // its largest l / T
-  int held;    // the fetched bin
-  bool kept;   // whether its tokens are in the list
+  int here;    // the fetched bin
+  bool kept;   // whether its tokens are in the list, which holds the bins
+  int list_from, list_to;
 
   __device__ __forceinline__ double weight(float l) const { return exp((double)l * grid.per / kPerNat - top); }
 
@@ -610,43 +618,69 @@ struct Picker {
     return found_bin();
   }
 
-  // Every token of a bin from the chunks' lists, 16 lanes a chunk: begin(n) is called
-  // with a chunk's n tokens and says the number of its first, use(number, o) with each
-  // token's place in the order.
+  // A token's place in the order as a number that rises along it: the complement of
+  // the key without its dead bits, then the index.
+  static constexpr int kIndexBits = 21;
+  static_assert(kSampleMaxVocab <= 1ll << kIndexBits, "a token's index");
+  static __device__ __forceinline__ uint64_t order_of(float l, int token) {
+    return (uint64_t)(~key_of(l) >> L::kDead) << kIndexBits | (uint32_t)token;
+  }
+  static __device__ __forceinline__ float logit_at(uint64_t order) {
+    const uint32_t k = ~((uint32_t)(order >> kIndexBits) << L::kDead);  // dead bits set
+    return logit_of(k & 0x80000000u ? k & ~0u << L::kDead : k);
+  }
+  static __device__ __forceinline__ int token_at(uint64_t order) { return (int)(order & ((1u << kIndexBits) - 1)); }
+
+  // Every token of the bins from `b0` to `b` from the chunks' lists: begin(n) is called
+  // by the lanes of a chunk with its n tokens and says the number of its first,
+  // use(number, o) with each token's place in the order.
   template <class Begin, class Use>
-  __device__ __forceinline__ void read_tokens(int b, Begin begin, Use use) {
-    const int lane = threadIdx.x & 15;
-    for (int i = threadIdx.x >> 4; i < ws.n; i += kSampThreads / 16) {
+  __device__ __forceinline__ void read_tokens(int b0, int b, Begin begin, Use use) {
+    const int lanes = ws.n > 16 ? 16 : ws.n > 8 ? 32 : 64;  // of a chunk
+    const int lane = threadIdx.x & (lanes - 1);
+    for (int i = threadIdx.x / lanes; i < ws.n; i += kSampThreads / lanes) {
       const int d = s.dist[i];
       if (d > b) continue;
-      const int64_t at = (int64_t)i * kBins + b - d;
-      const int n = (int)(ws.hists[at] >> kCountShift);
-      const uint16_t* from = ws.tokens + (int64_t)i * ws.len + ws.begins[at];
+      const int64_t at = (int64_t)i * kBins;
+      const int first = b0 > d ? ws.begins[at + b0 - d] : 0;
+      const int n = ws.begins[at + b - d] + (int)(ws.hists[at + b - d] >> kCountShift) - first;
       if (n == 0) continue;
-      const int to = begin(n);
-      for (int j = lane; j < n; j += 16) {
-        const int token = i * ws.len + from[j];
-        use(to + j, (uint64_t)~key_of(Logit<TYPE>::f32(((const typename Logit<TYPE>::T*)row)[token])) << 32 |
-                        (uint32_t)token);
+      const uint16_t* from = ws.tokens + (int64_t)i * ws.len + first;
+      const int to = begin(n, lanes);
+      for (int j = lane; j < n; j += 4 * lanes) {  // four at a time on their way
+        int token[4];
+        float l[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) token[q] = i * ws.len + from[min(j + q * lanes, n - 1)];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) l[q] = L::f32(((const typename L::T*)row)[token[q]]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (j + q * lanes < n) use(to + j + q * lanes, order_of(l[q], token[q]));
       }
     }
   }
 
-  // Makes bin b the one that the functions below look at.
+  // Makes bin b the one that the functions below look at.  The list holds the bins up
+  // to the first border that is asked for if that is possible: later borders lie
+  // before it.
   __device__ void fetch(int b) {
-    if (held == b) return;
-    held = b;
+    here = b;
+    if (kept && b >= list_from && b <= list_to) return;
+    __syncthreads();
     const int n = (int)(s.count[b] - count_before(b));
+    list_from = s.count[b] <= (uint32_t)kList ? 0 : b;
+    list_to = b;
     kept = n <= kList;
-    if (threadIdx.x == 0) s.n = kept ? 0 : n;
+    if (threadIdx.x == 0) s.n = 0;
     __syncthreads();
     if (kept) {
       read_tokens(
-          b,
-          [&](int more) {
+          list_from, b,
+          [&](int more, int lanes) {
             int to = 0;
-            if ((threadIdx.x & 15) == 0) to = atomicAdd(&s.n, more);
-            return __shfl(to, threadIdx.x & 48, 64);
+            if ((threadIdx.x & (lanes - 1)) == 0) to = atomicAdd(&s.n, more);
+            return __shfl(to, threadIdx.x & 63 & -lanes, 64);
           },
           [&](int at, uint64_t o) { s.s.order[at] = o; });
       __syncthreads();
@@ -656,16 +690,18 @@ struct Picker {
   template <class Use>
   __device__ __forceinline__ void each(Use use) {
     if (kept) {
-      for (int i = threadIdx.x; i < s.n; i += kSampThreads) use(s.s.order[i]);
+      for (int i = threadIdx.x; i < s.n; i += kSampThreads) {
+        const uint64_t o = s.s.order[i];
+        if (list_from == list_to || edge - grid.bin(logit_at(o)) == (float)here) use(o);
+      }
     } else {
-      read_tokens(held, [](int) { return 0; }, [&](int, uint64_t o) { use(o); });
+      read_tokens(here, here, [](int, int) { return 0; }, [&](int, uint64_t o) { use(o); });
     }
   }
 
-  static __device__ __forceinline__ float logit_at(uint64_t order) { return logit_of(~(uint32_t)(order >> 32)); }
   __device__ __forceinline__ uint64_t unit_at(uint64_t order) const {
     const float l = logit_at(order);
-    return grid.unit(l, grid.bin(l));
+    return grid.template unit<false>(l, grid.bin(l));
   }
 
   // The token of the fetched bin with which its count (COUNT) or its units of mass
@@ -675,7 +711,7 @@ struct Picker {
   __device__ uint64_t select(uint64_t target, uint64_t& cum) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     uint64_t lo = 0, hi = ~0ull, before_units = 0;
-    uint32_t left = (uint32_t)s.n, before_count = 0;
+    uint32_t left = s.count[here] - count_before(here), before_count = 0;
     while (left > (uint32_t)kFew) {
       uint64_t mn = ~0ull, mx = 0;
       each([&](uint64_t o) {
@@ -764,19 +800,26 @@ struct Picker {
     });
     __syncthreads();
     const int few = s.n_few;
-    if (t < few) {
-      const uint64_t o = s.few[t].order, m = s.few[t].units;
+    // as many lanes to a token as there are, up to a wave
+    const int per = few > 1 ? max(0, min(6, __clz(few - 1) - 23)) : 6;
+    const int i0 = t & ((1 << per) - 1);
+    if (t >> per < few) {
+      const uint64_t o = s.few[t >> per].order, m = s.few[t >> per].units;
       uint64_t c = 0;
       uint32_t r = 0;
 #pragma unroll 4
-      for (int i = 0; i < few; ++i) {
+      for (int i = i0; i < few; i += 1 << per) {
         const Pick::Few f = s.few[i];
         const bool first = f.order < o;
         r += first ? 1 : 0;
         c += first ? f.units : 0;
       }
+      for (int x = 1; x < 1 << per; x <<= 1) {
+        r += __shfl_xor(r, x, 64);
+        c += __shfl_xor(c, x, 64);
+      }
       const uint64_t was = COUNT ? before_count + (uint64_t)r : before_units + c, is = was + (COUNT ? 1 : m);
-      if (was < target && is >= target) {
+      if (i0 == 0 && was < target && is >= target) {
         s.answer = o;
         s.before = before_units + c + m;
       }
@@ -842,6 +885,8 @@ struct Picker {
       const double floor_w = mp < 1.0 ? mp : 1.0;
       const int near = (int)fmin(fmax((double)edge - floor((log(floor_w) + top) * kPerNat), 0.0), (double)kBins);
       bool found = false;
+      const int far = min(min(near + 1, end), kBins - 1);
+      if (near <= far && s.count[far] <= (uint32_t)kList) fetch(far);  // the three bins at once
       for (int bin = max(0, near - 1); bin <= near + 1 && bin <= end && bin < kBins && !found; ++bin) {
         if (s.count[bin] == count_before(bin)) continue;
         fetch(bin);
@@ -867,7 +912,7 @@ struct Picker {
     // the last token with mass stands in for a u of 1 or more
     if (u < 1.0) place(u * held_mass, true, bin, at, cum);
     else place(held_mass, false, bin, at, cum);
-    token = (int)(uint32_t)at;
+    token = token_at(at);
     prob = weight(logit_at(at)) / held_mass;
   }
 };
@@ -906,7 +951,7 @@ __global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs
   } else if (t > 0.f && k != 1) {
     const double p = (double)pf, mp = (double)mpf, u = (double)uf;
     const float top = logit_of(top_key);
-    Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, ws, s, Grid(t), 0.f, 0.0, -1, false};
+    Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, ws, s, Grid(t), 0.f, 0.0, -1, false, 0, 0};
     pick.edge = pick.grid.bin(top);
     pick.top = (double)top * pick.grid.per / kPerNat;
     bool done = false;
