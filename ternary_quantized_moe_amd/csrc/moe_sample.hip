@@ -21,6 +21,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "fp8_internal.h"
 
@@ -96,22 +98,42 @@ struct Shared {
   int found;
 };
 
-__device__ __forceinline__ uint64_t scan_u64(uint64_t v, int lane) {
+// A step of a scan over a wave: combine(v, w) where w is v of the lane that the step
+// looks back at, or `none`.  Six of them, without a trip through LDS.
+template <class V, class Combine>
+__device__ __forceinline__ V scan_wave(V v, V none, Combine combine) {
+  union Bits {
+    V v;
+    int w[sizeof(V) / 4];
+  };
+  auto step = [&](auto ctrl, auto rows) {
+    Bits in, out;
+    in.v = v;
+    out.v = none;
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint64_t t = __shfl_up(v, o, 64);
-    if (lane >= o) v += t;
-  }
+    for (int i = 0; i < (int)(sizeof(V) / 4); ++i)
+      out.w[i] = __builtin_amdgcn_update_dpp(out.w[i], in.w[i], decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+    v = combine(v, out.v);
+  };
+  typedef std::integral_constant<int, 0xF> All;
+  step(std::integral_constant<int, 0x111>(), All());  // row_shr:1, 2, 4, 8: rows of 16
+  step(std::integral_constant<int, 0x112>(), All());
+  step(std::integral_constant<int, 0x114>(), All());
+  step(std::integral_constant<int, 0x118>(), All());
+  step(std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xA>());  // lane 15 of a row to the next
+  step(std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xC>());  // lane 31 to the upper half
   return v;
 }
-__device__ __forceinline__ uint32_t scan_u32(uint32_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const uint32_t t = __shfl_up(v, o, 64);
-    if (lane >= o) v += t;
-  }
-  return v;
+template <class V>
+__device__ __forceinline__ V scan_sum(V v) {
+  return scan_wave(v, (V)0, [](V a, V b) { return a + b; });
 }
+__device__ __forceinline__ uint64_t last_lane(uint64_t v) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), 63) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) { return last_lane(scan_wave(v, (uint64_t)0, max_u64)); }
 
 template <int TYPE>
 struct Row {
@@ -200,8 +222,8 @@ struct Row {
         c += s.count[b0 + h];
         m += s.mass[b0 + h];
       }
-      uint32_t ci = scan_u32(c, lane);
-      uint64_t mi = scan_u64(m, lane);
+      uint32_t ci = scan_sum(c);
+      uint64_t mi = scan_sum(m);
       if (lane == 63) {
         s.wave_count[wave] = ci;
         s.wave_mass[wave] = mi;
@@ -343,13 +365,6 @@ struct Grid {
   }
 };
 
-__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v = max_u64(v, __shfl_xor(v, o, 64));
-  return v;
-}
-
 // VE neighbouring logits of a row from index i on; past the row -inf.
 template <int TYPE>
 struct Vec {
@@ -381,7 +396,7 @@ struct Chunks {
   int n, len;       // chunks of a row, tokens in a chunk
   ChunkHead* heads;
   uint64_t* hists;  // [kBins] count and units of each bin below the chunk's top one
-  uint16_t* begins; // [kBins] where a bin's tokens begin among the chunk's
+  uint16_t* ends;   // [kBins] where a bin's tokens end among the chunk's
   uint16_t* tokens; // [len] places in the chunk, by bin
 };
 
@@ -410,15 +425,15 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
 #pragma unroll
     for (int e = 0; e < VE; ++e) mine = fmaxf(mine, x[j].v[e]);
   float top = mine;
-#pragma unroll
-  for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
-  if (lane == 0) tops[tid >> 6] = top;
+  top = scan_wave(top, -__builtin_inff(), [](float p, float q) { return fmaxf(p, q); });
+  if (lane == 63) tops[tid >> 6] = top;
   if (tid == 0) top_index = 0x7FFFFFFF;
   hist[tid] = 0;
   hist[tid + kScanThreads] = 0;
   __syncthreads();
+  top = tops[0];
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) top = fmaxf(top, tops[w]);
+  for (int w = 1; w < WAVES; ++w) top = fmaxf(top, tops[w]);
   if (mine == top) {
     int first = 0x7FFFFFFF;
 #pragma unroll
@@ -451,7 +466,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   if (!counted) return;
   const uint64_t h0 = hist[2 * tid], h1 = hist[2 * tid + 1];
   const uint32_t c0 = (uint32_t)(h0 >> kCountShift), c1 = (uint32_t)(h1 >> kCountShift);
-  uint32_t ci = scan_u32(c0 + c1, lane);
+  uint32_t ci = scan_sum(c0 + c1);
   if (lane == 63) counts[tid >> 6] = ci;
   if (tid == 0) end_bin = kBins;
   __syncthreads();
@@ -474,7 +489,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   }
   const int64_t at = (int64_t)blockIdx.x * kBins + 2 * tid;
   *(u32x4*)(ws.hists + at) = u32x4{(uint32_t)h0, (uint32_t)(h0 >> 32), (uint32_t)h1, (uint32_t)(h1 >> 32)};
-  *(uint32_t*)(ws.begins + at) = b0 | b1 << 16;
+  *(uint32_t*)(ws.ends + at) = b1 | ci << 16;
   __syncthreads();
   const uint32_t limit = (uint32_t)end_bin << 16;
 #pragma unroll
@@ -493,12 +508,13 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
 // One block per row: the chunks' histograms added up say in which bin of the order
 // each filter ends and the answer lies; a border bin's tokens are fetched from the
 // chunks' lists.  A place within a bin is found among its tokens: each counts what
-// stands before it, at most 256 of them; a fuller bin is first divided by the order
-// of its tokens (logit, then index), 2048 ways.  Up to 4096 tokens are kept in LDS
+// stands before it, at most 128 of them; a fuller bin is first divided by the order
+// of its tokens (logit, then index), 1024 ways.  Up to 4096 tokens are kept in LDS
 // for that, more are read from the chunks' lists every time.  Only rows whose grid is
 // not exact (an infinite logit, a temperature near 0) go through the radix descents.
 constexpr int kList = 4096;  // tokens kept
-constexpr int kFew = 256;
+constexpr int kFew = 128, kPartBits = 10, kParts = 1 << kPartBits;
+constexpr int kNearChunks = 32;  // of a row, for the ends of their bins to be in LDS
 constexpr int kMaxChunks = (int)(kSampleMaxVocab / (kScanThreads * 32));
 
 struct Pick {
@@ -506,8 +522,8 @@ struct Pick {
     Shared radix;
     struct {
       uint64_t order[kList];
-      uint64_t hist[kRadix];
-      uint32_t parts[kRadix];
+      uint64_t hist[kParts];
+      uint32_t parts[kParts];
     } s;
   };
   struct __attribute__((aligned(16))) Few {
@@ -517,23 +533,15 @@ struct Pick {
   double mass[kBins];     // and their mass, relative to the largest weight
   double unit[kBins];     // weight of a bin's unit of mass
   uint64_t units[kBins];  // a bin's units
-  uint64_t wave_u64[kSampWaves], wave_min[kSampWaves];
+  uint64_t wave_u64[kSampWaves];
   double wave_f64[kSampWaves];
   uint32_t wave_u32[kSampWaves];
   short dist[kMaxChunks];    // bins between the row's top and a chunk's, kBins for a chunk out of reach
   uint64_t before, answer;
   uint32_t before_count, bin_count;
+  uint64_t heavy[3];
   int n, found, n_few;
 };
-
-__device__ __forceinline__ double scan_f64(double v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const double t = __shfl_up(v, o, 64);
-    if (lane >= o) v += t;
-  }
-  return v;
-}
 
 template <int TYPE>
 struct Picker {
@@ -548,6 +556,9 @@ struct Picker {
   int here;    // the fetched bin
   bool kept;   // whether its tokens are in the list, which holds the bins
   int list_from, list_to;
+  uint16_t* ends;  // [n x kBins] where a row's bin ends in a chunk's list, in LDS
+  bool near;       // if there is room for it
+  int index_bits;  // of a token's index
 
   __device__ __forceinline__ double weight(float l) const { return exp((double)l * grid.per / kPerNat - top); }
 
@@ -564,17 +575,29 @@ struct Picker {
     static_assert(kBins == kSampThreads, "a bin a thread");
     uint64_t m = 0;
     uint32_t c = 0;
-#pragma unroll 16
-    for (int i = 0; i < ws.n; ++i) {
-      const int at = t - s.dist[i];
-      const uint64_t h = at >= 0 ? ws.hists[(int64_t)i * kBins + at] : 0;
-      m += h & ((1ull << kCountShift) - 1);
-      c += (uint32_t)(h >> kCountShift);
+    for (int i0 = 0; i0 < ws.n; i0 += 16) {  // 16 chunks' numbers on their way at once
+      uint64_t h[16];
+      uint32_t end[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int i = min(i0 + q, ws.n - 1);
+        const int64_t at = (int64_t)i * kBins + max(t - s.dist[i], 0);
+        h[q] = ws.hists[at];
+        end[q] = ws.ends[at];
+      }
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int i = min(i0 + q, ws.n - 1);
+        const bool in = i == i0 + q && t >= s.dist[i];
+        m += in ? h[q] & ((1ull << kCountShift) - 1) : 0;
+        c += in ? (uint32_t)(h[q] >> kCountShift) : 0;
+        if (near && i == i0 + q) ends[i * kBins + t] = in ? end[q] : 0;
+      }
     }
     // e^(upper edge - top) 2^-35
     const double unit = exp(((double)edge - (double)t + 1.0) / kPerNat - top) / kBinUnit;
-    uint32_t ci = scan_u32(c, lane);
-    double mi = scan_f64((double)m * unit, lane);
+    uint32_t ci = scan_sum(c);
+    double mi = scan_sum((double)m * unit);
     if (lane == 63) {
       s.wave_u32[wave] = ci;
       s.wave_f64[wave] = mi;
@@ -620,16 +643,14 @@ struct Picker {
 
   // A token's place in the order as a number that rises along it: the complement of
   // the key without its dead bits, then the index.
-  static constexpr int kIndexBits = 21;
-  static_assert(kSampleMaxVocab <= 1ll << kIndexBits, "a token's index");
-  static __device__ __forceinline__ uint64_t order_of(float l, int token) {
-    return (uint64_t)(~key_of(l) >> L::kDead) << kIndexBits | (uint32_t)token;
+  __device__ __forceinline__ uint64_t order_of(float l, int token) const {
+    return (uint64_t)(~key_of(l) >> L::kDead) << index_bits | (uint32_t)token;
   }
-  static __device__ __forceinline__ float logit_at(uint64_t order) {
-    const uint32_t k = ~((uint32_t)(order >> kIndexBits) << L::kDead);  // dead bits set
+  __device__ __forceinline__ float logit_at(uint64_t order) const {
+    const uint32_t k = ~((uint32_t)(order >> index_bits) << L::kDead);  // dead bits set
     return logit_of(k & 0x80000000u ? k & ~0u << L::kDead : k);
   }
-  static __device__ __forceinline__ int token_at(uint64_t order) { return (int)(order & ((1u << kIndexBits) - 1)); }
+  __device__ __forceinline__ int token_at(uint64_t order) const { return (int)(order & ((1u << index_bits) - 1)); }
 
   // Every token of the bins from `b0` to `b` from the chunks' lists: begin(n) is called
   // by the lanes of a chunk with its n tokens and says the number of its first,
@@ -639,11 +660,16 @@ struct Picker {
     const int lanes = ws.n > 16 ? 16 : ws.n > 8 ? 32 : 64;  // of a chunk
     const int lane = threadIdx.x & (lanes - 1);
     for (int i = threadIdx.x / lanes; i < ws.n; i += kSampThreads / lanes) {
-      const int d = s.dist[i];
-      if (d > b) continue;
-      const int64_t at = (int64_t)i * kBins;
-      const int first = b0 > d ? ws.begins[at + b0 - d] : 0;
-      const int n = ws.begins[at + b - d] + (int)(ws.hists[at + b - d] >> kCountShift) - first;
+      int first, n;
+      if (near) {
+        first = b0 ? ends[i * kBins + b0 - 1] : 0;
+        n = ends[i * kBins + b] - first;
+      } else {
+        const int d = s.dist[i];
+        const uint16_t* e = ws.ends + (int64_t)i * kBins - d;
+        first = b0 > d ? e[b0 - 1] : 0;
+        n = (b >= d ? e[b] : 0) - first;
+      }
       if (n == 0) continue;
       const uint16_t* from = ws.tokens + (int64_t)i * ws.len + first;
       const int to = begin(n, lanes);
@@ -711,43 +737,32 @@ struct Picker {
   __device__ uint64_t select(uint64_t target, uint64_t& cum) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     uint64_t lo = 0, hi = ~0ull, before_units = 0;
+    // where the bin's tokens should lie; the end parts take what does not
+    const float slack = 1.f / (1 << 20), b0 = edge - (float)here, b1 = b0 + 1.f;
+    uint64_t from = order_of((b1 + fabsf(b1) * slack) / grid.perf, 0),
+             to = order_of((b0 - fabsf(b0) * slack) / grid.perf, (1 << index_bits) - 1);
+    if (from > to) {
+      from = 0;
+      to = hi;
+    }
     uint32_t left = s.count[here] - count_before(here), before_count = 0;
     while (left > (uint32_t)kFew) {
-      uint64_t mn = ~0ull, mx = 0;
-      each([&](uint64_t o) {
-        if (o >= lo && o <= hi) {
-          mn = ~max_u64(~mn, ~o);
-          mx = max_u64(mx, o);
-        }
-      });
-      mn = ~wave_max(~mn);
-      mx = wave_max(mx);
-      if (lane == 0) {
-        s.wave_u64[wave] = mx;
-        s.wave_min[wave] = mn;
-      }
-      for (int i = t; i < kRadix; i += kSampThreads) {
+      for (int i = t; i < kParts; i += kSampThreads) {
         s.s.hist[i] = 0;
         s.s.parts[i] = 0;
       }
       __syncthreads();
-      for (int w = 0; w < kSampWaves; ++w) {
-        mx = max_u64(mx, s.wave_u64[w]);
-        mn = ~max_u64(~mn, ~s.wave_min[w]);
-      }
-      __syncthreads();
-      lo = mn;
-      hi = mx;
-      const int shift = max(0, 53 - __clzll(mn ^ mx));  // at most 2048 parts
+      const int shift = max(0, 64 - kPartBits - __clzll(to - from));
+      const int parts = (int)((to - from) >> shift) + 1;  // at most kParts
       each([&](uint64_t o) {
         if (o >= lo && o <= hi) {
-          const int part = (int)((o >> shift) - (mn >> shift));
+          const int part = o <= from ? 0 : o >= to ? parts - 1 : (int)((o - from) >> shift);
           atomicAdd((unsigned long long*)&s.s.hist[part], (unsigned long long)unit_at(o));
           atomicAdd(&s.s.parts[part], 1u);
         }
       });
       __syncthreads();
-      constexpr int PER = kRadix / kSampThreads;
+      constexpr int PER = kParts / kSampThreads;
       uint64_t m = 0;
       uint32_t c = 0;
 #pragma unroll
@@ -755,8 +770,8 @@ struct Picker {
         m += s.s.hist[PER * t + h];
         c += s.s.parts[PER * t + h];
       }
-      uint64_t e = scan_u64(m, lane);
-      uint32_t f = scan_u32(c, lane);
+      uint64_t e = scan_sum(m);
+      uint32_t f = scan_sum(c);
       if (lane == 63) {
         s.wave_u64[wave] = e;
         s.wave_u32[wave] = f;
@@ -782,15 +797,16 @@ struct Picker {
         f += c;
       }
       __syncthreads();
-      const uint64_t part = (mn >> shift) + (uint64_t)s.found;
+      const int part = s.found;
       left = s.bin_count;
       before_units = s.before;
       before_count = s.before_count;
-      lo = max_u64(lo, part << shift);
-      hi = ~max_u64(~hi, ~((part << shift) | ((1ull << shift) - 1)));
+      if (part > 0) lo = from + ((uint64_t)part << shift);
+      if (part < parts - 1) hi = from + ((uint64_t)(part + 1) << shift) - 1;
+      from = lo;
+      to = hi;
       __syncthreads();
       if (t == 0) s.found = kBins;
-      if (shift == 0) left = 1;
     }
     // at most kFew are left: each counts what stands before it
     if (t == 0) s.n_few = 0;
@@ -831,22 +847,6 @@ struct Picker {
     return o;
   }
 
-  // Units of mass of the fetched tokens up to `last` in the order with weight >= floor.
-  __device__ uint64_t heavy_units(uint64_t last, double floor) {
-    uint64_t m = 0;
-    each([&](uint64_t o) {
-      if (o <= last && weight(logit_at(o)) >= floor) m += unit_at(o);
-    });
-#pragma unroll
-    for (int o = 32; o; o >>= 1) m += __shfl_xor(m, o, 64);
-    if ((threadIdx.x & 63) == 0) s.wave_u64[threadIdx.x >> 6] = m;
-    __syncthreads();
-    m = 0;
-    for (int w = 0; w < kSampWaves; ++w) m += s.wave_u64[w];
-    __syncthreads();
-    return m;
-  }
-
   // The filters and the choice.
   __device__ void choose(int k, double p, double mp, double u, int& token, double& prob) {
     // what is kept: the bins before `end`, and of bin `end` the tokens up to `last`,
@@ -883,25 +883,40 @@ struct Picker {
     if (mp > 0.0) {
       // the bin that weight mp falls into; rounding may put it into a neighbour
       const double floor_w = mp < 1.0 ? mp : 1.0;
-      const int near = (int)fmin(fmax((double)edge - floor((log(floor_w) + top) * kPerNat), 0.0), (double)kBins);
+      const int near_bin = (int)fmin(fmax((double)edge - floor((log(floor_w) + top) * kPerNat), 0.0), (double)kBins);
+      const int first = max(0, near_bin - 1), far = min(min(near_bin + 1, end), kBins - 1);
       bool found = false;
-      const int far = min(min(near + 1, end), kBins - 1);
-      if (near <= far && s.count[far] <= (uint32_t)kList) fetch(far);  // the three bins at once
-      for (int bin = max(0, near - 1); bin <= near + 1 && bin <= end && bin < kBins && !found; ++bin) {
-        if (s.count[bin] == count_before(bin)) continue;
-        fetch(bin);
-        const uint64_t whole_units = bin == end ? part : s.units[bin],
-                       heavy = heavy_units(bin == end ? last : ~0ull, floor_w);
-        if (heavy < whole_units) {  // this bin holds the border
-          found = true;
-          end = bin;
-          part = heavy;
-          held_mass = mass_before(bin) + (double)heavy * s.unit[bin];
-          if (heavy) last = select<false>(heavy, part);
+      if (first <= far) {
+        if (threadIdx.x < 3) s.heavy[threadIdx.x] = 0;
+        if (threadIdx.x == 0) s.answer = 0;
+        __syncthreads();
+        auto weigh = [&](uint64_t o) {
+          const float l = logit_at(o);
+          const int bin = (int)fminf(edge - grid.bin(l), (float)kBins);
+          if (bin >= first && (bin < end || o <= last) && bin <= far && weight(l) >= floor_w) {
+            atomicAdd((unsigned long long*)&s.heavy[bin - first], (unsigned long long)unit_at(o));
+            atomicMax((unsigned long long*)&s.answer, (unsigned long long)o);
+          }
+        };
+        if (kept && list_from <= first && far <= list_to)
+          for (int i = threadIdx.x; i < s.n; i += kSampThreads) weigh(s.s.order[i]);
+        else
+          read_tokens(first, far, [](int, int) { return 0; }, [&](int, uint64_t o) { weigh(o); });
+        __syncthreads();
+        for (int bin = first; bin <= far && !found; ++bin) {
+          const uint64_t heavy = s.heavy[bin - first];
+          if (heavy < (bin == end ? part : s.units[bin])) {  // this bin holds the border
+            found = true;
+            end = bin;
+            part = heavy;
+            last = s.answer;  // the last heavy token lies here if any does
+            held_mass = mass_before(bin) + (double)heavy * s.unit[bin];
+          }
         }
+        __syncthreads();
       }
-      if (!found && end > near + 1) {  // no token near the border: nothing beyond it stays
-        end = min(near + 2, kBins);
+      if (!found && end > near_bin + 1) {  // no token near the border: nothing beyond it stays
+        end = min(near_bin + 2, kBins);
         part = 0;
         held_mass = s.mass[end - 1];
       }
@@ -920,11 +935,12 @@ struct Picker {
 template <int TYPE>
 __global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs a, Chunks ws) {
   __shared__ Pick s;
+  extern __shared__ uint16_t ends[];
   typedef Logit<TYPE> L;
   const int64_t b = blockIdx.x;
   ws.heads += b * ws.n;
   ws.hists += b * ws.n * kBins;
-  ws.begins += b * ws.n * kBins;
+  ws.ends += b * ws.n * kBins;
   ws.tokens += b * ws.n * ws.len;
   // everything the row is told, read at once
   const float t = a.temperature ? a.temperature[b] : 1.0f, pf = a.top_p ? a.top_p[b] : 1.0f,
@@ -951,7 +967,8 @@ __global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs
   } else if (t > 0.f && k != 1) {
     const double p = (double)pf, mp = (double)mpf, u = (double)uf;
     const float top = logit_of(top_key);
-    Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, ws, s, Grid(t), 0.f, 0.0, -1, false, 0, 0};
+    Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, ws, s, Grid(t), 0.f, 0.0, -1, false, 0, 0,
+                      ends, ws.n <= kNearChunks, 32 - __clz(a.V | 1)};
     pick.edge = pick.grid.bin(top);
     pick.top = (double)top * pick.grid.per / kPerNat;
     bool done = false;
@@ -978,7 +995,7 @@ int chunks_of(int V, int pt) { return (V + kScanThreads * pt - 1) / (kScanThread
 // with 64 chunks 26 us, with 32 24), else 16 or 32.
 int scan_pt(int64_t B, int V) {
   int pt = 8;
-  while (pt < 32 && (chunks_of(V, pt) > 32 || B * chunks_of(V, pt) > 1024)) pt *= 2;
+  while (pt < 32 && (chunks_of(V, pt) > 16 || B * chunks_of(V, pt) > 1024)) pt *= 2;
   return pt;
 }
 
@@ -994,7 +1011,7 @@ Chunks chunks_in(char* ws, int64_t B, int V, int64_t& bytes) {
   int64_t at = 0;
   c.heads = (ChunkHead*)(ws + at); at += up256(n * (int64_t)sizeof(ChunkHead));
   c.hists = (uint64_t*)(ws + at); at += n * kBins * 8;
-  c.begins = (uint16_t*)(ws + at); at += n * kBins * 2;
+  c.ends = (uint16_t*)(ws + at); at += n * kBins * 2;
   c.tokens = (uint16_t*)(ws + at); at += n * c.len * 2;
   bytes = at;
   return c;
@@ -1010,7 +1027,8 @@ hipError_t launch_type(const SampleArgs& a, void* ws, hipStream_t stream) {
   scan<<<(unsigned)(a.B * c.n), kScanThreads, 0, stream>>>(a, c);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  sample_pick_kernel<TYPE><<<(unsigned)a.B, kSampThreads, 0, stream>>>(a, c);
+  const size_t lds = c.n <= kNearChunks ? (size_t)c.n * kBins * 2 : 0;
+  sample_pick_kernel<TYPE><<<(unsigned)a.B, kSampThreads, lds, stream>>>(a, c);
   return hipGetLastError();
 }
 
