@@ -291,9 +291,9 @@ int32_t moe_fp8_linear(const uint8_t* a, const float* a_scales, int64_t m, const
  *   probs        device fp32 [batch], the token's share of the mass left, or NULL
  *   workspace    >= moe_sample_workspace_bytes(batch, vocab), 256-byte aligned
  *                (NULL if that is 0)
- * Weights are fp64 and sums 64-bit integers in units of 2^-42 of l_max's weight,
- * so no result depends on an order of additions; a token of less than half a unit
- * has no mass.  vocab is at most 2^21, batch 2^22.  batch = 0 is a no-op.  Ordered on
+ * Weights are fp64 (good to 3e-11 of themselves) and sums 64-bit integers, so no
+ * result depends on an order of additions; a token some 30 nats below l_max may
+ * count as having no mass.  vocab is at most 2^21, batch 2^22.  batch = 0 is a no-op.  Ordered on
  * `stream`; nothing is allocated.  Errors: MOE_E_FORMAT (type), MOE_E_SHAPE,
  * MOE_E_ARG, MOE_E_SPACE, MOE_E_DEVICE. */
 int64_t moe_sample_workspace_bytes(int64_t batch, int32_t vocab);

@@ -8,16 +8,21 @@
 // answer is the first token whose cumulative weight exceeds u times the mass of
 // what is left.
 //
-// Weights are evaluated in fp64 and summed as 64-bit integers in units of
-// 2^-42 of the largest, so the sums do not depend on their order and a decision
-// is the same for every launch shape; a token below half a unit (e^-29.8 of the
-// most likely one) has no mass.  Up to 2^21 tokens a sum stays below 2^63.
+// Weights are evaluated in fp64 and summed as 64-bit integers, in units of 2^-35
+// relative to a bin of 1 / 16 nat, so that no sum depends on an order of additions.
+// Two launches.  The scan reads the logits once (HBM floor 6.5 us at 64 x 131072
+// fp32, 14.3 us measured: 17 vector instructions a token for its bin, weight and
+// place bound it beside the read) and leaves 512-bin histograms and lists of
+// tokens by bin; the choice works on those alone (22.6 us there, one block a row:
+// a chain of dependent steps, each a memory's or a barrier's latency; 8 us at the
+// least for 1 x 50304).
 //
-// A place in the order is found by radix descent on the logits' ordered bits,
-// 11 + 11 + 10 of them: a histogram of counts and masses over the digit of the
-// tokens that share the higher digits, a scan from the top, and the digit where
-// the target is reached.  After three digits the logit is exact, its tokens
-// weigh the same, and the place among them is a division.
+// Rows whose bins are not exact take radix descents on the logits' ordered bits,
+// 11 + 11 + 10 of them, with units of 2^-42 of the largest weight: a histogram of
+// counts and masses over the digit of the tokens that share the higher digits, a
+// scan from the top, and the digit where the target is reached.  After three digits
+// the logit is exact, its tokens weigh the same, and the place among them is a
+// division.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -991,8 +996,8 @@ __global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs
 
 int chunks_of(int V, int pt) { return (V + kScanThreads * pt - 1) / (kScanThreads * pt); }
 // Logits per thread of a scan block: 8 where that is enough for 1024 blocks at most
-// and 32 chunks a row (a chunk's histogram costs the row's block a read; 1 x 131072
-// with 64 chunks 26 us, with 32 24), else 16 or 32.
+// and 16 chunks a row (which the choice reads at once: 1 x 50304 takes 17.2 us in 13
+// chunks, 18.5 in 25), else 16 or 32.
 int scan_pt(int64_t B, int V) {
   int pt = 8;
   while (pt < 32 && (chunks_of(V, pt) > 16 || B * chunks_of(V, pt) > 1024)) pt *= 2;

@@ -2,9 +2,8 @@
 
 Tokens are equal wherever the oracle's decisions are further than 1e-9 of the
 mass from going the other way: the kernel's weights are integers in units of
-2^-42 of the largest, so a sum of n of them is off by at most n 2^-43 of it, under
-2^-26 at the largest vocabulary here if every rounding went one way and some
-1e-11 as they fall; the oracle's own sums are good to 1e-12.  Probabilities are
+2^-35 of their bin's largest, off by one unit, so a weight and a sum of weights is
+good to e^(1/16) 2^-35, 3e-11 of itself; the oracle's own sums are good to 1e-12.  Probabilities are
 fp32: half a step, 2^-24, and the same 1e-9.
 """
 import sys
@@ -109,6 +108,23 @@ def test_full_borders(tq, dtype):
     settings = dict(temperature=[1.3] * 7, top_k=[0, 0, 60000, 0, 90000, 0, 170000], top_p=[0.5, 1.0, 1.0, 0.99, 0.7, 0.2, 1.0],
                     min_p=[0.0, 0.0, 0.0, 0.3, 0.2, 0.0, 0.5])
     check(tq, logits_of(7, V, 3, dtype, spread=1.0), np.random.default_rng(5).random(7), **settings)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("V", [70001, 300001])
+def test_borders_anywhere(tq, V, dtype):
+    """More and fewer chunks than a row's block keeps bounds of; borders near logits of zero and of powers of two."""
+    logits = logits_of(8, V, 9, dtype, spread=1.0)
+    logits[4:] = (logits[4:] * 0.05 + torch.tensor([[-0.0], [2.0], [-4.0], [0.25]], device="cuda")).to(dtype)
+    settings = dict(temperature=[1.0, 0.5, 0.7, 2.0, 0.05, 0.01, 1.0, 0.02], top_k=[0, 5000, 0, 0, 0, 30000, 60000, 0],
+                    top_p=[0.6, 1.0, 0.9, 0.5, 0.5, 0.9, 0.3, 0.8], min_p=[0.0, 0.001, 0.02, 0.1, 0.0, 0.05, 0.9, 0.4])
+    check(tq, logits, np.random.default_rng(8).random(8), **settings)
+
+
+def test_temperatures(tq):
+    V, t = 9000, [1e-38, 1e-30, 1e-6, 1e-5, 1e-2, 300.0, 1e30, 3e38, float("inf")]
+    for settings in (dict(), dict(top_k=[700] * 9), dict(top_p=[0.7] * 9), dict(min_p=[0.5] * 9, top_k=[8000] * 9)):
+        check(tq, logits_of(9, V, 12), np.random.default_rng(3).random(9), temperature=t, **settings)
 
 
 def test_ties_take_the_lowest_index(tq):
