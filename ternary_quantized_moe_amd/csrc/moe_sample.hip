@@ -11,9 +11,9 @@
 // Weights are evaluated in fp64 and summed as 64-bit integers, in units of 2^-35
 // relative to a bin of 1 / 16 nat, so that no sum depends on an order of additions.
 // Two launches.  The scan reads the logits once (HBM floor 6.5 us at 64 x 131072
-// fp32, 14.3 us measured: 17 vector instructions a token for its bin, weight and
+// fp32, 14.2 us measured: 30 vector instructions a token for its bin, weight and
 // place bound it beside the read) and leaves 512-bin histograms and lists of
-// tokens by bin; the choice works on those alone (22.6 us there, one block a row:
+// tokens by bin; the choice works on those alone (21.8 us there, one block a row:
 // a chain of dependent steps, each a memory's or a barrier's latency; 8 us at the
 // least for 1 x 50304).
 //
@@ -410,11 +410,11 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   constexpr int VE = Vec<TYPE>::VE, N = PT / VE, LEN = kScanThreads * PT, WAVES = kScanThreads / 64;
   static_assert(kBins == 2 * kScanThreads, "two bins a thread");
   __shared__ uint64_t hist[kBins + 64];
-  __shared__ uint32_t begin[kBins];
+  __shared__ uint32_t begin[kBins + 64];
   __shared__ float tops[WAVES];
   __shared__ uint32_t counts[WAVES];
   __shared__ int end_bin, end_count, top_index;
-  __shared__ __attribute__((aligned(16))) uint16_t places[LEN];
+  __shared__ __attribute__((aligned(16))) uint16_t places[LEN + 64];
   const int64_t b = blockIdx.x / ws.n;
   const int chunk = (int)(blockIdx.x - b * ws.n), base = chunk * LEN, tid = threadIdx.x, lane = tid & 63;
   const void* row = (const typename Logit<TYPE>::T*)a.logits + b * a.ld;
@@ -453,18 +453,22 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   const bool counted = t > 0.f && k != 1 && fabsf(edge) <= kFarthestBin;
   // the first token needs no histogram; a grid too far out is not exact
   if (counted) {
-    // a token's seat: its bin and its number there.  What is too far below the top
+    // a token's value gives way to its seat: its bin and its number there.  What is too far below the top
     // has one in the bins behind, one for each lane of a wave
     const float nowhere = (float)(kBins + lane);
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+    for (int j = 0; j < N; ++j) {
+      uint32_t at[VE];
+      uint64_t was[VE];
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         const float l = x[j].v[e], bin = grid.bin(l);
-        const uint32_t at = (uint32_t)fminf(edge - bin, nowhere);  // a NaN is passed over
-        const uint64_t was = atomicAdd((unsigned long long*)&hist[at], (unsigned long long)grid.template unit<true>(l, bin));
-        x[j].v[e] = __uint_as_float(at << 16 | (uint32_t)(was >> kCountShift));  // from here on a seat
+        at[e] = (uint32_t)fminf(edge - bin, nowhere);  // a NaN is passed over
+        was[e] = atomicAdd((unsigned long long*)&hist[at[e]], (unsigned long long)grid.template unit<true>(l, bin));
       }
+#pragma unroll
+      for (int e = 0; e < VE; ++e) x[j].v[e] = __uint_as_float(at[e] << 16 | (uint32_t)(was[e] >> kCountShift));
+    }
   }
   __syncthreads();
   if (tid == 0) ws.heads[blockIdx.x] = ChunkHead{(uint64_t)key_of(top) << 32 | (uint32_t)~top_index, edge, 0.f};
@@ -498,12 +502,16 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   __syncthreads();
   const uint32_t limit = (uint32_t)end_bin << 16;
 #pragma unroll
-  for (int j = 0; j < N; ++j)
+  for (int j = 0; j < N; ++j) {
+    uint32_t to[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) to[e] = begin[__float_as_uint(x[j].v[e]) >> 16];
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
       const uint32_t seat = __float_as_uint(x[j].v[e]);
-      if (seat < limit) places[begin[seat >> 16] + (seat & 0xFFFFu)] = (uint16_t)((j * kScanThreads + tid) * VE + e);
+      places[seat < limit ? to[e] + (seat & 0xFFFFu) : LEN + lane] = (uint16_t)((j * kScanThreads + tid) * VE + e);
     }
+  }
   __syncthreads();
   u32x4* out = (u32x4*)(ws.tokens + (int64_t)blockIdx.x * LEN);
   for (int i = tid; i < (end_count + 7) / 8; i += kScanThreads) out[i] = ((const u32x4*)places)[i];
@@ -518,6 +526,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
 // for that, more are read from the chunks' lists every time.  Only rows whose grid is
 // not exact (an infinite logit, a temperature near 0) go through the radix descents.
 constexpr int kList = 4096;  // tokens kept
+constexpr int kPrefix = 1024;  // as many are fetched where later borders may need them
 constexpr int kFew = 128, kPartBits = 10, kParts = 1 << kPartBits;
 constexpr int kNearChunks = 32;  // of a row, for the ends of their bins to be in LDS
 constexpr int kMaxChunks = (int)(kSampleMaxVocab / (kScanThreads * 32));
@@ -700,7 +709,7 @@ struct Picker {
     if (kept && b >= list_from && b <= list_to) return;
     __syncthreads();
     const int n = (int)(s.count[b] - count_before(b));
-    list_from = s.count[b] <= (uint32_t)kList ? 0 : b;
+    list_from = s.count[b] <= (uint32_t)kPrefix ? 0 : b;
     list_to = b;
     kept = n <= kList;
     if (threadIdx.x == 0) s.n = 0;
