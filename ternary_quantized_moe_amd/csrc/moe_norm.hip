@@ -65,6 +65,7 @@ __device__ __forceinline__ u32x2 codes8(const float (&f)[8], float r) {
 constexpr int kQThreads = 256;
 
 // One scale per row and group of 128: 16 lanes hold a group, eight values each.
+// Bound by HBM from some 4096 rows on; 64 x 4096 is one launch, 2.3 us.
 template <bool F16>
 __global__ __launch_bounds__(kQThreads) void fp8_quantize_rows_kernel(const u32x4* __restrict__ x, int64_t n8,
                                                                       u32x2* __restrict__ q,
@@ -78,7 +79,9 @@ __global__ __launch_bounds__(kQThreads) void fp8_quantize_rows_kernel(const u32x
   if ((i & 15) == 0) scales[i >> 4] = m / kE4m3Max;
 }
 
-// One scale per 128 x 128 block: a block of threads holds it in registers.
+// One scale per 128 x 128 block: a block of threads holds it in registers, so it is
+// read once.  Bound by HBM: 50304 x 2048 takes 54.4 us, 5.7 TB/s with what the
+// Infinity Cache still holds of it.
 template <bool F16>
 __global__ __launch_bounds__(kQThreads) void fp8_quantize_tiles_kernel(const uint16_t* __restrict__ x, int64_t rows,
                                                                        int cols, uint8_t* __restrict__ q,
@@ -120,7 +123,8 @@ __global__ __launch_bounds__(kQThreads) void fp8_quantize_tiles_kernel(const uin
 // y = h / sqrt(mean(h^2) + eps) * g with h = x + residual in fp32.  One block
 // per row; thread t holds values 8 (t + i threads) .. + 7, so 16 lanes of a DPP
 // row hold one group of 128.  The row is read once, before anything is written,
-// so the outputs may be the inputs.
+// so the outputs may be the inputs.  Bound by HBM: 16384 x 2048 with a residual
+// to codes and the sum takes 39.8 us, 5.9 TB/s likewise; one row 2.3 us.
 template <int VPT>
 __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
   __shared__ float part[16];
