@@ -61,6 +61,13 @@ __device__ __forceinline__ u32x2 codes8(const float (&f)[8], float r) {
   return u32x2{pack_e4m3(f[0] * r, f[1] * r, f[2] * r, f[3] * r), pack_e4m3(f[4] * r, f[5] * r, f[6] * r, f[7] * r)};
 }
 
+// A launch holds fewer than 2^32 threads along x: more blocks than 2^20 go on along y.
+dim3 grid_of(int64_t blocks) {
+  const int64_t x = blocks < 1 << 20 ? blocks : 1 << 20;
+  return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+}
+__device__ __forceinline__ int64_t block_number() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 // ------------------------------------------------------------------ quantizer
 constexpr int kQThreads = 256;
 
@@ -70,7 +77,7 @@ template <bool F16>
 __global__ __launch_bounds__(kQThreads) void fp8_quantize_rows_kernel(const u32x4* __restrict__ x, int64_t n8,
                                                                       u32x2* __restrict__ q,
                                                                       float* __restrict__ scales) {
-  const int64_t i = (int64_t)blockIdx.x * kQThreads + threadIdx.x;
+  const int64_t i = block_number() * kQThreads + threadIdx.x;
   if (i >= n8) return;  // n8 is a multiple of 16: whole groups leave together
   float f[8];
   widen8<F16>(x[i], f);
@@ -89,8 +96,9 @@ __global__ __launch_bounds__(kQThreads) void fp8_quantize_tiles_kernel(const uin
   constexpr int PER = kF8Group * kF8Group / 8 / kQThreads;  // 16-byte pieces per thread
   __shared__ uint32_t part[kQThreads / 64];
   const int groups = cols / kF8Group;
-  const int64_t rb = blockIdx.x / groups;
-  const int g = (int)(blockIdx.x - rb * groups);
+  const int64_t block = block_number(), rb = block / groups;
+  if (rb * kF8Group >= rows) return;
+  const int g = (int)(block - rb * groups);
   const int c = threadIdx.x & 15;
   const int64_t r0 = rb * kF8Group + (threadIdx.x >> 4);
   float f[PER][8];
@@ -128,7 +136,8 @@ __global__ __launch_bounds__(kQThreads) void fp8_quantize_tiles_kernel(const uin
 template <int VPT>
 __global__ __launch_bounds__(1024) void rms_norm_kernel(NormArgs a) {
   __shared__ float part[16];
-  const int64_t row = (int64_t)blockIdx.x * a.d;
+  const int64_t token = block_number(), row = token * a.d;
+  if (token >= a.T) return;
   const int threads = blockDim.x, n8 = a.d / 8;
   float h[VPT][8];
   float ss = 0.f;
@@ -184,11 +193,11 @@ hipError_t launch_fp8_quantize(bool f16, const uint16_t* x, int64_t rows, int co
                                float* scales, hipStream_t stream) {
   if (block_rows == 1) {
     const int64_t n8 = rows * (int64_t)cols / 8;
-    const unsigned blocks = (unsigned)((n8 + kQThreads - 1) / kQThreads);
+    const dim3 blocks = grid_of((n8 + kQThreads - 1) / kQThreads);
     auto kernel = f16 ? fp8_quantize_rows_kernel<true> : fp8_quantize_rows_kernel<false>;
     kernel<<<blocks, kQThreads, 0, stream>>>((const u32x4*)x, n8, (u32x2*)q, scales);
   } else {
-    const unsigned blocks = (unsigned)((rows + kF8Group - 1) / kF8Group * (cols / kF8Group));
+    const dim3 blocks = grid_of((rows + kF8Group - 1) / kF8Group * (cols / kF8Group));
     auto kernel = f16 ? fp8_quantize_tiles_kernel<true> : fp8_quantize_tiles_kernel<false>;
     kernel<<<blocks, kQThreads, 0, stream>>>(x, rows, cols, q, scales);
   }
@@ -200,7 +209,7 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
   const int threads = std::min(1024, (n8 + 63) / 64 * 64);
   const int vpt = (n8 + threads - 1) / threads;
   auto kernel = vpt == 1 ? rms_norm_kernel<1> : vpt == 2 ? rms_norm_kernel<2> : rms_norm_kernel<4>;
-  kernel<<<(unsigned)a.T, threads, 0, stream>>>(a);
+  kernel<<<grid_of(a.T), threads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

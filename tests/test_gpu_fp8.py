@@ -263,6 +263,26 @@ def test_norm_and_quantize_past_32_bits(tq):
     torch.cuda.empty_cache()
 
 
+def test_norm_and_quantize_of_many_rows(tq):
+    """More blocks than one dimension of a launch holds: the last rows are those of a small call."""
+    for rows, fn in (((1 << 26) + 3, "norm"), ((1 << 28) + 5, "rows"), ((1 << 28) + 5, "tiles")):
+        say("many rows", fn, rows)
+        x = torch.zeros((rows, 128), dtype=torch.bfloat16, device="cuda")
+        last = rows // 128 * 128                              # whole blocks of 128 rows before
+        x[last:] = torch.randn((rows - last, 128), device="cuda").bfloat16()
+        if fn == "norm":
+            weight = torch.ones(128, device="cuda")
+            got, want = (tq.rms_norm(v, weight, 1e-6, bf16=False, fp8=True) for v in (x, x[last:].clone()))
+            got, want = (got["q"], got["scales"]), (want["q"], want["scales"])
+        else:
+            got, want = (tq.fp8_quantize(v, 1 if fn == "rows" else 128) for v in (x, x[last:].clone()))
+        assert torch.equal(got[0][last:].view(torch.uint8), want[0].view(torch.uint8))
+        assert torch.equal(got[1][-want[1].shape[0]:], want[1])
+        assert not bool(got[0][last - 128:last].view(torch.uint8).any())
+        del x, got, want
+        torch.cuda.empty_cache()
+
+
 def test_linear_long_k(tq):
     ops = operands(tq, 5, 130, 128 * 150)
     check_linear(tq.fp8_linear(*ops, out_dtype=torch.float32), *ops)
