@@ -13,7 +13,7 @@ constexpr float kE4m3Max = 448.0f;       // largest e4m3 value
 constexpr float kAmaxFloor = 1e-30f;     // keeps a block's scale and its reciprocal normal numbers
 constexpr int kNormMaxD = 32768;         // widest row the norm keeps in registers
 constexpr int kLinearMaxK = 1 << 22;     // 256 rows of it stay inside 32 bits
-constexpr int64_t kLinearMaxOut = (int64_t)1 << 40;  // at most 2^29 tiles
+constexpr int64_t kLinearMaxOut = (int64_t)1 << 37;  // with m, n <= 2^29 a launch of fewer than 2^32 threads
 constexpr int64_t kSampleMaxVocab = 1 << 21, kSampleMaxBatch = 1 << 22;  // at most 2^30 chunks of a row
 
 // e4m3 codes and scales of a [rows x cols] bf16 (f16 = false) or fp16 matrix,

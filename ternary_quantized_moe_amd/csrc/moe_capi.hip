@@ -422,10 +422,10 @@ int32_t moe_fp8_linear(const uint8_t* a, const float* a_scales, int64_t M, const
     return fail(MOE_E_FORMAT, "output type %d is neither MOE_BF16 nor MOE_F32", (int)y_type);
   if (K <= 0 || K % 128 || K > moe::kLinearMaxK)
     return fail(MOE_E_SHAPE, "K %d is not a positive multiple of 128 up to %d", (int)K, moe::kLinearMaxK);
-  if (M < 0 || N < 0 || M > (1 << 30) || N > (1 << 30))
-    return fail(MOE_E_SHAPE, "M %lld and N %lld must lie in [0, 2^30]", (long long)M, (long long)N);
+  if (M < 0 || N < 0 || M > (1 << 29) || N > (1 << 29))
+    return fail(MOE_E_SHAPE, "M %lld and N %lld must lie in [0, 2^29]", (long long)M, (long long)N);
   if (M * N > moe::kLinearMaxOut)
-    return fail(MOE_E_SHAPE, "%lld x %lld results exceed one launch (2^40)", (long long)M, (long long)N);
+    return fail(MOE_E_SHAPE, "%lld x %lld results exceed one launch (2^37)", (long long)M, (long long)N);
   if (ldy < N) return fail(MOE_E_SHAPE, "row stride %lld below N %lld", (long long)ldy, (long long)N);
   if (M == 0 || N == 0) return ok();
   if (!a || !a_scales || !w || !w_scales || !y) return fail(MOE_E_ARG, "NULL pointer");

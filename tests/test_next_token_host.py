@@ -65,6 +65,16 @@ def test_linear_refusals():
     assert rc(m=0) == 0 and rc(n=0, ldy=0) == 0
 
 
+def test_linear_sizes_of_one_launch():
+    """What would be 2^32 threads or more is refused before the launch."""
+    L = tq.lib()
+
+    def rc(m, n):
+        return L.moe_fp8_linear(0x1000000, 0x2000000, m, 0x3000000, 0x4000000, n, 128, BF16, 0x5000000, n, None)
+    assert rc((1 << 29) + 1, 1) == SHAPE and rc(1, (1 << 29) + 1) == SHAPE
+    assert rc(1 << 19, (1 << 18) + 1) == SHAPE
+
+
 def test_sample_refusals():
     L = tq.lib()
 
