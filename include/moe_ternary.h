@@ -290,7 +290,8 @@ int32_t moe_fp8_linear(const uint8_t* a, const float* a_scales, int64_t m, const
  *   tokens       device int32 [batch]
  *   probs        device fp32 [batch], the token's share of the mass left, or NULL
  *   workspace    >= moe_sample_workspace_bytes(batch, vocab), 256-byte aligned
- *                (NULL if that is 0)
+ *                (NULL if that is 0); it carries nothing from one call to the next
+ * tokens, probs and the workspace overlap neither each other nor an input.
  * Weights are fp64 (good to 3e-11 of themselves) and sums 64-bit integers, so no
  * result depends on an order of additions; a token some 30 nats below l_max may
  * count as having no mass.  vocab is at most 2^21, batch 2^22.  batch = 0 is a no-op.  Ordered on

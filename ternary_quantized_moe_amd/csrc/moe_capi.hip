@@ -469,6 +469,14 @@ int32_t moe_sample(int32_t type, const void* logits, int64_t batch, int32_t voca
     return fail(MOE_E_ARG, "logits must be element and every other array 4-byte aligned");
   if (ws_bytes < need)
     return fail(MOE_E_SPACE, "workspace holds %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
+  const int64_t size = type == MOE_F32 ? 4 : 2, row4 = 4 * batch;
+  const struct { const void* p; int64_t n; } buf[] = {
+      {ws, need}, {tokens, row4}, {probs, row4}, {logits, ((batch - 1) * ld + vocab) * size},
+      {u, row4}, {temperature, row4}, {top_k, row4}, {top_p, row4}, {min_p, row4}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 9; ++j)
+      if (overlaps(buf[i].p, buf[i].n, buf[j].p, buf[j].n))
+        return fail(MOE_E_ARG, "tokens, probs and the workspace must not overlap each other or an input");
   const moe::SampleType t = type == MOE_F32 ? moe::kSampleF32 : type == MOE_BF16 ? moe::kSampleBf16 : moe::kSampleF16;
   const hipError_t e = moe::launch_sample(
       t, {logits, batch, vocab, ld, temperature, top_k, top_p, min_p, u, tokens, probs}, ws, (hipStream_t)stream);

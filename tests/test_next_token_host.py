@@ -94,6 +94,23 @@ def test_sample_refusals():
     assert L.moe_sample_workspace_bytes(1, 1 << 22) == -1 and L.moe_sample_workspace_bytes(0, 100) >= 0
 
 
+def test_sample_overlaps_are_refused():
+    L = tq.lib()
+    places = dict(logits=0x100000, t=0x200000, k=0x210000, p=0x220000, mp=0x230000, u=0x240000, tokens=0x300000,
+                  probs=0x310000, ws=0x400000)
+
+    def rc(**at):
+        a = {**places, **at}
+        return L.moe_sample(F32, a["logits"], 2, 1000, 1200, a["t"], a["k"], a["p"], a["mp"], a["u"], a["tokens"],
+                            a["probs"], a["ws"], 1 << 20, None)
+    inputs = [places[k] for k in ("logits", "t", "k", "p", "mp", "u")]
+    for out in ("tokens", "probs", "ws"):
+        for at in inputs:
+            assert rc(**{out: at}) == ARG and "overlap" in L.moe_last_error().decode()
+    assert rc(probs=places["tokens"] + 4) == ARG and rc(tokens=places["ws"] + 256) == ARG
+    assert rc(tokens=places["logits"] + 4 * (1200 + 999)) == ARG
+
+
 def test_host_tensors_are_refused():
     x = torch.zeros(2, 128, dtype=torch.bfloat16)
     w = torch.ones(128)
