@@ -453,6 +453,18 @@ def _rows(name, t, dtypes):
     return t.data_ptr(), rows, cols, stride if rows > 1 else max(cols, 1)
 
 
+def _on(stream, device, *made):
+    """Handle of a given stream of this device.  What is made for the call goes to no
+    other use before the stream is done with it; the caller orders the stream behind
+    the work that the current one still has (wait_stream), as for any input."""
+    if stream.device.index != device:
+        raise MoeError(-1, f"the stream is on {stream.device}, the tensors on cuda:{device}")
+    for t in made:
+        if t is not None:
+            t.record_stream(stream)
+    return stream.cuda_stream
+
+
 BF16, F16, F32 = 0, 1, 2
 _TYPES = {}
 
@@ -465,8 +477,10 @@ def _types():
         device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _TYPES.update(
-            device=device, stream=raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), like=torch.empty_like, u8=torch.uint8, f8=torch.float8_e4m3fn, bf16=torch.bfloat16, f32=torch.float32, i32=torch.int32,
-            codes=(torch.float8_e4m3fn, torch.uint8), half=(torch.bfloat16, torch.int16), f32s=(torch.float32,), i32s=(torch.int32,),
+            device=device, stream=raw or (lambda d: torch.cuda.current_stream(d).cuda_stream), like=torch.empty_like,
+            u8=torch.uint8, f8=torch.float8_e4m3fn, bf16=torch.bfloat16, f32=torch.float32, i32=torch.int32,
+            codes=(torch.float8_e4m3fn, torch.uint8), half=(torch.bfloat16, torch.int16), f32s=(torch.float32,),
+            i32s=(torch.int32,),
             quant={torch.bfloat16: BF16, torch.int16: BF16, torch.float16: F16},
             out={torch.bfloat16: BF16, torch.float32: F32},
             logits={torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32})
@@ -496,7 +510,8 @@ def fp8_quantize(x, block_rows: int, q=None, scales=None, stream=None):
         sp = scales.data_ptr()
     else:
         sp = _operand("scales", scales, dev, T["f32s"], size)
-    rc = fn(T["quant"][x.dtype], xp, rows, cols, block_rows, qp, sp, T["stream"](dev) if stream is None else stream.cuda_stream)
+    rc = fn(T["quant"][x.dtype], xp, rows, cols, block_rows, qp, sp,
+            T["stream"](dev) if stream is None else _on(stream, dev, q, scales))
     if rc:
         _check(rc)
     return q, scales
@@ -552,7 +567,8 @@ def rms_norm(x, weight, eps: float, residual=None, bf16: bool = True, fp8: bool 
         out["scales"] = scales
     elif q is not None or scales is not None:
         raise MoeError(-1, "q or scales is given, but fp8 is off")
-    rc = lib().moe_rms_norm(xp, rp, n, d, wp, eps, sump, yp, qp, sp, T["stream"](dev) if stream is None else stream.cuda_stream)
+    rc = lib().moe_rms_norm(xp, rp, n, d, wp, eps, sump, yp, qp, sp,
+                            T["stream"](dev) if stream is None else _on(stream, dev, *out.values()))
     if rc:
         _check(rc)
     return out
@@ -581,7 +597,8 @@ def fp8_linear(a, a_scales, w, w_scales, y=None, out_dtype=None, stream=None):
     yp, ym, yn, ldy = _rows("y", y, T["out"])
     if ym != m or yn != n:
         raise MoeError(-3, f"y has shape {(ym, yn)}, {(m, n)} wanted")
-    rc = lib().moe_fp8_linear(ap, asp, m, wp, wsp, n, K, T["out"][y.dtype], yp, ldy, T["stream"](dev) if stream is None else stream.cuda_stream)
+    rc = lib().moe_fp8_linear(ap, asp, m, wp, wsp, n, K, T["out"][y.dtype], yp, ldy,
+                              T["stream"](dev) if stream is None else _on(stream, dev, y))
     if rc:
         _check(rc)
     return y
@@ -616,7 +633,8 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     elif workspace.get_device() != dev:
         raise MoeError(-1, f"the workspace is on {workspace.device}, not on the current device cuda:{dev}")
     ws, wn = _aligned(workspace)
-    rc = L.moe_sample(T["logits"][logits.dtype], lp, B, V, ld, tp, kp, pp, mp, up, tokp, prp, ws, wn, T["stream"](dev) if stream is None else stream.cuda_stream)
+    rc = L.moe_sample(T["logits"][logits.dtype], lp, B, V, ld, tp, kp, pp, mp, up, tokp, prp, ws, wn,
+                      T["stream"](dev) if stream is None else _on(stream, dev, tokens, probs, workspace))
     if rc:
         _check(rc)
     return tokens, probs

@@ -103,6 +103,27 @@ def test_graph_replays(tq, T):
         torch.cuda.synchronize()
 
 
+def test_given_stream_keeps_what_the_call_made(tq):
+    """A workspace of a call on another stream is nobody's until that stream is done with it."""
+    logits, u = torch.randn((4, 50000), device="cuda"), torch.rand(4, device="cuda")
+    want = tq.sample(logits, u)
+    n = tq.lib().moe_sample_workspace_bytes(4, 50000) + 256
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    first = torch.empty(n, dtype=torch.uint8, device="cuda")
+    place = first.data_ptr()
+    del first                                             # the call's workspace will be here
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        torch.cuda._sleep(20_000_000)                     # some 10 ms of work before the call's
+    got = tq.sample(logits, u, stream=st)
+    later = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert later.data_ptr() != place
+    torch.cuda.current_stream().wait_stream(st)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_two_graphs_and_two_streams(tq):
     """Two captured steps with inputs of their own, replayed side by side."""
     heads = [Head(tq, 24, 512, 4000, seed=s) for s in (1, 2)]
