@@ -169,3 +169,16 @@ def test_behind_the_block_and_the_draft_head(tq):
         for t in range(T):
             token, prob, margin = sampler.sample_row(logits[t].cpu().double().numpy(), float(u[t]))
             assert margin < 1e-9 or int(tokens[t]) == token
+
+
+def test_a_stream_of_another_device_is_refused(tq):
+    from types import SimpleNamespace
+    st = SimpleNamespace(device=torch.device("cuda", torch.cuda.current_device() + 1), cuda_stream=0)
+    x = torch.zeros((4, 256), dtype=torch.bfloat16, device="cuda")
+    q, s = tq.fp8_quantize(x, 1)
+    for call in (lambda: tq.fp8_quantize(x, 1, stream=st), lambda: tq.rms_norm(x, torch.ones(256, device="cuda"), 1e-6, stream=st),
+                 lambda: tq.fp8_linear(q, s, q, s[:1].contiguous(), stream=st),
+                 lambda: tq.sample(torch.zeros((2, 8), device="cuda"), torch.zeros(2, device="cuda"), stream=st)):
+        with pytest.raises(tq.MoeError) as e:
+            call()
+        assert e.value.code == -1 and "stream" in str(e.value)
