@@ -554,7 +554,8 @@ struct Pick {
   uint64_t before, answer;
   uint32_t before_count, bin_count;
   uint64_t heavy[3];
-  int n, found, n_few;
+  int found[3];  // answers of three searches for a bin in turn
+  int n, part, n_few;
 };
 
 template <int TYPE>
@@ -573,6 +574,7 @@ struct Picker {
   uint16_t* ends;  // [n x kBins] where a row's bin ends in a chunk's list, in LDS
   bool near;       // if there is room for it
   int index_bits;  // of a token's index
+  int turn;        // which of s.found the next search writes
 
   __device__ __forceinline__ double weight(float l) const { return exp((double)l * grid.per / kPerNat - top); }
 
@@ -625,7 +627,7 @@ struct Picker {
     s.mass[t] = mi;
     s.unit[t] = unit;
     s.units[t] = m;
-    if (t == 0) s.found = kBins;
+    if (t < 3) s.found[t] = kBins;
     __syncthreads();
   }
   __device__ __forceinline__ uint32_t count_before(int b) const { return b ? s.count[b - 1] : 0; }
@@ -633,17 +635,20 @@ struct Picker {
 
   // First bin whose running count reaches k (kBins if none does), or whose running
   // mass reaches `target` (`over`: exceeds it; the last bin with mass if none does).
-  // s.found is kBins between calls.
+  // The searches take the three places of s.found in turn.  One that ends sets the
+  // next one's place back, before its barrier: that place was read before the barrier
+  // of the search in between, and is written after this one.
   __device__ int found_bin() {
+    const int next = turn == 2 ? 0 : turn + 1;
+    if (threadIdx.x == 0) s.found[next] = kBins;
     __syncthreads();
-    const int f = s.found;
-    __syncthreads();
-    if (threadIdx.x == 0) s.found = kBins;
+    const int f = s.found[turn];
+    turn = next;
     return f;
   }
   __device__ int bin_of_count(uint32_t k) {
     const int t = threadIdx.x;
-    if (s.count[t] >= k && count_before(t) < k) s.found = t;
+    if (s.count[t] >= k && count_before(t) < k) s.found[turn] = t;
     return found_bin();
   }
   __device__ int bin_of_mass(double target, bool over) {
@@ -651,7 +656,7 @@ struct Picker {
     auto reached = [&](int i) { return over ? s.mass[i] > target : s.mass[i] >= target; };
     if (s.count[t] > count_before(t) &&
         (reached(t) ? t == 0 || !reached(t - 1) : s.count[t] == s.count[kBins - 1]))
-      s.found = t;
+      s.found[turn] = t;
     return found_bin();
   }
 
@@ -802,7 +807,7 @@ struct Picker {
         m = s.s.hist[PER * t + h];
         c = s.s.parts[PER * t + h];
         if (COUNT ? (f < target && f + (uint64_t)c >= target) : (e < target && e + m >= target)) {
-          s.found = PER * t + h;
+          s.part = PER * t + h;
           s.before = e;
           s.before_count = f;
           s.bin_count = c;
@@ -811,7 +816,7 @@ struct Picker {
         f += c;
       }
       __syncthreads();
-      const int part = s.found;
+      const int part = s.part;
       left = s.bin_count;
       before_units = s.before;
       before_count = s.before_count;
@@ -820,7 +825,6 @@ struct Picker {
       from = lo;
       to = hi;
       __syncthreads();
-      if (t == 0) s.found = kBins;
     }
     // at most kFew are left: each counts what stands before it
     if (t == 0) s.n_few = 0;
@@ -982,7 +986,7 @@ __global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs
     const double p = (double)pf, mp = (double)mpf, u = (double)uf;
     const float top = logit_of(top_key);
     Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, ws, s, Grid(t), 0.f, 0.0, -1, false, 0, 0,
-                      ends, ws.n <= kNearChunks, 32 - __clz(a.V | 1)};
+                      ends, ws.n <= kNearChunks, 32 - __clz(a.V | 1), 0};
     pick.edge = pick.grid.bin(top);
     pick.top = (double)top * pick.grid.per / kPerNat;
     bool done = false;

@@ -1,0 +1,70 @@
+"""GPU parity of the sampler where a row's decisions lie at the ends of its bins,
+against the float64 oracle, through the binding.
+
+Tokens are equal wherever the oracle's decisions are further than 1e-9 of the
+mass from going the other way, and probabilities agree to half an fp32 step,
+2^-24, and the same 1e-9: a weight is good to 4e-11 of itself, and so is every
+sum of weights.
+"""
+import sys
+
+import numpy as np
+import pytest
+
+from oracle import sampler
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def tq():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import ternary_quantized_moe_amd as tq
+    tq.lib()
+    return tq
+
+
+OFF = {"temperature": 1.0, "top_k": 0, "top_p": 1.0, "min_p": 0.0}
+
+
+def check(tq, logits, u, least=0.9, margin=1e-9, **settings):
+    """Every row of a float32 matrix against the oracle, with one setting each for all rows or a list of them; at
+    least this share of the rows must be decided by more than the margin."""
+    rows = np.asarray(logits, np.float32)
+    B = len(rows)
+    u = np.broadcast_to(np.asarray(u, np.float32), B)
+    per = {k: np.broadcast_to(np.asarray(settings.get(k, OFF[k]), np.int32 if k == "top_k" else np.float32), B)
+           for k in OFF}
+    dev = {k: torch.tensor(v.copy(), device="cuda") for k, v in per.items()}
+    tokens, probs = tq.sample(torch.tensor(rows, device="cuda"), torch.tensor(u.copy(), device="cuda"), **dev)
+    tokens, probs = tokens.cpu().numpy(), probs.cpu().numpy().astype(np.float64)
+    decided = 0
+    for b in range(B):
+        s = {k: v[b].item() for k, v in per.items()}
+        token, prob, m = sampler.sample_row(rows[b], float(u[b]), **s)
+        if m > margin:
+            decided += 1
+            assert tokens[b] == token, (b, s, u[b], m)
+            assert abs(probs[b] - prob) <= (2.0 ** -24 + 1e-9) * prob, (b, s, u[b])
+    assert decided >= least * B
+
+
+def test_top_k_beyond_the_tokens_with_mass(tq):
+    """A count that no bin reaches, and a border by mass right behind it."""
+    rng = np.random.default_rng(1)
+    B, V = 256, 3000
+    masked = np.full((B, V), -np.inf, np.float32)
+    for b in range(B):
+        at = rng.choice(V, 20, replace=False)
+        masked[b, at] = rng.normal(size=20) * 3
+    spread = (rng.normal(size=(B, V)) * 30).astype(np.float32)
+    for settings in (dict(), dict(top_p=0.9), dict(min_p=0.05), dict(top_p=0.95, min_p=0.01), dict(temperature=0.3)):
+        say("top-k beyond the mass", settings)
+        check(tq, masked, rng.random(B), top_k=50, **settings)
+        check(tq, spread, rng.random(B), top_k=700, **settings)
