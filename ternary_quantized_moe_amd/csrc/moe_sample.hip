@@ -613,18 +613,24 @@ struct Picker {
     // e^(upper edge - top) 2^-35
     const double unit = exp(((double)edge - (double)t + 1.0) / kPerNat - top) / kBinUnit;
     uint32_t ci = scan_sum(c);
+    // The lanes' sums are rounded in different orders: one can lie below its
+    // predecessor's, or an empty bin's above it.  Their running maximum over the bins
+    // with tokens never falls and rises at bins with tokens alone; adding the waves
+    // before, in one order for all, keeps that.
     double mi = scan_sum((double)m * unit);
+    mi = scan_wave(c ? mi : 0.0, 0.0, [](double p, double q) { return fmax(p, q); });
     if (lane == 63) {
       s.wave_u32[wave] = ci;
       s.wave_f64[wave] = mi;
     }
     __syncthreads();
+    double waves = 0.0;
     for (int i = 0; i < wave; ++i) {
       ci += s.wave_u32[i];
-      mi += s.wave_f64[i];
+      waves += s.wave_f64[i];
     }
     s.count[t] = ci;
-    s.mass[t] = mi;
+    s.mass[t] = waves + mi;
     s.unit[t] = unit;
     s.units[t] = m;
     if (t < 3) s.found[t] = kBins;
@@ -634,7 +640,8 @@ struct Picker {
   __device__ __forceinline__ double mass_before(int b) const { return b ? s.mass[b - 1] : 0.0; }
 
   // First bin whose running count reaches k (kBins if none does), or whose running
-  // mass reaches `target` (`over`: exceeds it; the last bin with mass if none does).
+  // mass reaches `target` (`over`: exceeds it; the last bin with tokens if none does).
+  // Either has tokens: counts and masses rise nowhere else.
   // The searches take the three places of s.found in turn.  One that ends sets the
   // next one's place back, before its barrier: that place was read before the barrier
   // of the search in between, and is written after this one.
@@ -770,6 +777,7 @@ struct Picker {
         s.s.hist[i] = 0;
         s.s.parts[i] = 0;
       }
+      if (t == 0) s.bin_count = 0;  // the loop ends even if the logits change under it
       __syncthreads();
       const int shift = max(0, 64 - kPartBits - __clzll(to - from));
       const int parts = (int)((to - from) >> shift) + 1;  // at most kParts
@@ -830,10 +838,10 @@ struct Picker {
     if (t == 0) s.n_few = 0;
     __syncthreads();
     each([&](uint64_t o) {
-      if (o >= lo && o <= hi) s.few[atomicAdd(&s.n_few, 1)] = Pick::Few{o, unit_at(o)};
+      if (o >= lo && o <= hi) s.few[min(atomicAdd(&s.n_few, 1), kFew - 1)] = Pick::Few{o, unit_at(o)};
     });
     __syncthreads();
-    const int few = s.n_few;
+    const int few = min(s.n_few, kFew);
     // as many lanes to a token as there are, up to a wave
     const int per = few > 1 ? max(0, min(6, __clz(few - 1) - 23)) : 6;
     const int i0 = t & ((1 << per) - 1);
@@ -868,7 +876,8 @@ struct Picker {
   // The filters and the choice.
   __device__ void choose(int k, double p, double mp, double u, int& token, double& prob) {
     // what is kept: the bins before `end`, and of bin `end` the tokens up to `last`,
-    // which hold `part` of its units; `held_mass` is the mass of it all
+    // which hold `part` of its units (none of them if it is 0; never so for the first
+    // bin, which has the largest logit); `held_mass` is the mass of it all
     uint64_t last = ~0ull, part = 0;
     int end = kBins;
     double held_mass = s.mass[kBins - 1];
@@ -881,7 +890,8 @@ struct Picker {
         held_mass = mass_before(b) + (double)part * s.unit[b];
       }
     }
-    // the place in the order where the mass reaches (exceeds) a target, at most `held_mass`
+    // the place in the order where the mass reaches (exceeds) a target below `held_mass`,
+    // which is therefore not in a bin `end` of which nothing is kept
     auto place = [&](double target, bool over, int& bin, uint64_t& at, uint64_t& cum) {
       bin = min(bin_of_mass(target, over), end);
       fetch(bin);
@@ -942,9 +952,13 @@ struct Picker {
     int bin;
     uint64_t at, cum;
     if (!(u >= 0.0)) u = 0.0;
-    // the last token with mass stands in for a u of 1 or more
-    if (u < 1.0) place(u * held_mass, true, bin, at, cum);
-    else place(held_mass, false, bin, at, cum);
+    if (u < 1.0) {
+      place(u * held_mass, true, bin, at, cum);
+    } else {  // the last token with mass, by units and counts: a small one does not show in the sums
+      bin = part > 0 ? end : bin_of_count(s.count[end - 1]);
+      fetch(bin);
+      at = select<false>(bin == end ? part : s.units[bin], cum);
+    }
     token = token_at(at);
     prob = weight(logit_at(at)) / held_mass;
   }
