@@ -341,6 +341,11 @@ constexpr int kCountShift = 50;                            // 2^13 tokens of abo
 constexpr int kScanThreads = 256;
 constexpr float kFarthestBin = 4194304.f;                  // 2^22: bin numbers are exact in fp32 up to it
 
+// Whether a chunk with this top bin is counted, and whether a row with it is answered
+// from its chunks' bins: all within its reach are counted then.
+__device__ __forceinline__ bool chunk_on_grid(float edge) { return fabsf(edge) <= kFarthestBin; }
+__device__ __forceinline__ bool row_on_grid(float edge) { return edge >= kBins - kFarthestBin && edge <= kFarthestBin; }
+
 struct ChunkHead {
   uint64_t top;  // largest key, then the complement of its lowest index
   float edge;    // number of the top bin
@@ -450,7 +455,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   }
   const Grid grid(t);
   const float edge = grid.bin(top);
-  const bool counted = t > 0.f && k != 1 && fabsf(edge) <= kFarthestBin;
+  const bool counted = t > 0.f && k != 1 && chunk_on_grid(edge);
   // the first token needs no histogram; a grid too far out is not exact
   if (counted) {
     // a token's value gives way to its seat: its bin and its number there.  What is too far below the top
@@ -585,7 +590,7 @@ struct Picker {
     static_assert(kMaxChunks <= kSampThreads, "a thread a chunk");
     if (t < ws.n) {
       const float d = edge - e;  // a chunk too far out has no histogram
-      s.dist[t] = (short)(fabsf(e) <= kFarthestBin && d < (float)kBins ? (int)d : kBins);
+      s.dist[t] = (short)(chunk_on_grid(e) && d < (float)kBins ? (int)d : kBins);
     }
     __syncthreads();
     static_assert(kBins == kSampThreads, "a bin a thread");
@@ -1004,7 +1009,7 @@ __global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs
     pick.edge = pick.grid.bin(top);
     pick.top = (double)top * pick.grid.per / kPerNat;
     bool done = false;
-    if (fabsf(pick.edge) <= kFarthestBin) {
+    if (row_on_grid(pick.edge)) {
       pick.merge(chunk_edge);
       pick.choose(k, p, mp, u, token, prob);
       done = true;

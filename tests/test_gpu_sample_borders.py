@@ -113,3 +113,23 @@ def test_last_token_with_mass(tq):
     rows = rng.permuted(rows, axis=1).astype(np.float32)
     check(tq, rows, [1.0, 1.5, 3.0, float("inf")])
     check(tq, rows, 1.0, top_k=20010)
+
+
+def test_rows_across_the_end_of_the_grid(tq):
+    """Rows whose l / T lies around -2^18 and 2^18, where bins of 1 / 16 nat end to be numbered: their chunks lie on
+    both sides of it."""
+    V, step = 6000, 0.03125
+    row = np.full(V, -262144.0 - step, np.float32)
+    row[0] = -262144.0
+    check(tq, row[None].repeat(3, 0), [0.9, 0.3, 0.0])
+    rng = np.random.default_rng(6)
+    for sign in (-1, 1):
+        say("around the end of the grid", sign)
+        top = sign * 262144.0 + np.arange(-40, 41, 4)[:, None]
+        rows = top - step * rng.integers(0, 900, (len(top), V)) * rng.random((len(top), V)) ** 3 // step * step
+        rows = rows.astype(np.float32)
+        assert np.all(np.abs(rows / step) < 2 ** 24)
+        for settings in (dict(), dict(top_p=0.8), dict(top_k=4000, min_p=0.01)):
+            check(tq, rows, rng.random(len(top)), **settings)
+        small = (rows * 2.0 ** -17).astype(np.float32)                      # the same at a temperature of 2^-17
+        check(tq, small, rng.random(len(top)), temperature=2.0 ** -17, top_p=0.95)
