@@ -549,8 +549,8 @@ struct Pick {
     uint64_t order, units;
   } few[kFew];
   uint32_t count[kBins];  // tokens in the bins up to and with this one
-  double mass[kBins];     // and their mass, relative to the largest weight
-  double unit[kBins];     // weight of a bin's unit of mass
+  double mass[kBins];     // and their mass, in units of the top bin
+  double unit[kBins];     // a unit of mass of a bin, in units of the top bin
   uint64_t units[kBins];  // a bin's units
   uint64_t wave_u64[kSampWaves];
   double wave_f64[kSampWaves];
@@ -615,8 +615,9 @@ struct Picker {
         if (near && i == i0 + q) ends[i * kBins + t] = in ? end[q] : 0;
       }
     }
-    // e^(upper edge - top) 2^-35
-    const double unit = exp(((double)edge - (double)t + 1.0) / kPerNat - top) / kBinUnit;
+    // e^(difference of the upper edges); 1 for the top bin, whose sums and shares are
+    // therefore exact up to 2^53: tokens that weigh the same are counted
+    const double unit = exp(-(double)t / kPerNat);
     uint32_t ci = scan_sum(c);
     // The lanes' sums are rounded in different orders: one can lie below its
     // predecessor's, or an empty bin's above it.  Their running maximum over the bins
@@ -965,7 +966,8 @@ struct Picker {
       at = select<false>(bin == end ? part : s.units[bin], cum);
     }
     token = token_at(at);
-    prob = weight(logit_at(at)) / held_mass;
+    // a unit of the top bin: e^(its upper edge - top) 2^-35
+    prob = weight(logit_at(at)) / (held_mass * (exp(((double)edge + 1.0) / kPerNat - top) / kBinUnit));
   }
 };
 

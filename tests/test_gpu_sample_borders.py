@@ -133,3 +133,20 @@ def test_rows_across_the_end_of_the_grid(tq):
             check(tq, rows, rng.random(len(top)), **settings)
         small = (rows * 2.0 ** -17).astype(np.float32)                      # the same at a temperature of 2^-17
         check(tq, small, rng.random(len(top)), temperature=2.0 ** -17, top_p=0.95)
+
+
+@pytest.mark.parametrize("temperature", [1.0, 0.7])
+def test_equal_logits_are_counted(tq, temperature):
+    """Tokens of equal weight: u and top-p on the border between two of them are exact."""
+    rng = np.random.default_rng(8)
+    B, V = 400, 4096
+    rows, share = np.full((B, V), -np.inf, np.float32), np.empty(B, np.float32)
+    for b in range(B):
+        parts = 1 << int(rng.integers(1, 6))
+        n = parts * int(rng.integers(1, 1 + (V if b % 4 == 0 else 128) // parts))
+        rows[b, rng.choice(V, n, replace=False)] = rng.normal() * 5
+        share[b] = rng.integers(1, parts) / parts                          # n share is a whole number
+    say("equal logits", temperature)
+    check(tq, rows, share, least=1.0, temperature=temperature)
+    check(tq, rows, np.float32(0.999999), least=1.0, temperature=temperature, top_p=share)
+    check(tq, rows, rng.random(B), least=1.0, temperature=temperature, top_p=share, top_k=V // 2)
