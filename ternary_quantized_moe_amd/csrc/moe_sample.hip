@@ -9,7 +9,8 @@
 // what is left.
 //
 // Weights are evaluated in fp64 and summed as 64-bit integers, in units of 2^-35
-// relative to a bin of 1 / 16 nat, so that no sum depends on an order of additions.
+// relative to a bin of 1 / 16 nat; the bins' sums are added in fp64 in one fixed
+// order.
 // Two launches.  The scan reads the logits once (HBM floor 6.5 us at 64 x 131072
 // fp32, 14.2 us measured: 30 vector instructions a token for its bin, weight and
 // place bound it beside the read) and leaves 512-bin histograms and lists of
@@ -17,7 +18,7 @@
 // a chain of dependent steps, each a memory's or a barrier's latency; 8 us at the
 // least for 1 x 50304).
 //
-// Rows whose bins are not exact take radix descents on the logits' ordered bits,
+// Rows off the grid of bins (an infinite logit, l / T beyond some 2^18) take radix descents on the logits' ordered bits,
 // 11 + 11 + 10 of them, with units of 2^-42 of the largest weight: a histogram of
 // counts and masses over the digit of the tokens that share the higher digits, a
 // scan from the top, and the digit where the target is reached.  After three digits
@@ -326,12 +327,12 @@ __device__ void solve_by_radix(Row<TYPE>& row, Weigher& w, int k, double p, doub
 // ------------------------------------------------------------------ histograms
 // One read of the logits: blocks take a chunk of a row each, keep it in registers
 // for its largest value, and count it into 512 bins of 1 / 16 nat below that, on a
-// grid that all chunks of the row share: bin floor(16 l / T), in fp32 (a rounding
-// moves a bin's edge, the same way for everyone).  A bin holds a count and a mass:
-// the weight of a token relative to the bin's upper edge, in fp64, lies in
-// (e^-1/16, 1] but for that rounding and becomes an integer of 35 bits, so a
-// chunk's sums are exact in whatever order they come, count and mass in one 64-bit
-// number.  32 nats below the chunk's largest value a token has no mass (2^-46 of it).
+// grid that all chunks of the row share: bin floor(16 l / T), in fp64 (in fp32 a
+// rounding moves an edge by up to half a bin near 2^22, and the polynomial below is
+// left to extrapolate: weights off by 6e-9).  A bin holds a count and a mass: the
+// weight of a token relative to the bin's upper edge lies in (e^-1/16, 1] and
+// becomes an integer of 35 bits, so a chunk's sums are exact in whatever order they
+// come, count and mass in one 64-bit number.  32 nats below the chunk's largest value a token has no mass (2^-46 of it).
 // The chunk's tokens are also written down by bin (their places in the chunk, in no
 // order within a bin), so that whoever wants a bin's tokens need not search the row;
 // with a top-k only as many bins as hold the chunk's own first k.
@@ -339,33 +340,33 @@ constexpr int kBins = 512;
 constexpr double kPerNat = 16.0, kBinUnit = 34359738368.0;  // 2^35
 constexpr int kCountShift = 50;                            // 2^13 tokens of about 2^35 below it
 constexpr int kScanThreads = 256;
-constexpr float kFarthestBin = 4194304.f;                  // 2^22: bin numbers are exact in fp32 up to it
+constexpr double kFarthestBin = 4194304.0;                 // 2^22: the places of tokens are good to 2^-31 of a bin up to it
 
 // Whether a chunk with this top bin is counted, and whether a row with it is answered
 // from its chunks' bins: all within its reach are counted then.
-__device__ __forceinline__ bool chunk_on_grid(float edge) { return fabsf(edge) <= kFarthestBin; }
-__device__ __forceinline__ bool row_on_grid(float edge) { return edge >= kBins - kFarthestBin && edge <= kFarthestBin; }
+__device__ __forceinline__ bool chunk_on_grid(double edge) { return fabs(edge) <= kFarthestBin; }
+__device__ __forceinline__ bool row_on_grid(double edge) { return edge >= kBins - kFarthestBin && edge <= kFarthestBin; }
 
 struct ChunkHead {
   uint64_t top;  // largest key, then the complement of its lowest index
-  float edge;    // number of the top bin
-  float pad;
+  double edge;   // number of the top bin
 };
 
 // l / T on the grid: the bin number, and the weight in units of 2^-35 relative to
 // the bin's upper edge.
 struct Grid {
   double per;  // 16 / T
-  float perf;
-  __device__ __forceinline__ explicit Grid(float t) : per(kPerNat / (double)t), perf((float)per) {}
-  __device__ __forceinline__ float place(float l) const { return l * perf; }
-  __device__ __forceinline__ float bin(float l) const { return floorf(place(l)); }
+  __device__ __forceinline__ explicit Grid(float t) : per(kPerNat / (double)t) {}
+  __device__ __forceinline__ double bin(float l) const { return floor((double)l * per); }
+  // Place in the bin, from 0 to 1: the product is not rounded again.
+  __device__ __forceinline__ double in_bin(float l, double bin) const { return fma((double)l, per, -bin); }
   // COUNTED: with 2^50 on top.  The polynomial of degree 4 that meets
   // 2^35 e^((y - 1) / 16) at the Chebyshev nodes of y in [0, 1] is off by 0.52 units
-  // at most.  Adding 2^52 leaves the rounded integer in a double's low bits.
+  // at most.  Adding 2^52 leaves the rounded integer in a double's low bits and takes
+  // the constant's 0.27 with it: 1.29 units in all, 4e-11 of the lightest weight.
   template <bool COUNTED>
-  __device__ __forceinline__ uint64_t unit(float l, float bin) const {
-    const double y = fma((double)l, per, -(double)bin);
+  __device__ __forceinline__ uint64_t unit(float l, double bin) const {
+    const double y = in_bin(l, bin);
     double e = 21174.08417495729;
     e = fma(e, y, 1312820.8186157919);
     e = fma(e, y, 63043148.908760265);
@@ -454,21 +455,23 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
     atomicMin(&top_index, first);
   }
   const Grid grid(t);
-  const float edge = grid.bin(top);
+  const double edge = grid.bin(top);
   const bool counted = t > 0.f && k != 1 && chunk_on_grid(edge);
   // the first token needs no histogram; a grid too far out is not exact
   if (counted) {
     // a token's value gives way to its seat: its bin and its number there.  What is too far below the top
     // has one in the bins behind, one for each lane of a wave
-    const float nowhere = (float)(kBins + lane);
+    const double nowhere = (double)(kBins + lane), edge52 = edge + 4503599627370496.0;  // 2^52: see below
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       uint32_t at[VE];
       uint64_t was[VE];
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
-        const float l = x[j].v[e], bin = grid.bin(l);
-        at[e] = (uint32_t)fminf(edge - bin, nowhere);  // a NaN is passed over
+        const float l = x[j].v[e];
+        const double bin = grid.bin(l);
+        // edge - bin as the low bits of a double; a NaN is passed over
+        at[e] = (uint32_t)__double_as_longlong(fmin(edge52 - bin, nowhere + 4503599627370496.0));
         was[e] = atomicAdd((unsigned long long*)&hist[at[e]], (unsigned long long)grid.template unit<true>(l, bin));
       }
 #pragma unroll
@@ -476,7 +479,7 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
     }
   }
   __syncthreads();
-  if (tid == 0) ws.heads[blockIdx.x] = ChunkHead{(uint64_t)key_of(top) << 32 | (uint32_t)~top_index, edge, 0.f};
+  if (tid == 0) ws.heads[blockIdx.x] = ChunkHead{(uint64_t)key_of(top) << 32 | (uint32_t)~top_index, edge};
   if (!counted) return;
   const uint64_t h0 = hist[2 * tid], h1 = hist[2 * tid + 1];
   const uint32_t c0 = (uint32_t)(h0 >> kCountShift), c1 = (uint32_t)(h1 >> kCountShift);
@@ -528,8 +531,8 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
 // chunks' lists.  A place within a bin is found among its tokens: each counts what
 // stands before it, at most 128 of them; a fuller bin is first divided by the order
 // of its tokens (logit, then index), 1024 ways.  Up to 4096 tokens are kept in LDS
-// for that, more are read from the chunks' lists every time.  Only rows whose grid is
-// not exact (an infinite logit, a temperature near 0) go through the radix descents.
+// for that, more are read from the chunks' lists every time.  Only rows off the grid
+// (an infinite logit, a temperature near 0) go through the radix descents.
 constexpr int kList = 4096;  // tokens kept
 constexpr int kPrefix = 1024;  // as many are fetched where later borders may need them
 constexpr int kFew = 128, kPartBits = 10, kParts = 1 << kPartBits;
@@ -571,8 +574,8 @@ struct Picker {
   const Chunks& ws;  // this row's
   Pick& s;
   Grid grid;
-  float edge;  // the row's top bin
-  double top;  // its largest l / T
+  float top;    // the row's largest logit
+  double edge;  // its bin
   int here;    // the fetched bin
   bool kept;   // whether its tokens are in the list, which holds the bins
   int list_from, list_to;
@@ -581,16 +584,19 @@ struct Picker {
   int index_bits;  // of a token's index
   int turn;        // which of s.found the next search writes
 
-  __device__ __forceinline__ double weight(float l) const { return exp((double)l * grid.per / kPerNat - top); }
+  // 1 for the largest logit, from an exact difference for the others
+  __device__ __forceinline__ double weight(float l) const {
+    return exp(((double)l - (double)top) * (grid.per / kPerNat));
+  }
 
   // The row's running counts and masses from the chunks' histograms; `e` is the top
   // bin of the thread's own chunk, if it has one.
-  __device__ void merge(float e) {
+  __device__ void merge(double e) {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     static_assert(kMaxChunks <= kSampThreads, "a thread a chunk");
     if (t < ws.n) {
-      const float d = edge - e;  // a chunk too far out has no histogram
-      s.dist[t] = (short)(chunk_on_grid(e) && d < (float)kBins ? (int)d : kBins);
+      const double d = edge - e;  // a chunk too far out has no histogram
+      s.dist[t] = (short)(chunk_on_grid(e) && d < (double)kBins ? (int)d : kBins);
     }
     __syncthreads();
     static_assert(kBins == kSampThreads, "a bin a thread");
@@ -750,7 +756,7 @@ struct Picker {
     if (kept) {
       for (int i = threadIdx.x; i < s.n; i += kSampThreads) {
         const uint64_t o = s.s.order[i];
-        if (list_from == list_to || edge - grid.bin(logit_at(o)) == (float)here) use(o);
+        if (list_from == list_to || edge - grid.bin(logit_at(o)) == (double)here) use(o);
       }
     } else {
       read_tokens(here, here, [](int, int) { return 0; }, [&](int, uint64_t o) { use(o); });
@@ -770,9 +776,9 @@ struct Picker {
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
     uint64_t lo = 0, hi = ~0ull, before_units = 0;
     // where the bin's tokens should lie; the end parts take what does not
-    const float slack = 1.f / (1 << 20), b0 = edge - (float)here, b1 = b0 + 1.f;
-    uint64_t from = order_of((b1 + fabsf(b1) * slack) / grid.perf, 0),
-             to = order_of((b0 - fabsf(b0) * slack) / grid.perf, (1 << index_bits) - 1);
+    const double slack = 1.0 / (1 << 20), b0 = edge - (double)here, b1 = b0 + 1.0;
+    uint64_t from = order_of((float)((b1 + fabs(b1) * slack) / grid.per), 0),
+             to = order_of((float)((b0 - fabs(b0) * slack) / grid.per), (1 << index_bits) - 1);
     if (from > to) {
       from = 0;
       to = hi;
@@ -917,7 +923,7 @@ struct Picker {
     if (mp > 0.0) {
       // the bin that weight mp falls into; rounding may put it into a neighbour
       const double floor_w = mp < 1.0 ? mp : 1.0;
-      const int near_bin = (int)fmin(fmax((double)edge - floor((log(floor_w) + top) * kPerNat), 0.0), (double)kBins);
+      const int near_bin = (int)fmin(fmax(-floor(grid.in_bin(top, edge) + log(floor_w) * kPerNat), 0.0), (double)kBins);
       const int first = max(0, near_bin - 1), far = min(min(near_bin + 1, end), kBins - 1);
       bool found = false;
       if (first <= far) {
@@ -926,7 +932,7 @@ struct Picker {
         __syncthreads();
         auto weigh = [&](uint64_t o) {
           const float l = logit_at(o);
-          const int bin = (int)fminf(edge - grid.bin(l), (float)kBins);
+          const int bin = (int)fmin(edge - grid.bin(l), (double)kBins);
           if (bin >= first && (bin < end || o <= last) && bin <= far && weight(l) >= floor_w) {
             atomicAdd((unsigned long long*)&s.heavy[bin - first], (unsigned long long)unit_at(o));
             atomicMax((unsigned long long*)&s.answer, (unsigned long long)o);
@@ -967,7 +973,7 @@ struct Picker {
     }
     token = token_at(at);
     // a unit of the top bin: e^(its upper edge - top) 2^-35
-    prob = weight(logit_at(at)) / (held_mass * (exp(((double)edge + 1.0) / kPerNat - top) / kBinUnit));
+    prob = weight(logit_at(at)) / (held_mass * (exp((1.0 - grid.in_bin(top, edge)) / kPerNat) / kBinUnit));
   }
 };
 
@@ -986,7 +992,7 @@ __global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs
               mpf = a.min_p ? a.min_p[b] : 0.0f, uf = a.u[b];
   const int k = a.top_k ? a.top_k[b] : 0;
   uint64_t best = 0;
-  float chunk_edge = 0.f;
+  double chunk_edge = 0.0;
   if ((int)threadIdx.x < ws.n) {
     const ChunkHead h = ws.heads[threadIdx.x];
     best = h.top;
@@ -1006,17 +1012,13 @@ __global__ __launch_bounds__(kSampThreads, 4) void sample_pick_kernel(SampleArgs
   } else if (t > 0.f && k != 1) {
     const double p = (double)pf, mp = (double)mpf, u = (double)uf;
     const float top = logit_of(top_key);
-    Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, ws, s, Grid(t), 0.f, 0.0, -1, false, 0, 0,
+    Picker<TYPE> pick{(const typename L::T*)a.logits + b * a.ld, a.V, ws, s, Grid(t), top, 0.0, -1, false, 0, 0,
                       ends, ws.n <= kNearChunks, 32 - __clz(a.V | 1), 0};
     pick.edge = pick.grid.bin(top);
-    pick.top = (double)top * pick.grid.per / kPerNat;
-    bool done = false;
     if (row_on_grid(pick.edge)) {
       pick.merge(chunk_edge);
       pick.choose(k, p, mp, u, token, prob);
-      done = true;
-    }
-    if (!done) {
+    } else {
       Row<TYPE> row{(const typename L::T*)a.logits + b * a.ld, a.V, s.radix};
       Weigher w{(double)top, (double)t, top_key};
       solve_by_radix(row, w, k, p, mp, u, token, prob);

@@ -150,3 +150,45 @@ def test_equal_logits_are_counted(tq, temperature):
     check(tq, rows, share, least=1.0, temperature=temperature)
     check(tq, rows, np.float32(0.999999), least=1.0, temperature=temperature, top_p=share)
     check(tq, rows, rng.random(B), least=1.0, temperature=temperature, top_p=share, top_k=V // 2)
+
+
+def outside_its_bin(l, t):
+    """How far l / T lies outside the bin of 1 / 16 nat that a product in fp32 puts it into, in bins."""
+    y = float(l) * 16 / float(t) - float(np.floor(np.float32(l) * np.float32(16 / float(t))))
+    return max(-y, y - 1)
+
+
+@pytest.mark.parametrize("far", [1e3, 2.0 ** 17, 2.0 ** 18 - 33])
+def test_weights_of_far_logits(tq, far):
+    """Rows of two logits whose l / T is `far` and a little more, each at the edge of its bin: u is put 1.6e-10 to
+    3e-10 of the mass from the border between two tokens.  Two weights good to 4e-11 move it by 8e-11 at most."""
+    rng = np.random.default_rng(int(far))
+    V, per_row = 50000, 16
+    say("far logits", far)
+    rows, us, ts, want = [], [], [], []
+    for sign in (-1, 1, -1, 1, -1, 1, -1, 1):
+        tries = []
+        for _ in range(2000):
+            t = np.float32(rng.uniform(0.01, 3))
+            hi = np.float32(sign * far * t * rng.uniform(0.97, 0.999))
+            lo = np.float32(hi - t * rng.uniform(0.3, 1.5))
+            tries.append((max(outside_its_bin(hi, t), outside_its_bin(lo, t)), t, hi, lo))
+        _, t, hi, lo = max(tries)
+        assert lo < hi and abs(float(lo) / float(t)) < 2 ** 18 - 32
+        n0 = V // 4
+        r = np.exp((float(lo) - float(hi)) / float(t))
+        total = n0 + (V - n0) * r
+        u = rng.permutation(1 << 24) / 2.0 ** 24
+        u = u[u * total > n0 + 0.3 * (V - n0) * r]
+        place = (u * total - n0) / r                                       # the answer is n0 + floor(place)
+        off = np.abs(place - np.round(place)) * r / total
+        u, place = (v[(off > 1.6e-10) & (off < 3e-10)][:per_row] for v in (u, place))
+        assert len(u) == per_row
+        for x, i in zip(u, place):
+            rows.append(np.where(np.arange(V) < n0, hi, lo))
+            us.append(x)
+            ts.append(t)
+            want.append(n0 + int(np.floor(i)))
+    dev = [torch.tensor(np.array(v, np.float32), device="cuda") for v in (rows, us, ts)]
+    tokens, _ = tq.sample(dev[0], dev[1], temperature=dev[2])
+    assert tokens.tolist() == want
