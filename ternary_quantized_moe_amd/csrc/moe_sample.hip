@@ -149,26 +149,6 @@ struct Row {
   Shared& s;
   __device__ __forceinline__ uint32_t key(int i) const { return key_of(L::f32(p[i])); }
 
-  // The largest key and the lowest index that has it.
-  __device__ void top(uint32_t& key_out, int& index_out) {
-    uint64_t best = 0;  // key, then the complement of the index
-    for (int i = threadIdx.x; i < V; i += kSampThreads) {
-      const uint64_t v = (uint64_t)key(i) << 32 | (uint32_t)~i;
-      best = v > best ? v : best;
-    }
-#pragma unroll
-    for (int o = 32; o; o >>= 1) {
-      const uint64_t v = __shfl_xor(best, o, 64);
-      best = v > best ? v : best;
-    }
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) s.wave_mass[threadIdx.x >> 6] = best;
-    __syncthreads();
-    for (int w = 0; w < kSampWaves; ++w) best = s.wave_mass[w] > best ? s.wave_mass[w] : best;
-    key_out = (uint32_t)(best >> 32);
-    index_out = (int)~(uint32_t)best;
-  }
-
   // Mass of a prefix's tokens with weight >= floor.
   __device__ uint64_t total(const Weigher& w, const Prefix& in) {
     uint64_t m = 0;
