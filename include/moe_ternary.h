@@ -258,8 +258,11 @@ int32_t moe_rms_norm(const uint16_t* x, const uint16_t* residual, int64_t n_toke
  * Each group of 128 is a matrix-core sum, scaled and added in fp32; y is rounded
  * once.  For an fp32 y the products are exact and the sums fp32.  For a bf16 y the
  * matrix cores' 8-bit instruction is used, which cuts eight neighbouring products
- * at 2^-13 of the largest of the eight before it adds them in fp32 (an error some
- * hundred times below the rounding of y).  m and n are arbitrary up to 2^29 (m n <= 2^37), K is
+ * at 2^-13 of the largest of the eight before it adds them in fp32, so at most
+ * 7 2^-13 of that largest product is lost of each eight.  On normal data that is
+ * some hundred times below the rounding of y; where the largest products of an eight
+ * cancel, the ones they hid are missing from y.  A caller whose data does that asks
+ * for an fp32 y, which has no such loss, at half the matrix rate.  m and n are arbitrary up to 2^29 (m n <= 2^37), K is
  * a multiple of 128 up to 2^22.  a and w are 16-byte aligned; y must not overlap an
  * input.  m = 0 or n = 0 is a no-op.  Results depend on the shapes and
  * the input bits alone; a token's y can differ in its last bits between batches of

@@ -12,7 +12,10 @@
 //         a product 2^-13 of the largest counts, one of 2^-14 does not), then
 //         adds in fp32: at most 7 2^-13 of that largest product is lost per eight.
 //         On normal data S is off by 1.6e-5 of its size, a hundredth of the
-//         output's own rounding.
+//         output's own rounding, which is why fewer bits than fp32's are taken here;
+//         an eight whose largest products cancel loses what they hid.  (The other
+//         8-bit instructions, 16x16x32 and 32x32x16, cut the same and run at a third
+//         to a half of the rate.)
 //   fp32  e4m3 widened to bf16 (exact) and v_mfma_f32_16x16x32_bf16, whose products
 //         are exact and whose sums are fp32 (4e-9 on the same data), at half the
 //         matrix rate.
