@@ -299,8 +299,8 @@ int32_t moe_fp8_linear(const uint8_t* a, const float* a_scales, int64_t m, const
  * |l_max / temperature| from 2^18 - 32 on, to 2^-43 of the largest weight instead.
  * Weights of the same 1 / 16 nat are summed as 64-bit integers and all sums have a
  * fixed order, so results are a function of the input bits; shares of tokens of
- * equal weight are exact for up to 2^18 of them.  A token more than 30 nats below
- * l_max may count as having no mass.  vocab is at most 2^21, batch 2^22.  batch = 0 is a no-op.  Ordered on
+ * equal weight are exact for up to 2^18 of them.  A token lighter than
+ * 2^-43 of the largest weight (29.8 nats below l_max) may count as having no mass.  vocab is at most 2^21, batch 2^22.  batch = 0 is a no-op.  Ordered on
  * `stream`; nothing is allocated.  Errors: MOE_E_FORMAT (type), MOE_E_SHAPE,
  * MOE_E_ARG, MOE_E_SPACE, MOE_E_DEVICE. */
 int64_t moe_sample_workspace_bytes(int64_t batch, int32_t vocab);

@@ -51,9 +51,10 @@ def check(tq, logits, u, least=0.9, margin=1e-9, **settings):
         if m > margin:
             decided += 1
             if u[b] >= 1 and tokens[b] != token:
-                # The last token with mass: one more than 30 nats below the largest logit may count as having
-                # none, so the answer may be any from the last token that is nearer on.
-                reach = np.where(rows[b] < rows[b].max() - 30 * s["temperature"], -np.inf, rows[b])
+                # The last token with mass: one lighter than 2^-43 of the largest weight may count as having
+                # none, so the answer may be any from the last heavier token on.
+                down = (rows[b].max().astype(np.float64) - rows[b]) / s["temperature"]
+                reach = np.where(down > 43 * np.log(2), -np.inf, rows[b])
                 near = sampler.sample_row(reach, float(u[b]), **s)[0]
                 got = rows[b, tokens[b]].item()
                 assert rows[b, token] <= got <= rows[b, near], (b, s, u[b])
@@ -192,3 +193,18 @@ def test_weights_of_far_logits(tq, far):
     dev = [torch.tensor(np.array(v, np.float32), device="cuda") for v in (rows, us, ts)]
     tokens, _ = tq.sample(dev[0], dev[1], temperature=dev[2])
     assert tokens.tolist() == want
+
+
+def test_rows_off_the_grid(tq):
+    """|l / T| of 3 million nats, logits an fp32 step or a few apart, 0.24 nats each: weights there are good to 2^-43 of
+    the largest, so 3000 of them to 3.4e-10 of the mass together."""
+    rng = np.random.default_rng(14)
+    B, V = 24, 3000
+    k = rng.integers(0, 200, (B, V))
+    k[:, rng.integers(0, V, 20)] = 0
+    for sign in (1, -1):
+        rows = (sign * 3.0 - 2.0 ** -22 * k).astype(np.float32)
+        for settings in (dict(), dict(top_k=300), dict(top_p=0.9), dict(min_p=0.1), dict(top_k=1500, top_p=0.7, min_p=0.2)):
+            say("off the grid", sign, settings)
+            check(tq, rows, rng.random(B), temperature=1e-6, **settings)
+            check(tq, rows, [0.0, 1.0, 7.0] * 8, temperature=1e-6, **settings)
