@@ -409,12 +409,13 @@ __global__ __launch_bounds__(kScanThreads) void sample_scan_kernel(SampleArgs a,
   for (int j = 0; j < N; ++j) x[j].load(row, base + (j * kScanThreads + tid) * VE, a.V);
   const float t = a.temperature ? a.temperature[b] : 1.0f;
   const int k = a.top_k ? a.top_k[b] : 0;
-  // the largest value (a NaN is passed over), then the lowest index that has it
+  // the largest value, then the lowest index that has it; a comparison passes over every
+  // NaN (a maximum answers a signalling one with a NaN)
   float mine = -__builtin_inff();
 #pragma unroll
   for (int j = 0; j < N; ++j)
 #pragma unroll
-    for (int e = 0; e < VE; ++e) mine = fmaxf(mine, x[j].v[e]);
+    for (int e = 0; e < VE; ++e) mine = x[j].v[e] > mine ? x[j].v[e] : mine;
   float top = mine;
   top = scan_wave(top, -__builtin_inff(), [](float p, float q) { return fmaxf(p, q); });
   if (lane == 63) tops[tid >> 6] = top;

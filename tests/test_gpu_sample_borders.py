@@ -208,3 +208,19 @@ def test_rows_off_the_grid(tq):
             say("off the grid", sign, settings)
             check(tq, rows, rng.random(B), temperature=1e-6, **settings)
             check(tq, rows, [0.0, 1.0, 7.0] * 8, temperature=1e-6, **settings)
+
+
+@pytest.mark.parametrize("dtype,bits", [(torch.float32, 0x7F800001), (torch.bfloat16, 0x7F81), (torch.float16, 0x7C01)])
+def test_signalling_nans_count_as_minus_infinity(tq, dtype, bits):
+    ints = torch.int32 if dtype == torch.float32 else torch.int16
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    logits = (torch.randn((8, 5000), generator=g, device="cuda") * 3).to(dtype)
+    at = torch.rand((8, 5000), generator=g, device="cuda") < 0.3
+    at[0], at[1, 1:], at[1, 0] = True, True, False
+    u = torch.rand(8, generator=g, device="cuda")
+    want = tq.sample(logits.masked_fill(at, float("-inf")), u, top_p=torch.full((8,), 0.8, device="cuda"))
+    for b in (bits, bits - (1 << 32 if dtype == torch.float32 else 1 << 16) + (1 << 31 if dtype == torch.float32 else 1 << 15)):
+        got = tq.sample(logits.view(ints).masked_fill(at, b).view(dtype), u, top_p=torch.full((8,), 0.8, device="cuda"))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert int(want[0][0]) == -1 and int(want[0][1]) == 0
