@@ -79,7 +79,7 @@ __device__ __forceinline__ f32x4 group_product(const Frag<kWide>& w, const Frag<
 // 32 matrix-core tiles.  One group of every row of the block, BN + BM rows of 128
 // bytes, is staged in LDS by loads that go there directly; two buffers, so the
 // next group arrives while this one is multiplied.
-// 4096 x 8192 x 4096 (tokens x rows x K) to bf16: 139 us, 1970 TFLOP/s, the matrix
+// 4096 x 8192 x 4096 (tokens x rows x K) to bf16: 137 us, 2010 TFLOP/s, the matrix
 // cores busy 47% of the time, the rest the staging and the reads of LDS beside
 // them (1.9 us a group, its products 0.9).  1 x 50304 x 2048 to fp32, 128 x 32
 // tiles: 19.7 us, 5.2 TB/s of weights.
@@ -516,6 +516,10 @@ hipError_t launch_split(const F8LinearArgs& a, hipStream_t stream) {
 //   128 x 128   94   26   22   23
 //   128 x 64    -    36   19   19
 //    64 x 64    -    39   21   14
+// Between one and two rounds of 256 x 256 tiles, 4096 x n x 4096 (another run):
+//     n        4096 4352 5120 6144 7168 8192
+//   256 x 256    78  113  113  117  126  137
+//   128 x 128   104  109  113  130  157  187
 // Four buffers where a CU has one block (1024 tokens: 26 us, two: 29), two where
 // a second block fills the gaps (2048 x 4096 x 2048: 25.5 us, four: 28).  Where even
 // the small tiles are too few, the split kernel with the largest block that there

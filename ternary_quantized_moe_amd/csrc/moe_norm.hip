@@ -72,7 +72,9 @@ __device__ __forceinline__ int64_t block_number() { return (int64_t)blockIdx.y *
 constexpr int kQThreads = 256;
 
 // One scale per row and group of 128: 16 lanes hold a group, eight values each.
-// Bound by HBM from some 4096 rows on; 64 x 4096 is one launch, 2.3 us.
+// Bound by HBM for many rows: 16384 x 2048 takes 16.8 us (6.0 TB/s with what the
+// Infinity Cache holds of it), 4096 x 2048 6.2 us (4.1 TB/s); 64 x 4096 is one
+// launch, 2.3 us.
 template <bool F16>
 __global__ __launch_bounds__(kQThreads) void fp8_quantize_rows_kernel(const u32x4* __restrict__ x, int64_t n8,
                                                                       u32x2* __restrict__ q,

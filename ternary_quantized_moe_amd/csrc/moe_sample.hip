@@ -12,18 +12,19 @@
 // relative to a bin of 1 / 16 nat; the bins' sums are added in fp64 in one fixed
 // order.
 // Two launches.  The scan reads the logits once (HBM floor 6.5 us at 64 x 131072
-// fp32, 14.2 us measured: 30 vector instructions a token for its bin, weight and
+// fp32, 14.6 us measured: some 30 vector instructions a token for its bin, weight and
 // place bound it beside the read) and leaves 512-bin histograms and lists of
-// tokens by bin; the choice works on those alone (21.8 us there, one block a row:
-// a chain of dependent steps, each a memory's or a barrier's latency; 8 us at the
-// least for 1 x 50304).
+// tokens by bin; the choice works on those alone (22.8 us there, one block a row:
+// a chain of dependent steps, each a memory's or a barrier's latency; 12.0 us for
+// 1 x 50304).
 //
 // Rows off the grid of bins (an infinite logit, l / T beyond some 2^18) take radix descents on the logits' ordered bits,
 // 11 + 11 + 10 of them, with units of 2^-42 of the largest weight: a histogram of
 // counts and masses over the digit of the tokens that share the higher digits, a
 // scan from the top, and the digit where the target is reached.  After three digits
 // the logit is exact, its tokens weigh the same, and the place among them is a
-// division.
+// division.  One block re-reads its row for each digit: 64 x 131072 with top-p takes
+// 690 us there (11 on the grid).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
