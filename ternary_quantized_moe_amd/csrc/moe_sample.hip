@@ -284,6 +284,16 @@ struct Row {
   }
 };
 
+// The first of `all` units (from 1) with which a mass reaches `target` (`over`: exceeds
+// it); the last one if none does.  A whole number of units above 2^53 has no room for
+// one more in a double.
+__device__ __forceinline__ uint64_t first_unit(double target, bool over, uint64_t all) {
+  if (target >= (double)all) return all;
+  if (!(target > 0.0)) return 1;
+  const uint64_t n = over ? (uint64_t)target + 1 : (uint64_t)ceil(target);
+  return n < all ? n : all;
+}
+
 // The whole row by radix descents alone: right for every row, and taken where the
 // histogram below does not hold the answer.
 template <int TYPE>
@@ -293,13 +303,11 @@ __device__ void solve_by_radix(Row<TYPE>& row, Weigher& w, int k, double p, doub
   if (k > 0 && k < row.V) keep = row.template find<true>(w, keep, (uint64_t)k);
   if (p < 1.0) {
     const uint64_t all = row.total(w, keep);
-    const double x = ceil(p * (double)all);
-    keep = row.template find<false>(w, keep, x >= 1.0 ? (uint64_t)x : 1);
+    keep = row.template find<false>(w, keep, first_unit(p * (double)all, false, all));
   }
   if (mp > 0.0) keep.floor = mp;
   const uint64_t all = row.total(w, keep);
-  const double x = floor(u * (double)all) + 1.0;
-  const uint64_t target = x >= (double)all ? all : x >= 1.0 ? (uint64_t)x : 1;
+  const uint64_t target = first_unit(u * (double)all, true, all);
   const Prefix at = row.template find<false>(w, keep, target);
   token = at.last;
   prob = w.weight(at.key) / ((double)all / kMassUnit);
@@ -889,9 +897,8 @@ struct Picker {
     auto place = [&](double target, bool over, int& bin, uint64_t& at, uint64_t& cum) {
       bin = min(bin_of_mass(target, over), end);
       fetch(bin);
-      const double in = (target - mass_before(bin)) / s.unit[bin], need = over ? floor(in) + 1.0 : ceil(in);
-      const uint64_t all = bin == end ? part : s.units[bin];
-      at = select<false>(need >= (double)all ? all : need >= 1.0 ? (uint64_t)need : 1, cum);
+      const double in = (target - mass_before(bin)) / s.unit[bin];
+      at = select<false>(first_unit(in, over, bin == end ? part : s.units[bin]), cum);
     };
     if (p < 1.0) {
       int bin;

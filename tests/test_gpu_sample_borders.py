@@ -136,7 +136,7 @@ def test_rows_across_the_end_of_the_grid(tq):
         check(tq, small, rng.random(len(top)), temperature=2.0 ** -17, top_p=0.95)
 
 
-@pytest.mark.parametrize("temperature", [1.0, 0.7])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 1e-7])  # the last off the grid
 def test_equal_logits_are_counted(tq, temperature):
     """Tokens of equal weight: u and top-p on the border between two of them are exact."""
     rng = np.random.default_rng(8)
