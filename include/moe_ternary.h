@@ -240,7 +240,9 @@ int32_t moe_fp8_quantize(int32_t type, const uint16_t* x, int64_t rows, int32_t 
  * At least one of y and q.  h, the mean and y are fp32; sum, y and q are each
  * rounded once from them (q is not taken from the rounded y).  A row with a NaN, or
  * with values whose squares pass fp32 (beyond about 1e19), gives NaN or zeros, as the
- * formula does in fp32; other rows are not touched by it.  sum and y may be
+ * formula does in fp32; other rows are not touched by it.  Squares of values below
+ * about 1e-19 lose bits or vanish in fp32, which shows only where eps is as small (with
+ * eps = 0 a row of zeros gives NaN).  sum and y may be
  * x or residual themselves (an in-place update of the residual stream); no other
  * overlap is allowed.  d is a multiple of 128, at most 32768; every buffer but
  * scales is 16-byte aligned.  n_tokens = 0 is a no-op.  Ordered on `stream`;
