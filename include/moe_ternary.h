@@ -207,7 +207,7 @@ int32_t moe_draft_head(const uint16_t* hidden, const uint16_t* emb, int64_t n_to
                        uint16_t* y, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Element types of the operators below. */
-enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };
+enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2, MOE_E4M3 = 3 };
 
 /* Device: quantize a bf16 or fp16 matrix to 8-bit floating point (e4m3: 4
  * exponent and 3 mantissa bits, largest value 448) with one fp32 scale per block
@@ -310,6 +310,169 @@ int32_t moe_sample(int32_t type, const void* logits, int64_t batch, int32_t voca
                    const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                    const float* u, int32_t* tokens, float* probs, void* workspace, int64_t workspace_bytes,
                    void* stream);
+
+/* Device: attention over whole prompts, for packed sequences and grouped heads:
+ *   y_i = sum_j p_ij v_j,   p_ij = exp(s_ij) / sum_j exp(s_ij),   s_ij = scale q_i . k_j
+ * over the keys j of the query's sequence; with causal != 0 over those that stand no
+ * later: lq queries are the last ones of lk keys, so query i sees j <= i + lk - lq (a
+ * chunk of a prompt behind the keys of earlier chunks; with lk < lq the first lq - lk
+ * queries see none).
+ *   type      MOE_BF16 or MOE_F16, of q, k, v and y
+ *   q         device [q_tokens x heads x head_dim], strides q_token and q_head in elements
+ *   k, v      device [k_tokens x kv_heads x head_dim], strides alike; query head h reads
+ *             head h / (heads / kv_heads).  q, k and v may be parts of one matrix
+ *   q_starts, k_starts  device int32 [n_seqs + 1], rising: sequence s has the queries
+ *             q_starts[s] .. q_starts[s + 1] - 1 and the keys of k_starts (NULL: q_starts)
+ *   y         device [q_tokens x heads x head_dim], contiguous
+ *   lse       device fp32 [q_tokens x heads], the logarithm of sum_j exp(s_ij), or NULL
+ * A query that sees no key, or scores of -inf alone, gets y = 0 and lse = -inf.  What a
+ * query must not see does not reach it, infinities and NaN included.  Tokens outside
+ * every sequence leave their y and lse as they were.  Starts outside [0, tokens] are
+ * taken as the nearer end, and one below the start before it as that one.
+ * Numerics: scores, the softmax's maximum and sum and y's sums are fp32; the weights
+ * are rounded to `type` for the matrix cores (each off by half a step of itself), y is
+ * rounded once.  head_dim is 64, 128 or 256; heads is a multiple of kv_heads, at most
+ * 4096; strides are multiples of 8, at most 2^24; q, k, v and y 16-byte aligned;
+ * tokens below 2^31, n_seqs at most 2^22; scale finite and positive.  q_tokens = 0 or n_seqs = 0 is a no-op.  y and lse
+ * overlap neither each other nor an input.  Results do not depend on the packing's other
+ * sequences.  Ordered on `stream`; nothing is allocated.  Errors: MOE_E_FORMAT (type),
+ * MOE_E_SHAPE, MOE_E_ARG, MOE_E_DEVICE. */
+int32_t moe_attention_prefill(int32_t type, const void* q, int64_t q_tokens, int32_t heads, int64_t q_token,
+                              int64_t q_head, const void* k, const void* v, int64_t k_tokens, int32_t kv_heads,
+                              int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, int32_t head_dim,
+                              const int32_t* q_starts, const int32_t* k_starts, int64_t n_seqs, int32_t causal,
+                              float scale, void* y, float* lse, void* stream);
+
+/* The key-value cache of one layer, in pages of page_size tokens (a power of two up to
+ * 4096), shared by the calls below:
+ *   k, v      device [n_pages x kv_heads x page_size x head_dim], of the activations' type
+ *             (cache_type MOE_BF16 or MOE_F16) or MOE_E4M3
+ *   k_scales, v_scales  device fp32 [n_pages x kv_heads x page_size] for MOE_E4M3 (one
+ *             scale for each head of each token, moe_fp8_quantize's rule over head_dim
+ *             values), else NULL
+ *   tables    device int32 [rows x width]: row r lists the pages of sequence r in order,
+ *             token i in page tables[r][i / page_size], place i % page_size; what stands
+ *             behind a row's last page is not read
+ * k and v are 16-byte aligned. */
+
+/* Device: attention of one new token of every sequence over the paged cache,
+ *   y_bh = sum_j p_bhj v_j,   p_bhj = exp(s) / sum_j exp(s),   s = scale q_bh . k_j,   j < lengths[b]
+ *   type      MOE_BF16 or MOE_F16, of q and y; cache_type that one or MOE_E4M3
+ *   q         device [batch x heads x head_dim], strides q_row and q_head in elements
+ *   tables    [batch x width], row b that of query b; width may be 0 (no tokens)
+ *   lengths   device int32 [batch], the cached tokens, the query's own among them; one
+ *             outside [0, width page_size] is taken as the nearer end
+ *   y         device [batch x heads x head_dim], contiguous
+ *   lse       device fp32 [batch x heads], as moe_attention_prefill's, or NULL
+ *   workspace >= moe_attention_decode_workspace_bytes(...), 256-byte aligned (NULL if that
+ *             is 0); it carries nothing from one call to the next
+ * A sequence of length 0 gets y = 0 and lse = -inf; cache places behind a sequence's last
+ * token may hold anything.  A page number outside [0, n_pages) reads nothing there and makes the
+ * sequence's results NaN.  Numerics are moe_attention_prefill's; e4m3 values enter exactly, their scales in fp32.
+ * Limits are moe_attention_prefill's; batch at most 65535, n_pages in [1, 2^31).  How a
+ * sequence is shared among workers, and so the last bits of y, depends on the batch's
+ * lengths.  batch = 0 is a no-op.  y, lse and the workspace overlap neither each other nor
+ * an input.  Ordered on `stream`; nothing is allocated.  Errors: MOE_E_FORMAT, MOE_E_SHAPE,
+ * MOE_E_ARG, MOE_E_SPACE, MOE_E_DEVICE. */
+int64_t moe_attention_decode_workspace_bytes(int64_t batch, int32_t heads, int32_t kv_heads, int32_t head_dim);
+int32_t moe_attention_decode(int32_t type, const void* q, int64_t batch, int32_t heads, int64_t q_row, int64_t q_head,
+                             int32_t cache_type, const void* k, const void* v, const float* k_scales,
+                             const float* v_scales, int64_t n_pages, int32_t kv_heads, int32_t page_size,
+                             int32_t head_dim, const int32_t* tables, int32_t width, const int32_t* lengths,
+                             float scale, void* y, float* lse, void* workspace, int64_t workspace_bytes,
+                             void* stream);
+
+/* Device: new keys and values into their pages, and the rotary embedding before that.
+ * Of every head of q and k the first `rotary` channels are turned in pairs (a, b), channels
+ * i and i + rotary / 2, or 2 i and 2 i + 1 (interleaved != 0), by positions[t] inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * (the angle in fp64, reduced to a fraction of a turn; the rest in fp32).  v is not turned.
+ * Token t goes to place positions[t] of sequence rows[t].
+ *   type      MOE_BF16 or MOE_F16, of q, k, v, q_out and k_out
+ *   q         device [n_tokens x heads x head_dim], or NULL; strides q_token, q_head
+ *   k, v      device [n_tokens x kv_heads x head_dim], strides alike
+ *   tables    device int32 [rows x width]
+ *   rows, positions  device int32 [n_tokens]; a row below 0 is padding: nothing of that token
+ *             is read or written.  A position outside the row's table, a row outside it or a page number
+ *             outside [0, n_pages) writes nothing to the cache and NaN to q_out and k_out
+ *   inv_freq  device fp32 [rotary / 2], or NULL with rotary = 0 and q = NULL
+ *   q_out     device [n_tokens x heads x head_dim], strides alike: q turned; given with q,
+ *             may be q itself
+ *   k_out     device [n_tokens x kv_heads x head_dim]: k turned, or NULL; may be k itself
+ * Each output is rounded once from the turned fp32 values (e4m3 from these, not from k_out).
+ * Two tokens for one place leave there a mix of both.  rotary is a multiple of 16 up to
+ * head_dim; the other limits are those of moe_attention_decode and its n_pages, page_size.
+ * No output overlaps another or an input, but for q_out = q and k_out = k.  n_tokens = 0 is
+ * a no-op.  Ordered on `stream`; nothing is allocated.  Errors: MOE_E_FORMAT, MOE_E_SHAPE,
+ * MOE_E_ARG, MOE_E_DEVICE. */
+int32_t moe_kv_append(int32_t type, const void* q, int64_t q_token, int64_t q_head, int32_t heads, const void* k,
+                      int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
+                      int64_t n_tokens, int32_t cache_type, void* k_cache, void* v_cache, float* k_scales,
+                      float* v_scales, int64_t n_pages, int32_t kv_heads, int32_t page_size, int32_t head_dim,
+                      const int32_t* tables, int64_t n_rows, int32_t width, const int32_t* rows,
+                      const int32_t* positions, const float* inv_freq, int32_t rotary, int32_t interleaved, void* q_out,
+                      int64_t q_out_token, int64_t q_out_head, void* k_out, int64_t k_out_token, int64_t k_out_head,
+                      void* stream);
+
+/* Pages of a cache.  Row r of tables holds ceil(lengths[r] / page_size) pages; refs[p] is
+ * the number of rows that hold page p, 0 for a free one.  All three are device int32 and
+ * the caller's; the calls below keep them in step, so that they can run ahead of the host.
+ * A call that needs pages takes the lowest free ones, for the rows in rising order; results
+ * are a function of the inputs alone.
+ *   pools    host array of the caches that belong to the pages (keys, values and scales of
+ *            all layers): base [planes x n_pages x page_bytes], page_bytes and base multiples
+ *            of 4 (16 for speed); at most MOE_MAX_POOLS
+ *   status   device int32 [n_rows], written for every row
+ *   workspace  >= moe_kv_pages_workspace_bytes(n_rows, n_pages), 256-byte aligned; it carries
+ *            nothing from one call to the next
+ * n_rows and n_pages are below 2^24 and 2^31, width is positive.  tables, lengths and refs
+ * that disagree give wrong pages, but page numbers outside [0, n_pages) are never followed.
+ * No buffer overlaps another.  n_rows = 0 is a no-op.  Ordered on `stream`; nothing is
+ * allocated.  Errors: MOE_E_SHAPE, MOE_E_ARG, MOE_E_SPACE, MOE_E_DEVICE. */
+enum { MOE_MAX_POOLS = 8 };
+typedef struct moe_kv_pool {
+  void* base;
+  int64_t planes;      /* layers, or 1 */
+  int64_t page_bytes;
+} moe_kv_pool;
+int64_t moe_kv_pages_workspace_bytes(int64_t n_rows, int64_t n_pages);
+
+/* Room for grow[r] (device int32 [n_rows]) more tokens in every row: new pages where the last
+ * one does not hold them, lengths[r] += grow[r].  status: the number of new pages; -1 if
+ * grow[r] is negative or the table too narrow; -2 if the free pages end before this row's
+ * (then it and every later row that needs one is left as it was). */
+int32_t moe_kv_reserve(int32_t* tables, int64_t n_rows, int32_t width, int32_t* lengths, int32_t* refs,
+                       int64_t n_pages, int32_t page_size, const int32_t* grow, int32_t* status, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
+/* Row r with parents[r] >= 0 (device int32 [n_rows]) becomes a copy of row parents[r]: it
+ * shares the full pages, and the last one, where it is partly filled, is copied to a page of
+ * its own in every pool.  status: the number of new pages (0 or 1), 0 for rows without a
+ * parent; -1 if the row is not empty (length 0), its parent is not a row or has a parent itself; -2 if the free
+ * pages end before this row's. */
+int32_t moe_kv_fork(int32_t* tables, int64_t n_rows, int32_t width, int32_t* lengths, int32_t* refs, int64_t n_pages,
+                    int32_t page_size, const int32_t* parents, const moe_kv_pool* pools, int32_t n_pools,
+                    int32_t* status, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Rows with drop[r] != 0 (device int32 [n_rows]) give their pages back and get length 0;
+ * their table entries stay. */
+int32_t moe_kv_free(const int32_t* tables, int64_t n_rows, int32_t width, int32_t* lengths, int32_t* refs,
+                    int64_t n_pages, int32_t page_size, const int32_t* drop, void* stream);
+
+/* The pages in use become pages 0 .. n - 1: those from n on move to the free ones below, both
+ * in rising order, in every pool.  new_tables [n_rows x width] and new_refs [n_pages] take
+ * the tables and counts after that (they may be tables and refs); entries behind a row's
+ * last page are copied.  live: device int32 [1], n.  The pages moved from keep their content. */
+int32_t moe_kv_compact(const int32_t* tables, int64_t n_rows, int32_t width, const int32_t* lengths,
+                       const int32_t* refs, int64_t n_pages, int32_t page_size, const moe_kv_pool* pools,
+                       int32_t n_pools, int32_t* new_tables, int32_t* new_refs, int32_t* live, void* workspace,
+                       int64_t workspace_bytes, void* stream);
+
+/* Page dst[i] becomes a copy of page src[i] (device int32 [n]) in every pool.  A pair with a
+ * number outside [0, n_pages) is passed over; no page is both a source and a destination, or
+ * a destination twice. */
+int32_t moe_kv_copy_pages(const moe_kv_pool* pools, int32_t n_pools, int64_t n_pages, const int32_t* src,
+                          const int32_t* dst, int64_t n, void* stream);
 
 /* Host: reorder the blocks of a [rows x cols] container (rows % 16 == 0,
  * cols % 128 == 0) between the row-major order moe_pack writes and the

@@ -25,7 +25,8 @@ routing and its own expert evaluation, written from the release pages:
   * the k=1 draft head (fc1, gelu, fc2): 35B-A3B card, "Shipped Components"
     (mtp.py);
   * the e4m3 quantizer, the residual RMS norm, the block-scaled product and the
-    sampler, from their formulas (fp8.py, sampler.py).
+    sampler, from their formulas (fp8.py, sampler.py);
+  * attention, the rotary embedding and the pages of a cache (attention.py).
 
 Where the pages are silent the readings are those listed in the package's design
 notes (two's-complement 2-bit codes, little-endian base-3 digits, SwiGLU,
@@ -33,4 +34,4 @@ softmax over the selected k, ties to the lower expert index, correction input =
 block input).  Everything is evaluated in float64 from the exact bits the GPU
 receives.
 """
-from . import codec, fp8, moe, mtp, ple, quant, sampler  # noqa: F401
+from . import attention, codec, fp8, moe, mtp, ple, quant, sampler  # noqa: F401

@@ -28,6 +28,9 @@ EXPORTS = [
     "moe_quantize_device", "moe_ple_gather_q4_0", "moe_ternary_forward_q", "moe_draft_head_workspace_bytes",
     "moe_draft_head", "moe_lowrank_workspace_bytes", "moe_lowrank_apply",
     "moe_fp8_quantize", "moe_rms_norm", "moe_fp8_linear", "moe_sample_workspace_bytes", "moe_sample",
+    "moe_attention_prefill", "moe_attention_decode_workspace_bytes", "moe_attention_decode", "moe_kv_append",
+    "moe_kv_pages_workspace_bytes", "moe_kv_reserve", "moe_kv_fork", "moe_kv_free", "moe_kv_compact",
+    "moe_kv_copy_pages",
     "moe_workspace_bytes_factored", "moe_ternary_forward_factored",
     "moe_tile_container", "moe_untile_container", "moe_workspace_bytes", "moe_ternary_forward", "moe_route_workspace_bytes", "moe_route",
     "moe_route_workspace_bytes_factored", "moe_route_factored", "moe_ternary_forward_noalloc",
@@ -55,6 +58,11 @@ class ExpertBanksC(ctypes.Structure):
     ]
 
 
+class KvPoolC(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("planes", ctypes.c_int64), ("page_bytes", ctypes.c_int64)]
+
+
+MAX_POOLS = 8
 BANKS_ROW_MAJOR, BANKS_TILE_MAJOR = 1, 2
 
 
@@ -88,6 +96,20 @@ def lib():
             "moe_fp8_linear": (i32, [vp, vp, i64, vp, vp, i64, i32, i32, vp, i64, vp]),
             "moe_sample_workspace_bytes": (i64, [i64, i32]),
             "moe_sample": (i32, [i32, vp, i64, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]),
+            "moe_attention_prefill": (i32, [i32, vp, i64, i32, i64, i64, vp, vp, i64, i32, i64, i64, i64, i64, i32, vp,
+                                            vp, i64, i32, ctypes.c_float, vp, vp, vp]),
+            "moe_attention_decode_workspace_bytes": (i64, [i64, i32, i32, i32]),
+            "moe_attention_decode": (i32, [i32, vp, i64, i32, i64, i64, i32, vp, vp, vp, vp, i64, i32, i32, i32, vp, i32,
+                                           vp, ctypes.c_float, vp, vp, vp, i64, vp]),
+            "moe_kv_append": (i32, [i32, vp, i64, i64, i32, vp, i64, i64, vp, i64, i64, i64, i32, vp, vp, vp, vp, i64,
+                                    i32, i32, i32, vp, i64, i32, vp, vp, vp, i32, i32, vp, i64, i64, vp, i64, i64,
+                                    vp]),
+            "moe_kv_pages_workspace_bytes": (i64, [i64, i64]),
+            "moe_kv_reserve": (i32, [vp, i64, i32, vp, vp, i64, i32, vp, vp, vp, i64, vp]),
+            "moe_kv_fork": (i32, [vp, i64, i32, vp, vp, i64, i32, vp, vp, i32, vp, vp, i64, vp]),
+            "moe_kv_free": (i32, [vp, i64, i32, vp, vp, i64, i32, vp, vp]),
+            "moe_kv_compact": (i32, [vp, i64, i32, vp, vp, i64, i32, vp, i32, vp, vp, vp, vp, i64, vp]),
+            "moe_kv_copy_pages": (i32, [vp, i32, i64, vp, vp, i64, vp]),
             "moe_workspace_bytes_factored": (i64, [ctypes.POINTER(ExpertBanksC), i64, i32, i32, i32]),
             "moe_ternary_forward_factored": (i32, [vp, i64, vp, vp, vp, i32, ctypes.POINTER(ExpertBanksC), vp, vp,
                                                    i32, i32, vp, vp, i64, vp]),
@@ -465,7 +487,7 @@ def _on(stream, device, *made):
     return stream.cuda_stream
 
 
-BF16, F16, F32 = 0, 1, 2
+BF16, F16, F32, E4M3 = 0, 1, 2, 3
 _TYPES = {}
 
 
@@ -483,6 +505,7 @@ def _types():
             i32s=(torch.int32,),
             quant={torch.bfloat16: BF16, torch.int16: BF16, torch.float16: F16},
             out={torch.bfloat16: BF16, torch.float32: F32},
+            heads={torch.bfloat16: BF16, torch.float16: F16},
             logits={torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32})
     return _TYPES
 
@@ -640,6 +663,317 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     if rc:
         _check(rc)
     return tokens, probs
+
+
+def _heads(name, t, device, dtype, heads=None, dim=None, tokens=None):
+    """(pointer, token stride, head stride) of [tokens, heads, dim] with contiguous heads."""
+    if t.get_device() != device:
+        raise MoeError(-1, f"{name} is on {t.device}, not on the current device cuda:{device}")
+    if t.dtype != dtype:
+        raise MoeError(-2, f"{name} has type {t.dtype}, {dtype} wanted")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim) or (
+            tokens is not None and t.shape[0] != tokens):
+        want = tuple("any" if x is None else x for x in (tokens, heads, dim))
+        raise MoeError(-3, f"{name} has shape {tuple(t.shape)}, {want} wanted")
+    n, h, d = t.shape
+    token, head, step = t.stride()
+    if step != 1 and d > 1 and n and h:
+        raise MoeError(-1, f"the heads of {name} are not contiguous")
+    head = head if h > 1 else d
+    return t.data_ptr(), token if n > 1 else h * d, head
+
+
+def _ints(name, t, device, T, size):
+    return _operand(name, t, device, T["i32s"], size)
+
+
+def _cache(k, v, k_scales, v_scales, device, dtype, T):
+    """(cache type, k, v, k_scales, v_scales, n_pages, kv_heads, page_size, dim) of a layer's cache."""
+    if k.dim() != 4:
+        raise MoeError(-3, f"k_cache has {k.dim()} dimensions, 4 wanted")
+    shape = k.shape
+    kind = T["heads"].get(k.dtype, E4M3 if k.dtype in T["codes"] else None)
+    kinds = T["codes"] if kind == E4M3 else (dtype,)
+    kp = _operand("k_cache", k, device, kinds, shape)
+    vp = _operand("v_cache", v, device, kinds, shape)
+    ksp = vsp = None
+    if kind == E4M3:
+        if k_scales is None or v_scales is None:
+            raise MoeError(-1, "an e4m3 cache needs k_scales and v_scales")
+        ksp = _operand("k_scales", k_scales, device, T["f32s"], shape[:3])
+        vsp = _operand("v_scales", v_scales, device, T["f32s"], shape[:3])
+    elif k_scales is not None or v_scales is not None:
+        raise MoeError(-1, "k_scales and v_scales go with e4m3 caches only")
+    return kind, kp, vp, ksp, vsp, shape[0], shape[1], shape[2], shape[3]
+
+
+def attention_prefill(q, k, v, starts, k_starts=None, causal: bool = True, scale: Optional[float] = None, y=None,
+                      lse=None, stream=None):
+    """Attention of packed sequences: q [tokens, heads, dim], k and v [k tokens, kv heads,
+    dim], bf16 or fp16, dim 64, 128 or 256; heads are contiguous, tokens and heads may be
+    strided (parts of one projection's rows).  starts int32 [sequences + 1]: where each
+    sequence's queries begin; k_starts likewise for its keys (None: starts).  causal: query
+    i of lq sees the keys up to i + lk - lq of lk.  scale None: dim ** -0.5.  lse: an fp32
+    buffer [tokens, heads] for the logarithms of the softmax sums.  -> y [tokens, heads,
+    dim]; tokens outside every sequence are not written."""
+    T = _types()
+    dev = _current(q, T)
+    kind = T["heads"].get(q.dtype)
+    if kind is None:
+        raise MoeError(-2, f"q has type {q.dtype}")
+    qp, q_token, q_head = _heads("q", q, dev, q.dtype)
+    n, H, D = q.shape
+    kp, k_token, k_head = _heads("k", k, dev, q.dtype, None, D)
+    m, Hk, _ = k.shape
+    vp, v_token, v_head = _heads("v", v, dev, q.dtype, Hk, D, m)
+    size = starts.shape
+    if len(size) != 1 or size[0] < 1:
+        raise MoeError(-3, f"starts has shape {tuple(size)}, one more than the sequences wanted")
+    sp = _ints("starts", starts, dev, T, size)
+    ksp = None if k_starts is None else _ints("k_starts", k_starts, dev, T, size)
+    if y is None:
+        y = q.new_empty((n, H, D))
+        yp = y.data_ptr()
+    else:
+        yp = _operand("y", y, dev, (q.dtype,), (n, H, D))
+    lp = None if lse is None else _operand("lse", lse, dev, T["f32s"], (n, H))
+    rc = lib().moe_attention_prefill(kind, qp, n, H, q_token, q_head, kp, vp, m, Hk, k_token, k_head, v_token, v_head, D,
+                                     sp, ksp, size[0] - 1, causal, D ** -0.5 if scale is None else scale, yp, lp,
+                                     T["stream"](dev) if stream is None else _on(stream, dev, y))
+    if rc:
+        _check(rc)
+    return y
+
+
+def attention_decode(q, k_cache, v_cache, tables, lengths, k_scales=None, v_scales=None, scale: Optional[float] = None,
+                     y=None, lse=None, workspace=None, stream=None):
+    """Attention of one new token of every sequence over its cached ones: q [batch, heads,
+    dim] (strided as attention_prefill's), a layer's cache k_cache, v_cache [pages, kv heads,
+    page, dim] of q's type or e4m3 with fp32 scales [pages, kv heads, page], tables int32
+    [batch, width] of page numbers, lengths int32 [batch] (the new token included).
+    -> y [batch, heads, dim]."""
+    T = _types()
+    dev = _current(q, T)
+    kind = T["heads"].get(q.dtype)
+    if kind is None:
+        raise MoeError(-2, f"q has type {q.dtype}")
+    qp, q_row, q_head = _heads("q", q, dev, q.dtype)
+    B, H, D = q.shape
+    ck, kp, vp, ksp, vsp, pages, Hk, P, cd = _cache(k_cache, v_cache, k_scales, v_scales, dev, q.dtype, T)
+    if cd != D:
+        raise MoeError(-3, f"the cache has dim {cd}, q has {D}")
+    width = tables.shape[1] if tables.dim() == 2 else -1
+    tp = _ints("tables", tables, dev, T, (B, width))
+    lenp = _ints("lengths", lengths, dev, T, (B,))
+    if y is None:
+        y = q.new_empty((B, H, D))
+        yp = y.data_ptr()
+    else:
+        yp = _operand("y", y, dev, (q.dtype,), (B, H, D))
+    lp = None if lse is None else _operand("lse", lse, dev, T["f32s"], (B, H))
+    L = lib()
+    if workspace is None:
+        need = L.moe_attention_decode_workspace_bytes(B, H, Hk, D)
+        if need < 0:
+            raise MoeError(-3, f"invalid attention shape batch={B} heads={H} kv_heads={Hk} dim={D}")
+        workspace = q.new_empty(need + 256, dtype=T["u8"])
+    elif workspace.get_device() != dev:
+        raise MoeError(-1, f"the workspace is on {workspace.device}, not on the current device cuda:{dev}")
+    ws, wn = _aligned(workspace)
+    rc = L.moe_attention_decode(kind, qp, B, H, q_row, q_head, ck, kp, vp, ksp, vsp, pages, Hk, P, D, tp, width, lenp,
+                                D ** -0.5 if scale is None else scale, yp, lp, ws, wn,
+                                T["stream"](dev) if stream is None else _on(stream, dev, y, workspace))
+    if rc:
+        _check(rc)
+    return y
+
+
+def kv_append(k, v, k_cache, v_cache, tables, rows, positions, k_scales=None, v_scales=None, q=None, inv_freq=None,
+              interleaved: bool = False, rotated_k: bool = False, q_out=None, k_out=None, stream=None):
+    """New keys and values k, v [tokens, kv heads, dim] (strided as attention_prefill's) into
+    the pages of a layer's cache (attention_decode's), token t at place positions[t] of row
+    rows[t] of tables (int32; a row below 0 is padding and left alone).  With inv_freq (fp32
+    [n]) the first 2 n channels of every head of k, and of q [tokens, heads, dim] if given, are
+    turned by positions * inv_freq first: channels i and i + n, or 2 i and 2 i + 1
+    (interleaved).  Returns a dict: "q" (turned q; with q) and "k" (turned k; rotated_k=True or
+    a k_out).  q_out, k_out: buffers for them, which may be q and k themselves."""
+    T = _types()
+    dev = _current(k, T)
+    kind = T["heads"].get(k.dtype)
+    if kind is None:
+        raise MoeError(-2, f"k has type {k.dtype}")
+    kp, k_token, k_head = _heads("k", k, dev, k.dtype)
+    n, Hk, D = k.shape
+    vp, v_token, v_head = _heads("v", v, dev, k.dtype, Hk, D, n)
+    ck, kcp, vcp, ksp, vsp, pages, ch, P, cd = _cache(k_cache, v_cache, k_scales, v_scales, dev, k.dtype, T)
+    if ch != Hk or cd != D:
+        raise MoeError(-3, f"the cache has {ch} heads of {cd}, k has {Hk} of {D}")
+    if tables.dim() != 2:
+        raise MoeError(-3, f"tables has {tables.dim()} dimensions, 2 wanted")
+    tp = _ints("tables", tables, dev, T, tables.shape)
+    rp = _ints("rows", rows, dev, T, (n,))
+    pp = _ints("positions", positions, dev, T, (n,))
+    out = {}
+    fp = qp = qop = kop = None
+    H = rotary = q_token = q_head = qo_token = qo_head = ko_token = ko_head = 0
+    if inv_freq is not None:
+        rotary = 2 * inv_freq.numel()
+        fp = _operand("inv_freq", inv_freq, dev, T["f32s"], (rotary // 2,))
+    if q is not None:
+        qp, q_token, q_head = _heads("q", q, dev, k.dtype, None, D, n)
+        H = q.shape[1]
+        if q_out is None:
+            q_out = q.new_empty((n, H, D))
+        qop, qo_token, qo_head = _heads("q_out", q_out, dev, k.dtype, H, D, n)
+        out["q"] = q_out
+    elif q_out is not None:
+        raise MoeError(-1, "q_out needs a q")
+    if rotated_k or k_out is not None:
+        if k_out is None:
+            k_out = k.new_empty((n, Hk, D))
+        kop, ko_token, ko_head = _heads("k_out", k_out, dev, k.dtype, Hk, D, n)
+        out["k"] = k_out
+    rc = lib().moe_kv_append(kind, qp, q_token, q_head, H, kp, k_token, k_head, vp, v_token, v_head, n, ck, kcp, vcp, ksp,
+                             vsp, pages, Hk, P, D, tp, tables.shape[0], tables.shape[1], rp, pp, fp, rotary, interleaved,
+                             qop, qo_token, qo_head, kop, ko_token, ko_head,
+                             T["stream"](dev) if stream is None else _on(stream, dev, *out.values()))
+    if rc:
+        _check(rc)
+    return out
+
+
+def _pools(pools, device, n_pages):
+    """(moe_kv_pool array, count) of cache tensors [layers, pages, ...] or a list of them."""
+    c = (KvPoolC * MAX_POOLS)()
+    if len(pools) > MAX_POOLS:
+        raise MoeError(-1, f"{len(pools)} pools, at most {MAX_POOLS} wanted")
+    for i, p in enumerate(pools):
+        if p.get_device() != device:
+            raise MoeError(-1, f"pool {i} is on {p.device}, not on the current device cuda:{device}")
+        if p.dim() < 3 or p.shape[1] != n_pages:
+            raise MoeError(-3, f"pool {i} has shape {tuple(p.shape)}, (layers, {n_pages}, ...) wanted")
+        if not p.is_contiguous():
+            raise MoeError(-1, f"pool {i} is not contiguous")
+        c[i].base, c[i].planes = p.data_ptr(), p.shape[0]
+        c[i].page_bytes = p.stride(1) * p.element_size()
+    return c, len(pools)
+
+
+def _pages(tables, lengths, refs, T):
+    """(device, leading arguments) of a call on the pages of a cache."""
+    dev = _current(tables, T)
+    if tables.dim() != 2 or refs.dim() != 1:
+        raise MoeError(-3, f"tables has {tables.dim()} dimensions and refs {refs.dim()}, 2 and 1 wanted")
+    R, W = tables.shape
+    n = refs.shape[0]
+    return dev, R, n, (_ints("tables", tables, dev, T, (R, W)), R, W, _ints("lengths", lengths, dev, T, (R,)),
+                       _ints("refs", refs, dev, T, (n,)), n)
+
+
+def _pages_space(workspace, like, R, n, T):
+    if workspace is None:
+        need = lib().moe_kv_pages_workspace_bytes(R, n)
+        if need < 0:
+            raise MoeError(-3, f"invalid cache shape rows={R} pages={n}")
+        workspace = like.new_empty(need + 256, dtype=T["u8"])
+    elif workspace.get_device() != like.get_device():
+        raise MoeError(-1, f"the workspace is on {workspace.device}, not on {like.device}")
+    return (workspace, *_aligned(workspace))
+
+
+def _status(status, like, dev, R, T):
+    if status is None:
+        status = like.new_empty((R,))
+    return status, _ints("status", status, dev, T, (R,))
+
+
+def kv_reserve(tables, lengths, refs, grow, page_size: int, status=None, workspace=None, stream=None):
+    """Room for grow[r] more tokens in row r of tables (int32 [rows, width]): new pages, the
+    lowest free ones, where the row's last does not hold them, and lengths[r] += grow[r].
+    refs int32 [pages] counts the rows that hold a page.  -> status int32 [rows]: new pages, -1
+    for a negative grow or a table too narrow, -2 where the free pages did not reach."""
+    T = _types()
+    dev, R, n, head = _pages(tables, lengths, refs, T)
+    gp = _ints("grow", grow, dev, T, (R,))
+    status, sp = _status(status, lengths, dev, R, T)
+    workspace, ws, wn = _pages_space(workspace, tables, R, n, T)
+    rc = lib().moe_kv_reserve(*head, page_size, gp, sp, ws, wn,
+                              T["stream"](dev) if stream is None else _on(stream, dev, status, workspace))
+    if rc:
+        _check(rc)
+    return status
+
+
+def kv_fork(tables, lengths, refs, parents, page_size: int, pools, status=None, workspace=None, stream=None):
+    """Every row r with parents[r] >= 0 (int32 [rows]), which has to be empty, becomes a copy of
+    that row: full pages are shared, a partly filled last one is copied in every pool
+    (cache tensors [layers, pages, ...]).  -> status int32 [rows]: new pages (0 or 1), -1 for a
+    row or parent that does not do, -2 where the free pages did not reach."""
+    T = _types()
+    dev, R, n, head = _pages(tables, lengths, refs, T)
+    pp = _ints("parents", parents, dev, T, (R,))
+    status, sp = _status(status, lengths, dev, R, T)
+    c, count = _pools(pools, dev, n)
+    workspace, ws, wn = _pages_space(workspace, tables, R, n, T)
+    rc = lib().moe_kv_fork(*head, page_size, pp, c, count, sp, ws, wn,
+                           T["stream"](dev) if stream is None else _on(stream, dev, status, workspace))
+    if rc:
+        _check(rc)
+    return status
+
+
+def kv_free(tables, lengths, refs, drop, page_size: int, stream=None):
+    """The rows with drop[r] != 0 (int32 [rows]) give their pages back and get length 0."""
+    T = _types()
+    dev, R, n, head = _pages(tables, lengths, refs, T)
+    dp = _ints("drop", drop, dev, T, (R,))
+    rc = lib().moe_kv_free(*head, page_size, dp, T["stream"](dev) if stream is None else _on(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def kv_compact(tables, lengths, refs, page_size: int, pools, new_tables=None, new_refs=None, live=None, workspace=None,
+               stream=None):
+    """The n pages in use become pages 0 .. n - 1 of every pool (cache tensors [layers, pages,
+    ...]); those above move to the free ones below.  -> (new_tables, new_refs, live), live
+    int32 [1] = n; new_tables and new_refs may be tables and refs themselves."""
+    T = _types()
+    dev, R, n, head = _pages(tables, lengths, refs, T)
+    if new_tables is None:
+        new_tables = T["like"](tables)
+    if new_refs is None:
+        new_refs = T["like"](refs)
+    if live is None:
+        live = refs.new_empty((1,))
+    tp = _ints("new_tables", new_tables, dev, T, tables.shape)
+    rp = _ints("new_refs", new_refs, dev, T, (n,))
+    lp = _ints("live", live, dev, T, (1,))
+    c, count = _pools(pools, dev, n)
+    workspace, ws, wn = _pages_space(workspace, tables, R, n, T)
+    rc = lib().moe_kv_compact(*head, page_size, c, count, tp, rp, lp, ws, wn,
+                              T["stream"](dev) if stream is None else _on(stream, dev, new_tables, new_refs, live,
+                                                                          workspace))
+    if rc:
+        _check(rc)
+    return new_tables, new_refs, live
+
+
+def kv_copy_pages(pools, src, dst, stream=None):
+    """Page dst[i] becomes a copy of page src[i] (int32) in every pool [layers, pages, ...]."""
+    T = _types()
+    dev = _current(src, T)
+    size = src.shape
+    if len(size) != 1:
+        raise MoeError(-3, f"src has shape {tuple(size)}, one dimension wanted")
+    sp, dp = _ints("src", src, dev, T, size), _ints("dst", dst, dev, T, size)
+    if not pools:
+        return
+    n = pools[0].shape[1] if pools[0].dim() > 1 else 0
+    c, count = _pools(pools, dev, n)
+    rc = lib().moe_kv_copy_pages(c, count, n, sp, dp, size[0],
+                                 T["stream"](dev) if stream is None else _on(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def _route_outputs(T, n_experts, top_k, dev):

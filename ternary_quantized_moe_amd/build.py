@@ -13,7 +13,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmoe_ternary.so")
 OBJ = os.path.join(PKG, "_build")
-SOURCES = ["host_codec.cpp", "moe_capi.hip", "moe_kernels.hip", "moe_experts.hip", "moe_dense.hip", "moe_quant.hip", "moe_ple.hip", "moe_mtp.hip", "moe_router_delta.hip", "moe_norm.hip", "moe_fp8_linear.hip", "moe_sample.hip"]
+SOURCES = ["host_codec.cpp", "moe_capi.hip", "moe_kernels.hip", "moe_experts.hip", "moe_dense.hip", "moe_quant.hip", "moe_ple.hip", "moe_mtp.hip", "moe_router_delta.hip", "moe_norm.hip", "moe_fp8_linear.hip", "moe_sample.hip", "moe_attention.hip", "moe_decode.hip", "moe_kv_cache.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -1,0 +1,76 @@
+// Device helpers of the attention kernels: matrix-core wrappers for 16-bit values of
+// either kind, their conversion from fp32, and LDS reads that transpose.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_common.h"
+
+namespace moe {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+// 16-bit values of one kind: their products, their rounding (nearest even), their ones
+// and the bits that all are set in an infinity or a NaN.
+template <bool F16>
+struct Half {
+  static constexpr uint32_t kOne = F16 ? 0x3C00 : 0x3F80, kExponent = F16 ? 0x7C00 : 0x7F80;
+  // D = A(32 x 16) B(16 x 32) + C.  Lane l supplies row l % 32 of A and column l % 32 of
+  // B, k 8 (l / 32) .. + 7; it holds column l % 32 of D, row 8 (i / 4) + 4 (l / 32) + i % 4 in element i.
+  static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    if constexpr (F16)
+      return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                    0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                     0, 0, 0);
+  }
+  // D = A(16 x 32) B(32 x 16) + C.  Lane l supplies row l % 16 of A and column l % 16 of B,
+  // k 8 (l / 16) .. + 7; it holds column l % 16 of D, row 4 (l / 16) + i in element i.
+  static __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
+    if constexpr (F16)
+      return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                    0, 0);
+    else
+      return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                     0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    if constexpr (F16)
+      return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){lo, hi}, f16x2_t));
+    else
+      return f32x2_to_bf16x2(lo, hi);
+  }
+  static __device__ __forceinline__ float widen(uint32_t bits) {
+    return F16 ? f16_to_f32(bits & 0xFFFFu) : __uint_as_float(bits << 16);
+  }
+};
+
+// The other half of the wave: both halves' values of v, the lower lanes' first.
+__device__ __forceinline__ f32x2_t both_halves(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return f32x2_t{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+
+// Reads four rows of 16 values transposed: within 16 lanes, lane i gives the address of
+// values 4 (i % 4) .. + 3 of row i / 4 and gets value i of the four rows.
+__device__ __forceinline__ u32x2 read_transposed(const uint8_t* p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                       (__attribute__((address_space(3))) s16x4*)(p)));
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_from(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, -1, 0x00027000);
+}
+// 16 bytes a lane to LDS, lane after lane from dst on.
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t src, uint32_t lane_off, uint8_t* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void*)dst, 16, (int)lane_off, 0, 0, 0);
+}
+
+}  // namespace moe

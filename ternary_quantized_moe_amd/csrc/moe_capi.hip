@@ -9,10 +9,12 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 
 #include "moe_ternary.h"
+#include "attention_internal.h"
 #include "fp8_internal.h"
 #include "host_error.h"
 #include "moe_internal.h"
@@ -481,6 +483,381 @@ int32_t moe_sample(int32_t type, const void* logits, int64_t batch, int32_t voca
   const hipError_t e = moe::launch_sample(
       t, {logits, batch, vocab, ld, temperature, top_k, top_p, min_p, u, tokens, probs}, ws, (hipStream_t)stream);
   if (e != hipSuccess) return device_fail(e, "moe_sample launch");
+  return ok();
+}
+
+// ------------------------------------------------------- attention and its cache
+namespace {
+
+struct Bytes {
+  const void* p;
+  int64_t n;
+};
+// Whether one of the first `out` ranges shares a byte with another range.
+bool collide(std::initializer_list<Bytes> ranges, int out) {
+  const Bytes* r = ranges.begin();
+  for (int i = 0; i < out; ++i)
+    for (int j = i + 1; j < (int)ranges.size(); ++j)
+      if (overlaps(r[i].p, r[i].n, r[j].p, r[j].n)) return true;
+  return false;
+}
+
+Bytes extent(const moe::HeadRows& x, int64_t tokens, int heads, int D) {
+  return {x.p, tokens > 0 ? ((tokens - 1) * x.token + (heads - 1) * x.head + D) * 2 : 0};
+}
+// Whether two matrices of heads share no value: apart, or side by side in the rows of one
+// matrix.
+bool apart(const moe::HeadRows& a, int ha, const moe::HeadRows& b, int hb, int64_t tokens, int D) {
+  const Bytes x = extent(a, tokens, ha, D), y = extent(b, tokens, hb, D);
+  if (!overlaps(x.p, x.n, y.p, y.n)) return true;
+  if (a.token != b.token || a.token <= 0) return false;
+  const int64_t d = (((const char*)b.p - (const char*)a.p) % (2 * a.token) + 2 * a.token) % (2 * a.token);
+  return d >= ((ha - 1) * a.head + D) * 2 && 2 * a.token - d >= ((hb - 1) * b.head + D) * 2;
+}
+
+bool half_type(int32_t type) { return type == MOE_BF16 || type == MOE_F16; }
+int32_t bad_type(int32_t type) { return fail(MOE_E_FORMAT, "type %d is neither MOE_BF16 nor MOE_F16", (int)type); }
+
+int32_t check_heads(int32_t heads, int32_t kv_heads, int32_t D) {
+  if (D != 64 && D != 128 && D != 256) return fail(MOE_E_SHAPE, "head_dim %d is none of 64, 128 and 256", (int)D);
+  if (kv_heads < 1 || heads < 1 || heads > moe::kAttnMaxHeads || heads % kv_heads)
+    return fail(MOE_E_SHAPE, "heads %d must be a multiple of kv_heads %d, up to %d", (int)heads, (int)kv_heads,
+                moe::kAttnMaxHeads);
+  return MOE_OK;
+}
+
+// Strides of a matrix of heads: heads and tokens do not share values.
+int32_t check_rows(const char* name, const moe::HeadRows& x, int64_t tokens, int heads, int D) {
+  if (x.token < 0 || x.head < 0 || x.token > moe::kAttnMaxStride || x.head > moe::kAttnMaxStride || x.token % 8 || x.head % 8)
+    return fail(MOE_E_SHAPE, "strides %lld and %lld of %s must be multiples of 8 up to 2^24", (long long)x.token,
+                (long long)x.head, name);
+  if ((heads > 1 && x.head < D) || (tokens > 1 && x.token < D))
+    return fail(MOE_E_SHAPE, "strides %lld and %lld of %s are below head_dim %d", (long long)x.token, (long long)x.head,
+                name, D);
+  if (!x.p) return fail(MOE_E_ARG, "NULL pointer (%s)", name);
+  if ((uintptr_t)x.p % 16) return fail(MOE_E_ARG, "%s must be 16-byte aligned", name);
+  return MOE_OK;
+}
+// An output's tokens and heads must not lie in each other either.
+bool dense_rows(const moe::HeadRows& x, int64_t tokens, int heads, int D) {
+  return tokens <= 1 || heads <= 1 || x.token >= (heads - 1) * x.head + D || x.head >= (tokens - 1) * x.token + D;
+}
+
+int32_t check_cache(int32_t type, int32_t cache_type, const moe::CacheArgs& c) {
+  if (cache_type != type && cache_type != MOE_E4M3)
+    return fail(MOE_E_FORMAT, "cache type %d is neither the type %d nor MOE_E4M3", (int)cache_type, (int)type);
+  if (c.P < 1 || c.P > moe::kMaxPage || (c.P & (c.P - 1)))
+    return fail(MOE_E_SHAPE, "page_size %d is not a power of two up to %d", c.P, moe::kMaxPage);
+  if (c.n_pages < 1 || c.n_pages > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "n_pages %lld outside [1, 2^31)", (long long)c.n_pages);
+  if (c.width < 0) return fail(MOE_E_SHAPE, "negative table width %d", c.width);
+  if (c.kv_heads > moe::kAttnMaxHeads) return fail(MOE_E_SHAPE, "kv_heads %d above %d", c.kv_heads, moe::kAttnMaxHeads);
+  if (!c.k || !c.v || (!c.tables && c.width > 0)) return fail(MOE_E_ARG, "NULL pointer (cache or tables)");
+  if ((cache_type == MOE_E4M3) != (c.k_scales != nullptr) || (cache_type == MOE_E4M3) != (c.v_scales != nullptr))
+    return fail(MOE_E_ARG, "k_scales and v_scales go with MOE_E4M3 caches, and only with these");
+  if ((uintptr_t)c.k % 16 || (uintptr_t)c.v % 16 || (uintptr_t)c.k_scales % 4 || (uintptr_t)c.v_scales % 4 ||
+      (uintptr_t)c.tables % 4)
+    return fail(MOE_E_ARG, "caches must be 16-byte, scales and tables 4-byte aligned");
+  return MOE_OK;
+}
+int64_t cache_rows(const moe::CacheArgs& c) { return c.n_pages * c.kv_heads * c.P; }
+int64_t cache_bytes(const moe::CacheArgs& c) { return cache_rows(c) * c.D * (c.k_scales ? 1 : 2); }
+int64_t scale_bytes(const moe::CacheArgs& c) { return c.k_scales ? 4 * cache_rows(c) : 0; }
+int log2_of(int v) { return 31 - __builtin_clz((unsigned)v); }
+
+bool good_scale(float scale) { return scale > 0.f && !std::isinf(scale); }
+
+}  // namespace
+
+int32_t moe_attention_prefill(int32_t type, const void* q, int64_t q_tokens, int32_t heads, int64_t q_token,
+                              int64_t q_head, const void* k, const void* v, int64_t k_tokens, int32_t kv_heads,
+                              int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, int32_t head_dim,
+                              const int32_t* q_starts, const int32_t* k_starts, int64_t n_seqs, int32_t causal,
+                              float scale, void* y, float* lse, void* stream) {
+  if (!half_type(type)) return bad_type(type);
+  if (const int32_t rc = check_heads(heads, kv_heads, head_dim)) return rc;
+  if (q_tokens < 0 || k_tokens < 0 || q_tokens > moe::kAttnMaxTokens || k_tokens > moe::kAttnMaxTokens)
+    return fail(MOE_E_SHAPE, "token counts %lld and %lld outside [0, 2^31)", (long long)q_tokens, (long long)k_tokens);
+  if (n_seqs < 0 || n_seqs > (1 << 22)) return fail(MOE_E_SHAPE, "sequence count %lld outside [0, 2^22]", (long long)n_seqs);
+  if (!good_scale(scale)) return fail(MOE_E_ARG, "scale must be finite and positive");
+  if (q_tokens == 0 || n_seqs == 0) return ok();
+  moe::PrefillArgs a{{(const uint16_t*)q, q_token, q_head}, {(const uint16_t*)k, k_token, k_head},
+                     {(const uint16_t*)v, v_token, v_head}, q_tokens, k_tokens, heads, kv_heads, head_dim,
+                     q_starts, k_starts ? k_starts : q_starts, n_seqs, causal != 0, type == MOE_F16, scale,
+                     (uint16_t*)y, lse};
+  if (const int32_t rc = check_rows("q", a.q, q_tokens, heads, head_dim)) return rc;
+  if (k_tokens > 0) {
+    if (const int32_t rc = check_rows("k", a.k, k_tokens, kv_heads, head_dim)) return rc;
+    if (const int32_t rc = check_rows("v", a.v, k_tokens, kv_heads, head_dim)) return rc;
+  }
+  if (!q_starts || !y) return fail(MOE_E_ARG, "NULL pointer (q_starts or y)");
+  if ((uintptr_t)y % 16 || (uintptr_t)lse % 4 || (uintptr_t)q_starts % 4 || (uintptr_t)k_starts % 4)
+    return fail(MOE_E_ARG, "y must be 16-byte, lse and the starts 4-byte aligned");
+  if (moe::prefill_blocks(a) > ((int64_t)1 << 36))
+    return fail(MOE_E_SHAPE, "%lld tokens of %d heads exceed one launch", (long long)q_tokens, (int)heads);
+  if (collide({{y, q_tokens * heads * head_dim * 2}, {lse, q_tokens * heads * 4}, extent(a.q, q_tokens, heads, head_dim),
+               extent(a.k, k_tokens, kv_heads, head_dim), extent(a.v, k_tokens, kv_heads, head_dim),
+               {q_starts, 4 * (n_seqs + 1)}, {k_starts, 4 * (n_seqs + 1)}}, 2))
+    return fail(MOE_E_ARG, "y or lse overlaps the other or an input");
+  const hipError_t e = moe::launch_attention_prefill(a, (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_attention_prefill launch");
+  return ok();
+}
+
+int64_t moe_attention_decode_workspace_bytes(int64_t batch, int32_t heads, int32_t kv_heads, int32_t head_dim) {
+  if (batch < 0 || batch > moe::kAttnMaxBatch || check_heads(heads, kv_heads, head_dim)) return -1;
+  return moe::decode_workspace_bytes(batch, heads, kv_heads, head_dim);
+}
+
+int32_t moe_attention_decode(int32_t type, const void* q, int64_t batch, int32_t heads, int64_t q_row, int64_t q_head,
+                             int32_t cache_type, const void* k, const void* v, const float* k_scales,
+                             const float* v_scales, int64_t n_pages, int32_t kv_heads, int32_t page_size,
+                             int32_t head_dim, const int32_t* tables, int32_t width, const int32_t* lengths,
+                             float scale, void* y, float* lse, void* ws, int64_t ws_bytes, void* stream) {
+  if (!half_type(type)) return bad_type(type);
+  if (const int32_t rc = check_heads(heads, kv_heads, head_dim)) return rc;
+  if (batch < 0 || batch > moe::kAttnMaxBatch)
+    return fail(MOE_E_SHAPE, "batch %lld outside [0, %lld]", (long long)batch, (long long)moe::kAttnMaxBatch);
+  if (!good_scale(scale)) return fail(MOE_E_ARG, "scale must be finite and positive");
+  if (batch == 0) return ok();
+  moe::DecodeArgs a{{(const uint16_t*)q, q_row, q_head}, batch, heads,
+                    {k, v, k_scales, v_scales, n_pages, kv_heads, page_size, page_size > 0 ? log2_of(page_size) : 0,
+                     head_dim, tables, batch, width},
+                    lengths, type == MOE_F16, scale, (uint16_t*)y, lse};
+  if (const int32_t rc = check_cache(type, cache_type, a.c)) return rc;
+  if (const int32_t rc = check_rows("q", a.q, batch, heads, head_dim)) return rc;
+  if (!lengths || !y) return fail(MOE_E_ARG, "NULL pointer (lengths or y)");
+  if ((uintptr_t)y % 16 || (uintptr_t)lse % 4 || (uintptr_t)lengths % 4)
+    return fail(MOE_E_ARG, "y must be 16-byte, lse and lengths 4-byte aligned");
+  const int64_t need = moe::decode_workspace_bytes(batch, heads, kv_heads, head_dim);
+  if (need && !ws) return fail(MOE_E_ARG, "NULL workspace");
+  if ((uintptr_t)ws % kAlign) return fail(MOE_E_ARG, "workspace must be 256-byte aligned");
+  if (ws_bytes < need)
+    return fail(MOE_E_SPACE, "workspace holds %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
+  if (collide({{y, batch * heads * head_dim * 2}, {lse, batch * heads * 4}, {ws, need},
+               extent(a.q, batch, heads, head_dim), {k, cache_bytes(a.c)}, {v, cache_bytes(a.c)},
+               {k_scales, scale_bytes(a.c)}, {v_scales, scale_bytes(a.c)}, {tables, 4 * batch * width},
+               {lengths, 4 * batch}}, 3))
+    return fail(MOE_E_ARG, "y, lse and the workspace must not overlap each other or an input");
+  const hipError_t e = moe::launch_attention_decode(a, ws, (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_attention_decode launch");
+  return ok();
+}
+
+int32_t moe_kv_append(int32_t type, const void* q, int64_t q_token, int64_t q_head, int32_t heads, const void* k,
+                      int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head, int64_t T,
+                      int32_t cache_type, void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                      int64_t n_pages, int32_t kv_heads, int32_t page_size, int32_t head_dim, const int32_t* tables,
+                      int64_t n_rows, int32_t width, const int32_t* rows, const int32_t* positions,
+                      const float* inv_freq, int32_t rotary, int32_t interleaved, void* q_out, int64_t q_out_token,
+                      int64_t q_out_head, void* k_out, int64_t k_out_token, int64_t k_out_head, void* stream) {
+  if (!half_type(type)) return bad_type(type);
+  if (const int32_t rc = check_heads(q ? heads : kv_heads, kv_heads, head_dim)) return rc;
+  if (T < 0 || T > moe::kAttnMaxTokens) return fail(MOE_E_SHAPE, "token count %lld outside [0, 2^31)", (long long)T);
+  if (n_rows < 1 || n_rows > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "row count %lld outside [1, 2^31)", (long long)n_rows);
+  if (rotary < 0 || rotary % 16 || rotary > head_dim)
+    return fail(MOE_E_SHAPE, "rotary %d is not a multiple of 16 up to head_dim %d", (int)rotary, (int)head_dim);
+  if ((rotary > 0) != (inv_freq != nullptr)) return fail(MOE_E_ARG, "inv_freq and rotary go together");
+  if ((q != nullptr) != (q_out != nullptr)) return fail(MOE_E_ARG, "q and q_out go together");
+  if (q && !rotary) return fail(MOE_E_ARG, "q is only turned: it needs inv_freq");
+  if (T == 0) return ok();
+  moe::AppendArgs a{{(const uint16_t*)q, q_token, q_head}, {(const uint16_t*)k, k_token, k_head},
+                    {(const uint16_t*)v, v_token, v_head}, T, heads,
+                    {k_cache, v_cache, k_scales, v_scales, n_pages, kv_heads, page_size,
+                     page_size > 0 ? log2_of(page_size) : 0, head_dim, tables, n_rows, width},
+                    rows, positions, inv_freq, rotary, interleaved != 0, type == MOE_F16,
+                    {(const uint16_t*)q_out, q_out_token, q_out_head}, {(const uint16_t*)k_out, k_out_token, k_out_head}};
+  if (const int32_t rc = check_cache(type, cache_type, a.c)) return rc;
+  if (q) {
+    if (const int32_t rc = check_rows("q", a.q, T, heads, head_dim)) return rc;
+    if (const int32_t rc = check_rows("q_out", a.q_out, T, heads, head_dim)) return rc;
+  }
+  if (const int32_t rc = check_rows("k", a.k, T, kv_heads, head_dim)) return rc;
+  if (const int32_t rc = check_rows("v", a.v, T, kv_heads, head_dim)) return rc;
+  if (k_out)
+    if (const int32_t rc = check_rows("k_out", a.k_out, T, kv_heads, head_dim)) return rc;
+  if ((q && !dense_rows(a.q_out, T, heads, head_dim)) || (k_out && !dense_rows(a.k_out, T, kv_heads, head_dim)))
+    return fail(MOE_E_SHAPE, "the strides of q_out or k_out make it overlap itself");
+  if (!rows || !positions) return fail(MOE_E_ARG, "NULL pointer (rows or positions)");
+  if ((uintptr_t)rows % 4 || (uintptr_t)positions % 4 || (uintptr_t)inv_freq % 4)
+    return fail(MOE_E_ARG, "rows, positions and inv_freq must be 4-byte aligned");
+  const Bytes qx = extent(a.q, T, heads, head_dim), kx = extent(a.k, T, kv_heads, head_dim),
+              vx = extent(a.v, T, kv_heads, head_dim), qo = extent(a.q_out, T, heads, head_dim),
+              ko = extent(a.k_out, T, kv_heads, head_dim);
+  const Bytes tab{tables, 4 * n_rows * width}, row{rows, 4 * T}, pos{positions, 4 * T}, inv{inv_freq, 2 * (int64_t)rotary};
+  if (collide({{k_cache, cache_bytes(a.c)}, {v_cache, cache_bytes(a.c)}, {k_scales, scale_bytes(a.c)},
+               {v_scales, scale_bytes(a.c)}, qx, kx, vx, qo, ko, tab, row, pos, inv}, 4) ||
+      collide({qo, tab, row, pos, inv}, 1) || collide({ko, tab, row, pos, inv}, 1))
+    return fail(MOE_E_ARG, "an output overlaps another or an input");
+  auto same = [](const moe::HeadRows& x, const moe::HeadRows& y) {
+    return x.p == y.p && x.token == y.token && x.head == y.head;
+  };
+  const bool q_ok = !q || ((same(a.q_out, a.q) || apart(a.q_out, heads, a.q, heads, T, head_dim)) &&
+                           apart(a.q_out, heads, a.k, kv_heads, T, head_dim) &&
+                           apart(a.q_out, heads, a.v, kv_heads, T, head_dim));
+  const bool k_ok = !k_out || ((same(a.k_out, a.k) || apart(a.k_out, kv_heads, a.k, kv_heads, T, head_dim)) &&
+                               (!q || (apart(a.k_out, kv_heads, a.q, heads, T, head_dim) &&
+                                       apart(a.k_out, kv_heads, a.q_out, heads, T, head_dim))) &&
+                               apart(a.k_out, kv_heads, a.v, kv_heads, T, head_dim));
+  if (!q_ok || !k_ok) return fail(MOE_E_ARG, "q_out may be q and k_out may be k, but overlap nothing else");
+  const hipError_t e = moe::launch_kv_append(a, (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_kv_append launch");
+  return ok();
+}
+
+namespace {
+
+int32_t check_table(const moe::TableArgs& t) {
+  if (t.rows < 0 || t.rows >= (1 << 24)) return fail(MOE_E_SHAPE, "row count %lld outside [0, 2^24)", (long long)t.rows);
+  if (t.width < 1) return fail(MOE_E_SHAPE, "table width %d is not positive", t.width);
+  if (t.n_pages < 1 || t.n_pages > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "n_pages %lld outside [1, 2^31)", (long long)t.n_pages);
+  if (t.P < 1 || t.P > moe::kMaxPage || (t.P & (t.P - 1)))
+    return fail(MOE_E_SHAPE, "page_size %d is not a power of two up to %d", t.P, moe::kMaxPage);
+  if (t.rows == 0) return MOE_OK;
+  if (!t.tables || !t.lengths || !t.refs) return fail(MOE_E_ARG, "NULL pointer (tables, lengths or refs)");
+  if ((uintptr_t)t.tables % 4 || (uintptr_t)t.lengths % 4 || (uintptr_t)t.refs % 4)
+    return fail(MOE_E_ARG, "tables, lengths and refs must be 4-byte aligned");
+  return MOE_OK;
+}
+moe::TableArgs table_of(const int32_t* tables, int64_t rows, int32_t width, const int32_t* lengths, const int32_t* refs,
+                        int64_t n_pages, int32_t page_size) {
+  return {(int32_t*)tables, rows, width, (int32_t*)lengths, (int32_t*)refs, n_pages, page_size,
+          page_size > 0 ? log2_of(page_size) : 0};
+}
+
+int32_t check_space(const void* ws, int64_t ws_bytes, const moe::TableArgs& t) {
+  if (!ws) return fail(MOE_E_ARG, "NULL workspace");
+  if ((uintptr_t)ws % kAlign) return fail(MOE_E_ARG, "workspace must be 256-byte aligned");
+  const int64_t need = moe::pages_workspace_bytes(t.rows, t.n_pages);
+  if (ws_bytes < need)
+    return fail(MOE_E_SPACE, "workspace holds %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
+  return MOE_OK;
+}
+
+int32_t check_pools(const moe_kv_pool* pools, int32_t n, int64_t n_pages, moe::PoolArgs& out) {
+  if (n < 0 || n > MOE_MAX_POOLS) return fail(MOE_E_ARG, "%d pools, 0 to %d wanted", (int)n, MOE_MAX_POOLS);
+  if (n && !pools) return fail(MOE_E_ARG, "NULL pointer (pools)");
+  static_assert((int)MOE_MAX_POOLS == moe::kMaxPools, "one limit");
+  out = moe::PoolArgs{};
+  out.n = n;
+  out.n_pages = n_pages;
+  for (int i = 0; i < n; ++i) {
+    const moe_kv_pool& p = pools[i];
+    if (p.planes < 1 || p.planes > (1 << 16) || p.page_bytes < 4 || p.page_bytes % 4 || p.page_bytes > ((int64_t)1 << 30))
+      return fail(MOE_E_SHAPE, "pool %d: %lld planes of pages of %lld bytes", i, (long long)p.planes, (long long)p.page_bytes);
+    if (!p.base || (uintptr_t)p.base % 4) return fail(MOE_E_ARG, "pool %d is NULL or not 4-byte aligned", i);
+    out.pool[i] = {(char*)p.base, p.planes, p.page_bytes};
+  }
+  return MOE_OK;
+}
+// Whether a pool shares a byte with another or with one of the ranges.
+bool pools_collide(const moe::PoolArgs& p, std::initializer_list<Bytes> ranges) {
+  auto bytes = [&](int i) { return p.pool[i].planes * p.n_pages * p.pool[i].page_bytes; };
+  for (int i = 0; i < p.n; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlaps(p.pool[i].base, bytes(i), p.pool[j].base, bytes(j))) return true;
+    for (const Bytes& r : ranges)
+      if (overlaps(p.pool[i].base, bytes(i), r.p, r.n)) return true;
+  }
+  return false;
+}
+const char* kPagesOverlap = "the buffers must not overlap";
+
+}  // namespace
+
+int64_t moe_kv_pages_workspace_bytes(int64_t n_rows, int64_t n_pages) {
+  if (n_rows < 0 || n_rows >= (1 << 24) || n_pages < 1 || n_pages > 0x7FFFFFFFll) return -1;
+  return moe::pages_workspace_bytes(n_rows, n_pages);
+}
+
+int32_t moe_kv_reserve(int32_t* tables, int64_t n_rows, int32_t width, int32_t* lengths, int32_t* refs,
+                       int64_t n_pages, int32_t page_size, const int32_t* grow, int32_t* status, void* ws,
+                       int64_t ws_bytes, void* stream) {
+  const moe::TableArgs t = table_of(tables, n_rows, width, lengths, refs, n_pages, page_size);
+  if (const int32_t rc = check_table(t)) return rc;
+  if (n_rows == 0) return ok();
+  if (!grow || !status) return fail(MOE_E_ARG, "NULL pointer (grow or status)");
+  if ((uintptr_t)grow % 4 || (uintptr_t)status % 4) return fail(MOE_E_ARG, "grow and status must be 4-byte aligned");
+  if (const int32_t rc = check_space(ws, ws_bytes, t)) return rc;
+  if (collide({{tables, 4 * n_rows * width}, {lengths, 4 * n_rows}, {refs, 4 * n_pages}, {status, 4 * n_rows},
+               {ws, moe::pages_workspace_bytes(n_rows, n_pages)}, {grow, 4 * n_rows}}, 5))
+    return fail(MOE_E_ARG, "%s", kPagesOverlap);
+  const hipError_t e = moe::launch_kv_reserve(t, grow, status, ws, (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_kv_reserve launch");
+  return ok();
+}
+
+int32_t moe_kv_fork(int32_t* tables, int64_t n_rows, int32_t width, int32_t* lengths, int32_t* refs, int64_t n_pages,
+                    int32_t page_size, const int32_t* parents, const moe_kv_pool* pools, int32_t n_pools,
+                    int32_t* status, void* ws, int64_t ws_bytes, void* stream) {
+  const moe::TableArgs t = table_of(tables, n_rows, width, lengths, refs, n_pages, page_size);
+  if (const int32_t rc = check_table(t)) return rc;
+  moe::PoolArgs p;
+  if (const int32_t rc = check_pools(pools, n_pools, n_pages, p)) return rc;
+  if (n_rows == 0) return ok();
+  if (!parents || !status) return fail(MOE_E_ARG, "NULL pointer (parents or status)");
+  if ((uintptr_t)parents % 4 || (uintptr_t)status % 4) return fail(MOE_E_ARG, "parents and status must be 4-byte aligned");
+  if (const int32_t rc = check_space(ws, ws_bytes, t)) return rc;
+  const Bytes tab{tables, 4 * n_rows * width}, len{lengths, 4 * n_rows}, ref{refs, 4 * n_pages}, st{status, 4 * n_rows},
+      space{ws, moe::pages_workspace_bytes(n_rows, n_pages)}, ask{parents, 4 * n_rows};
+  if (collide({tab, len, ref, st, space, ask}, 5) || pools_collide(p, {tab, len, ref, st, space, ask}))
+    return fail(MOE_E_ARG, "%s", kPagesOverlap);
+  const hipError_t e = moe::launch_kv_fork(t, parents, p, status, ws, (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_kv_fork launch");
+  return ok();
+}
+
+int32_t moe_kv_free(const int32_t* tables, int64_t n_rows, int32_t width, int32_t* lengths, int32_t* refs,
+                    int64_t n_pages, int32_t page_size, const int32_t* drop, void* stream) {
+  const moe::TableArgs t = table_of(tables, n_rows, width, lengths, refs, n_pages, page_size);
+  if (const int32_t rc = check_table(t)) return rc;
+  if (n_rows == 0) return ok();
+  if (!drop) return fail(MOE_E_ARG, "NULL pointer (drop)");
+  if ((uintptr_t)drop % 4) return fail(MOE_E_ARG, "drop must be 4-byte aligned");
+  if (collide({{lengths, 4 * n_rows}, {refs, 4 * n_pages}, {tables, 4 * n_rows * width}, {drop, 4 * n_rows}}, 2))
+    return fail(MOE_E_ARG, "%s", kPagesOverlap);
+  const hipError_t e = moe::launch_kv_free(t, drop, (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_kv_free launch");
+  return ok();
+}
+
+int32_t moe_kv_compact(const int32_t* tables, int64_t n_rows, int32_t width, const int32_t* lengths,
+                       const int32_t* refs, int64_t n_pages, int32_t page_size, const moe_kv_pool* pools,
+                       int32_t n_pools, int32_t* new_tables, int32_t* new_refs, int32_t* live, void* ws,
+                       int64_t ws_bytes, void* stream) {
+  const moe::TableArgs t = table_of(tables, n_rows, width, lengths, refs, n_pages, page_size);
+  if (const int32_t rc = check_table(t)) return rc;
+  moe::PoolArgs p;
+  if (const int32_t rc = check_pools(pools, n_pools, n_pages, p)) return rc;
+  if (n_rows == 0) return ok();
+  if (!new_tables || !new_refs || !live) return fail(MOE_E_ARG, "NULL pointer (new_tables, new_refs or live)");
+  if ((uintptr_t)new_tables % 4 || (uintptr_t)new_refs % 4 || (uintptr_t)live % 4)
+    return fail(MOE_E_ARG, "new_tables, new_refs and live must be 4-byte aligned");
+  if (const int32_t rc = check_space(ws, ws_bytes, t)) return rc;
+  const int64_t tab_n = 4 * n_rows * width, ref_n = 4 * n_pages;
+  const Bytes tab{new_tables, tab_n}, ref{new_refs, ref_n}, lv{live, 4}, space{ws, moe::pages_workspace_bytes(n_rows, n_pages)},
+      len{lengths, 4 * n_rows}, old_tab{tables, tab_n}, old_ref{refs, ref_n};
+  if (collide({tab, ref, lv, space, len}, 4) || !same_or_apart(new_tables, tables, tab_n) ||
+      !same_or_apart(new_refs, refs, ref_n) || collide({tab, old_ref}, 1) || collide({ref, old_tab}, 1) ||
+      collide({lv, old_tab, old_ref}, 1) || collide({space, old_tab, old_ref}, 1) ||
+      pools_collide(p, {tab, ref, lv, space, len, old_tab, old_ref}))
+    return fail(MOE_E_ARG, "new_tables may be tables and new_refs refs; no other buffers may overlap");
+  const hipError_t e = moe::launch_kv_compact(t, p, new_tables, new_refs, live, ws, (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_kv_compact launch");
+  return ok();
+}
+
+int32_t moe_kv_copy_pages(const moe_kv_pool* pools, int32_t n_pools, int64_t n_pages, const int32_t* src,
+                          const int32_t* dst, int64_t n, void* stream) {
+  if (n < 0 || n > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "pair count %lld outside [0, 2^31)", (long long)n);
+  if (n_pages < 1 || n_pages > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "n_pages %lld outside [1, 2^31)", (long long)n_pages);
+  moe::PoolArgs p;
+  if (const int32_t rc = check_pools(pools, n_pools, n_pages, p)) return rc;
+  if (n == 0 || n_pools == 0) return ok();
+  if (!src || !dst) return fail(MOE_E_ARG, "NULL pointer (src or dst)");
+  if ((uintptr_t)src % 4 || (uintptr_t)dst % 4) return fail(MOE_E_ARG, "src and dst must be 4-byte aligned");
+  if (pools_collide(p, {{src, 4 * n}, {dst, 4 * n}})) return fail(MOE_E_ARG, "%s", kPagesOverlap);
+  const hipError_t e = moe::launch_kv_copy_pages(p, src, dst, n, (hipStream_t)stream);
+  if (e != hipSuccess) return device_fail(e, "moe_kv_copy_pages launch");
   return ok();
 }
 

@@ -1,0 +1,537 @@
+// Attention of one new token of every sequence over a paged cache, for gfx950:
+//   y_h = sum_j p_hj v_j,   p_hj = exp(s_hj - m_h) / sum_j exp(s_hj - m_h),   s_hj = scale q_h k_j
+// over the lengths[b] cached tokens j of sequence b.  Every key and value is read once
+// for all query heads that share it, so HBM bounds it.
+//
+// The tiles (a few dozen tokens for each wave of a block) of all sequences stand in one
+// row, which the workers of a kv head share equally, however ragged the lengths are; a
+// worker takes a run of tiles that may begin and end inside a sequence.  What it has of
+// a sequence that others share goes to the workspace as (m, l, sum), and a second launch
+// joins these in the order of the workers.
+//
+// A wave copies 32 tokens of keys and values into LDS of its own by loads that go there
+// directly, some tiles ahead, and needs no barrier until a sequence ends and the waves
+// join.  Scores are formed transposed, S^T = K Q^T, with the query heads on the matrix
+// core's columns (16 of them; fewer leave columns idle, which HBM hides); the softmax is
+// then within a lane and the four lanes of a column, and P stands as the second operand
+// of y^T = V^T P^T, whose first is read from LDS transposed.  P is rounded to 16 bits for
+// the matrix cores (half a step of itself, as y's own rounding).
+// e4m3 codes are widened exactly; a key's scale multiplies its scores, a value's scale
+// the weights before they are rounded.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "attention_device.h"
+#include "attention_internal.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kBlocks = 256;   // one a CU: a block's tiles fill the LDS
+constexpr int kHeadTile = 16;  // query heads of a block
+constexpr int kKeys = 32;      // tokens of a wave's tile
+
+template <int D>
+constexpr int kWaves = D == 256 ? 2 : 4;
+
+int64_t groups_of(int heads, int kv_heads) {
+  return (int64_t)kv_heads * ((heads / kv_heads + kHeadTile - 1) / kHeadTile);
+}
+int64_t record_floats(int D) { return kHeadTile * D + 2 * kHeadTile; }
+int64_t workers_of(int64_t groups) { return std::max<int64_t>(1, kBlocks / groups); }
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+
+struct DecodeWork {
+  int groups, per_kv;  // groups of query heads, and those of one kv head
+  int workers;
+  float* parts;   // [groups x workers x 2] records: sums [16 x D], m [16], l [16]
+  int2* shared;   // [B]: first and last worker of a sequence
+};
+
+// Piece p (16 bytes) of row r of a tile is kept at place p ^ f(r) of the row, which
+// spreads the rows that are read together over all banks.
+template <int ROW>
+__device__ __forceinline__ int swizzle(int r) {
+  return ROW == 64 ? (r >> 2) & 3 : ROW == 128 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 3) : (r & 3) << 2 | ((r >> 2) & 3);
+}
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Four e4m3 codes -> four 16-bit values (exact).
+template <bool F16>
+__device__ __forceinline__ u32x2 widen4(uint32_t v) {
+  if constexpr (F16)
+    return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)v, 1.0f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)v, 1.0f, true))};
+  else
+    return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v, 1.0f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v, 1.0f, true))};
+}
+
+// The value of lanes l ^ 16 and of l ^ 32 joined with the lane's own.
+template <class F>
+__device__ __forceinline__ float over_column(float v, F f) {
+  v = f(v, __shfl_xor(v, 16, 64));
+  return f(v, __shfl_xor(v, 32, 64));
+}
+
+template <bool F16, bool F8, int D>
+struct Decode {
+  using H = Half<F16>;
+  static constexpr int W = kWaves<D>, ROW = D * (F8 ? 1 : 2), kTile = kKeys * ROW, PER = ROW / 16;
+  static constexpr int kLoads = kTile / 1024, kPerStage = 2 * kLoads + (F8 ? 1 : 0);
+  static constexpr int kStage = 2 * kTile + (F8 ? 256 : 0);
+  static constexpr int kFit = 126 * 1024 / (W * kStage), kStages = kFit > 4 ? 4 : kFit < 2 ? 2 : kFit;
+  static constexpr int kBlockKeys = W * kKeys;
+  static constexpr int kRecord = 64 * (D / 4 + 2);  // floats of a wave's state
+  static constexpr int QS = D / 32, DT = D / 16;
+
+  const DecodeArgs& a;
+  int lane, wave, col, quad, kv;
+  uint8_t* mine;
+  u32x4 q[QS];
+  f32x4 o[DT];
+  float m, l;
+  bool bad;
+
+  __device__ __forceinline__ Decode(const DecodeArgs& args) : a(args) {}
+
+  // A place in the row of all tiles.
+  struct Walk {
+    int b, tile, tiles, len;
+    int64_t left;
+  };
+  __device__ __forceinline__ int tiles_of(int len) const { return max(1, (len + kBlockKeys - 1) / kBlockKeys); }
+  __device__ __forceinline__ int length(int64_t b) const {
+    const int64_t room = (int64_t)a.c.width * a.c.P;
+    return (int)min((int64_t)max(a.lengths[b], 0), room);
+  }
+  __device__ __forceinline__ void enter(Walk& w) const {
+    w.len = uniform(length(w.b));
+    w.tiles = tiles_of(w.len);
+  }
+  __device__ __forceinline__ void step(Walk& w) const {
+    if (--w.left > 0 && ++w.tile == w.tiles) {
+      w.tile = 0;
+      ++w.b;
+      enter(w);
+    }
+  }
+
+  // The page of lane % 32's token of the wave's tile.
+  __device__ __forceinline__ int page_of(const Walk& w) const {
+    const int key = min(w.tile * kBlockKeys + wave * kKeys + (lane & 31), max(w.len - 1, 0));
+    return a.c.width ? a.c.tables[(int64_t)w.b * a.c.width + (key >> a.c.shift)] : -1;
+  }
+
+  // The wave's tile into LDS.  Rows behind the last token repeat it; they are masked.  A
+  // page that is none makes the sequence's results NaN and is read as page 0.
+  __device__ __forceinline__ bool stage(const Walk& w, int page, uint8_t* dst) const {
+    const bool wrong = w.len > 0 && (page < 0 || page >= a.c.n_pages);
+    if (page < 0 || page >= a.c.n_pages) page = 0;
+    const int first = w.tile * kBlockKeys + wave * kKeys, last = max(w.len - 1, 0);
+    constexpr int ROWS = 64 / PER;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = i * ROWS + lane / PER, piece = (lane % PER) ^ swizzle<ROW>(row);
+      const int64_t p = __shfl(page, row, 64);
+      const int64_t at = ((p * a.c.kv_heads + kv) * a.c.P + (min(first + row, last) & (a.c.P - 1))) * ROW + 16 * piece;
+      const auto to = (__attribute__((address_space(3))) void*)(dst + i * 1024);
+      const auto to_v = (__attribute__((address_space(3))) void*)(dst + kTile + i * 1024);
+      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)((const uint8_t*)a.c.k + at), to, 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)((const uint8_t*)a.c.v + at), to_v, 16, 0,
+                                       0);
+    }
+    if (F8) {
+      const int row = lane & 31;
+      const int64_t at = ((int64_t)page * a.c.kv_heads + kv) * a.c.P + (min(first + row, last) & (a.c.P - 1));
+      const float* from = (lane < 32 ? a.c.k_scales : a.c.v_scales) + at;
+      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)from,
+                                       (__attribute__((address_space(3))) void*)(dst + 2 * kTile), 4, 0, 0);
+    }
+    return wrong;
+  }
+
+  __device__ __forceinline__ void begin(int64_t b, int head0, int heads) {
+    m = -INFINITY;
+    l = 0.f;
+    bad = false;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = f32x4{};
+    const uint16_t* p = a.q.p + b * a.q.token + (head0 + min(col, heads - 1)) * a.q.head;
+#pragma unroll
+    for (int k = 0; k < QS; ++k)
+      q[k] = *(const u32x4*)(p + (F8 ? 64 * (k / 2) + 16 * quad + 8 * (k & 1) : 32 * k + 8 * quad));
+  }
+
+  __device__ __forceinline__ void tile(const uint8_t* ks, int first, int len, float c) {
+    const uint8_t* vs = ks + kTile;
+    f32x4 s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      s[t] = f32x4{};
+      const int row = 16 * t + col, at = row * ROW, f = swizzle<ROW>(row);
+      if (F8) {
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          const u32x4 v = *(const u32x4*)(ks + at + 16 * ((4 * j + quad) ^ f));
+          const u32x2 w0 = widen4<F16>(v.x), w1 = widen4<F16>(v.y), w2 = widen4<F16>(v.z), w3 = widen4<F16>(v.w);
+          s[t] = H::mfma16(u32x4{w0.x, w0.y, w1.x, w1.y}, q[2 * j], s[t]);
+          s[t] = H::mfma16(u32x4{w2.x, w2.y, w3.x, w3.y}, q[2 * j + 1], s[t]);
+        }
+        const f32x4 scale = *(const f32x4*)(ks + 2 * kTile + 4 * (16 * t + 4 * quad));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][i] *= scale[i];
+      } else {
+#pragma unroll
+        for (int k = 0; k < QS; ++k)
+          s[t] = H::mfma16(*(const u32x4*)(ks + at + 16 * ((4 * k + quad) ^ f)), q[k], s[t]);
+      }
+    }
+    const int there = len - first;  // tokens of the tile that exist
+    const bool whole = there >= kKeys;
+    if (!whole) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (16 * t + 4 * quad + i >= there) s[t][i] = -INFINITY;
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
+    top = over_column(top, [](float x, float y) { return fmaxf(x, y); }) * c;
+    if (__any(top > m + 8.f)) {  // the maximum that is subtracted may lag 2^8 behind
+      const float now = fmaxf(m, top), f = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
+      m = now;
+      l *= f;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) o[d] *= f;
+    }
+    const float off = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[t][i] = __builtin_amdgcn_exp2f(s[t][i] * c - off);
+        l += s[t][i];
+      }
+    if (F8) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x4 scale = *(const f32x4*)(ks + 2 * kTile + 128 + 4 * (16 * t + 4 * quad));
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (16 * t + 4 * quad + i >= there) scale[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][i] *= scale[i];
+      }
+    }
+    const u32x4 p = {H::pack(s[0][0], s[0][1]), H::pack(s[0][2], s[0][3]), H::pack(s[1][0], s[1][1]),
+                     H::pack(s[1][2], s[1][3])};
+    // k slot 8 quad + e of the product is token 16 (e / 4) + 4 quad + e % 4.  Values behind
+    // the last token become zeros: they may hold anything.
+    u32x4 keep = {~0u, ~0u, ~0u, ~0u};
+    if (!whole) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = 16 * (e / 2) + 4 * quad + 2 * (e & 1);
+        keep[e] = (row < there ? 0xFFFFu : 0u) | (row + 1 < there ? 0xFFFF0000u : 0u);
+      }
+    }
+    if (F8) {
+      const int j = col >> 1, row = 16 * (j / 4) + 4 * quad + (j & 3), f = swizzle<ROW>(row);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        typedef int i32x2_t __attribute__((ext_vector_type(2)));
+        const i32x2_t v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) i32x2_t*)(vs + row * ROW + 16 * (d ^ f) + 8 * (col & 1)));
+        const u32x2 lo = widen4<F16>((uint32_t)v.x), hi = widen4<F16>((uint32_t)v.y);
+        u32x4 w = {lo.x, lo.y, hi.x, hi.y};
+        if (!whole) w &= keep;
+        o[d] = H::mfma16(w, p, o[d]);
+      }
+    } else {
+      int at[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int row = 16 * t + 4 * quad + (col >> 2);
+        at[t] = row * ROW + 16 * (((col & 3) >> 1) ^ swizzle<ROW>(row)) + 8 * (col & 1);
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const u32x2 lo = read_transposed(vs + (at[0] ^ (d << 5))), hi = read_transposed(vs + (at[1] ^ (d << 5)));
+        u32x4 w = {lo.x, lo.y, hi.x, hi.y};
+        if (!whole) w &= keep;
+        o[d] = H::mfma16(w, p, o[d]);
+      }
+    }
+  }
+
+  // The waves' shares of a sequence, joined in wave 0: half of them hand theirs over, and
+  // so on.
+  __device__ __forceinline__ void join(float* room) {
+    l = over_column(l, [](float x, float y) { return x + y; });
+    if (__any(bad)) l = NAN;
+#pragma unroll
+    for (int n = W / 2; n; n /= 2) {
+      float* at = room + (wave % n) * kRecord + lane;
+      if (wave >= n && wave < 2 * n) {
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) at[64 * (4 * d + i)] = o[d][i];
+        at[64 * 4 * DT] = m;
+        at[64 * (4 * DT + 1)] = l;
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (wave < n) {
+        const float m2 = at[64 * 4 * DT], l2 = at[64 * (4 * DT + 1)];
+        const float now = fmaxf(m, m2);
+        const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
+        const float f2 = m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m2 - now);
+        m = now;
+        l = (l == 0.f ? 0.f : l * f) + (l2 == 0.f ? 0.f : l2 * f2);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[d][i] = o[d][i] * f + at[64 * (4 * d + i)] * f2;
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+  }
+};
+
+template <bool F16, bool F8, int D>
+__global__ __launch_bounds__(64 * kWaves<D>) void attention_decode_kernel(DecodeArgs a, DecodeWork work) {
+  using W = Decode<F16, F8, D>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[W::W * W::kStages * W::kStage];
+  __shared__ float room[W::W / 2 * W::kRecord];
+  __shared__ int64_t found[2], sums[W::W];
+  W w(a);
+  w.lane = threadIdx.x & 63;
+  w.wave = uniform(threadIdx.x >> 6);
+  w.col = w.lane & 15;
+  w.quad = w.lane >> 4;
+  const int group = blockIdx.x % work.groups, worker = blockIdx.x / work.groups;
+  w.kv = group / work.per_kv;
+  const int shared = a.heads / a.c.kv_heads;
+  const int head0 = w.kv * shared + group % work.per_kv * kHeadTile, heads = min(kHeadTile, shared - (head0 - w.kv * shared));
+
+  // the tiles of all sequences, and the sequence in which this worker's begin
+  constexpr int THREADS = 64 * W::W;
+  int64_t total = 0, before = 0, workers = 1;  // workers: as many as have a tile
+  for (int pass = 0; pass < 2; ++pass) {
+    const int64_t start = pass ? total * worker / workers : 0;
+    int64_t base = 0;
+    for (int64_t b0 = 0; b0 < a.B; b0 += THREADS) {
+      const int64_t b = b0 + threadIdx.x;
+      const int n = b < a.B ? w.tiles_of(w.length(b)) : 0;
+      int64_t upto = n;
+#pragma unroll
+      for (int s = 1; s < 64; s <<= 1) {
+        const int64_t other = __shfl_up(upto, s, 64);
+        if (w.lane >= s) upto += other;
+      }
+      if (w.lane == 63) sums[w.wave] = upto;
+      __syncthreads();
+      int64_t all = 0;
+#pragma unroll
+      for (int i = 0; i < W::W; ++i) {
+        if (i < w.wave) upto += sums[i];
+        all += sums[i];
+      }
+      if (pass && n && start < base + upto && start >= base + upto - n) {
+        found[0] = b;
+        found[1] = start - (base + upto - n);
+      }
+      __syncthreads();
+      base += all;
+    }
+    if (!pass) {
+      total = base;
+      workers = min((int64_t)work.workers, total);
+      if (worker >= workers) return;
+    } else {
+      before = start;
+    }
+  }
+  const int64_t end = total * (worker + 1) / workers;
+  typename W::Walk now;
+  now.b = uniform((int)found[0]);
+  now.tile = uniform((int)found[1]);
+  now.left = end - before;
+  w.enter(now);
+  typename W::Walk ahead = now;
+
+  w.mine = lds + w.wave * W::kStages * W::kStage;
+  const float c = a.scale * kLog2e;
+  bool wrong[W::kStages];
+  int page = w.page_of(ahead);
+#pragma unroll
+  for (int i = 0; i < W::kStages - 1; ++i)
+    if (ahead.left > 0) {
+      wrong[i] = w.stage(ahead, page, w.mine + i * W::kStage);
+      w.step(ahead);
+      if (ahead.left > 0) page = w.page_of(ahead);
+    }
+  w.begin(now.b, head0, heads);
+  int from = now.tile;  // the first tile of the present sequence that this worker has
+  int64_t tile0 = before - now.tile;  // the number of the sequence's first tile
+  bool first_part = true;
+  for (;;) {
+#pragma unroll
+    for (int slot = 0; slot < W::kStages; ++slot) {
+      constexpr int AHEAD = W::kStages - 1;
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (ahead.left > 0) {
+        wrong[(slot + AHEAD) % W::kStages] = w.stage(ahead, page, w.mine + (slot + AHEAD) % W::kStages * W::kStage);
+        w.step(ahead);
+        if (ahead.left > 0) page = w.page_of(ahead);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(AHEAD * W::kPerStage) : "memory");
+      } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
+      w.bad |= wrong[slot];
+      const int first = now.tile * W::kBlockKeys + w.wave * kKeys;
+      if (first < now.len) w.tile(w.mine + slot * W::kStage, first, now.len, c);
+      const bool last = now.left == 1, ends = now.tile + 1 == now.tiles;
+      if (last || ends) {
+        w.join(room);
+        const bool whole = from == 0 && ends;
+        if (w.wave == 0) {
+          if (whole) {
+            const float inv = w.l == 0.f ? 0.f : 1.f / w.l;
+            if (w.col < heads) {
+              const int64_t row = (int64_t)now.b * a.heads + head0 + w.col;
+              uint16_t* y = a.y + row * D + 4 * w.quad;
+#pragma unroll
+              for (int d = 0; d < W::DT; ++d)
+                *(u32x2*)(y + 16 * d) = u32x2{W::H::pack(w.o[d].x * inv, w.o[d].y * inv),
+                                              W::H::pack(w.o[d].z * inv, w.o[d].w * inv)};
+              if (a.lse && w.quad == 0) a.lse[row] = w.l == 0.f ? -INFINITY : w.m * kLn2 + logf(w.l);
+            }
+          } else {
+            float* part = work.parts + (((int64_t)group * work.workers + worker) * 2 + (first_part ? 0 : 1)) *
+                                           (kHeadTile * D + 2 * kHeadTile);
+#pragma unroll
+            for (int d = 0; d < W::DT; ++d) *(f32x4*)(part + w.col * D + 16 * d + 4 * w.quad) = w.o[d];
+            if (w.quad == 0) {
+              part[kHeadTile * D + w.col] = w.m;
+              part[kHeadTile * D + kHeadTile + w.col] = w.l;
+            }
+          }
+          // the worker that has a sequence's first tile says who else has some of it
+          if (work.workers > 1 && group == 0 && from == 0 && w.lane == 0) {
+            const int64_t t = tile0 + now.tiles - 1;
+            int64_t to = t * workers / total;
+            while (total * (to + 1) / workers <= t) ++to;
+            while (total * to / workers > t) --to;
+            work.shared[now.b] = int2{(int)(first_part ? worker : ~worker), (int)to};
+          }
+        }
+        if (last) return;
+        first_part = false;
+        from = 0;
+        tile0 += now.tiles;
+        w.step(now);
+        w.begin(now.b, head0, heads);
+      } else {
+        w.step(now);
+      }
+    }
+  }
+}
+
+// The shares of a sequence that several workers have, one block for each query head.
+template <bool F16, int D>
+__global__ __launch_bounds__(256) void attention_join_kernel(DecodeArgs a, DecodeWork work) {
+  constexpr int PER = D / 4, SETS = 256 / PER;
+  __shared__ f32x4 sums[256];
+  __shared__ float weights[SETS];
+  const int64_t b = blockIdx.y;
+  const int head = blockIdx.x;
+  const int2 who = work.shared[b];
+  const int w0 = who.x < 0 ? ~who.x : who.x, n = who.y - w0 + 1;
+  if (n <= 1) return;
+  const int shared = a.heads / a.c.kv_heads, kv = head / shared, in_kv = head - kv * shared;
+  const int group = kv * work.per_kv + in_kv / kHeadTile, row = in_kv % kHeadTile;
+  constexpr int64_t RECORD = kHeadTile * D + 2 * kHeadTile;
+  const float* base = work.parts + ((int64_t)group * work.workers + w0) * 2 * RECORD;
+  auto record = [&](int i) { return base + (2 * i + (i == 0 && who.x < 0 ? 1 : 0)) * RECORD; };
+  float top = -INFINITY;
+  for (int i = threadIdx.x & 63; i < n; i += 64) top = fmaxf(top, record(i)[kHeadTile * D + row]);
+#pragma unroll
+  for (int s = 32; s; s >>= 1) top = fmaxf(top, __shfl_xor(top, s, 64));
+  const int set = threadIdx.x / PER, d = threadIdx.x % PER;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  float l = 0.f;
+  for (int i = set; i < n; i += SETS) {
+    const float* r = record(i);
+    const float m = r[kHeadTile * D + row], lr = r[kHeadTile * D + kHeadTile + row];
+    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+    l += lr == 0.f ? 0.f : lr * f;
+    sum += *(const f32x4*)(r + row * D + 4 * d) * f;
+  }
+  sums[threadIdx.x] = sum;
+  if (d == 0) weights[set] = l;
+  __syncthreads();
+  if (set) return;
+#pragma unroll
+  for (int i = 1; i < SETS; ++i) {
+    sum += sums[i * PER + d];
+    l += weights[i];
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int64_t out = b * a.heads + head;
+  *(u32x2*)(a.y + out * D + 4 * d) = u32x2{Half<F16>::pack(sum.x * inv, sum.y * inv), Half<F16>::pack(sum.z * inv, sum.w * inv)};
+  if (a.lse && d == 0) a.lse[out] = l == 0.f ? -INFINITY : top * kLn2 + logf(l);
+}
+
+template <bool F16, bool F8, int D>
+hipError_t launch(const DecodeArgs& a, DecodeWork w, hipStream_t stream) {
+  // at most a worker a tile that can be there
+  const int64_t room = std::min<int64_t>((int64_t)a.c.width * a.c.P, 0x7FFFFFFF);
+  constexpr int KEYS = Decode<F16, F8, D>::kBlockKeys;
+  const int64_t most = a.B * std::max<int64_t>(1, (room + KEYS - 1) / KEYS);
+  w.workers = (int)std::min<int64_t>(w.workers, most);
+  if (most <= 2) w.workers = 1;
+  attention_decode_kernel<F16, F8, D><<<(unsigned)(w.groups * w.workers), 64 * kWaves<D>, 0, stream>>>(a, w);
+  if (w.workers > 1)
+    attention_join_kernel<F16, D><<<dim3((unsigned)a.heads, (unsigned)a.B), 256, 0, stream>>>(a, w);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t decode_workspace_bytes(int64_t B, int heads, int kv_heads, int D) {
+  const int64_t groups = groups_of(heads, kv_heads), workers = workers_of(groups);
+  if (workers == 1) return 0;
+  return up256(groups * workers * 2 * record_floats(D) * 4) + up256(B * 8);
+}
+
+hipError_t launch_attention_decode(const DecodeArgs& a, void* ws, hipStream_t stream) {
+  DecodeWork w{};
+  w.groups = (int)groups_of(a.heads, a.c.kv_heads);
+  w.per_kv = w.groups / a.c.kv_heads;
+  w.workers = (int)workers_of(w.groups);
+  w.parts = (float*)ws;
+  w.shared = (int2*)((char*)ws + up256((int64_t)w.groups * w.workers * 2 * record_floats(a.c.D) * 4));
+  const bool f8 = a.c.k_scales != nullptr;
+  auto by_dim = [&](auto f16, auto e4m3) {
+    constexpr bool F = decltype(f16)::value, E = decltype(e4m3)::value;
+    return a.c.D == 64 ? launch<F, E, 64>(a, w, stream) : a.c.D == 128 ? launch<F, E, 128>(a, w, stream)
+                                                                      : launch<F, E, 256>(a, w, stream);
+  };
+  if (a.f16) return f8 ? by_dim(std::true_type{}, std::true_type{}) : by_dim(std::true_type{}, std::false_type{});
+  return f8 ? by_dim(std::false_type{}, std::true_type{}) : by_dim(std::false_type{}, std::false_type{});
+}
+
+}  // namespace moe
