@@ -104,9 +104,8 @@ struct Prefill {
     }
   }
 
-  // One tile of keys and values.  `masked`: some query does not see all of it.
-  template <bool MASKED>
-  __device__ __forceinline__ void tile(const uint8_t* ks, const uint8_t* vs, int first, float c, bool careful) {
+  // One tile of keys and values.  masked: some query of the wave does not see all of it.
+  __device__ __forceinline__ void tile(const uint8_t* ks, const uint8_t* vs, int first, float c, bool masked) {
     f32x16 s[KT];
     const int krow = lane & 31, kat = krow * kRow + ((half ^ swizzle<D>(krow)) << 4);
 #pragma unroll
@@ -115,8 +114,8 @@ struct Prefill {
 #pragma unroll
       for (int k = 0; k < KS; ++k) s[t] = H::mfma32(*(const u32x4*)(ks + 32 * t * kRow + (kat ^ (k << 5))), q[k], s[t]);
     }
-    const int seen = lim - first - 4 * half;
-    if (MASKED) {
+    if (masked) {
+      const int seen = lim - first - 4 * half;
 #pragma unroll
       for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -165,49 +164,44 @@ struct Prefill {
         u32x4 p;
 #pragma unroll
         for (int e = 0; e < 4; ++e) p[e] = H::pack(s[t][8 * k + 2 * e], s[t][8 * k + 2 * e + 1]);
+        const uint8_t* at = vs + (32 * t + 16 * k) * kRow;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const uint8_t* at = vs + (32 * t + 16 * k) * kRow;
           const u32x2 lo = read_transposed(at + (vat[0] ^ (d << 6))), hi = read_transposed(at + (vat[1] ^ (d << 6)));
-          u32x4 v = {lo.x, lo.y, hi.x, hi.y};
-          if (MASKED && careful) {
-            add_careful(v, p, seen - 32 * t - 16 * k, d);
-          } else {
-            o[d] = H::mfma32(v, p, o[d]);
-          }
+          o[d] = H::mfma32(u32x4{lo.x, lo.y, hi.x, hi.y}, p, o[d]);
         }
       }
   }
 
-  // The same product where a hidden value may be an infinity or a NaN, which a zero weight
-  // does not remove: such values take part as zeros, and then count, with each sign apart,
-  // for the queries that see them.
-  __device__ __forceinline__ void add_careful(u32x4 v, u32x4 p, int seen, int d) {
-    u32x4 up, down, sees;
+  // A weight of zero does not remove a value that is infinite or NaN.  Where a tile is
+  // hidden in part and holds such values, they take part in the product as zeros and are
+  // added here to the queries that see them.
+  __device__ __forceinline__ void clear(uint8_t* vs) const {
+    for (int i = threadIdx.x; i < kTile / 16; i += 256) {
+      u32x4 v = *(const u32x4*)(vs + 16 * i);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t keep = 0, pos = 0, neg = 0, see = 0;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t b = (v[e] >> (16 * x)) & 0xFFFFu;
-        const bool finite = (b & H::kExponent) != H::kExponent, nan = !finite && (b & 0x7FFFu) != H::kExponent;
-        const int key = 2 * e + x;  // element of the fragment: key 8 (key / 4) + key % 4 of the 16
-        keep |= (finite ? b : 0u) << (16 * x);
-        pos |= (!finite && (nan || !(b & 0x8000u)) ? H::kOne : 0u) << (16 * x);
-        neg |= (!finite && (nan || (b & 0x8000u)) ? H::kOne : 0u) << (16 * x);
-        see |= (8 * (key / 4) + key % 4 <= seen ? H::kOne : 0u) << (16 * x);
+      for (int e = 0; e < 4; ++e) {
+        if ((v[e] & H::kExponent) == H::kExponent) v[e] &= 0xFFFF0000u;
+        if ((v[e] >> 16 & H::kExponent) == H::kExponent) v[e] &= 0xFFFFu;
       }
-      v[e] = keep;
-      up[e] = pos;
-      down[e] = neg;
-      sees[e] = see;
+      *(u32x4*)(vs + 16 * i) = v;
     }
-    o[d] = H::mfma32(v, p, o[d]);
-    const f32x16 ups = H::mfma32(up, sees, f32x16{}), downs = H::mfma32(down, sees, f32x16{});
+  }
+  __device__ __forceinline__ void add_cleared(const uint16_t* v, int64_t stride, int first, int end) {
+#pragma unroll 1
+    for (int j = first; j < end; ++j) {
+      const uint16_t* row = v + j * stride + 4 * half;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (ups[i] > 0.f) o[d][i] += INFINITY;
-      if (downs[i] > 0.f) o[d][i] -= INFINITY;
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const u32x2 x = *(const u32x2*)(row + 32 * d + 8 * e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t b = x[i / 2] >> (16 * (i & 1));
+            if ((b & H::kExponent) == H::kExponent && j <= lim) o[d][4 * e + i] += H::widen(b & 0xFFFFu);
+          }
+        }
     }
   }
 };
@@ -238,6 +232,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attention_prefill_kerne
   // keys that the block's and the wave's queries see, and those that all of the wave's see
   auto end = [&](int r) { return a.causal ? max(min(min(r, at.lq - 1) + behind + 1, at.lk), 0) : at.lk; };
   const int block_end = end(at.tile * kQRows + kQRows - 1);
+  const int seen_by_all = a.causal ? end(at.tile * kQRows) : at.lk;
   const int wave_end = first_row < at.lq ? end(first_row + 31) : 0, all_end = a.causal ? end(first_row) : at.lk;
   const float c = a.scale * kLog2e;
   const int tiles = (block_end + W::BN - 1) / W::BN;
@@ -259,9 +254,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attention_prefill_kerne
         w.stage(kp, a.k.token, first + W::BN, at.lk, then);
         w.stage(vp, a.v.token, first + W::BN, at.lk, then + W::kTile);
       }
+      const bool cleared = careful && first + W::BN > seen_by_all;
+      if (cleared) {
+        w.clear(now + W::kTile);
+        __syncthreads();
+      }
       if (first >= wave_end) continue;
-      if (first + W::BN <= all_end) w.template tile<false>(now, now + W::kTile, first, c, false);
-      else w.template tile<true>(now, now + W::kTile, first, c, careful != 0);
+      w.tile(now, now + W::kTile, first, c, first + W::BN > all_end);
+      if (cleared) w.add_cleared(vp, a.v.token, first, min(first + W::BN, at.lk));
     }
     // A result that is not finite: a value that a query must not see may have got in, so
     // the tiles that are hidden in part are gone through with care.
