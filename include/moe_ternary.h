@@ -325,6 +325,9 @@ int32_t moe_sample(int32_t type, const void* logits, int64_t batch, int32_t voca
  *             q_starts[s] .. q_starts[s + 1] - 1 and the keys of k_starts (NULL: q_starts)
  *   y         device [q_tokens x heads x head_dim], contiguous
  *   lse       device fp32 [q_tokens x heads], the logarithm of sum_j exp(s_ij), or NULL
+ *   workspace >= moe_attention_prefill_workspace_bytes(...), 256-byte aligned (NULL if that
+ *             is 0, as it is unless a few queries have many keys); it carries nothing from
+ *             one call to the next
  * A query that sees no key, or scores of -inf alone, gets y = 0 and lse = -inf.  What a
  * query must not see does not reach it, infinities and NaN included.  Tokens outside
  * every sequence leave their y and lse as they were.  Starts outside [0, tokens] are
@@ -333,15 +336,19 @@ int32_t moe_sample(int32_t type, const void* logits, int64_t batch, int32_t voca
  * are rounded to `type` for the matrix cores (each off by half a step of itself), y is
  * rounded once.  head_dim is 64, 128 or 256; heads is a multiple of kv_heads, at most
  * 4096; strides are multiples of 8, at most 2^24; q, k, v and y 16-byte aligned;
- * tokens below 2^31, n_seqs at most 2^22; scale finite and positive.  q_tokens = 0 or n_seqs = 0 is a no-op.  y and lse
- * overlap neither each other nor an input.  Results do not depend on the packing's other
- * sequences.  Ordered on `stream`; nothing is allocated.  Errors: MOE_E_FORMAT (type),
- * MOE_E_SHAPE, MOE_E_ARG, MOE_E_DEVICE. */
+ * tokens below 2^31, n_seqs at most 2^22; scale finite and positive.  q_tokens = 0 or n_seqs = 0 is a no-op.  y, lse and the
+ * workspace overlap neither each other nor an input.  A sequence's results depend on the others
+ * only where q_tokens, n_seqs and k_tokens ask for a workspace, and then in their last bits.
+ * Ordered on `stream`; nothing is allocated.  Errors: MOE_E_FORMAT (type), MOE_E_SHAPE,
+ * MOE_E_ARG, MOE_E_SPACE, MOE_E_DEVICE. */
+int64_t moe_attention_prefill_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64_t n_seqs, int32_t heads,
+                                              int32_t kv_heads, int32_t head_dim);
 int32_t moe_attention_prefill(int32_t type, const void* q, int64_t q_tokens, int32_t heads, int64_t q_token,
                               int64_t q_head, const void* k, const void* v, int64_t k_tokens, int32_t kv_heads,
                               int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, int32_t head_dim,
                               const int32_t* q_starts, const int32_t* k_starts, int64_t n_seqs, int32_t causal,
-                              float scale, void* y, float* lse, void* stream);
+                              float scale, void* y, float* lse, void* workspace, int64_t workspace_bytes,
+                              void* stream);
 
 /* The key-value cache of one layer, in pages of page_size tokens (a power of two up to
  * 4096), shared by the calls below:

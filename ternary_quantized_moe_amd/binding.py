@@ -28,7 +28,7 @@ EXPORTS = [
     "moe_quantize_device", "moe_ple_gather_q4_0", "moe_ternary_forward_q", "moe_draft_head_workspace_bytes",
     "moe_draft_head", "moe_lowrank_workspace_bytes", "moe_lowrank_apply",
     "moe_fp8_quantize", "moe_rms_norm", "moe_fp8_linear", "moe_sample_workspace_bytes", "moe_sample",
-    "moe_attention_prefill", "moe_attention_decode_workspace_bytes", "moe_attention_decode", "moe_kv_append",
+    "moe_attention_prefill_workspace_bytes", "moe_attention_prefill", "moe_attention_decode_workspace_bytes", "moe_attention_decode", "moe_kv_append",
     "moe_kv_pages_workspace_bytes", "moe_kv_reserve", "moe_kv_fork", "moe_kv_free", "moe_kv_compact",
     "moe_kv_copy_pages",
     "moe_workspace_bytes_factored", "moe_ternary_forward_factored",
@@ -96,8 +96,9 @@ def lib():
             "moe_fp8_linear": (i32, [vp, vp, i64, vp, vp, i64, i32, i32, vp, i64, vp]),
             "moe_sample_workspace_bytes": (i64, [i64, i32]),
             "moe_sample": (i32, [i32, vp, i64, i32, i64, vp, vp, vp, vp, vp, vp, vp, vp, i64, vp]),
+            "moe_attention_prefill_workspace_bytes": (i64, [i64, i64, i64, i32, i32, i32]),
             "moe_attention_prefill": (i32, [i32, vp, i64, i32, i64, i64, vp, vp, i64, i32, i64, i64, i64, i64, i32, vp,
-                                            vp, i64, i32, ctypes.c_float, vp, vp, vp]),
+                                            vp, i64, i32, ctypes.c_float, vp, vp, vp, i64, vp]),
             "moe_attention_decode_workspace_bytes": (i64, [i64, i32, i32, i32]),
             "moe_attention_decode": (i32, [i32, vp, i64, i32, i64, i64, i32, vp, vp, vp, vp, i64, i32, i32, i32, vp, i32,
                                            vp, ctypes.c_float, vp, vp, vp, i64, vp]),
@@ -708,7 +709,7 @@ def _cache(k, v, k_scales, v_scales, device, dtype, T):
 
 
 def attention_prefill(q, k, v, starts, k_starts=None, causal: bool = True, scale: Optional[float] = None, y=None,
-                      lse=None, stream=None):
+                      lse=None, workspace=None, stream=None):
     """Attention of packed sequences: q [tokens, heads, dim], k and v [k tokens, kv heads,
     dim], bf16 or fp16, dim 64, 128 or 256; heads are contiguous, tokens and heads may be
     strided (parts of one projection's rows).  starts int32 [sequences + 1]: where each
@@ -737,9 +738,19 @@ def attention_prefill(q, k, v, starts, k_starts=None, causal: bool = True, scale
     else:
         yp = _operand("y", y, dev, (q.dtype,), (n, H, D))
     lp = None if lse is None else _operand("lse", lse, dev, T["f32s"], (n, H))
-    rc = lib().moe_attention_prefill(kind, qp, n, H, q_token, q_head, kp, vp, m, Hk, k_token, k_head, v_token, v_head, D,
-                                     sp, ksp, size[0] - 1, causal, D ** -0.5 if scale is None else scale, yp, lp,
-                                     T["stream"](dev) if stream is None else _on(stream, dev, y))
+    L = lib()
+    ws, wn = None, 0
+    if workspace is None:
+        need = L.moe_attention_prefill_workspace_bytes(n, m, size[0] - 1, H, Hk, D)
+        if need > 0:
+            workspace = q.new_empty(need + 256, dtype=T["u8"])
+    elif workspace.get_device() != dev:
+        raise MoeError(-1, f"the workspace is on {workspace.device}, not on the current device cuda:{dev}")
+    if workspace is not None:
+        ws, wn = _aligned(workspace)
+    rc = L.moe_attention_prefill(kind, qp, n, H, q_token, q_head, kp, vp, m, Hk, k_token, k_head, v_token, v_head, D, sp,
+                                 ksp, size[0] - 1, causal, D ** -0.5 if scale is None else scale, yp, lp, ws, wn,
+                                 T["stream"](dev) if stream is None else _on(stream, dev, y, workspace))
     if rc:
         _check(rc)
     return y

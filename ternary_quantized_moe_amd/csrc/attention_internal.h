@@ -30,9 +30,9 @@ struct PrefillArgs {
   uint16_t* y;  // [Tq x heads x D]
   float* lse;   // [Tq x heads] or NULL
 };
-// Tiles of queries that a launch covers, every head included.
 int64_t prefill_blocks(const PrefillArgs& a);
-hipError_t launch_attention_prefill(const PrefillArgs& a, hipStream_t stream);
+int64_t prefill_workspace_bytes(const PrefillArgs& a);
+hipError_t launch_attention_prefill(const PrefillArgs& a, void* ws, hipStream_t stream);
 
 // One layer's cache: [n_pages x kv_heads x P x D] keys and values, 16-bit or e4m3 with
 // fp32 scales [n_pages x kv_heads x P]; row r of the table lists a sequence's pages.

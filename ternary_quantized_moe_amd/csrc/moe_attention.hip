@@ -4,14 +4,19 @@
 // i + lk - lq for lq queries that end where lk keys end.  One pass over the keys with
 // the running maximum m and sum l of the softmax in fp32.
 //
-// A block takes 128 queries of one head, a wave 32 of them, and walks over tiles of
-// keys and values in LDS.  Scores are formed transposed, S^T = K Q^T: a lane's results
-// belong to one query, so the softmax needs one exchange between the wave's halves, and
-// they stand as the second operand of y^T = V^T P^T wants them: the order of the keys
-// inside a product is free, and the transposing reads of V follow the order in which
-// the scores lie.  P is rounded to the values' type (nearest even) for the matrix cores;
-// each p is off by half a step of itself, as y is by its own rounding, and l is summed
-// before the rounding.
+// A block takes 128 rows, a wave 32 of them: 128 queries of one head, or 64 of two or 32 of
+// four heads that share their keys (then the waves see the same keys, and short or ragged
+// sequences fill the rows better).  It walks over tiles of keys and values in LDS.  Scores
+// are formed transposed, S^T = K Q^T: a lane's results belong to one query, so the softmax
+// needs one exchange between the wave's halves, and they stand as the second operand of
+// y^T = V^T P^T wants them: the order of the keys inside a product is free, and the
+// transposing reads of V follow the order in which the scores lie.  Two blocks share a CU,
+// and one's products run beside the other's softmax.  P is rounded to the values' type (nearest even) for the
+// matrix cores; each p is off by half a step of itself, as y is by its own rounding, and l
+// is summed before the rounding.
+//
+// Where a launch has too few blocks for the card, several share the keys of a tile of
+// queries, and a second launch joins what they leave in the workspace.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -24,7 +29,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kQRows = 128;  // queries of a block
+constexpr int kRows = 128;         // rows (queries times heads) of a block
+constexpr int kMaxSplits = 8;      // blocks that share the keys of a tile of queries
+constexpr int kSplitTiles = 8;     // tiles of keys that make a share worth its joining
 
 // Keys of a tile: 64, of the widest heads 32, so that two tiles of keys and values take
 // 64 KB of LDS and two blocks share a CU.
@@ -38,23 +45,43 @@ __device__ __forceinline__ int swizzle(int r) {
   return D == 64 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 3) : (r & 3) << 2 | ((r >> 2) & 3);
 }
 
+// A number that the compiler no longer knows.  The widest heads leave no registers for the
+// sixteen places in a tile that differ in a few address bits: they are made anew each time
+// (1021 queries over 8191 keys 173 us, 205 with them kept and others spilled; at 128 channels
+// they fit, and keeping them is 4% faster).
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+struct PrefillWork {
+  int heads;        // query heads of a block: 1, 2 or 4
+  int groups;       // blocks that share a tile of queries, one for each such set of heads
+  int splits;       // blocks that may share the keys of a tile of queries
+  int64_t units;    // tiles of queries, at most
+  float* parts;     // [units x groups x splits] records: 128 x D sums, m and l
+};
+
 // The unit-th tile of queries: its sequence's first query and key, their numbers, and
 // the tile's place, counted from the end (the last queries see the most keys).
 struct Place {
   int q0, k0, lq, lk, tile;
   bool found;
 };
-__device__ __forceinline__ Place find_tile(const PrefillArgs& a, int64_t unit) {
+__device__ __forceinline__ Place find_tile(const PrefillArgs& a, int queries, int64_t unit) {
   const int lane = threadIdx.x & 63;
   Place r{};
   for (int64_t c = 0; c < a.n; c += 64) {
     const int64_t i = c + lane;
-    int from = 0, to = 0;
+    int from = 0, to = 0, k_from = 0, k_to = 0;
     if (i < a.n) {
-      from = (int)min((int64_t)max(a.q_starts[i], 0), a.Tq);
-      to = (int)min((int64_t)max(a.q_starts[i + 1], from), a.Tq);
+      from = a.q_starts[i], to = a.q_starts[i + 1];
+      k_from = a.k_starts[i], k_to = a.k_starts[i + 1];
+      from = (int)min((int64_t)max(from, 0), a.Tq);
+      to = (int)min((int64_t)max(to, from), a.Tq);
+      k_from = (int)min((int64_t)max(k_from, 0), a.Tk);
+      k_to = (int)min((int64_t)max(k_to, k_from), a.Tk);
     }
-    const int tiles = (int)(((int64_t)to - from + kQRows - 1) / kQRows);
+    const int tiles = (int)(((int64_t)to - from + queries - 1) / queries);
     int upto = tiles;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -67,16 +94,39 @@ __device__ __forceinline__ Place find_tile(const PrefillArgs& a, int64_t unit) {
       r.q0 = __builtin_amdgcn_readlane(from, l);
       r.lq = __builtin_amdgcn_readlane(to, l) - r.q0;
       r.tile = __builtin_amdgcn_readlane(upto, l) - 1 - (int)unit;
-      const int64_t s = c + l;
-      const int k0 = (int)min((int64_t)max(a.k_starts[s], 0), a.Tk);
-      r.k0 = __builtin_amdgcn_readfirstlane(k0);
-      r.lk = __builtin_amdgcn_readfirstlane((int)min((int64_t)max(a.k_starts[s + 1], k0), a.Tk) - k0);
+      r.k0 = __builtin_amdgcn_readlane(k_from, l);
+      r.lk = __builtin_amdgcn_readlane(k_to, l) - r.k0;
       r.found = true;
       return r;
     }
     unit -= __builtin_amdgcn_readlane(upto, 63);
   }
   return r;
+}
+
+// A block's place: which tile of queries, set of heads and share of the keys.
+struct Share {
+  Place at;
+  int group, split;
+  int64_t record;  // of split 0
+};
+__device__ __forceinline__ Share share_of(const PrefillArgs& a, const PrefillWork& w, int64_t block, int splits) {
+  Share s;
+  s.group = (int)(block % w.groups);  // neighbours on the card's eight parts take different heads
+  const int64_t rest = block / w.groups;
+  s.split = (int)(rest % splits);
+  const int64_t unit = rest / splits;
+  s.at = find_tile(a, kRows / w.heads, unit);
+  s.record = (unit * w.groups + s.group) * w.splits;
+  return s;
+}
+// Keys that the queries up to r of the sequence see.
+__device__ __forceinline__ int keys_seen(const PrefillArgs& a, const Place& at, int r) {
+  return a.causal ? max(min(min(r, at.lq - 1) + at.lk - at.lq + 1, at.lk), 0) : at.lk;
+}
+// How many blocks really share `tiles` tiles of keys.
+__device__ __forceinline__ int shares(int tiles, int splits) {
+  return max(1, min(splits, tiles / kSplitTiles));
 }
 
 template <bool F16, int D>
@@ -87,7 +137,8 @@ struct Prefill {
   static constexpr int kLoads = kTile / 1024 / 4;        // staging loads of a wave
 
   u32x4 q[KS];
-  f32x16 o[DT];
+  f32x16 o[DT], s[KT];
+  u32x4 p[KT][2];  // the weights as the second operand wants them
   float m, l;
   int lane, wave, half, lim;  // lim: the last key that the lane's query sees
 
@@ -104,16 +155,21 @@ struct Prefill {
     }
   }
 
-  // One tile of keys and values.  masked: some query of the wave does not see all of it.
-  __device__ __forceinline__ void tile(const uint8_t* ks, const uint8_t* vs, int first, float c, bool masked) {
-    f32x16 s[KT];
-    const int krow = lane & 31, kat = krow * kRow + ((half ^ swizzle<D>(krow)) << 4);
+  // S^T = K Q^T.
+  __device__ __forceinline__ void scores(const uint8_t* ks) {
+    const int row = lane & 31, place = row * kRow + ((half ^ swizzle<D>(row)) << 4), 
+              at = D == 256 ? opaque(place) : place;
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      s[t] = f32x16{};
+    for (int t = 0; t < KT; ++t) s[t] = f32x16{};
 #pragma unroll
-      for (int k = 0; k < KS; ++k) s[t] = H::mfma32(*(const u32x4*)(ks + 32 * t * kRow + (kat ^ (k << 5))), q[k], s[t]);
-    }
+    for (int k = 0; k < KS; ++k)
+#pragma unroll
+      for (int t = 0; t < KT; ++t) s[t] = H::mfma32(*(const u32x4*)(ks + 32 * t * kRow + (at ^ (k << 5))), q[k], s[t]);
+  }
+
+  // The softmax of the tile whose scores are in s: its weights in p.  masked: some query
+  // of the wave does not see all of the tile.
+  __device__ __forceinline__ void softmax(int first, float c, bool masked) {
     if (masked) {
       const int seen = lim - first - 4 * half;
 #pragma unroll
@@ -150,25 +206,33 @@ struct Prefill {
         sum += s[t][i];
       }
     l += sum;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[t][k][e] = H::pack(s[t][8 * k + 2 * e], s[t][8 * k + 2 * e + 1]);
+  }
+
+  // y^T += V^T P^T.
+  __device__ __forceinline__ void values(const uint8_t* vs) {
     const int g = lane >> 4, i16 = lane & 15;
     int vat[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = 8 * r + 4 * half + (i16 >> 2), piece = 2 * (g & 1) + ((i16 & 3) >> 1);
       vat[r] = row * kRow + ((piece ^ swizzle<D>(row)) << 4) + 8 * (i16 & 1);
+      if (D == 256) vat[r] = opaque(vat[r]);
     }
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        u32x4 p;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = H::pack(s[t][8 * k + 2 * e], s[t][8 * k + 2 * e + 1]);
         const uint8_t* at = vs + (32 * t + 16 * k) * kRow;
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           const u32x2 lo = read_transposed(at + (vat[0] ^ (d << 6))), hi = read_transposed(at + (vat[1] ^ (d << 6)));
-          o[d] = H::mfma32(u32x4{lo.x, lo.y, hi.x, hi.y}, p, o[d]);
+          o[d] = H::mfma32(u32x4{lo.x, lo.y, hi.x, hi.y}, p[t][k], o[d]);
         }
       }
   }
@@ -204,24 +268,45 @@ struct Prefill {
         }
     }
   }
+
+  // The row's y from its sums, rounded once, and the logarithm of its sum.
+  __device__ __forceinline__ void store(const PrefillArgs& a, int64_t token, int head, float sum) const {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint16_t* y = a.y + (token * a.heads + head) * D + 4 * half;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *(u32x2*)(y + 32 * d + 8 * e) = u32x2{H::pack(o[d][4 * e] * inv, o[d][4 * e + 1] * inv),
+                                              H::pack(o[d][4 * e + 2] * inv, o[d][4 * e + 3] * inv)};
+    if (a.lse && !half) a.lse[token * a.heads + head] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
+  }
 };
 
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+// All loads have arrived but the last N.
+template <int N = 0>
+__device__ __forceinline__ void arrived() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 template <bool F16, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attention_prefill_kernel(PrefillArgs a, int64_t units) {
+__global__ __launch_bounds__(256, 2) void attention_prefill_kernel(PrefillArgs a, PrefillWork work) {
   using W = Prefill<F16, D>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * W::kTile];
   __shared__ int redo;
   const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-  const int head = (int)(block % a.heads);
-  const Place at = find_tile(a, block / a.heads);
+  const Share share = share_of(a, work, block, work.splits);
+  const Place& at = share.at;
   if (!at.found) return;
   W w;
   w.lane = threadIdx.x & 63;
   w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   w.half = w.lane >> 5;
-  const int first_row = at.tile * kQRows + 32 * w.wave, row = first_row + (w.lane & 31);
-  const int behind = a.causal ? at.lk - at.lq : 0;  // keys before the first query's own
-  w.lim = a.causal ? min(row + behind, at.lk - 1) : at.lk - 1;
+  const int queries = kRows / work.heads, first_query = at.tile * queries;
+  const int head = share.group * work.heads + w.wave % work.heads, first_row = first_query + 32 * (w.wave / work.heads);
+  const int row = first_row + (w.lane & 31);
+  w.lim = a.causal ? min(row + at.lk - at.lq, at.lk - 1) : at.lk - 1;
   const int64_t token = at.q0 + min(row, at.lq - 1);
   const uint16_t* qp = a.q.p + token * a.q.token + head * a.q.head + 8 * w.half;
 #pragma unroll
@@ -229,39 +314,56 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attention_prefill_kerne
   const int kv = head / (a.heads / a.kv_heads);
   const uint16_t* kp = a.k.p + at.k0 * a.k.token + kv * a.k.head;
   const uint16_t* vp = a.v.p + at.k0 * a.v.token + kv * a.v.head;
-  // keys that the block's and the wave's queries see, and those that all of the wave's see
-  auto end = [&](int r) { return a.causal ? max(min(min(r, at.lq - 1) + behind + 1, at.lk), 0) : at.lk; };
-  const int block_end = end(at.tile * kQRows + kQRows - 1);
-  const int seen_by_all = a.causal ? end(at.tile * kQRows) : at.lk;
-  const int wave_end = first_row < at.lq ? end(first_row + 31) : 0, all_end = a.causal ? end(first_row) : at.lk;
+  // the block's tiles of keys; the keys that all its queries see, and that the wave's do
+  const int tiles = (keys_seen(a, at, first_query + queries - 1) + W::BN - 1) / W::BN, n = shares(tiles, work.splits);
+  if (share.split >= n) return;
+  const int from = (int)((int64_t)tiles * share.split / n), to = (int)((int64_t)tiles * (share.split + 1) / n);
+  const int seen_by_all = a.causal ? keys_seen(a, at, first_query) : at.lk;
+  const int wave_end = first_row < at.lq ? keys_seen(a, at, first_row + 31) : 0;
+  const int all_end = a.causal ? keys_seen(a, at, first_row) : at.lk;
   const float c = a.scale * kLog2e;
-  const int tiles = (block_end + W::BN - 1) / W::BN;
+  uint8_t* const kbuf = lds;
+  uint8_t* const vbuf = lds + 2 * W::kTile;
   for (int careful = 0;; ++careful) {
     w.m = -INFINITY;
     w.l = 0.f;
 #pragma unroll
     for (int d = 0; d < W::DT; ++d) w.o[d] = f32x16{};
-    if (tiles > 0) {
-      w.stage(kp, a.k.token, 0, at.lk, lds);
-      w.stage(vp, a.v.token, 0, at.lk, lds + W::kTile);
-    }
-    for (int t = 0; t < tiles; ++t) {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      uint8_t* now = lds + (t & 1) * 2 * W::kTile;
-      uint8_t* then = lds + (~t & 1) * 2 * W::kTile;
-      const int first = t * W::BN;
-      if (t + 1 < tiles) {
-        w.stage(kp, a.k.token, first + W::BN, at.lk, then);
-        w.stage(vp, a.v.token, first + W::BN, at.lk, then + W::kTile);
+    // Tile t's keys and values are in buffer t - from modulo 2.
+    auto stage_next = [&](int t) {
+      const int now = (t - from) & 1;
+      if (t + 1 < to) w.stage(vp, a.v.token, (t + 1) * W::BN, at.lk, vbuf + (now ^ 1) * W::kTile);
+      if (t + 2 < to) w.stage(kp, a.k.token, (t + 2) * W::BN, at.lk, kbuf + now * W::kTile);
+    };
+    if (from < to) {
+      w.stage(kp, a.k.token, from * W::BN, at.lk, kbuf);
+      w.stage(vp, a.v.token, from * W::BN, at.lk, vbuf);
+      if (from + 1 < to) {
+        w.stage(kp, a.k.token, (from + 1) * W::BN, at.lk, kbuf + W::kTile);
+        arrived<2 * W::kLoads>();
+      } else {
+        arrived<W::kLoads>();
       }
+      meet();
+      if (from * W::BN < wave_end) w.scores(kbuf);
+    }
+    for (int t = from; t < to; ++t) {
+      const int now = (t - from) & 1, first = t * W::BN;
+      uint8_t* const vs = vbuf + now * W::kTile;
+      if (first < wave_end) w.softmax(first, c, first + W::BN > all_end);
+      arrived();
+      meet();
+      stage_next(t);
       const bool cleared = careful && first + W::BN > seen_by_all;
       if (cleared) {
-        w.clear(now + W::kTile);
-        __syncthreads();
+        w.clear(vs);
+        meet();
       }
-      if (first >= wave_end) continue;
-      w.tile(now, now + W::kTile, first, c, first + W::BN > all_end);
-      if (cleared) w.add_cleared(vp, a.v.token, first, min(first + W::BN, at.lk));
+      if (first < wave_end) {
+        w.values(vs);
+        if (cleared) w.add_cleared(vp, a.v.token, first, min(first + W::BN, at.lk));
+        if (t + 1 < to && first + W::BN < wave_end) w.scores(kbuf + (now ^ 1) * W::kTile);
+      }
     }
     // A result that is not finite: a value that a query must not see may have got in, so
     // the tiles that are hidden in part are gone through with care.
@@ -279,32 +381,108 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attention_prefill_kerne
   }
   const f32x2_t sums = both_halves(w.l);
   const float sum = sums.x + sums.y;
-  if (row >= at.lq) return;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  uint16_t* y = a.y + (token * a.heads + head) * D + 4 * w.half;
+  if (n > 1) {
+    float* part = work.parts + (share.record + share.split) * (kRows * (D + 2));
+    float* ml = part + kRows * D + 64 * w.wave;
+    part += w.wave * (32 * D);
 #pragma unroll
-  for (int d = 0; d < W::DT; ++d)
+    for (int d = 0; d < W::DT; ++d)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      *(u32x2*)(y + 32 * d + 8 * e) = u32x2{W::H::pack(w.o[d][4 * e] * inv, w.o[d][4 * e + 1] * inv),
-                                            W::H::pack(w.o[d][4 * e + 2] * inv, w.o[d][4 * e + 3] * inv)};
-  if (a.lse && !w.half) a.lse[token * a.heads + head] = sum == 0.f ? -INFINITY : w.m * kLn2 + logf(sum);
+      for (int e = 0; e < 4; ++e)
+        *(f32x4*)(part + 4 * (64 * (4 * d + e) + w.lane)) =
+            f32x4{w.o[d][4 * e], w.o[d][4 * e + 1], w.o[d][4 * e + 2], w.o[d][4 * e + 3]};
+    ml[w.lane] = w.half ? sum : w.m;
+    return;
+  }
+  if (row < at.lq) w.store(a, token, head, sum);
+}
+
+// Rows whose keys several blocks shared.
+template <bool F16, int D>
+__global__ __launch_bounds__(256) void attention_prefill_join_kernel(PrefillArgs a, PrefillWork work) {
+  using W = Prefill<F16, D>;
+  const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const Share share = share_of(a, work, block, 1);
+  const Place& at = share.at;
+  if (!at.found) return;
+  W w;
+  w.lane = threadIdx.x & 63;
+  w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  w.half = w.lane >> 5;
+  const int queries = kRows / work.heads, first_query = at.tile * queries;
+  const int tiles = (keys_seen(a, at, first_query + queries - 1) + W::BN - 1) / W::BN, n = shares(tiles, work.splits);
+  if (n == 1) return;
+  const int head = share.group * work.heads + w.wave % work.heads;
+  const int row = first_query + 32 * (w.wave / work.heads) + (w.lane & 31);
+  const float* part = work.parts + share.record * (kRows * (D + 2));
+  w.m = -INFINITY;
+  for (int i = 0; i < n; ++i) w.m = fmaxf(w.m, part[(int64_t)i * (kRows * (D + 2)) + kRows * D + 64 * w.wave + (w.lane & 31)]);
+  float sum = 0.f;
+#pragma unroll
+  for (int d = 0; d < W::DT; ++d) w.o[d] = f32x16{};
+  for (int i = 0; i < n; ++i) {
+    const float* r = part + (int64_t)i * (kRows * (D + 2));
+    const float* ml = r + kRows * D + 64 * w.wave + (w.lane & 31);
+    const float f = ml[0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[0] - w.m);
+    sum += ml[32] == 0.f ? 0.f : ml[32] * f;
+#pragma unroll
+    for (int d = 0; d < W::DT; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f32x4 x = *(const f32x4*)(r + w.wave * (32 * D) + 4 * (64 * (4 * d + e) + w.lane));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w.o[d][4 * e + j] += x[j] * f;
+      }
+  }
+  if (row < at.lq) w.store(a, at.q0 + row, head, sum);
+}
+
+PrefillWork work_of(const PrefillArgs& a) {
+  PrefillWork w{};
+  const int shared = a.heads / a.kv_heads;
+  w.heads = shared % 4 == 0 ? 4 : shared % 2 == 0 ? 2 : 1;
+  w.groups = a.heads / w.heads;
+  w.units = a.Tq / (kRows / w.heads) + std::min(a.n, a.Tq);
+  // Two blocks fill a CU.  With fewer, several take the keys of one, if there are enough
+  // of these.
+  const int64_t fill = 512, blocks = w.units * w.groups;
+  const int64_t tiles = a.Tk / ((a.D == 256 ? 32 : 64) * kSplitTiles);
+  w.splits = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, (fill + blocks / 2) / blocks, tiles}));
+  return w;
 }
 
 }  // namespace
 
 int64_t prefill_blocks(const PrefillArgs& a) {
-  return (a.Tq / kQRows + std::min(a.n, a.Tq)) * a.heads;
+  const PrefillWork w = work_of(a);
+  return w.units * w.groups * w.splits;
 }
 
-hipError_t launch_attention_prefill(const PrefillArgs& a, hipStream_t stream) {
-  const int64_t blocks = prefill_blocks(a), x = std::min<int64_t>(blocks, 1 << 20);
-  const dim3 grid((unsigned)x, (unsigned)((blocks + x - 1) / x));
-  auto kernel = a.f16 ? (a.D == 64 ? attention_prefill_kernel<true, 64> : a.D == 128 ? attention_prefill_kernel<true, 128>
-                                                                                     : attention_prefill_kernel<true, 256>)
-                      : (a.D == 64 ? attention_prefill_kernel<false, 64> : a.D == 128 ? attention_prefill_kernel<false, 128>
-                                                                                      : attention_prefill_kernel<false, 256>);
-  kernel<<<grid, 256, 0, stream>>>(a, blocks);
+int64_t prefill_workspace_bytes(const PrefillArgs& a) {
+  const PrefillWork w = work_of(a);
+  return w.splits > 1 ? w.units * w.groups * w.splits * kRows * (a.D + 2) * 4 : 0;
+}
+
+hipError_t launch_attention_prefill(const PrefillArgs& a, void* ws, hipStream_t stream) {
+  PrefillWork w = work_of(a);
+  w.parts = (float*)ws;
+  auto grid = [](int64_t blocks) {
+    const int64_t x = std::min<int64_t>(blocks, 1 << 20);
+    return dim3((unsigned)x, (unsigned)((blocks + x - 1) / x));
+  };
+  auto by_dim = [&](auto f16, auto dim) {
+    constexpr bool F = decltype(f16)::value;
+    constexpr int D = decltype(dim)::value;
+    attention_prefill_kernel<F, D><<<grid(w.units * w.groups * w.splits), 256, 0, stream>>>(a, w);
+    if (w.splits > 1) attention_prefill_join_kernel<F, D><<<grid(w.units * w.groups), 256, 0, stream>>>(a, w);
+  };
+  auto by_type = [&](auto f16) {
+    if (a.D == 64) by_dim(f16, std::integral_constant<int, 64>{});
+    else if (a.D == 128) by_dim(f16, std::integral_constant<int, 128>{});
+    else by_dim(f16, std::integral_constant<int, 256>{});
+  };
+  if (a.f16) by_type(std::true_type{});
+  else by_type(std::false_type{});
   return hipGetLastError();
 }
 

@@ -568,11 +568,22 @@ bool good_scale(float scale) { return scale > 0.f && !std::isinf(scale); }
 
 }  // namespace
 
+int64_t moe_attention_prefill_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64_t n_seqs, int32_t heads,
+                                              int32_t kv_heads, int32_t head_dim) {
+  if (q_tokens < 0 || k_tokens < 0 || q_tokens > moe::kAttnMaxTokens || k_tokens > moe::kAttnMaxTokens || n_seqs < 0 ||
+      n_seqs > (1 << 22) || check_heads(heads, kv_heads, head_dim))
+    return -1;
+  if (q_tokens == 0 || n_seqs == 0) return 0;
+  moe::PrefillArgs a{};
+  a.Tq = q_tokens, a.Tk = k_tokens, a.n = n_seqs, a.heads = heads, a.kv_heads = kv_heads, a.D = head_dim;
+  return moe::prefill_workspace_bytes(a);
+}
+
 int32_t moe_attention_prefill(int32_t type, const void* q, int64_t q_tokens, int32_t heads, int64_t q_token,
                               int64_t q_head, const void* k, const void* v, int64_t k_tokens, int32_t kv_heads,
                               int64_t k_token, int64_t k_head, int64_t v_token, int64_t v_head, int32_t head_dim,
                               const int32_t* q_starts, const int32_t* k_starts, int64_t n_seqs, int32_t causal,
-                              float scale, void* y, float* lse, void* stream) {
+                              float scale, void* y, float* lse, void* ws, int64_t ws_bytes, void* stream) {
   if (!half_type(type)) return bad_type(type);
   if (const int32_t rc = check_heads(heads, kv_heads, head_dim)) return rc;
   if (q_tokens < 0 || k_tokens < 0 || q_tokens > moe::kAttnMaxTokens || k_tokens > moe::kAttnMaxTokens)
@@ -594,11 +605,16 @@ int32_t moe_attention_prefill(int32_t type, const void* q, int64_t q_tokens, int
     return fail(MOE_E_ARG, "y must be 16-byte, lse and the starts 4-byte aligned");
   if (moe::prefill_blocks(a) > ((int64_t)1 << 36))
     return fail(MOE_E_SHAPE, "%lld tokens of %d heads exceed one launch", (long long)q_tokens, (int)heads);
-  if (collide({{y, q_tokens * heads * head_dim * 2}, {lse, q_tokens * heads * 4}, extent(a.q, q_tokens, heads, head_dim),
+  const int64_t need = moe::prefill_workspace_bytes(a);
+  if (need && !ws) return fail(MOE_E_ARG, "NULL workspace");
+  if ((uintptr_t)ws % kAlign) return fail(MOE_E_ARG, "workspace must be 256-byte aligned");
+  if (ws_bytes < need)
+    return fail(MOE_E_SPACE, "workspace holds %lld bytes, %lld needed", (long long)ws_bytes, (long long)need);
+  if (collide({{y, q_tokens * heads * head_dim * 2}, {lse, q_tokens * heads * 4}, {ws, need}, extent(a.q, q_tokens, heads, head_dim),
                extent(a.k, k_tokens, kv_heads, head_dim), extent(a.v, k_tokens, kv_heads, head_dim),
-               {q_starts, 4 * (n_seqs + 1)}, {k_starts, 4 * (n_seqs + 1)}}, 2))
-    return fail(MOE_E_ARG, "y or lse overlaps the other or an input");
-  const hipError_t e = moe::launch_attention_prefill(a, (hipStream_t)stream);
+               {q_starts, 4 * (n_seqs + 1)}, {k_starts, 4 * (n_seqs + 1)}}, 3))
+    return fail(MOE_E_ARG, "y, lse or the workspace overlaps another or an input");
+  const hipError_t e = moe::launch_attention_prefill(a, ws, (hipStream_t)stream);
   if (e != hipSuccess) return device_fail(e, "moe_attention_prefill launch");
   return ok();
 }

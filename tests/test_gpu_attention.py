@@ -145,6 +145,61 @@ def test_keys_before_and_missing(tq, D, causal):
     assert none.any() and torch.all(y[none] == 0)
 
 
+@pytest.mark.parametrize("lens,k_lens", [([3], [5000]), ([33, 1, 0, 64], [3000, 1100, 500, 40]), ([200], [2100])])
+@pytest.mark.parametrize("D,dtype", [(64, F16), (128, BF16), (256, BF16)])
+def test_few_queries_share_many_keys(tq, D, dtype, lens, k_lens):
+    """Several blocks have the keys of a tile of queries; the workspace holds rubbish before."""
+    H, Hk = 4, 1
+    say(f"shared keys {lens} over {k_lens} dim {D}")
+    need = tq.lib().moe_attention_prefill_workspace_bytes(sum(lens), sum(k_lens), len(lens), H, Hk, D)
+    assert need > 0
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    q, k, v = inputs(20, lens, k_lens, H, Hk, D, dtype)
+    for causal in (True, False):
+        lse = torch.empty((sum(lens), H), device="cuda")
+        y = tq.attention_prefill(q, k, v, starts_of(lens), starts_of(k_lens), causal=causal, lse=lse, workspace=ws)
+        want = oracle_of(q, k, v, lens, k_lens, causal, D ** -0.5)
+        want["size"] = 2 * want["size"]           # the shares are scaled and added once more
+        check(y, lse, want, dtype, D, max(k_lens), float(v.abs().max()))
+        assert torch.equal(y, tq.attention_prefill(q, k, v, starts_of(lens), starts_of(k_lens), causal=causal))
+
+
+def test_shared_keys_with_hidden_and_seen_infinities(tq):
+    say("shared keys, infinities")
+    q, k, v = (x.clone() for x in inputs(21, [40], [4000], 4, 2, 64, BF16, spread=0.1))
+    v[3970:, 0], v[3999, 1] = float("nan"), float("inf")   # the last 30 keys: query 10 is the first to see one
+    v[100, 1, 5], v[3900, 1, 6] = float("inf"), float("-inf")
+    y = tq.attention_prefill(q, k, v, ints([0, 40]), ints([0, 4000]))
+    assert torch.isfinite(y[:10, :2]).all() and torch.isnan(y[10:, :2]).all()
+    assert torch.isfinite(y[:39, 2:, 7:]).all() and torch.all(y[39, 2:, 7:] == float("inf"))
+    assert torch.all(y[:39, 2:, 5] == float("inf")) and torch.all(y[:39, 2:, 6] == float("-inf"))
+    assert torch.isnan(y[39, 2:, 6]).all()
+
+
+def test_graphs_share_a_workspace(tq):
+    say("graphs share a workspace")
+    a, b = inputs(22, [40], [3000], 4, 2, 64, BF16), inputs(23, [9], [5000], 4, 2, 64, BF16)
+    starts = [(ints([0, 40]), ints([0, 3000])), (ints([0, 9]), ints([0, 5000]))]
+    need = max(tq.lib().moe_attention_prefill_workspace_bytes(n, m, 1, 4, 2, 64) for n, m in ((40, 3000), (9, 5000)))
+    ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    ys, graphs = [torch.empty((n, 4, 64), dtype=BF16, device="cuda") for n in (40, 9)], []
+    for x, s, y in zip((a, b), starts, ys):
+        tq.attention_prefill(*x, *s, y=y, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            tq.attention_prefill(*x, *s, y=y, workspace=ws)
+        graphs.append(g)
+    for i in range(3):
+        for x in (a, b):
+            x[0].mul_(1 + 0.25 * i)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for x, s, y in zip((a, b), starts, ys):
+            assert torch.equal(y, tq.attention_prefill(*x, *s))
+
+
 def test_many_sequences(tq):
     """More sequences than lanes of a wave, most of them tiny or empty."""
     lens = [(7 * i) % 5 for i in range(300)]
