@@ -25,6 +25,7 @@
 
 #include "attention_device.h"
 #include "attention_internal.h"
+#include "wave_ops.h"
 
 namespace moe {
 
@@ -32,10 +33,14 @@ namespace {
 
 constexpr int kBlocks = 256;   // one a CU: a block's tiles fill the LDS
 constexpr int kHeadTile = 16;  // query heads of a block
-constexpr int kKeys = 32;      // tokens of a wave's tile
 
 template <int D>
 constexpr int kWaves = D == 256 ? 2 : 4;
+// Tokens of a wave's tile: what a wave does between a tile's arrival and its end is a chain
+// of latencies, so a tile has 64 tokens where these are short (64 channels, or 8 bits) and
+// 32 otherwise.
+template <bool F8, int D>
+constexpr int kTileTokens = F8 || D == 64 ? 64 : 32;
 
 int64_t groups_of(int heads, int kv_heads) {
   return (int64_t)kv_heads * ((heads / kv_heads + kHeadTile - 1) / kHeadTile);
@@ -58,7 +63,48 @@ __device__ __forceinline__ int swizzle(int r) {
   return ROW == 64 ? (r >> 2) & 3 : ROW == 128 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 3) : (r & 3) << 2 | ((r >> 2) & 3);
 }
 
+// A number at an address that the whole wave shares, read past the vector loads in flight:
+// those are waited for in order, and waiting for one waits for the tiles before it.
+__device__ __forceinline__ int scalar_load(const int32_t* p) {
+  return *(const int32_t __attribute__((address_space(4)))*)(uintptr_t)p;
+}
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Loads that go to LDS, lane after lane from dst on (the same in the whole wave).  They are
+// written out, since the compiler waits for every such load of its own before any read of
+// LDS, the tiles in flight among them; they write no register, and what needs them waits for
+// them here.  Between a scalar that the vector unit wrote and its use as a descriptor stand
+// five wait states, one between m0 and its use.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is set by every statement that uses it
+__device__ __forceinline__ uint32_t lds_address(uint8_t* p) {
+  return (uint32_t)uniform((int)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)p);
+}
+// A buffer over the bytes from p on (p the same in the whole wave), and 16 bytes a lane of it.
+__device__ __forceinline__ u32x4 buffer_from(const void* p) {
+  const uint64_t at = (uint64_t)(uintptr_t)p;
+  return u32x4{(uint32_t)uniform((int)at), (uint32_t)uniform((int)(at >> 32)), 0xFFFFFFFFu, 0x00027000u};
+}
+__device__ __forceinline__ void buffer_to_lds(u32x4 src, uint32_t lane_off, uint8_t* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds_address(dst)), "v"(lane_off),
+               "s"(src)
+               : "memory", "m0");
+}
+// 16 or 4 bytes a lane from the lane's address.
+__device__ __forceinline__ void copy16_to_lds(const void* src, uint8_t* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_address(dst)), "v"(src)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void copy4_to_lds(const void* src, uint8_t* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_address(dst)), "v"(src)
+               : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// a / b, in 32 bits where these do.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
 
 // Four e4m3 codes -> four 16-bit values (exact).
 template <bool F16>
@@ -71,19 +117,35 @@ __device__ __forceinline__ u32x2 widen4(uint32_t v) {
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v, 1.0f, true))};
 }
 
-// The value of lanes l ^ 16 and of l ^ 32 joined with the lane's own.
+// The value of the four lanes of a column, 16 apart, joined.
 template <class F>
 __device__ __forceinline__ float over_column(float v, F f) {
-  v = f(v, __shfl_xor(v, 16, 64));
-  return f(v, __shfl_xor(v, 32, 64));
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  const f32x2_t h = both_halves(f(__uint_as_float(r[0]), __uint_as_float(r[1])));
+  return f(h.x, h.y);
+}
+
+// Sums over the lanes up to each.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t shifted(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, true);
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += shifted<kDppShr1, 0xF>(v);
+  v += shifted<kDppShr2, 0xF>(v);
+  v += shifted<kDppShr4, 0xF>(v);
+  v += shifted<kDppShr8, 0xF>(v);
+  v += shifted<kDppBcast15, 0xA>(v);
+  return v + shifted<kDppBcast31, 0xC>(v);
 }
 
 template <bool F16, bool F8, int D>
 struct Decode {
   using H = Half<F16>;
-  static constexpr int W = kWaves<D>, ROW = D * (F8 ? 1 : 2), kTile = kKeys * ROW, PER = ROW / 16;
-  static constexpr int kLoads = kTile / 1024, kPerStage = 2 * kLoads + (F8 ? 1 : 0);
-  static constexpr int kStage = 2 * kTile + (F8 ? 256 : 0);
+  static constexpr int W = kWaves<D>, ROW = D * (F8 ? 1 : 2), kKeys = kTileTokens<F8, D>, PER = ROW / 16;
+  static constexpr int kTile = kKeys * ROW, ST = kKeys / 16;  // ST: score tiles
+  static constexpr int kLoads = kTile / 1024, kPerStage = 2 * kLoads + (F8 ? 2 : 0);
+  static constexpr int kStage = 2 * kTile + (F8 ? 8 * kKeys : 0);
   static constexpr int kFit = 126 * 1024 / (W * kStage), kStages = kFit > 4 ? 4 : kFit < 2 ? 2 : kFit;
   static constexpr int kBlockKeys = W * kKeys;
   static constexpr int kRecord = 64 * (D / 4 + 2);  // floats of a wave's state
@@ -110,7 +172,8 @@ struct Decode {
     return (int)min((int64_t)max(a.lengths[b], 0), room);
   }
   __device__ __forceinline__ void enter(Walk& w) const {
-    w.len = uniform(length(w.b));
+    const int64_t room = (int64_t)a.c.width * a.c.P;
+    w.len = (int)min((int64_t)max(scalar_load(a.lengths + w.b), 0), room);
     w.tiles = tiles_of(w.len);
   }
   __device__ __forceinline__ void step(Walk& w) const {
@@ -121,57 +184,76 @@ struct Decode {
     }
   }
 
-  // The page of lane % 32's token of the wave's tile.
+  static constexpr int ROWS = 64 / PER;  // rows of a load
+  __device__ __forceinline__ int first_of(const Walk& w) const { return w.tile * kBlockKeys + wave * kKeys; }
+  __device__ __forceinline__ const int32_t* table_of(const Walk& w) const { return a.c.tables + (int64_t)w.b * a.c.width; }
+
+  // Where a tile lies in one page, that page.
   __device__ __forceinline__ int page_of(const Walk& w) const {
-    const int key = min(w.tile * kBlockKeys + wave * kKeys + (lane & 31), max(w.len - 1, 0));
-    return a.c.width ? a.c.tables[(int64_t)w.b * a.c.width + (key >> a.c.shift)] : -1;
+    return a.c.width > 0 ? scalar_load(table_of(w) + (min(first_of(w), max(w.len - 1, 0)) >> a.c.shift)) : -1;
+  }
+  // Otherwise the page of every token goes to LDS, lane after lane, ahead of its tile.
+  __device__ __forceinline__ void pages_to_lds(const Walk& w, uint8_t* dst) const {
+    const int key = min(first_of(w) + (lane & (kKeys - 1)), max(w.len - 1, 0));
+    copy4_to_lds(a.c.width > 0 ? table_of(w) + (key >> a.c.shift) : a.lengths, dst);
   }
 
   // The wave's tile into LDS.  Rows behind the last token repeat it; they are masked.  A
   // page that is none makes the sequence's results NaN and is read as page 0.
-  __device__ __forceinline__ bool stage(const Walk& w, int page, uint8_t* dst) const {
-    const bool wrong = w.len > 0 && (page < 0 || page >= a.c.n_pages);
-    if (page < 0 || page >= a.c.n_pages) page = 0;
-    const int first = w.tile * kBlockKeys + wave * kKeys, last = max(w.len - 1, 0);
-    constexpr int ROWS = 64 / PER;
+  __device__ __forceinline__ bool stage(const Walk& w, int page, bool one_page, uint8_t* dst) const {
+    const int first = first_of(w), last = max(w.len - 1, 0);
+    const bool wrong = page < 0 || page >= a.c.n_pages || a.c.width == 0;
+    if (wrong) page = 0;
+    const int place = min(first + (lane & (kKeys - 1)), last) & (a.c.P - 1);  // of the lane's token in its page
+    if (one_page) {
+      const int from = min(first, last), end = last - from;
+      const int64_t at = (((int64_t)uniform(page) * a.c.kv_heads + kv) * a.c.P + (from & (a.c.P - 1))) * ROW;
+      const u32x4 from_k = buffer_from((const uint8_t*)a.c.k + at), from_v = buffer_from((const uint8_t*)a.c.v + at);
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int row = i * ROWS + lane / PER, piece = (lane % PER) ^ swizzle<ROW>(row);
-      const int64_t p = __shfl(page, row, 64);
-      const int64_t at = ((p * a.c.kv_heads + kv) * a.c.P + (min(first + row, last) & (a.c.P - 1))) * ROW + 16 * piece;
-      const auto to = (__attribute__((address_space(3))) void*)(dst + i * 1024);
-      const auto to_v = (__attribute__((address_space(3))) void*)(dst + kTile + i * 1024);
-      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)((const uint8_t*)a.c.k + at), to, 16, 0, 0);
-      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)((const uint8_t*)a.c.v + at), to_v, 16, 0,
-                                       0);
+      for (int i = 0; i < kLoads; ++i) {
+        const int row = i * ROWS + lane / PER;
+        const uint32_t off = min(row, end) * ROW + 16 * ((lane % PER) ^ swizzle<ROW>(row));
+        buffer_to_lds(from_k, off, dst + i * 1024);
+        buffer_to_lds(from_v, off, dst + kTile + i * 1024);
+      }
+    } else {
+      const int64_t mine = ((int64_t)page * a.c.kv_heads + kv) * a.c.P + place;  // the lane's token's row of the cache
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i) {
+        const int row = i * ROWS + lane / PER;
+        const int64_t at = __shfl(mine, row, 64) * ROW + 16 * ((lane % PER) ^ swizzle<ROW>(row));
+        copy16_to_lds((const uint8_t*)a.c.k + at, dst + i * 1024);
+        copy16_to_lds((const uint8_t*)a.c.v + at, dst + kTile + i * 1024);
+      }
     }
-    if (F8) {
-      const int row = lane & 31;
-      const int64_t at = ((int64_t)page * a.c.kv_heads + kv) * a.c.P + (min(first + row, last) & (a.c.P - 1));
-      const float* from = (lane < 32 ? a.c.k_scales : a.c.v_scales) + at;
-      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) void*)from,
-                                       (__attribute__((address_space(3))) void*)(dst + 2 * kTile), 4, 0, 0);
+    if (F8) {  // the scales: the keys', then the values'
+      const int64_t at = ((int64_t)page * a.c.kv_heads + kv) * a.c.P + place;
+      copy4_to_lds(a.c.k_scales + at, dst + 2 * kTile);
+      copy4_to_lds(a.c.v_scales + at, dst + 2 * kTile + 256);
     }
-    return wrong;
+    return wrong && w.len > 0;
   }
 
-  __device__ __forceinline__ void begin(int64_t b, int head0, int heads) {
+  // The queries of sequence b.
+  __device__ __forceinline__ void fetch(int64_t b, int head0, int heads, u32x4 (&to)[QS]) const {
+    const uint16_t* p = a.q.p + b * a.q.token + (head0 + min(col, heads - 1)) * a.q.head;
+#pragma unroll
+    for (int k = 0; k < QS; ++k)
+      to[k] = *(const u32x4*)(p + (F8 ? 64 * (k / 2) + 16 * quad + 8 * (k & 1) : 32 * k + 8 * quad));
+  }
+  __device__ __forceinline__ void begin() {
     m = -INFINITY;
     l = 0.f;
     bad = false;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[d] = f32x4{};
-    const uint16_t* p = a.q.p + b * a.q.token + (head0 + min(col, heads - 1)) * a.q.head;
-#pragma unroll
-    for (int k = 0; k < QS; ++k)
-      q[k] = *(const u32x4*)(p + (F8 ? 64 * (k / 2) + 16 * quad + 8 * (k & 1) : 32 * k + 8 * quad));
   }
 
   __device__ __forceinline__ void tile(const uint8_t* ks, int first, int len, float c) {
     const uint8_t* vs = ks + kTile;
-    f32x4 s[2];
+    f32x4 s[ST];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+    for (int t = 0; t < ST; ++t) {
       s[t] = f32x4{};
       const int row = 16 * t + col, at = row * ROW, f = swizzle<ROW>(row);
       if (F8) {
@@ -195,14 +277,14 @@ struct Decode {
     const bool whole = there >= kKeys;
     if (!whole) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < ST; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (16 * t + 4 * quad + i >= there) s[t][i] = -INFINITY;
     }
     float top = s[0][0];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < ST; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
     top = over_column(top, [](float x, float y) { return fmaxf(x, y); }) * c;
@@ -215,7 +297,7 @@ struct Decode {
     }
     const float off = m == -INFINITY ? 0.f : m;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < ST; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         s[t][i] = __builtin_amdgcn_exp2f(s[t][i] * c - off);
@@ -223,8 +305,8 @@ struct Decode {
       }
     if (F8) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        f32x4 scale = *(const f32x4*)(ks + 2 * kTile + 128 + 4 * (16 * t + 4 * quad));
+      for (int t = 0; t < ST; ++t) {
+        f32x4 scale = *(const f32x4*)(ks + 2 * kTile + 4 * kKeys + 4 * (16 * t + 4 * quad));
         if (!whole) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -234,43 +316,47 @@ struct Decode {
         for (int i = 0; i < 4; ++i) s[t][i] *= scale[i];
       }
     }
-    const u32x4 p = {H::pack(s[0][0], s[0][1]), H::pack(s[0][2], s[0][3]), H::pack(s[1][0], s[1][1]),
-                     H::pack(s[1][2], s[1][3])};
-    // k slot 8 quad + e of the product is token 16 (e / 4) + 4 quad + e % 4.  Values behind
-    // the last token become zeros: they may hold anything.
-    u32x4 keep = {~0u, ~0u, ~0u, ~0u};
-    if (!whole) {
+    // k slot 8 quad + e of a product over 32 tokens is token 16 (e / 4) + 4 quad + e % 4.
+    // Values behind the last token become zeros: they may hold anything.
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int row = 16 * (e / 2) + 4 * quad + 2 * (e & 1);
-        keep[e] = (row < there ? 0xFFFFu : 0u) | (row + 1 < there ? 0xFFFF0000u : 0u);
+    for (int h = 0; h < ST / 2; ++h) {
+      const f32x4 &s0 = s[2 * h], &s1 = s[2 * h + 1];
+      const u32x4 p = {H::pack(s0[0], s0[1]), H::pack(s0[2], s0[3]), H::pack(s1[0], s1[1]), H::pack(s1[2], s1[3])};
+      const uint8_t* half = vs + 32 * h * ROW;
+      u32x4 keep = {~0u, ~0u, ~0u, ~0u};
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = 32 * h + 16 * (e / 2) + 4 * quad + 2 * (e & 1);
+          keep[e] = (row < there ? 0xFFFFu : 0u) | (row + 1 < there ? 0xFFFF0000u : 0u);
+        }
       }
-    }
-    if (F8) {
-      const int j = col >> 1, row = 16 * (j / 4) + 4 * quad + (j & 3), f = swizzle<ROW>(row);
+      if (F8) {
+        const int j = col >> 1, row = 16 * (j / 4) + 4 * quad + (j & 3), f = swizzle<ROW>(row);
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        typedef int i32x2_t __attribute__((ext_vector_type(2)));
-        const i32x2_t v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (__attribute__((address_space(3))) i32x2_t*)(vs + row * ROW + 16 * (d ^ f) + 8 * (col & 1)));
-        const u32x2 lo = widen4<F16>((uint32_t)v.x), hi = widen4<F16>((uint32_t)v.y);
-        u32x4 w = {lo.x, lo.y, hi.x, hi.y};
-        if (!whole) w &= keep;
-        o[d] = H::mfma16(w, p, o[d]);
-      }
-    } else {
-      int at[2];
+        for (int d = 0; d < DT; ++d) {
+          typedef int i32x2_t __attribute__((ext_vector_type(2)));
+          const i32x2_t v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (__attribute__((address_space(3))) i32x2_t*)(half + row * ROW + 16 * (d ^ f) + 8 * (col & 1)));
+          const u32x2 lo = widen4<F16>((uint32_t)v.x), hi = widen4<F16>((uint32_t)v.y);
+          u32x4 w = {lo.x, lo.y, hi.x, hi.y};
+          if (!whole) w &= keep;
+          o[d] = H::mfma16(w, p, o[d]);
+        }
+      } else {
+        int at[2];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int row = 16 * t + 4 * quad + (col >> 2);
-        at[t] = row * ROW + 16 * (((col & 3) >> 1) ^ swizzle<ROW>(row)) + 8 * (col & 1);
-      }
+        for (int t = 0; t < 2; ++t) {
+          const int row = 16 * t + 4 * quad + (col >> 2);
+          at[t] = row * ROW + 16 * (((col & 3) >> 1) ^ swizzle<ROW>(row)) + 8 * (col & 1);
+        }
 #pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        const u32x2 lo = read_transposed(vs + (at[0] ^ (d << 5))), hi = read_transposed(vs + (at[1] ^ (d << 5)));
-        u32x4 w = {lo.x, lo.y, hi.x, hi.y};
-        if (!whole) w &= keep;
-        o[d] = H::mfma16(w, p, o[d]);
+        for (int d = 0; d < DT; ++d) {
+          const u32x2 lo = read_transposed(half + (at[0] ^ (d << 5))), hi = read_transposed(half + (at[1] ^ (d << 5)));
+          u32x4 w = {lo.x, lo.y, hi.x, hi.y};
+          if (!whole) w &= keep;
+          o[d] = H::mfma16(w, p, o[d]);
+        }
       }
     }
   }
@@ -312,9 +398,8 @@ struct Decode {
 template <bool F16, bool F8, int D>
 __global__ __launch_bounds__(64 * kWaves<D>) void attention_decode_kernel(DecodeArgs a, DecodeWork work) {
   using W = Decode<F16, F8, D>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[W::W * W::kStages * W::kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[W::W * (W::kStages * W::kStage + 512)];
   __shared__ float room[W::W / 2 * W::kRecord];
-  __shared__ int64_t found[2], sums[W::W];
   W w(a);
   w.lane = threadIdx.x & 63;
   w.wave = uniform(threadIdx.x >> 6);
@@ -325,128 +410,148 @@ __global__ __launch_bounds__(64 * kWaves<D>) void attention_decode_kernel(Decode
   const int shared = a.heads / a.c.kv_heads;
   const int head0 = w.kv * shared + group % work.per_kv * kHeadTile, heads = min(kHeadTile, shared - (head0 - w.kv * shared));
 
-  // the tiles of all sequences, and the sequence in which this worker's begin
-  constexpr int THREADS = 64 * W::W;
-  int64_t total = 0, before = 0, workers = 1;  // workers: as many as have a tile
-  for (int pass = 0; pass < 2; ++pass) {
-    const int64_t start = pass ? total * worker / workers : 0;
+  // The tiles of all sequences, and the sequence in which this worker's begin: every wave
+  // for itself, 64 sequences at a time (of fewer than 2^25 tiles each).
+  typename W::Walk now;
+  int64_t total = 0, before = 0, each = 0;
+  int extra = 0;  // a worker has `each` tiles, the first `extra` ones one more
+  {
+    int len = 0;
+    uint32_t n = 0, upto = 0;
+    auto chunk = [&](int64_t b0) {
+      const int64_t b = b0 + w.lane;
+      len = b < a.B ? w.length(b) : 0;
+      n = b < a.B ? w.tiles_of(len) : 0;
+      upto = wave_scan(n);
+      return (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+    };
+    for (int64_t b0 = 0; b0 < a.B; b0 += 64) total += chunk(b0);
+    each = quotient(total, work.workers);
+    extra = (int)(total - each * work.workers);
+    if (each == 0 && worker >= extra) return;
+    before = each * worker + min(worker, extra);
     int64_t base = 0;
-    for (int64_t b0 = 0; b0 < a.B; b0 += THREADS) {
-      const int64_t b = b0 + threadIdx.x;
-      const int n = b < a.B ? w.tiles_of(w.length(b)) : 0;
-      int64_t upto = n;
-#pragma unroll
-      for (int s = 1; s < 64; s <<= 1) {
-        const int64_t other = __shfl_up(upto, s, 64);
-        if (w.lane >= s) upto += other;
+    for (int64_t b0 = 0;; b0 += 64) {
+      if (a.B > 64) {
+        const uint32_t all = chunk(b0);
+        if (before - base >= all) {
+          base += all;
+          continue;
+        }
       }
-      if (w.lane == 63) sums[w.wave] = upto;
-      __syncthreads();
-      int64_t all = 0;
-#pragma unroll
-      for (int i = 0; i < W::W; ++i) {
-        if (i < w.wave) upto += sums[i];
-        all += sums[i];
-      }
-      if (pass && n && start < base + upto && start >= base + upto - n) {
-        found[0] = b;
-        found[1] = start - (base + upto - n);
-      }
-      __syncthreads();
-      base += all;
-    }
-    if (!pass) {
-      total = base;
-      workers = min((int64_t)work.workers, total);
-      if (worker >= workers) return;
-    } else {
-      before = start;
+      const int l = __builtin_ctzll(__ballot((uint32_t)(before - base) < upto));
+      now.b = (int)b0 + l;
+      now.len = __builtin_amdgcn_readlane(len, l);
+      now.tiles = __builtin_amdgcn_readlane((int)n, l);
+      now.tile = (int)(before - base) - (__builtin_amdgcn_readlane((int)upto, l) - now.tiles);
+      break;
     }
   }
-  const int64_t end = total * (worker + 1) / workers;
-  typename W::Walk now;
-  now.b = uniform((int)found[0]);
-  now.tile = uniform((int)found[1]);
-  now.left = end - before;
-  w.enter(now);
-  typename W::Walk ahead = now;
+  now.left = each + (worker < extra);
+  typename W::Walk ahead = now;  // the tile to load next
 
   w.mine = lds + w.wave * W::kStages * W::kStage;
   const float c = a.scale * kLog2e;
-  bool wrong[W::kStages];
-  int page = w.page_of(ahead);
-#pragma unroll
-  for (int i = 0; i < W::kStages - 1; ++i)
-    if (ahead.left > 0) {
-      wrong[i] = w.stage(ahead, page, w.mine + i * W::kStage);
-      w.step(ahead);
+  constexpr int AHEAD = W::kStages - 1;
+  uint32_t wrong = 0;  // a bit for each buffer: its tile's page is none
+  // The page numbers are read a tile before they are needed: one as a scalar, or the
+  // tokens' into LDS.
+  const bool one_page = a.c.P >= W::kKeys;
+  uint8_t* const ids = lds + W::W * W::kStages * W::kStage + w.wave * 512;
+  int page = 0, slot = 0, turn = 0;  // slot: the buffer of the next tile to load
+  if (one_page) {
+    page = w.page_of(ahead);
+  } else {
+    w.pages_to_lds(ahead, ids);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  }
+  auto load_next = [&] {
+    const typename W::Walk tile = ahead;
+    int of_tile = page;
+    w.step(ahead);
+    if (one_page) {
       if (ahead.left > 0) page = w.page_of(ahead);
+    } else {
+      // behind the numbers stand the loads of the tile before, and no others that were there
+      // when they were asked for
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(W::kPerStage) : "memory");
+      of_tile = *(const int*)(ids + 256 * turn + 4 * w.lane);
+      turn ^= 1;
+      w.pages_to_lds(ahead.left > 0 ? ahead : tile, ids + 256 * turn);
     }
-  w.begin(now.b, head0, heads);
+    const bool bad = w.stage(tile, of_tile, one_page, w.mine + slot * W::kStage);
+    wrong = (wrong & ~(1u << slot)) | (uint32_t)bad << slot;
+    slot = slot == AHEAD ? 0 : slot + 1;
+  };
+  for (int i = 0; i < AHEAD && ahead.left > 0; ++i) load_next();
+  w.fetch(now.b, head0, heads, w.q);
+  // the queries are waited for here: in the loop, waiting for them would wait for the tiles in flight
+#pragma unroll
+  for (int k = 0; k < W::QS; ++k) asm volatile("" : "+v"(w.q[k]));
+  w.begin();
   int from = now.tile;  // the first tile of the present sequence that this worker has
   int64_t tile0 = before - now.tile;  // the number of the sequence's first tile
   bool first_part = true;
+  int at = 0;           // the buffer of the present tile
   for (;;) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (ahead.left > 0) {
+      load_next();
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(AHEAD * W::kPerStage) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    w.bad |= wrong >> at & 1;
+    const bool last = now.left == 1, ends = now.tile + 1 == now.tiles;
+    u32x4 next_q[W::QS];
+    if (!last && ends) w.fetch(now.b + 1, head0, heads, next_q);
+    const int first = now.tile * W::kBlockKeys + w.wave * W::kKeys;
+    if (first < now.len) w.tile(w.mine + at * W::kStage, first, now.len, c);
+    at = at == AHEAD ? 0 : at + 1;
+    if (last || ends) {
+      w.join(room);
+      const bool whole = from == 0 && ends;
+      if (w.wave == 0) {
+        if (whole) {
+          const float inv = w.l == 0.f ? 0.f : 1.f / w.l;
+          if (w.col < heads) {
+            const int64_t row = (int64_t)now.b * a.heads + head0 + w.col;
+            uint16_t* y = a.y + row * D + 4 * w.quad;
 #pragma unroll
-    for (int slot = 0; slot < W::kStages; ++slot) {
-      constexpr int AHEAD = W::kStages - 1;
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (ahead.left > 0) {
-        wrong[(slot + AHEAD) % W::kStages] = w.stage(ahead, page, w.mine + (slot + AHEAD) % W::kStages * W::kStage);
-        w.step(ahead);
-        if (ahead.left > 0) page = w.page_of(ahead);
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(AHEAD * W::kPerStage) : "memory");
-      } else {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      }
-      w.bad |= wrong[slot];
-      const int first = now.tile * W::kBlockKeys + w.wave * kKeys;
-      if (first < now.len) w.tile(w.mine + slot * W::kStage, first, now.len, c);
-      const bool last = now.left == 1, ends = now.tile + 1 == now.tiles;
-      if (last || ends) {
-        w.join(room);
-        const bool whole = from == 0 && ends;
-        if (w.wave == 0) {
-          if (whole) {
-            const float inv = w.l == 0.f ? 0.f : 1.f / w.l;
-            if (w.col < heads) {
-              const int64_t row = (int64_t)now.b * a.heads + head0 + w.col;
-              uint16_t* y = a.y + row * D + 4 * w.quad;
-#pragma unroll
-              for (int d = 0; d < W::DT; ++d)
-                *(u32x2*)(y + 16 * d) = u32x2{W::H::pack(w.o[d].x * inv, w.o[d].y * inv),
-                                              W::H::pack(w.o[d].z * inv, w.o[d].w * inv)};
-              if (a.lse && w.quad == 0) a.lse[row] = w.l == 0.f ? -INFINITY : w.m * kLn2 + logf(w.l);
-            }
-          } else {
-            float* part = work.parts + (((int64_t)group * work.workers + worker) * 2 + (first_part ? 0 : 1)) *
-                                           (kHeadTile * D + 2 * kHeadTile);
-#pragma unroll
-            for (int d = 0; d < W::DT; ++d) *(f32x4*)(part + w.col * D + 16 * d + 4 * w.quad) = w.o[d];
-            if (w.quad == 0) {
-              part[kHeadTile * D + w.col] = w.m;
-              part[kHeadTile * D + kHeadTile + w.col] = w.l;
-            }
+            for (int d = 0; d < W::DT; ++d)
+              *(u32x2*)(y + 16 * d) = u32x2{W::H::pack(w.o[d].x * inv, w.o[d].y * inv),
+                                            W::H::pack(w.o[d].z * inv, w.o[d].w * inv)};
+            if (a.lse && w.quad == 0) a.lse[row] = w.l == 0.f ? -INFINITY : w.m * kLn2 + logf(w.l);
           }
-          // the worker that has a sequence's first tile says who else has some of it
-          if (work.workers > 1 && group == 0 && from == 0 && w.lane == 0) {
-            const int64_t t = tile0 + now.tiles - 1;
-            int64_t to = t * workers / total;
-            while (total * (to + 1) / workers <= t) ++to;
-            while (total * to / workers > t) --to;
-            work.shared[now.b] = int2{(int)(first_part ? worker : ~worker), (int)to};
+        } else {
+          float* part = work.parts + (((int64_t)group * work.workers + worker) * 2 + (first_part ? 0 : 1)) *
+                                         (kHeadTile * D + 2 * kHeadTile);
+#pragma unroll
+          for (int d = 0; d < W::DT; ++d) *(f32x4*)(part + w.col * D + 16 * d + 4 * w.quad) = w.o[d];
+          if (w.quad == 0) {
+            part[kHeadTile * D + w.col] = w.m;
+            part[kHeadTile * D + kHeadTile + w.col] = w.l;
           }
         }
-        if (last) return;
-        first_part = false;
-        from = 0;
-        tile0 += now.tiles;
-        w.step(now);
-        w.begin(now.b, head0, heads);
-      } else {
-        w.step(now);
+        // the worker that has a sequence's first tile says who else has some of it
+        if (work.workers > 1 && group == 0 && from == 0 && w.lane == 0) {
+          const int64_t t = tile0 + now.tiles - 1, more = extra * (each + 1);
+          const int64_t to = t < more ? quotient(t, each + 1) : extra + quotient(t - more, each);
+          work.shared[now.b] = int2{first_part ? worker : ~worker, (int)to};
+        }
+      }
+      if (last) return;
+      first_part = false;
+      from = 0;
+      tile0 += now.tiles;
+      w.begin();
+#pragma unroll
+      for (int k = 0; k < W::QS; ++k) {
+        w.q[k] = next_q[k];
+        asm volatile("" : "+v"(w.q[k]));
       }
     }
+    w.step(now);
   }
 }
 

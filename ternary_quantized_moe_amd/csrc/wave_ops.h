@@ -12,6 +12,8 @@ namespace moe {
 // rows are then combined from one lane each with readlane.
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
 constexpr int kDppShr1 = 0x111, kDppShr2 = 0x112, kDppShr4 = 0x114, kDppShr8 = 0x118;
+// Lane 15 of a row to the next row, and lane 31 to the rows 2 and 3.
+constexpr int kDppBcast15 = 0x142, kDppBcast31 = 0x143;
 
 template <int CTRL>
 __device__ __forceinline__ int dpp_i32(int v) {
