@@ -80,14 +80,14 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 __device__ __forceinline__ uint32_t lds_address(uint8_t* p) {
   return (uint32_t)uniform((int)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)p);
 }
-// A buffer over the bytes from p on (p the same in the whole wave), and 16 bytes a lane of it.
+// A buffer over the bytes from p on (p the same in the whole wave), and 16 bytes a lane of it, from lane_off + off on.
 __device__ __forceinline__ u32x4 buffer_from(const void* p) {
   const uint64_t at = (uint64_t)(uintptr_t)p;
   return u32x4{(uint32_t)uniform((int)at), (uint32_t)uniform((int)(at >> 32)), 0xFFFFFFFFu, 0x00027000u};
 }
-__device__ __forceinline__ void buffer_to_lds(u32x4 src, uint32_t lane_off, uint8_t* dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds_address(dst)), "v"(lane_off),
-               "s"(src)
+__device__ __forceinline__ void buffer_to_lds(u32x4 src, uint32_t lane_off, int off, uint8_t* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds_address(dst)), "v"(lane_off),
+               "s"(src), "s"(off)
                : "memory", "m0");
 }
 // 16 or 4 bytes a lane from the lane's address.
@@ -123,6 +123,13 @@ __device__ __forceinline__ float over_column(float v, F f) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   const f32x2_t h = both_halves(f(__uint_as_float(r[0]), __uint_as_float(r[1])));
   return f(h.x, h.y);
+}
+
+// Reads eight rows of 16 bytes transposed: within 16 lanes, lane i gives the address of
+// bytes 8 (i % 2) .. + 7 of row i / 2 and gets byte i of the eight rows.
+__device__ __forceinline__ u32x2 read_transposed8(const uint8_t* p) {
+  typedef int i32x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2_t*)(p)));
 }
 
 // Sums over the lanes up to each.
@@ -209,12 +216,23 @@ struct Decode {
       const int from = min(first, last), end = last - from;
       const int64_t at = (((int64_t)uniform(page) * a.c.kv_heads + kv) * a.c.P + (from & (a.c.P - 1))) * ROW;
       const u32x4 from_k = buffer_from((const uint8_t*)a.c.k + at), from_v = buffer_from((const uint8_t*)a.c.v + at);
+      if (end >= kKeys - 1) {
+        // a lane's places in the loads differ by whole loads and in the swizzle
+        const uint32_t lane_off = lane / PER * ROW + 16 * ((lane % PER) ^ swizzle<ROW>(lane / PER));
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int row = i * ROWS + lane / PER;
-        const uint32_t off = min(row, end) * ROW + 16 * ((lane % PER) ^ swizzle<ROW>(row));
-        buffer_to_lds(from_k, off, dst + i * 1024);
-        buffer_to_lds(from_v, off, dst + kTile + i * 1024);
+        for (int i = 0; i < kLoads; ++i) {
+          const uint32_t off = lane_off ^ (16 * swizzle<ROW>(i * ROWS));
+          buffer_to_lds(from_k, off, i * 1024, dst + i * 1024);
+          buffer_to_lds(from_v, off, i * 1024, dst + kTile + i * 1024);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+          const int row = i * ROWS + lane / PER;
+          const uint32_t off = min(row, end) * ROW + 16 * ((lane % PER) ^ swizzle<ROW>(row));
+          buffer_to_lds(from_k, off, 0, dst + i * 1024);
+          buffer_to_lds(from_v, off, 0, dst + kTile + i * 1024);
+        }
       }
     } else {
       const int64_t mine = ((int64_t)page * a.c.kv_heads + kv) * a.c.P + place;  // the lane's token's row of the cache
@@ -251,27 +269,66 @@ struct Decode {
 
   __device__ __forceinline__ void tile(const uint8_t* ks, int first, int len, float c) {
     const uint8_t* vs = ks + kTile;
-    f32x4 s[ST];
+    // All of the tile's keys are read before the first product: the reads' latencies then
+    // run side by side.
+    constexpr int KP = F8 ? D / 64 : QS;  // pieces of a row a lane reads
+    u32x4 kf[ST][KP];
 #pragma unroll
     for (int t = 0; t < ST; ++t) {
-      s[t] = f32x4{};
       const int row = 16 * t + col, at = row * ROW, f = swizzle<ROW>(row);
-      if (F8) {
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          const u32x4 v = *(const u32x4*)(ks + at + 16 * ((4 * j + quad) ^ f));
+      for (int k = 0; k < KP; ++k) kf[t][k] = *(const u32x4*)(ks + at + 16 * ((4 * k + quad) ^ f));
+    }
+    f32x4 k_scale[ST], v_scale[ST];
+    if (F8) {
+#pragma unroll
+      for (int t = 0; t < ST; ++t) {
+        k_scale[t] = *(const f32x4*)(ks + 2 * kTile + 4 * (16 * t + 4 * quad));
+        v_scale[t] = *(const f32x4*)(ks + 2 * kTile + 4 * kKeys + 4 * (16 * t + 4 * quad));
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4 s[ST];
+#pragma unroll
+    for (int t = 0; t < ST; ++t) s[t] = f32x4{};
+#pragma unroll
+    for (int k = 0; k < KP; ++k)
+#pragma unroll
+      for (int t = 0; t < ST; ++t) {
+        const u32x4 v = kf[t][k];
+        if (F8) {
           const u32x2 w0 = widen4<F16>(v.x), w1 = widen4<F16>(v.y), w2 = widen4<F16>(v.z), w3 = widen4<F16>(v.w);
-          s[t] = H::mfma16(u32x4{w0.x, w0.y, w1.x, w1.y}, q[2 * j], s[t]);
-          s[t] = H::mfma16(u32x4{w2.x, w2.y, w3.x, w3.y}, q[2 * j + 1], s[t]);
+          s[t] = H::mfma16(u32x4{w0.x, w0.y, w1.x, w1.y}, q[2 * k], s[t]);
+          s[t] = H::mfma16(u32x4{w2.x, w2.y, w3.x, w3.y}, q[2 * k + 1], s[t]);
+        } else {
+          s[t] = H::mfma16(v, q[k], s[t]);
         }
-        const f32x4 scale = *(const f32x4*)(ks + 2 * kTile + 4 * (16 * t + 4 * quad));
+      }
+    // So are the values of the first 32 tokens, beside the softmax.
+    constexpr int VR = F8 ? 1 : 2;  // reads of a fragment
+    u32x2 vf[DT][VR];
+    auto read_values = [&](int h) {
+      const uint8_t* half = vs + 32 * h * ROW;
+      if (F8) {
+        const int j = col >> 1, row = 16 * (j / 4) + 4 * quad + (j & 3), f = swizzle<ROW>(row);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] *= scale[i];
+        for (int d = 0; d < DT; ++d) vf[d][0] = read_transposed8(half + row * ROW + 16 * (d ^ f) + 8 * (col & 1));
       } else {
 #pragma unroll
-        for (int k = 0; k < QS; ++k)
-          s[t] = H::mfma16(*(const u32x4*)(ks + at + 16 * ((4 * k + quad) ^ f)), q[k], s[t]);
+        for (int t = 0; t < 2; ++t) {
+          const int row = 16 * t + 4 * quad + (col >> 2);
+          const int at = row * ROW + 16 * (((col & 3) >> 1) ^ swizzle<ROW>(row)) + 8 * (col & 1);
+#pragma unroll
+          for (int d = 0; d < DT; ++d) vf[d][VR - 1 < t ? VR - 1 : t] = read_transposed(half + (at ^ (d << 5)));
+        }
       }
+    };
+    __builtin_amdgcn_sched_barrier(0);
+    read_values(0);
+    __builtin_amdgcn_sched_barrier(0);
+    if (F8) {
+#pragma unroll
+      for (int t = 0; t < ST; ++t) s[t] *= k_scale[t];
     }
     const int there = len - first;  // tokens of the tile that exist
     const bool whole = there >= kKeys;
@@ -305,16 +362,9 @@ struct Decode {
       }
     if (F8) {
 #pragma unroll
-      for (int t = 0; t < ST; ++t) {
-        f32x4 scale = *(const f32x4*)(ks + 2 * kTile + 4 * kKeys + 4 * (16 * t + 4 * quad));
-        if (!whole) {
+      for (int t = 0; t < ST; ++t)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (16 * t + 4 * quad + i >= there) scale[i] = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] *= scale[i];
-      }
+        for (int i = 0; i < 4; ++i) s[t][i] *= whole || 16 * t + 4 * quad + i < there ? v_scale[t][i] : 0.f;
     }
     // k slot 8 quad + e of a product over 32 tokens is token 16 (e / 4) + 4 quad + e % 4.
     // Values behind the last token become zeros: they may hold anything.
@@ -322,7 +372,6 @@ struct Decode {
     for (int h = 0; h < ST / 2; ++h) {
       const f32x4 &s0 = s[2 * h], &s1 = s[2 * h + 1];
       const u32x4 p = {H::pack(s0[0], s0[1]), H::pack(s0[2], s0[3]), H::pack(s1[0], s1[1]), H::pack(s1[2], s1[3])};
-      const uint8_t* half = vs + 32 * h * ROW;
       u32x4 keep = {~0u, ~0u, ~0u, ~0u};
       if (!whole) {
 #pragma unroll
@@ -331,32 +380,21 @@ struct Decode {
           keep[e] = (row < there ? 0xFFFFu : 0u) | (row + 1 < there ? 0xFFFF0000u : 0u);
         }
       }
-      if (F8) {
-        const int j = col >> 1, row = 16 * (j / 4) + 4 * quad + (j & 3), f = swizzle<ROW>(row);
+      if (h) {
+        __builtin_amdgcn_sched_barrier(0);
+        read_values(h);
+        __builtin_amdgcn_sched_barrier(0);
+      }
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          typedef int i32x2_t __attribute__((ext_vector_type(2)));
-          const i32x2_t v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-              (__attribute__((address_space(3))) i32x2_t*)(half + row * ROW + 16 * (d ^ f) + 8 * (col & 1)));
-          const u32x2 lo = widen4<F16>((uint32_t)v.x), hi = widen4<F16>((uint32_t)v.y);
-          u32x4 w = {lo.x, lo.y, hi.x, hi.y};
-          if (!whole) w &= keep;
-          o[d] = H::mfma16(w, p, o[d]);
+      for (int d = 0; d < DT; ++d) {
+        u32x2 lo = vf[d][0], hi = vf[d][VR - 1];
+        if (F8) {
+          hi = widen4<F16>(lo.y);
+          lo = widen4<F16>(lo.x);
         }
-      } else {
-        int at[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int row = 16 * t + 4 * quad + (col >> 2);
-          at[t] = row * ROW + 16 * (((col & 3) >> 1) ^ swizzle<ROW>(row)) + 8 * (col & 1);
-        }
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const u32x2 lo = read_transposed(half + (at[0] ^ (d << 5))), hi = read_transposed(half + (at[1] ^ (d << 5)));
-          u32x4 w = {lo.x, lo.y, hi.x, hi.y};
-          if (!whole) w &= keep;
-          o[d] = H::mfma16(w, p, o[d]);
-        }
+        u32x4 w = {lo.x, lo.y, hi.x, hi.y};
+        if (!whole) w &= keep;
+        o[d] = H::mfma16(w, p, o[d]);
       }
     }
   }
@@ -368,27 +406,24 @@ struct Decode {
     if (__any(bad)) l = NAN;
 #pragma unroll
     for (int n = W / 2; n; n /= 2) {
-      float* at = room + (wave % n) * kRecord + lane;
+      float* at = room + (wave % n) * kRecord;
+      f32x4* const sums = (f32x4*)at + lane;
+      at += 256 * DT + lane;
       if (wave >= n && wave < 2 * n) {
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) at[64 * (4 * d + i)] = o[d][i];
-        at[64 * 4 * DT] = m;
-        at[64 * (4 * DT + 1)] = l;
+        for (int d = 0; d < DT; ++d) sums[64 * d] = o[d];
+        at[0] = m;
+        at[64] = l;
       }
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       if (wave < n) {
-        const float m2 = at[64 * 4 * DT], l2 = at[64 * (4 * DT + 1)];
-        const float now = fmaxf(m, m2);
+        const float m2 = at[0], l2 = at[64], now = fmaxf(m, m2);
         const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
         const float f2 = m2 == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m2 - now);
         m = now;
         l = (l == 0.f ? 0.f : l * f) + (l2 == 0.f ? 0.f : l2 * f2);
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[d][i] = o[d][i] * f + at[64 * (4 * d + i)] * f2;
+        for (int d = 0; d < DT; ++d) o[d] = o[d] * f + sums[64 * d] * f2;
       }
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
@@ -399,7 +434,7 @@ template <bool F16, bool F8, int D>
 __global__ __launch_bounds__(64 * kWaves<D>) void attention_decode_kernel(DecodeArgs a, DecodeWork work) {
   using W = Decode<F16, F8, D>;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[W::W * (W::kStages * W::kStage + 512)];
-  __shared__ float room[W::W / 2 * W::kRecord];
+  __shared__ __attribute__((aligned(16))) float room[W::W / 2 * W::kRecord];
   W w(a);
   w.lane = threadIdx.x & 63;
   w.wave = uniform(threadIdx.x >> 6);
