@@ -666,46 +666,48 @@ def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, toke
     return tokens, probs
 
 
-def _heads(name, t, device, dtype, heads=None, dim=None, tokens=None):
-    """(pointer, token stride, head stride) of [tokens, heads, dim] with contiguous heads."""
+def _wrong_heads(name, t, device, dtype, shape):
+    """The refusal of a matrix of heads that _heads found wrong."""
     if t.get_device() != device:
-        raise MoeError(-1, f"{name} is on {t.device}, not on the current device cuda:{device}")
+        return MoeError(-1, f"{name} is on {t.device}, not on the current device cuda:{device}")
     if t.dtype != dtype:
-        raise MoeError(-2, f"{name} has type {t.dtype}, {dtype} wanted")
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim) or (
-            tokens is not None and t.shape[0] != tokens):
-        want = tuple("any" if x is None else x for x in (tokens, heads, dim))
-        raise MoeError(-3, f"{name} has shape {tuple(t.shape)}, {want} wanted")
-    n, h, d = t.shape
-    token, head, step = t.stride()
-    if step != 1 and d > 1 and n and h:
-        raise MoeError(-1, f"the heads of {name} are not contiguous")
-    head = head if h > 1 else d
-    return t.data_ptr(), token if n > 1 else h * d, head
+        return MoeError(-2, f"{name} has type {t.dtype}, {dtype} wanted")
+    if t.dim() != 3 or any(x is not None and x != n for x, n in zip(shape, t.shape)):
+        want = tuple("any" if x is None else x for x in shape)
+        return MoeError(-3, f"{name} has shape {tuple(t.shape)}, {want} wanted")
+    return MoeError(-1, f"the heads of {name} are not contiguous")
 
 
-def _ints(name, t, device, T, size):
-    return _operand(name, t, device, T["i32s"], size)
+def _heads(name, t, device, dtype, tokens=None, heads=None, dim=None):
+    """(pointer, token stride, head stride, tokens, heads, dim) of [tokens, heads, dim] with
+    contiguous heads.  (The good path is kept short: these calls are a few microseconds long.)"""
+    if t.dtype == dtype and t.dim() == 3 and t.get_device() == device:
+        n, h, d = t.shape
+        token, head, step = t.stride()
+        if (step == 1 or d < 2 or not n or not h) and (heads is None or h == heads) and (dim is None or d == dim) and (
+                tokens is None or n == tokens):
+            return t.data_ptr(), token if n > 1 else h * d, head if h > 1 else d, n, h, d
+    raise _wrong_heads(name, t, device, dtype, (tokens, heads, dim))
 
 
 def _cache(k, v, k_scales, v_scales, device, dtype, T):
     """(cache type, k, v, k_scales, v_scales, n_pages, kv_heads, page_size, dim) of a layer's cache."""
-    if k.dim() != 4:
-        raise MoeError(-3, f"k_cache has {k.dim()} dimensions, 4 wanted")
-    shape = k.shape
-    kind = T["heads"].get(k.dtype, E4M3 if k.dtype in T["codes"] else None)
-    kinds = T["codes"] if kind == E4M3 else (dtype,)
-    kp = _operand("k_cache", k, device, kinds, shape)
-    vp = _operand("v_cache", v, device, kinds, shape)
-    ksp = vsp = None
-    if kind == E4M3:
-        if k_scales is None or v_scales is None:
-            raise MoeError(-1, "an e4m3 cache needs k_scales and v_scales")
-        ksp = _operand("k_scales", k_scales, device, T["f32s"], shape[:3])
-        vsp = _operand("v_scales", v_scales, device, T["f32s"], shape[:3])
-    elif k_scales is not None or v_scales is not None:
-        raise MoeError(-1, "k_scales and v_scales go with e4m3 caches only")
-    return kind, kp, vp, ksp, vsp, shape[0], shape[1], shape[2], shape[3]
+    shape, kind = k.shape, k.dtype
+    if len(shape) != 4:
+        raise MoeError(-3, f"k_cache has {len(shape)} dimensions, 4 wanted")
+    if kind == dtype:
+        if k_scales is not None or v_scales is not None:
+            raise MoeError(-1, "k_scales and v_scales go with e4m3 caches only")
+        kinds = (dtype,)
+        return (T["heads"][dtype], _operand("k_cache", k, device, kinds, shape), _operand("v_cache", v, device, kinds, shape),
+                None, None, *shape)
+    kinds = T["codes"]
+    if kind in kinds and (k_scales is None or v_scales is None):
+        raise MoeError(-1, "an e4m3 cache needs k_scales and v_scales")
+    kp, vp = _operand("k_cache", k, device, kinds, shape), _operand("v_cache", v, device, kinds, shape)
+    rows, f32s = shape[:3], T["f32s"]
+    return (E4M3, kp, vp, _operand("k_scales", k_scales, device, f32s, rows), _operand("v_scales", v_scales, device, f32s, rows),
+            *shape)
 
 
 def attention_prefill(q, k, v, starts, k_starts=None, causal: bool = True, scale: Optional[float] = None, y=None,
@@ -722,16 +724,15 @@ def attention_prefill(q, k, v, starts, k_starts=None, causal: bool = True, scale
     kind = T["heads"].get(q.dtype)
     if kind is None:
         raise MoeError(-2, f"q has type {q.dtype}")
-    qp, q_token, q_head = _heads("q", q, dev, q.dtype)
-    n, H, D = q.shape
-    kp, k_token, k_head = _heads("k", k, dev, q.dtype, None, D)
-    m, Hk, _ = k.shape
-    vp, v_token, v_head = _heads("v", v, dev, q.dtype, Hk, D, m)
-    size = starts.shape
+    dtype = q.dtype
+    qp, q_token, q_head, n, H, D = _heads("q", q, dev, dtype)
+    kp, k_token, k_head, m, Hk, _ = _heads("k", k, dev, dtype, None, None, D)
+    vp, v_token, v_head, _, _, _ = _heads("v", v, dev, dtype, m, Hk, D)
+    size, i32s = starts.shape, T["i32s"]
     if len(size) != 1 or size[0] < 1:
         raise MoeError(-3, f"starts has shape {tuple(size)}, one more than the sequences wanted")
-    sp = _ints("starts", starts, dev, T, size)
-    ksp = None if k_starts is None else _ints("k_starts", k_starts, dev, T, size)
+    sp = _operand("starts", starts, dev, i32s, size)
+    ksp = None if k_starts is None else _operand("k_starts", k_starts, dev, i32s, size)
     if y is None:
         y = q.new_empty((n, H, D))
         yp = y.data_ptr()
@@ -768,14 +769,14 @@ def attention_decode(q, k_cache, v_cache, tables, lengths, k_scales=None, v_scal
     kind = T["heads"].get(q.dtype)
     if kind is None:
         raise MoeError(-2, f"q has type {q.dtype}")
-    qp, q_row, q_head = _heads("q", q, dev, q.dtype)
-    B, H, D = q.shape
-    ck, kp, vp, ksp, vsp, pages, Hk, P, cd = _cache(k_cache, v_cache, k_scales, v_scales, dev, q.dtype, T)
+    dtype, i32s = q.dtype, T["i32s"]
+    qp, q_row, q_head, B, H, D = _heads("q", q, dev, dtype)
+    ck, kp, vp, ksp, vsp, pages, Hk, P, cd = _cache(k_cache, v_cache, k_scales, v_scales, dev, dtype, T)
     if cd != D:
         raise MoeError(-3, f"the cache has dim {cd}, q has {D}")
     width = tables.shape[1] if tables.dim() == 2 else -1
-    tp = _ints("tables", tables, dev, T, (B, width))
-    lenp = _ints("lengths", lengths, dev, T, (B,))
+    tp = _operand("tables", tables, dev, i32s, (B, width))
+    lenp = _operand("lengths", lengths, dev, i32s, (B,))
     if y is None:
         y = q.new_empty((B, H, D))
         yp = y.data_ptr()
@@ -813,39 +814,43 @@ def kv_append(k, v, k_cache, v_cache, tables, rows, positions, k_scales=None, v_
     kind = T["heads"].get(k.dtype)
     if kind is None:
         raise MoeError(-2, f"k has type {k.dtype}")
-    kp, k_token, k_head = _heads("k", k, dev, k.dtype)
-    n, Hk, D = k.shape
-    vp, v_token, v_head = _heads("v", v, dev, k.dtype, Hk, D, n)
-    ck, kcp, vcp, ksp, vsp, pages, ch, P, cd = _cache(k_cache, v_cache, k_scales, v_scales, dev, k.dtype, T)
+    dtype, i32s = k.dtype, T["i32s"]
+    kp, k_token, k_head, n, Hk, D = _heads("k", k, dev, dtype)
+    vp, v_token, v_head, _, _, _ = _heads("v", v, dev, dtype, n, Hk, D)
+    ck, kcp, vcp, ksp, vsp, pages, ch, P, cd = _cache(k_cache, v_cache, k_scales, v_scales, dev, dtype, T)
     if ch != Hk or cd != D:
         raise MoeError(-3, f"the cache has {ch} heads of {cd}, k has {Hk} of {D}")
     if tables.dim() != 2:
         raise MoeError(-3, f"tables has {tables.dim()} dimensions, 2 wanted")
-    tp = _ints("tables", tables, dev, T, tables.shape)
-    rp = _ints("rows", rows, dev, T, (n,))
-    pp = _ints("positions", positions, dev, T, (n,))
+    tp = _operand("tables", tables, dev, i32s, tables.shape)
+    R, width = tables.shape
+    rp = _operand("rows", rows, dev, i32s, (n,))
+    pp = _operand("positions", positions, dev, i32s, (n,))
     out = {}
     fp = qp = qop = kop = None
     H = rotary = q_token = q_head = qo_token = qo_head = ko_token = ko_head = 0
     if inv_freq is not None:
-        rotary = 2 * inv_freq.numel()
-        fp = _operand("inv_freq", inv_freq, dev, T["f32s"], (rotary // 2,))
+        half = inv_freq.numel()
+        rotary = 2 * half
+        fp = _operand("inv_freq", inv_freq, dev, T["f32s"], (half,))
     if q is not None:
-        qp, q_token, q_head = _heads("q", q, dev, k.dtype, None, D, n)
-        H = q.shape[1]
+        qp, q_token, q_head, _, H, _ = _heads("q", q, dev, dtype, n, None, D)
         if q_out is None:
             q_out = q.new_empty((n, H, D))
-        qop, qo_token, qo_head = _heads("q_out", q_out, dev, k.dtype, H, D, n)
+            qop, qo_token, qo_head = q_out.data_ptr(), H * D, D
+        else:
+            qop, qo_token, qo_head, _, _, _ = _heads("q_out", q_out, dev, dtype, n, H, D)
         out["q"] = q_out
     elif q_out is not None:
         raise MoeError(-1, "q_out needs a q")
-    if rotated_k or k_out is not None:
-        if k_out is None:
-            k_out = k.new_empty((n, Hk, D))
-        kop, ko_token, ko_head = _heads("k_out", k_out, dev, k.dtype, Hk, D, n)
+    if k_out is not None:
+        kop, ko_token, ko_head, _, _, _ = _heads("k_out", k_out, dev, dtype, n, Hk, D)
         out["k"] = k_out
+    elif rotated_k:
+        k_out = out["k"] = k.new_empty((n, Hk, D))
+        kop, ko_token, ko_head = k_out.data_ptr(), Hk * D, D
     rc = lib().moe_kv_append(kind, qp, q_token, q_head, H, kp, k_token, k_head, vp, v_token, v_head, n, ck, kcp, vcp, ksp,
-                             vsp, pages, Hk, P, D, tp, tables.shape[0], tables.shape[1], rp, pp, fp, rotary, interleaved,
+                             vsp, pages, Hk, P, D, tp, R, width, rp, pp, fp, rotary, interleaved,
                              qop, qo_token, qo_head, kop, ko_token, ko_head,
                              T["stream"](dev) if stream is None else _on(stream, dev, *out.values()))
     if rc:
@@ -877,8 +882,9 @@ def _pages(tables, lengths, refs, T):
         raise MoeError(-3, f"tables has {tables.dim()} dimensions and refs {refs.dim()}, 2 and 1 wanted")
     R, W = tables.shape
     n = refs.shape[0]
-    return dev, R, n, (_ints("tables", tables, dev, T, (R, W)), R, W, _ints("lengths", lengths, dev, T, (R,)),
-                       _ints("refs", refs, dev, T, (n,)), n)
+    i32s = T["i32s"]
+    return dev, R, n, (_operand("tables", tables, dev, i32s, (R, W)), R, W, _operand("lengths", lengths, dev, i32s, (R,)),
+                       _operand("refs", refs, dev, i32s, (n,)), n)
 
 
 def _pages_space(workspace, like, R, n, T):
@@ -894,8 +900,9 @@ def _pages_space(workspace, like, R, n, T):
 
 def _status(status, like, dev, R, T):
     if status is None:
-        status = like.new_empty((R,))
-    return status, _ints("status", status, dev, T, (R,))
+        status = T["like"](like)
+        return status, status.data_ptr()
+    return status, _operand("status", status, dev, T["i32s"], (R,))
 
 
 def kv_reserve(tables, lengths, refs, grow, page_size: int, status=None, workspace=None, stream=None):
@@ -905,7 +912,7 @@ def kv_reserve(tables, lengths, refs, grow, page_size: int, status=None, workspa
     for a negative grow or a table too narrow, -2 where the free pages did not reach."""
     T = _types()
     dev, R, n, head = _pages(tables, lengths, refs, T)
-    gp = _ints("grow", grow, dev, T, (R,))
+    gp = _operand("grow", grow, dev, T["i32s"], (R,))
     status, sp = _status(status, lengths, dev, R, T)
     workspace, ws, wn = _pages_space(workspace, tables, R, n, T)
     rc = lib().moe_kv_reserve(*head, page_size, gp, sp, ws, wn,
@@ -922,7 +929,7 @@ def kv_fork(tables, lengths, refs, parents, page_size: int, pools, status=None, 
     row or parent that does not do, -2 where the free pages did not reach."""
     T = _types()
     dev, R, n, head = _pages(tables, lengths, refs, T)
-    pp = _ints("parents", parents, dev, T, (R,))
+    pp = _operand("parents", parents, dev, T["i32s"], (R,))
     status, sp = _status(status, lengths, dev, R, T)
     c, count = _pools(pools, dev, n)
     workspace, ws, wn = _pages_space(workspace, tables, R, n, T)
@@ -937,7 +944,7 @@ def kv_free(tables, lengths, refs, drop, page_size: int, stream=None):
     """The rows with drop[r] != 0 (int32 [rows]) give their pages back and get length 0."""
     T = _types()
     dev, R, n, head = _pages(tables, lengths, refs, T)
-    dp = _ints("drop", drop, dev, T, (R,))
+    dp = _operand("drop", drop, dev, T["i32s"], (R,))
     rc = lib().moe_kv_free(*head, page_size, dp, T["stream"](dev) if stream is None else _on(stream, dev))
     if rc:
         _check(rc)
@@ -956,9 +963,9 @@ def kv_compact(tables, lengths, refs, page_size: int, pools, new_tables=None, ne
         new_refs = T["like"](refs)
     if live is None:
         live = refs.new_empty((1,))
-    tp = _ints("new_tables", new_tables, dev, T, tables.shape)
-    rp = _ints("new_refs", new_refs, dev, T, (n,))
-    lp = _ints("live", live, dev, T, (1,))
+    tp = _operand("new_tables", new_tables, dev, T["i32s"], tables.shape)
+    rp = _operand("new_refs", new_refs, dev, T["i32s"], (n,))
+    lp = _operand("live", live, dev, T["i32s"], (1,))
     c, count = _pools(pools, dev, n)
     workspace, ws, wn = _pages_space(workspace, tables, R, n, T)
     rc = lib().moe_kv_compact(*head, page_size, c, count, tp, rp, lp, ws, wn,
@@ -976,7 +983,7 @@ def kv_copy_pages(pools, src, dst, stream=None):
     size = src.shape
     if len(size) != 1:
         raise MoeError(-3, f"src has shape {tuple(size)}, one dimension wanted")
-    sp, dp = _ints("src", src, dev, T, size), _ints("dst", dst, dev, T, size)
+    sp, dp = _operand("src", src, dev, T["i32s"], size), _operand("dst", dst, dev, T["i32s"], size)
     if not pools:
         return
     n = pools[0].shape[1] if pools[0].dim() > 1 else 0

@@ -14,40 +14,64 @@ namespace moe {
 namespace {
 
 // ------------------------------------------------------------------ append
-// One token a block.  Of a rotated head, channels i and i + R / 2 (or 2 i and 2 i + 1)
+// One token a block, or where there are few tokens several blocks.  Of a rotated head, channels i and i + R / 2 (or 2 i and 2 i + 1)
 // are one pair, turned by the angle position * inv_freq[i]:
 //   (a, b) -> (a cos - b sin, b cos + a sin).
 // The angle is formed and reduced to a fraction of a turn in fp64 (far positions keep
 // their bits), its sine and cosine in fp32, once a token and for all its heads.
-// Sixteen-byte pieces of a head row sit on neighbouring lanes, so a row's largest
-// magnitude, for e4m3, is a reduction among these, and a lane reads its piece's partner
-// itself; a row is read whole before any of it is written, so q and k may be written in
-// place.
+// A lane has two pieces of 16 bytes of a head row, a pair that is turned together where
+// there is one, and a row's lanes are neighbours, so a row's largest magnitude, for e4m3, is
+// a reduction among these; a row is read whole before any of it is written, so q and k may
+// be written in place.  The first rows are asked for before the angles and the page are known.
 constexpr int kAppendThreads = 256;
+constexpr int kAppendDeep = 2;  // rows a lane has in hand
 
-template <int D>
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
 #pragma unroll
-  for (int s = 1; s < D / 8; s <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, s, 64));
+  for (int s = 1; s < LANES; s <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, s, 64));
   return v;
 }
 
 template <bool F16, bool F8, int D>
-__global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
+__global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a, int blocks) {
   using H = Half<F16>;
-  constexpr int PER = D / 8;  // lanes of a head row
-  __shared__ float turn[2][D / 2];
-  const int64_t t = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  constexpr int PER = D / 8, LANES = PER / 2, ROWS = kAppendThreads / LANES, DEEP = kAppendDeep;
+  __shared__ __attribute__((aligned(16))) float turn[2][D / 2];
+  const int64_t unit = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, t = unit / blocks;
+  const int part = (int)(unit - t * blocks);
   if (t >= a.T) return;
   const int row = a.rows[t], position = a.positions[t];
-  if (row < 0) return;  // padding: everything stays as it was
+  const int nq = a.q.p ? a.heads : 0, kvh = a.c.kv_heads, rows = nq + 2 * kvh;
+  const int lane = threadIdx.x % LANES, half = a.rotary / 2;
+  // The lane's two pieces: a pair that is turned together, or two that stay (interleaved
+  // pairs lie in one piece).
+  const int pairs = a.rotary / 16;
+  const bool turned = lane < pairs;
+  const int piece = turned ? lane : pairs + lane, other = turned ? lane + pairs : piece + LANES - pairs;
+
+  u32x4 own[DEEP][2];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int u = 0; u < DEEP; ++u) {
+      const int r = r0 + u * ROWS;
+      if (r >= rows) continue;
+      const bool is_q = r < nq, is_k = !is_q && r < nq + kvh;
+      const HeadRows& from = is_q ? a.q : is_k ? a.k : a.v;
+      const uint16_t* x = from.p + t * from.token + (is_q ? r : is_k ? r - nq : r - nq - kvh) * from.head;
+      own[u][0] = *(const u32x4*)(x + 8 * piece);
+      own[u][1] = *(const u32x4*)(x + 8 * other);
+    }
+  };
+  const int step = ROWS * blocks * DEEP, first = part * ROWS * DEEP + threadIdx.x / LANES;
+  if (row >= 0) load(first);
+
   int64_t page = -1;
-  if (row < a.c.rows && position >= 0 && (position >> a.c.shift) < a.c.width) {
+  if (row >= 0 && row < a.c.rows && position >= 0 && (position >> a.c.shift) < a.c.width) {
     page = a.c.tables[row * (int64_t)a.c.width + (position >> a.c.shift)];
     if (page >= a.c.n_pages) page = -1;
   }
   const bool wrong = page < 0;
-  const int half = a.rotary / 2;
   if (threadIdx.x < half) {
     const double turns = (double)position * (double)a.inv_freq[threadIdx.x] * 0.15915494309189533577;
     float s, c;
@@ -56,52 +80,75 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a)
     turn[1][threadIdx.x] = s;
   }
   __syncthreads();
-  const int nq = a.q.p ? a.heads : 0, kvh = a.c.kv_heads, rows = nq + 2 * kvh;
-  const int piece = threadIdx.x % PER;
-  for (int r = threadIdx.x / PER; r < rows; r += kAppendThreads / PER) {
-    const bool is_q = r < nq, is_k = !is_q && r < nq + kvh;
-    const HeadRows& from = is_q ? a.q : is_k ? a.k : a.v;
-    const HeadRows& to = is_q ? a.q_out : a.k_out;
-    const int h = is_q ? r : is_k ? r - nq : r - nq - kvh;
-    const uint16_t* x = from.p + t * from.token + h * from.head;
-    const u32x4 own = *(const u32x4*)(x + 8 * piece);
-    float f[8];
+  if (row < 0) return;  // padding: everything stays as it was
+  for (int r0 = first;;) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = H::widen(own[e / 2] >> (16 * (e & 1)));
-    if ((is_q || is_k) && 8 * piece < a.rotary) {
-      if (a.interleaved) {
+    for (int u = 0; u < DEEP; ++u) {
+      const int r = r0 + u * ROWS;
+      if (r >= rows) continue;
+      const bool is_q = r < nq, is_k = !is_q && r < nq + kvh;
+      const HeadRows& to = is_q ? a.q_out : a.k_out;
+      const int h = is_q ? r : is_k ? r - nq : r - nq - kvh;
+      float f[2][8];
+      const bool turn_it = (is_q || is_k) && turned;
+      u32x4 bits[2] = {own[u][0], own[u][1]};
+      if (turn_it || F8) {
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const float c = turn[0][4 * piece + e / 2], s = turn[1][4 * piece + e / 2], lo = f[e], hi = f[e + 1];
-          f[e] = lo * c - hi * s;
-          f[e + 1] = hi * c + lo * s;
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[i][e] = H::widen(own[u][i][e / 2] >> (16 * (e & 1)));
+      }
+      if (turn_it) {
+        if (a.interleaved) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int at = 4 * (i ? other : piece);
+            const f32x4 c = *(const f32x4*)(turn[0] + at), s = *(const f32x4*)(turn[1] + at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float lo = f[i][2 * e], hi = f[i][2 * e + 1];
+              f[i][2 * e] = lo * c[e] - hi * s[e];
+              f[i][2 * e + 1] = hi * c[e] + lo * s[e];
+            }
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const f32x4 c = *(const f32x4*)(turn[0] + 8 * piece + 4 * x), s = *(const f32x4*)(turn[1] + 8 * piece + 4 * x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float lo = f[0][4 * x + e], hi = f[1][4 * x + e];
+              f[0][4 * x + e] = lo * c[e] - hi * s[e];
+              f[1][4 * x + e] = hi * c[e] + lo * s[e];
+            }
+          }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          bits[i] = u32x4{H::pack(f[i][0], f[i][1]), H::pack(f[i][2], f[i][3]), H::pack(f[i][4], f[i][5]), H::pack(f[i][6], f[i][7])};
+      }
+      if ((is_q || is_k) && to.p) {
+        uint16_t* y = (uint16_t*)to.p + t * to.token + h * to.head;
+        const uint32_t nan = 0x7FFF7FFFu;  // a NaN of either kind
+        *(u32x4*)(y + 8 * piece) = wrong ? u32x4{nan, nan, nan, nan} : bits[0];
+        *(u32x4*)(y + 8 * other) = wrong ? u32x4{nan, nan, nan, nan} : bits[1];
+      }
+      if (is_q || wrong) continue;
+      const int64_t slot = (page * kvh + h) * a.c.P + (position & (a.c.P - 1));
+      void* cache = (void*)(is_k ? a.c.k : a.c.v);
+      if (F8) {
+        const float m = floor_amax(lanes_max<LANES>(max(amax8(f[0]), amax8(f[1]))));
+        ((u32x2*)cache)[slot * PER + piece] = codes8(f[0], kE4m3Max / m);
+        ((u32x2*)cache)[slot * PER + other] = codes8(f[1], kE4m3Max / m);
+        if (lane == 0) ((float*)(is_k ? a.c.k_scales : a.c.v_scales))[slot] = m / kE4m3Max;
       } else {
-        const bool lower = 8 * piece < half;
-        const u32x4 other = *(const u32x4*)(x + 8 * piece + (lower ? half : -half));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int i = 8 * piece + e - (lower ? 0 : half);
-          const float g = H::widen(other[e / 2] >> (16 * (e & 1))), c = turn[0][i], s = turn[1][i];
-          f[e] = lower ? f[e] * c - g * s : f[e] * c + g * s;
-        }
+        ((u32x4*)cache)[slot * PER + piece] = bits[0];
+        ((u32x4*)cache)[slot * PER + other] = bits[1];
       }
     }
-    const u32x4 bits = {H::pack(f[0], f[1]), H::pack(f[2], f[3]), H::pack(f[4], f[5]), H::pack(f[6], f[7])};
-    if ((is_q || is_k) && to.p) {
-      const uint32_t nan = 0x7FFF7FFFu;  // a NaN of either kind
-      *(u32x4*)((uint16_t*)to.p + t * to.token + h * to.head + 8 * piece) = wrong ? u32x4{nan, nan, nan, nan} : bits;
-    }
-    if (is_q || wrong) continue;
-    const int64_t slot = (page * kvh + h) * a.c.P + (position & (a.c.P - 1));
-    void* cache = (void*)(is_k ? a.c.k : a.c.v);
-    if (F8) {
-      const float m = floor_amax(row_max<D>(amax8(f)));
-      ((u32x2*)cache)[slot * PER + piece] = codes8(f, kE4m3Max / m);
-      if (piece == 0) ((float*)(is_k ? a.c.k_scales : a.c.v_scales))[slot] = m / kE4m3Max;
-    } else {
-      ((u32x4*)cache)[slot * PER + piece] = bits;
-    }
+    r0 += step;
+    if (r0 - threadIdx.x / LANES >= rows) break;
+    load(r0);
   }
 }
 
@@ -168,6 +215,26 @@ __device__ __forceinline__ bool wants(const TableArgs& t, const int32_t* ask, in
   return true;
 }
 
+// The first `needed` free pages into p.to; how many there are.
+__device__ __forceinline__ int64_t list_free(const TableArgs& t, const Plan& p, int64_t needed, int64_t* sums) {
+  int64_t found = 0, all;
+  for (int64_t p0 = 0; p0 < t.n_pages && found < needed; p0 += kPlanThreads * kPlanPer) {
+    const int64_t at = p0 + threadIdx.x * kPlanPer;
+    int free = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanPer; ++i) free |= (at + i < t.n_pages && t.refs[at + i] == 0) << i;
+    int64_t k = found + block_scan(__builtin_popcount(free), sums, all) - __builtin_popcount(free);
+#pragma unroll
+    for (int i = 0; i < kPlanPer; ++i)
+      if (free >> i & 1) {
+        if (k < needed) p.to[k] = (int)(at + i);
+        ++k;
+      }
+    found += all;
+  }
+  return min(found, needed);
+}
+
 template <Kind KIND>
 __global__ __launch_bounds__(kPlanThreads) void pages_plan_kernel(TableArgs t, const int32_t* ask, Plan p) {
   __shared__ int64_t sums[kPlanThreads / 64];
@@ -180,22 +247,7 @@ __global__ __launch_bounds__(kPlanThreads) void pages_plan_kernel(TableArgs t, c
     if (r < t.rows) p.upto[r] = upto;
     needed += all;
   }
-  int64_t found = 0;
-  for (int64_t p0 = 0; p0 < t.n_pages && found < needed; p0 += kPlanThreads * kPlanPer) {
-    const int64_t at = p0 + threadIdx.x * kPlanPer;
-    int free = 0;
-#pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) free += at + i < t.n_pages && t.refs[at + i] == 0;
-    int64_t k = found + block_scan(free, sums, all) - free;
-#pragma unroll
-    for (int i = 0; i < kPlanPer; ++i)
-      if (at + i < t.n_pages && t.refs[at + i] == 0) {
-        if (k < needed) p.to[k] = (int)(at + i);
-        ++k;
-      }
-    found += all;
-  }
-  found = min(found, needed);
+  const int64_t found = list_free(t, p, needed, sums);
   if (threadIdx.x == 0) *p.count = found;
   if (KIND == kFork) {
     for (int64_t r = threadIdx.x; r < t.rows; r += kPlanThreads) {
@@ -274,6 +326,43 @@ __device__ __forceinline__ void copy_pages(const PoolArgs& pools, const int32_t*
     } else {
       for (int64_t at = c + 4 * threadIdx.x; at < min(c + CHUNK, bytes); at += 4 * 256)
         *(uint32_t*)(d + at) = *(const uint32_t*)(s + at);
+    }
+  }
+}
+
+// The same in one launch, for up to a row a thread: each thread writes its row's new pages,
+// or the wave does where a row gets many.
+__global__ __launch_bounds__(kPlanThreads) void reserve_few_kernel(TableArgs t, const int32_t* grow, int32_t* status,
+                                                                   Plan p) {
+  __shared__ int64_t sums[kPlanThreads / 64];
+  const int64_t r = threadIdx.x;
+  const bool mine = r < t.rows;
+  int64_t need = 0, needed, found;
+  const bool ok = mine && wants<kReserve>(t, grow, r, need);
+  const int len = ok ? max(t.lengths[r], 0) : 0;
+  const int64_t upto = block_scan(need, sums, needed);
+  found = list_free(t, p, needed, sums);
+  __syncthreads();
+  const bool served = ok && (!need || upto <= found);
+  const int64_t have = pages_of(len, t.shift);
+  if (mine) status[r] = served ? (int)need : ok ? -2 : -1;
+  if (served) t.lengths[r] = len + grow[r];
+  constexpr int FEW = 4;
+  if (served && need <= FEW) {
+    for (int64_t i = 0; i < need; ++i) {
+      const int page = p.to[upto - need + i];
+      t.tables[r * t.width + have + i] = page;
+      t.refs[page] = 1;
+    }
+  }
+  for (uint64_t many = __ballot(served && need > FEW); many; many &= many - 1) {
+    const int l = __builtin_ctzll(many);
+    const int64_t n = __shfl(need, l, 64), from = __shfl(upto, l, 64) - n;
+    const int64_t to = __shfl(r, l, 64) * t.width + __shfl(have, l, 64);
+    for (int64_t i = threadIdx.x & 63; i < n; i += 64) {
+      const int page = p.to[from + i];
+      t.tables[to + i] = page;
+      t.refs[page] = 1;
     }
   }
 }
@@ -405,13 +494,17 @@ int64_t blocks_of_plane(int64_t planes) { return planes ? std::max<int64_t>(1, 4
 int64_t pages_workspace_bytes(int64_t rows, int64_t n_pages) { return 256 + up256(8 * rows) + 3 * up256(4 * n_pages); }
 
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
-  const int64_t x = std::min<int64_t>(a.T, 1 << 20);
-  const dim3 grid((unsigned)x, (unsigned)((a.T + x - 1) / x));
+  constexpr int PIECES = 2 * kAppendThreads * kAppendDeep;
+  // 256 tokens fill the card with a block each
+  const int pieces = ((a.q.p ? a.heads : 0) + 2 * a.c.kv_heads) * (a.c.D / 8);
+  const int blocks = a.T < 256 ? std::max(1, std::min((pieces + PIECES - 1) / PIECES, 64)) : 1;
+  const int64_t units = a.T * blocks, x = std::min<int64_t>(units, 1 << 20);
+  const dim3 grid((unsigned)x, (unsigned)((units + x - 1) / x));
   auto by_dim = [&](auto f16, auto e4m3) {
     constexpr bool F = decltype(f16)::value, E = decltype(e4m3)::value;
     auto kernel = a.c.D == 64 ? kv_append_kernel<F, E, 64> : a.c.D == 128 ? kv_append_kernel<F, E, 128>
                                                                           : kv_append_kernel<F, E, 256>;
-    kernel<<<grid, kAppendThreads, 0, stream>>>(a);
+    kernel<<<grid, kAppendThreads, 0, stream>>>(a, blocks);
   };
   const bool f8 = a.c.k_scales != nullptr;
   if (a.f16) f8 ? by_dim(std::true_type{}, std::true_type{}) : by_dim(std::true_type{}, std::false_type{});
@@ -421,6 +514,10 @@ hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
 
 hipError_t launch_kv_reserve(const TableArgs& t, const int32_t* grow, int32_t* status, void* ws, hipStream_t stream) {
   const Plan p = plan_in(ws, t.rows, t.n_pages);
+  if (t.rows <= kPlanThreads) {
+    reserve_few_kernel<<<1, kPlanThreads, 0, stream>>>(t, grow, status, p);
+    return hipGetLastError();
+  }
   pages_plan_kernel<kReserve><<<1, kPlanThreads, 0, stream>>>(t, grow, p);
   const int64_t row_blocks = (t.rows + 3) / 4;
   pages_do_kernel<kReserve><<<(unsigned)row_blocks, 256, 0, stream>>>(t, grow, p, status, PoolArgs{}, row_blocks, 1);
