@@ -30,13 +30,15 @@ namespace moe {
 namespace {
 
 constexpr int kRows = 128;         // rows (queries times heads) of a block
+constexpr int kFill = 512;         // blocks that fill the card, two a CU
 constexpr int kMaxSplits = 8;      // blocks that share the keys of a tile of queries
 constexpr int kSplitTiles = 8;     // tiles of keys that make a share worth its joining
 
 // Keys of a tile: 64, of the widest heads 32, so that two tiles of keys and values take
 // 64 KB of LDS and two blocks share a CU.
+constexpr int kTileKeysOf(int D) { return D == 256 ? 32 : 64; }
 template <int D>
-constexpr int kTileKeys = D == 256 ? 32 : 64;
+constexpr int kTileKeys = kTileKeysOf(D);
 
 // Piece p (16 bytes) of row r of a tile is kept at place p ^ f(r) of the row.  Sixteen
 // rows read at one piece, and four consecutive rows read at four, spread over all banks.
@@ -114,8 +116,12 @@ __device__ __forceinline__ Share share_of(const PrefillArgs& a, const PrefillWor
   Share s;
   s.group = (int)(block % w.groups);  // neighbours on the card's eight parts take different heads
   const int64_t rest = block / w.groups;
-  s.split = (int)(rest % splits);
-  const int64_t unit = rest / splits;
+  // The last shares come first, and the first, which all tiles have, at the end: blocks that
+  // have nothing to do stand together.  (Between the others they cost twice the time: blocks go
+  // to the card's parts in turn, whatever there is to do.)
+  const int from_end = (int)(rest / w.units);
+  s.split = splits - 1 - from_end;
+  const int64_t unit = rest - from_end * w.units;
   s.at = find_tile(a, kRows / w.heads, unit);
   s.record = (unit * w.groups + s.group) * w.splits;
   return s;
@@ -124,9 +130,10 @@ __device__ __forceinline__ Share share_of(const PrefillArgs& a, const PrefillWor
 __device__ __forceinline__ int keys_seen(const PrefillArgs& a, const Place& at, int r) {
   return a.causal ? max(min(min(r, at.lq - 1) + at.lk - at.lq + 1, at.lk), 0) : at.lk;
 }
-// How many blocks really share `tiles` tiles of keys.
-__device__ __forceinline__ int shares(int tiles, int splits) {
-  return max(1, min(splits, tiles / kSplitTiles));
+// How many blocks share `tiles` tiles of keys.  (Divisions come from the vector unit, and the
+// block's loop is to stay scalar.)
+__device__ __forceinline__ int shares(const PrefillWork& w, int tiles) {
+  return __builtin_amdgcn_readfirstlane(max(1, min(w.splits, tiles / kSplitTiles)));
 }
 
 template <bool F16, int D>
@@ -315,9 +322,10 @@ __global__ __launch_bounds__(256, 2) void attention_prefill_kernel(PrefillArgs a
   const uint16_t* kp = a.k.p + at.k0 * a.k.token + kv * a.k.head;
   const uint16_t* vp = a.v.p + at.k0 * a.v.token + kv * a.v.head;
   // the block's tiles of keys; the keys that all its queries see, and that the wave's do
-  const int tiles = (keys_seen(a, at, first_query + queries - 1) + W::BN - 1) / W::BN, n = shares(tiles, work.splits);
+  const int tiles = (keys_seen(a, at, first_query + queries - 1) + W::BN - 1) / W::BN, n = shares(work, tiles);
   if (share.split >= n) return;
-  const int from = (int)((int64_t)tiles * share.split / n), to = (int)((int64_t)tiles * (share.split + 1) / n);
+  const int each = __builtin_amdgcn_readfirstlane((uint32_t)tiles / (uint32_t)n), extra = tiles - each * n;
+  const int from = each * share.split + min(share.split, extra), to = from + each + (share.split < extra);
   const int seen_by_all = a.causal ? keys_seen(a, at, first_query) : at.lk;
   const int wave_end = first_row < at.lq ? keys_seen(a, at, first_row + 31) : 0;
   const int all_end = a.causal ? keys_seen(a, at, first_row) : at.lk;
@@ -397,44 +405,51 @@ __global__ __launch_bounds__(256, 2) void attention_prefill_kernel(PrefillArgs a
   if (row < at.lq) w.store(a, token, head, sum);
 }
 
-// Rows whose keys several blocks shared.
+// Rows whose keys several blocks shared: 32 of them and 64 channels a wave.
 template <bool F16, int D>
-__global__ __launch_bounds__(256) void attention_prefill_join_kernel(PrefillArgs a, PrefillWork work) {
+__global__ __launch_bounds__(64) void attention_prefill_join_kernel(PrefillArgs a, PrefillWork work) {
   using W = Prefill<F16, D>;
+  constexpr int PARTS = 4 * (D / 64), RECORD = kRows * (D + 2);
   const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
-  const Share share = share_of(a, work, block, 1);
+  const int part = (int)(block % PARTS), wave = part % 4, d0 = 2 * (part / 4);
+  const Share share = share_of(a, work, block / PARTS, 1);
   const Place& at = share.at;
   if (!at.found) return;
-  W w;
-  w.lane = threadIdx.x & 63;
-  w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  w.half = w.lane >> 5;
+  const int lane = threadIdx.x, half = lane >> 5;
   const int queries = kRows / work.heads, first_query = at.tile * queries;
-  const int tiles = (keys_seen(a, at, first_query + queries - 1) + W::BN - 1) / W::BN, n = shares(tiles, work.splits);
+  const int tiles = (keys_seen(a, at, first_query + queries - 1) + W::BN - 1) / W::BN, n = shares(work, tiles);
   if (n == 1) return;
-  const int head = share.group * work.heads + w.wave % work.heads;
-  const int row = first_query + 32 * (w.wave / work.heads) + (w.lane & 31);
-  const float* part = work.parts + share.record * (kRows * (D + 2));
-  w.m = -INFINITY;
-  for (int i = 0; i < n; ++i) w.m = fmaxf(w.m, part[(int64_t)i * (kRows * (D + 2)) + kRows * D + 64 * w.wave + (w.lane & 31)]);
-  float sum = 0.f;
+  const int row = first_query + 32 * (wave / work.heads) + (lane & 31);
+  const float* base = work.parts + share.record * RECORD;
+  const float* ml = base + kRows * D + 64 * wave + (lane & 31);
+  float m[kMaxSplits], l[kMaxSplits], top = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int d = 0; d < W::DT; ++d) w.o[d] = f32x16{};
-  for (int i = 0; i < n; ++i) {
-    const float* r = part + (int64_t)i * (kRows * (D + 2));
-    const float* ml = r + kRows * D + 64 * w.wave + (w.lane & 31);
-    const float f = ml[0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(ml[0] - w.m);
-    sum += ml[32] == 0.f ? 0.f : ml[32] * f;
-#pragma unroll
-    for (int d = 0; d < W::DT; ++d)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const f32x4 x = *(const f32x4*)(r + w.wave * (32 * D) + 4 * (64 * (4 * d + e) + w.lane));
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w.o[d][4 * e + j] += x[j] * f;
-      }
+  for (int i = 0; i < kMaxSplits; ++i) {
+    m[i] = i < n ? ml[(int64_t)i * RECORD] : -INFINITY;
+    l[i] = i < n ? ml[(int64_t)i * RECORD + 32] : 0.f;
   }
-  if (row < at.lq) w.store(a, at.q0 + row, head, sum);
+#pragma unroll
+  for (int i = 0; i < kMaxSplits; ++i) top = fmaxf(top, m[i]);
+  f32x4 o[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) o[e] = f32x4{};
+#pragma unroll
+  for (int i = 0; i < kMaxSplits; ++i) {
+    if (i >= n) break;
+    const float f = m[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[i] - top);
+    sum += l[i] == 0.f ? 0.f : l[i] * f;
+    const f32x4* r = (const f32x4*)(base + (int64_t)i * RECORD + wave * (32 * D)) + 256 * d0 + lane;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] += r[64 * e] * f;
+  }
+  if (row >= at.lq) return;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t out = (at.q0 + row) * (int64_t)a.heads + share.group * work.heads + wave % work.heads;
+  uint16_t* y = a.y + out * D + 32 * d0 + 4 * half;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    *(u32x2*)(y + 8 * e) = u32x2{W::H::pack(o[e].x * inv, o[e].y * inv), W::H::pack(o[e].z * inv, o[e].w * inv)};
+  if (a.lse && part < 4 && !half) a.lse[out] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
 }
 
 PrefillWork work_of(const PrefillArgs& a) {
@@ -443,11 +458,13 @@ PrefillWork work_of(const PrefillArgs& a) {
   w.heads = shared % 4 == 0 ? 4 : shared % 2 == 0 ? 2 : 1;
   w.groups = a.heads / w.heads;
   w.units = a.Tq / (kRows / w.heads) + std::min(a.n, a.Tq);
-  // Two blocks fill a CU.  With fewer, several take the keys of one, if there are enough
-  // of these.
-  const int64_t fill = 512, blocks = w.units * w.groups;
-  const int64_t tiles = a.Tk / ((a.D == 256 ? 32 : 64) * kSplitTiles);
-  w.splits = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, (fill + blocks / 2) / blocks, tiles}));
+  // Where there are fewer blocks than fill the card, several share the keys of one, if there
+  // are enough of these (1021 queries over 8191 keys, 16 heads of 256: 170 us, 478 without).
+  // Not to even out ragged sequences: blocks that turn out to have nothing to do, and the
+  // joining, cost more than that gains (1809 of 4099 tokens in one of 11 sequences: 72 us, 53
+  // without).
+  const int64_t blocks = w.units * w.groups, tiles = a.Tk / (kTileKeysOf(a.D) * kSplitTiles);
+  w.splits = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, (kFill + blocks / 2) / blocks, tiles}));
   return w;
 }
 
@@ -474,7 +491,7 @@ hipError_t launch_attention_prefill(const PrefillArgs& a, void* ws, hipStream_t 
     constexpr bool F = decltype(f16)::value;
     constexpr int D = decltype(dim)::value;
     attention_prefill_kernel<F, D><<<grid(w.units * w.groups * w.splits), 256, 0, stream>>>(a, w);
-    if (w.splits > 1) attention_prefill_join_kernel<F, D><<<grid(w.units * w.groups), 256, 0, stream>>>(a, w);
+    if (w.splits > 1) attention_prefill_join_kernel<F, D><<<grid(w.units * w.groups * 4 * (D / 64)), 64, 0, stream>>>(a, w);
   };
   auto by_type = [&](auto f16) {
     if (a.D == 64) by_dim(f16, std::integral_constant<int, 64>{});
