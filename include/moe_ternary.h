@@ -331,12 +331,14 @@ int32_t moe_sample(int32_t type, const void* logits, int64_t batch, int32_t voca
  * A query that sees no key, or scores of -inf alone, gets y = 0 and lse = -inf.  What a
  * query must not see does not reach it, infinities and NaN included.  Tokens outside
  * every sequence leave their y and lse as they were.  Starts outside [0, tokens] are
- * taken as the nearer end, and one below the start before it as that one.
+ * taken as the nearer end, and a sequence that ends before it starts has no tokens; where
+ * falling starts give a token to two sequences, either's result or none stands there.
  * Numerics: scores, the softmax's maximum and sum and y's sums are fp32; the weights
  * are rounded to `type` for the matrix cores (each off by half a step of itself), y is
- * rounded once.  head_dim is 64, 128 or 256; heads is a multiple of kv_heads, at most
- * 4096; strides are multiples of 8, at most 2^24; q, k, v and y 16-byte aligned;
- * tokens below 2^31, n_seqs at most 2^22; scale finite and positive.  q_tokens = 0 or n_seqs = 0 is a no-op.  y, lse and the
+ * rounded once.  A score beyond fp32 is infinite, and what exp underflows has no weight.
+ * head_dim is 64, 128 or 256; heads is a multiple of kv_heads, at most 4096; strides are
+ * multiples of 8 from head_dim up to 2^24; q, k, v and y 16-byte aligned; tokens below
+ * 2^31, n_seqs at most 65535; scale finite and positive.  q_tokens = 0 or n_seqs = 0 is a no-op.  y, lse and the
  * workspace overlap neither each other nor an input.  A sequence's results depend on the others
  * only where q_tokens, n_seqs and k_tokens ask for a workspace, and then in their last bits.
  * Ordered on `stream`; nothing is allocated.  Errors: MOE_E_FORMAT (type), MOE_E_SHAPE,

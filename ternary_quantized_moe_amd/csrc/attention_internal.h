@@ -11,7 +11,7 @@ constexpr int64_t kAttnMaxTokens = 0x7FFFFFFF;          // starts, lengths and p
 constexpr int kAttnMaxHeads = 4096;
 constexpr int64_t kAttnMaxStride = (int64_t)1 << 24;    // elements: a tile of 64 tokens stays inside 32 bits of bytes
 constexpr int kMaxPage = 4096;
-constexpr int64_t kAttnMaxBatch = 65535;                // one dimension of a launch
+constexpr int64_t kAttnMaxBatch = 65535;                // sequences: one dimension of a launch
 
 // A [tokens x heads x D] matrix of 16-bit values whose heads are contiguous.
 struct HeadRows {

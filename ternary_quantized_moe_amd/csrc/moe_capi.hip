@@ -571,7 +571,7 @@ bool good_scale(float scale) { return scale > 0.f && !std::isinf(scale); }
 int64_t moe_attention_prefill_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64_t n_seqs, int32_t heads,
                                               int32_t kv_heads, int32_t head_dim) {
   if (q_tokens < 0 || k_tokens < 0 || q_tokens > moe::kAttnMaxTokens || k_tokens > moe::kAttnMaxTokens || n_seqs < 0 ||
-      n_seqs > (1 << 22) || check_heads(heads, kv_heads, head_dim))
+      n_seqs > moe::kAttnMaxBatch || check_heads(heads, kv_heads, head_dim))
     return -1;
   if (q_tokens == 0 || n_seqs == 0) return 0;
   moe::PrefillArgs a{};
@@ -588,7 +588,8 @@ int32_t moe_attention_prefill(int32_t type, const void* q, int64_t q_tokens, int
   if (const int32_t rc = check_heads(heads, kv_heads, head_dim)) return rc;
   if (q_tokens < 0 || k_tokens < 0 || q_tokens > moe::kAttnMaxTokens || k_tokens > moe::kAttnMaxTokens)
     return fail(MOE_E_SHAPE, "token counts %lld and %lld outside [0, 2^31)", (long long)q_tokens, (long long)k_tokens);
-  if (n_seqs < 0 || n_seqs > (1 << 22)) return fail(MOE_E_SHAPE, "sequence count %lld outside [0, 2^22]", (long long)n_seqs);
+  if (n_seqs < 0 || n_seqs > moe::kAttnMaxBatch)
+    return fail(MOE_E_SHAPE, "sequence count %lld outside [0, %lld]", (long long)n_seqs, (long long)moe::kAttnMaxBatch);
   if (!good_scale(scale)) return fail(MOE_E_ARG, "scale must be finite and positive");
   if (q_tokens == 0 || n_seqs == 0) return ok();
   moe::PrefillArgs a{{(const uint16_t*)q, q_token, q_head}, {(const uint16_t*)k, k_token, k_head},
