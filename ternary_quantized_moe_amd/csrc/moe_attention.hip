@@ -49,12 +49,13 @@ __device__ __forceinline__ int swizzle(int r) {
 
 // A number that the compiler no longer knows.  The widest heads leave no registers for the
 // sixteen places in a tile that differ in a few address bits: they are made anew each time
-// (1021 queries over 8191 keys 173 us, 205 with them kept and others spilled; at 128 channels
-// they fit, and keeping them is 4% faster).
+// (1021 queries over 8191 keys 167 us, 226 with them kept and others spilled; at 128 and 64
+// channels they fit, and keeping them is 1% faster).
 __device__ __forceinline__ int opaque(int v) {
   asm volatile("" : "+v"(v));
   return v;
 }
+
 struct PrefillWork {
   int heads;        // query heads of a block: 1, 2 or 4
   int groups;       // blocks that share a tile of queries, one for each such set of heads
@@ -162,18 +163,6 @@ struct Prefill {
     }
   }
 
-  // S^T = K Q^T.
-  __device__ __forceinline__ void scores(const uint8_t* ks) {
-    const int row = lane & 31, place = row * kRow + ((half ^ swizzle<D>(row)) << 4), 
-              at = D == 256 ? opaque(place) : place;
-#pragma unroll
-    for (int t = 0; t < KT; ++t) s[t] = f32x16{};
-#pragma unroll
-    for (int k = 0; k < KS; ++k)
-#pragma unroll
-      for (int t = 0; t < KT; ++t) s[t] = H::mfma32(*(const u32x4*)(ks + 32 * t * kRow + (at ^ (k << 5))), q[k], s[t]);
-  }
-
   // The softmax of the tile whose scores are in s: its weights in p.  masked: some query
   // of the wave does not see all of the tile.
   __device__ __forceinline__ void softmax(int first, float c, bool masked) {
@@ -193,7 +182,8 @@ struct Prefill {
     const f32x2_t tops = both_halves(top);
     top = fmaxf(tops.x, tops.y) * c;
     // The maximum that is subtracted may lag 2^8 behind the true one: the sums stay far
-    // inside fp32, and y is scaled anew only when a query's maximum really moves.
+    // inside fp32, and y is scaled anew only when a query's maximum really moves (1 x 16384
+    // 1076 us, 1122 where it follows at once; 1 x 8192 of 256 channels 570 us, 625).
     if (__any(top > m + 8.f)) {
       const float now = fmaxf(m, top), f = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
       m = now;
@@ -221,27 +211,51 @@ struct Prefill {
         for (int e = 0; e < 4; ++e) p[t][k][e] = H::pack(s[t][8 * k + 2 * e], s[t][8 * k + 2 * e + 1]);
   }
 
-  // y^T += V^T P^T.
-  __device__ __forceinline__ void values(const uint8_t* vs) {
-    const int g = lane >> 4, i16 = lane & 15;
-    int vat[2];
+  // y^T += V^T P^T from the values at vs, then S^T = K Q^T from the keys at ks; without VALUES
+  // the scores alone.  The operands are read from LDS kAhead products ahead, in an order that
+  // the compiler is held to: a wave has one neighbour on its SIMD, which does not hide a read
+  // that is waited for where it is used (1 x 16384, 32 heads of 128: 1023 us, 1051 without the
+  // order; 1031 at 6 ahead, 1033 at 8, 1044 at 12).  At 256 channels, where registers are short, the
+  // order holds for groups of four (1 x 8192: 548 us, 594 for single products, 579 without).
+  template <bool VALUES>
+  __device__ __forceinline__ void products(const uint8_t* vs, const uint8_t* ks) {
+    constexpr int NV = VALUES ? 2 * KT * DT : 0, N = NV + KS * KT, kAhead = 4, kHeld = D == 256 ? 4 : 1;
+    const int i16 = lane & 15, g = lane >> 4, krow = lane & 31;
+    int vat[2], kat = krow * kRow + ((half ^ swizzle<D>(krow)) << 4);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = 8 * r + 4 * half + (i16 >> 2), piece = 2 * (g & 1) + ((i16 & 3) >> 1);
       vat[r] = row * kRow + ((piece ^ swizzle<D>(row)) << 4) + 8 * (i16 & 1);
-      if (D == 256) vat[r] = opaque(vat[r]);
     }
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint8_t* at = vs + (32 * t + 16 * k) * kRow;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const u32x2 lo = read_transposed(at + (vat[0] ^ (d << 6))), hi = read_transposed(at + (vat[1] ^ (d << 6)));
-          o[d] = H::mfma32(u32x4{lo.x, lo.y, hi.x, hi.y}, p[t][k], o[d]);
-        }
+    if (D == 256) vat[0] = opaque(vat[0]), vat[1] = opaque(vat[1]), kat = opaque(kat);
+    u32x4 f[kAhead];
+    auto read = [&](int j) {
+      if (j >= N) return;
+      if (j < NV) {
+        const uint8_t* at = vs + 16 * (j / DT) * kRow;
+        const int d = j % DT;
+        const u32x2 lo = read_transposed(at + (vat[0] ^ (d << 6))), hi = read_transposed(at + (vat[1] ^ (d << 6)));
+        f[j % kAhead] = u32x4{lo.x, lo.y, hi.x, hi.y};
+      } else {
+        const int k = (j - NV) / KT, t = (j - NV) % KT;
+        f[j % kAhead] = *(const u32x4*)(ks + 32 * t * kRow + (kat ^ (k << 5)));
       }
+    };
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) read(j);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (j % kHeld == 0) __builtin_amdgcn_sched_barrier(0);
+      if (j < NV) {
+        o[j % DT] = H::mfma32(f[j % kAhead], p[j / DT / 2][j / DT % 2], o[j % DT]);
+      } else {
+        const int k = (j - NV) / KT, t = (j - NV) % KT;
+        if (k == 0) s[t] = f32x16{};
+        s[t] = H::mfma32(f[j % kAhead], q[k], s[t]);
+      }
+      read(j + kAhead);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
 
   // A weight of zero does not remove a value that is infinite or NaN.  Where a tile is
@@ -353,7 +367,7 @@ __global__ __launch_bounds__(256, 2) void attention_prefill_kernel(PrefillArgs a
         arrived<W::kLoads>();
       }
       meet();
-      if (from * W::BN < wave_end) w.scores(kbuf);
+      if (from * W::BN < wave_end) w.template products<false>(nullptr, kbuf);
     }
     for (int t = from; t < to; ++t) {
       const int now = (t - from) & 1, first = t * W::BN;
@@ -368,9 +382,9 @@ __global__ __launch_bounds__(256, 2) void attention_prefill_kernel(PrefillArgs a
         meet();
       }
       if (first < wave_end) {
-        w.values(vs);
+        // Scores that no tile follows for are formed all the same and not looked at.
+        w.template products<true>(vs, kbuf + (now ^ 1) * W::kTile);
         if (cleared) w.add_cleared(vp, a.v.token, first, min(first + W::BN, at.lk));
-        if (t + 1 < to && first + W::BN < wave_end) w.scores(kbuf + (now ^ 1) * W::kTile);
       }
     }
     // A result that is not finite: a value that a query must not see may have got in, so
@@ -459,9 +473,10 @@ PrefillWork work_of(const PrefillArgs& a) {
   w.groups = a.heads / w.heads;
   w.units = a.Tq / (kRows / w.heads) + std::min(a.n, a.Tq);
   // Where there are fewer blocks than fill the card, several share the keys of one, if there
-  // are enough of these (1021 queries over 8191 keys, 16 heads of 256: 170 us, 478 without).
+  // are enough of these (1021 queries over 8191 keys, 16 heads of 256: 167 us, 389 without;
+  // shares of four tiles instead of eight: 1 x 1000, 33 us, 28 with eight).
   // Not to even out ragged sequences: blocks that turn out to have nothing to do, and the
-  // joining, cost more than that gains (1809 of 4099 tokens in one of 11 sequences: 72 us, 53
+  // joining, cost more than that gains (1809 of 4099 tokens in one of 11 sequences: 72 us, 55
   // without).
   const int64_t blocks = w.units * w.groups, tiles = a.Tk / (kTileKeysOf(a.D) * kSplitTiles);
   w.splits = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, (kFill + blocks / 2) / blocks, tiles}));
