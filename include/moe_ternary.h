@@ -337,10 +337,11 @@ int32_t moe_sample(int32_t type, const void* logits, int64_t batch, int32_t voca
  * are rounded to `type` for the matrix cores (each off by half a step of itself), y is
  * rounded once.  A score beyond fp32 is infinite, and what exp underflows has no weight.
  * head_dim is 64, 128 or 256; heads is a multiple of kv_heads, at most 4096; strides are
- * multiples of 8 from head_dim up to 2^24; q, k, v and y 16-byte aligned; tokens below
- * 2^31, n_seqs at most 65535; scale finite and positive.  q_tokens = 0 or n_seqs = 0 is a no-op.  y, lse and the
- * workspace overlap neither each other nor an input.  A sequence's results depend on the others
- * only where q_tokens, n_seqs and k_tokens ask for a workspace, and then in their last bits.
+ * multiples of 8 from head_dim up to 2^24; q, k, v and y 16-byte aligned; tokens at most
+ * 2^31 - 256, n_seqs at most 65535; scale finite and positive.  q_tokens = 0 or n_seqs = 0
+ * is a no-op.  y, lse and the workspace overlap neither each other nor an input.  A
+ * sequence's results depend on the others only where q_tokens, n_seqs and k_tokens ask for a
+ * workspace, and then in their last bits.
  * Ordered on `stream`; nothing is allocated.  Errors: MOE_E_FORMAT (type), MOE_E_SHAPE,
  * MOE_E_ARG, MOE_E_SPACE, MOE_E_DEVICE. */
 int64_t moe_attention_prefill_workspace_bytes(int64_t q_tokens, int64_t k_tokens, int64_t n_seqs, int32_t heads,

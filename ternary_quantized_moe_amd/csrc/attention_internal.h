@@ -7,7 +7,7 @@
 
 namespace moe {
 
-constexpr int64_t kAttnMaxTokens = 0x7FFFFFFF;          // starts, lengths and positions are int32
+constexpr int64_t kAttnMaxTokens = 0x7FFFFF00;          // int32, the end of a tile behind the last one included
 constexpr int kAttnMaxHeads = 4096;
 constexpr int64_t kAttnMaxStride = (int64_t)1 << 24;    // elements: a tile of 64 tokens stays inside 32 bits of bytes
 constexpr int kMaxPage = 4096;

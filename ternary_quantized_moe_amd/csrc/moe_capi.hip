@@ -391,7 +391,7 @@ int32_t moe_rms_norm(const uint16_t* x, const uint16_t* residual, int64_t T, int
                      uint16_t* sum, uint16_t* y, uint8_t* q, float* scales, void* stream) {
   if (d <= 0 || d % 128 || d > moe::kNormMaxD)
     return fail(MOE_E_SHAPE, "d %d is not a positive multiple of 128 up to %d", (int)d, moe::kNormMaxD);
-  if (T < 0 || T > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "token count %lld outside [0, 2^31)", (long long)T);
+  if (T < 0 || T > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "token count %lld outside [0, 2^31 - 256]", (long long)T);
   if (!(eps >= 0.f) || std::isinf(eps)) return fail(MOE_E_ARG, "eps must be finite and not negative");
   if (T == 0) return ok();
   if (!y && !q) return fail(MOE_E_ARG, "give y, q or both");
@@ -587,7 +587,7 @@ int32_t moe_attention_prefill(int32_t type, const void* q, int64_t q_tokens, int
   if (!half_type(type)) return bad_type(type);
   if (const int32_t rc = check_heads(heads, kv_heads, head_dim)) return rc;
   if (q_tokens < 0 || k_tokens < 0 || q_tokens > moe::kAttnMaxTokens || k_tokens > moe::kAttnMaxTokens)
-    return fail(MOE_E_SHAPE, "token counts %lld and %lld outside [0, 2^31)", (long long)q_tokens, (long long)k_tokens);
+    return fail(MOE_E_SHAPE, "token counts %lld and %lld outside [0, 2^31 - 256]", (long long)q_tokens, (long long)k_tokens);
   if (n_seqs < 0 || n_seqs > moe::kAttnMaxBatch)
     return fail(MOE_E_SHAPE, "sequence count %lld outside [0, %lld]", (long long)n_seqs, (long long)moe::kAttnMaxBatch);
   if (!good_scale(scale)) return fail(MOE_E_ARG, "scale must be finite and positive");
@@ -669,7 +669,7 @@ int32_t moe_kv_append(int32_t type, const void* q, int64_t q_token, int64_t q_he
                       int64_t q_out_head, void* k_out, int64_t k_out_token, int64_t k_out_head, void* stream) {
   if (!half_type(type)) return bad_type(type);
   if (const int32_t rc = check_heads(q ? heads : kv_heads, kv_heads, head_dim)) return rc;
-  if (T < 0 || T > moe::kAttnMaxTokens) return fail(MOE_E_SHAPE, "token count %lld outside [0, 2^31)", (long long)T);
+  if (T < 0 || T > moe::kAttnMaxTokens) return fail(MOE_E_SHAPE, "token count %lld outside [0, 2^31 - 256]", (long long)T);
   if (n_rows < 1 || n_rows > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "row count %lld outside [1, 2^31)", (long long)n_rows);
   if (rotary < 0 || rotary % 16 || rotary > head_dim)
     return fail(MOE_E_SHAPE, "rotary %d is not a multiple of 16 up to head_dim %d", (int)rotary, (int)head_dim);

@@ -173,7 +173,9 @@ struct Decode {
     int b, tile, tiles, len;
     int64_t left;
   };
-  __device__ __forceinline__ int tiles_of(int len) const { return max(1, (len + kBlockKeys - 1) / kBlockKeys); }
+  __device__ __forceinline__ int tiles_of(int len) const {
+    return max(1, (int)(((uint32_t)len + (kBlockKeys - 1)) / kBlockKeys));
+  }
   __device__ __forceinline__ int length(int64_t b) const {
     const int64_t room = (int64_t)a.c.width * a.c.P;
     return (int)min((int64_t)max(a.lengths[b], 0), room);

@@ -244,6 +244,30 @@ def test_offsets_past_32_bits(tq):
     assert torch.equal(y, c.run())
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_the_longest_length(tq, e4m3):
+    """2^31 - 1 tokens, one page over and over, keys that weigh alike.  Every share's sums of
+    weights and of integers are exact in fp32 (below 2^24); joining 256 of them rounds 263
+    times at most, each sum by 2^-24 of sum_j |v_j| < 2^31: y is off by 264 2^-24 < 2^-15 and
+    its rounding, lse by as much and its own."""
+    say("2^31 - 1 tokens", e4m3)
+    D, P, n = 64, 4096, (1 << 31) - 1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(14)
+    v = torch.randint(-1, 2, (1, 1, P, D), generator=g, device="cuda").float()
+    v[..., : D // 2] = v[..., : D // 2].abs()
+    k = torch.randn((1, 1, P, D), generator=g, device="cuda")
+    cache = torch.float8_e4m3fn if e4m3 else BF16
+    scales = {x: torch.ones((1, 1, P), device="cuda") for x in ("k_scales", "v_scales")} if e4m3 else {}
+    lse = torch.empty((1, 2), device="cuda")
+    y = tq.attention_decode(torch.zeros((1, 2, D), dtype=BF16, device="cuda"), k.to(cache), v.to(cache),
+                            torch.zeros((1, (n + 1) // P), dtype=torch.int32, device="cuda"), ints([n]), lse=lse, **scales)
+    v = host(v)[0, 0]
+    want = (v.sum(0) * ((n + 1) // P) - v[-1]) / n
+    assert np.all(np.abs(host(y)[0] - want) <= 2.0 ** -15 + 2.0 ** -8 * np.abs(want))
+    assert np.all(np.abs(host(lse) - np.log(n)) <= 2.0 ** -15 + 2.0 ** -24 * 4 * np.log(n))
+
+
 def test_two_graphs_share_a_workspace(tq):
     say("decode graphs")
     a, b = Case(tq, 14, [900, 31, 500], 8, 2, 128, 32), Case(tq, 15, [3000], 8, 2, 128, 32)
