@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "device_common.h"
+#include "wave_ops.h"
 
 namespace moe {
 
@@ -56,6 +57,25 @@ struct Half {
 __device__ __forceinline__ f32x2_t both_halves(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return f32x2_t{__uint_as_float(r[0]), __uint_as_float(r[1])};
+}
+
+// Sums over the lanes up to each.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t shifted(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, true);
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += shifted<kDppShr1, 0xF>(v);
+  v += shifted<kDppShr2, 0xF>(v);
+  v += shifted<kDppShr4, 0xF>(v);
+  v += shifted<kDppShr8, 0xF>(v);
+  v += shifted<kDppBcast15, 0xA>(v);
+  return v + shifted<kDppBcast31, 0xC>(v);
+}
+
+// a / b, in 32 bits where these do.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
 // Reads four rows of 16 values transposed: within 16 lanes, lane i gives the address of

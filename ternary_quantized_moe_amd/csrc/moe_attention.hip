@@ -11,12 +11,20 @@
 // needs one exchange between the wave's halves, and they stand as the second operand of
 // y^T = V^T P^T wants them: the order of the keys inside a product is free, and the
 // transposing reads of V follow the order in which the scores lie.  Two blocks share a CU,
-// and one's products run beside the other's softmax.  P is rounded to the values' type (nearest even) for the
-// matrix cores; each p is off by half a step of itself, as y is by its own rounding, and l
-// is summed before the rounding.
+// and one's products run beside the other's softmax.  P is rounded to the values' type
+// (nearest even) for the matrix cores; each p is off by half a step of itself, as y is by its
+// own rounding, and l is summed before the rounding.
 //
 // Where a launch has too few blocks for the card, several share the keys of a tile of
 // queries, and a second launch joins what they leave in the workspace.
+//
+// The matrix cores bound long prompts, and the power that they may draw: 1 x 16384, 32 heads of
+// 128, causal, takes 1012 us (1.09 PFLOP/s; a loop of bare products reaches 1.27), 8 x 2048 of
+// 16 heads, not causal, 471 us (1.02), 1 x 8192, 16 heads of 256, 503 us (1.09), 1 x 4096, 32
+// heads of 64, 86 us (0.80: the exponentials weigh twice as much).  In the first the matrix
+// cores are busy 57% of the cycles, the vector units as long, and LDS has no bank conflicts.
+// Ragged prompts are bound by the longest row's walk over its keys (4099 tokens in 11 sequences
+// 52 us), and the smallest by a launch and three trips to memory (61 tokens 6.7 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -29,7 +37,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kRows = 128;         // rows (queries times heads) of a block
+constexpr int kRowBits = 7, kRows = 1 << kRowBits;  // rows (queries times heads) of a block
 constexpr int kFill = 512;         // blocks that fill the card, two a CU
 constexpr int kMaxSplits = 8;      // blocks that share the keys of a tile of queries
 constexpr int kSplitTiles = 8;     // tiles of keys that make a share worth its joining
@@ -49,7 +57,7 @@ __device__ __forceinline__ int swizzle(int r) {
 
 // A number that the compiler no longer knows.  The widest heads leave no registers for the
 // sixteen places in a tile that differ in a few address bits: they are made anew each time
-// (1021 queries over 8191 keys 167 us, 226 with them kept and others spilled; at 128 and 64
+// (1021 queries over 8191 keys 148 us, 185 with them kept and others spilled; at 128 and 64
 // channels they fit, and keeping them is 1% faster).
 __device__ __forceinline__ int opaque(int v) {
   asm volatile("" : "+v"(v));
@@ -57,7 +65,7 @@ __device__ __forceinline__ int opaque(int v) {
 }
 
 struct PrefillWork {
-  int heads;        // query heads of a block: 1, 2 or 4
+  int shift;        // 1 << shift query heads to a block: 1, 2 or 4
   int groups;       // blocks that share a tile of queries, one for each such set of heads
   int splits;       // blocks that may share the keys of a tile of queries
   int64_t units;    // tiles of queries, at most
@@ -70,7 +78,7 @@ struct Place {
   int q0, k0, lq, lk, tile;
   bool found;
 };
-__device__ __forceinline__ Place find_tile(const PrefillArgs& a, int queries, int64_t unit) {
+__device__ __forceinline__ Place find_tile(const PrefillArgs& a, int shift, int64_t unit) {
   const int lane = threadIdx.x & 63;
   Place r{};
   for (int64_t c = 0; c < a.n; c += 64) {
@@ -84,25 +92,19 @@ __device__ __forceinline__ Place find_tile(const PrefillArgs& a, int queries, in
       k_from = (int)min((int64_t)max(k_from, 0), a.Tk);
       k_to = (int)min((int64_t)max(k_to, k_from), a.Tk);
     }
-    const int tiles = (int)(((int64_t)to - from + queries - 1) / queries);
-    int upto = tiles;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int other = __shfl_up(upto, o, 64);
-      if (lane >= o) upto += other;
-    }
+    const uint32_t upto = wave_scan(((uint32_t)(to - from) + ((kRows - 1) >> shift)) >> (kRowBits - shift));
     const uint64_t past = __ballot(unit < upto);
     if (past) {
       const int l = __builtin_ctzll(past);
       r.q0 = __builtin_amdgcn_readlane(from, l);
       r.lq = __builtin_amdgcn_readlane(to, l) - r.q0;
-      r.tile = __builtin_amdgcn_readlane(upto, l) - 1 - (int)unit;
+      r.tile = __builtin_amdgcn_readlane((int)upto, l) - 1 - (int)unit;
       r.k0 = __builtin_amdgcn_readlane(k_from, l);
       r.lk = __builtin_amdgcn_readlane(k_to, l) - r.k0;
       r.found = true;
       return r;
     }
-    unit -= __builtin_amdgcn_readlane(upto, 63);
+    unit -= (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
   }
   return r;
 }
@@ -115,15 +117,15 @@ struct Share {
 };
 __device__ __forceinline__ Share share_of(const PrefillArgs& a, const PrefillWork& w, int64_t block, int splits) {
   Share s;
-  s.group = (int)(block % w.groups);  // neighbours on the card's eight parts take different heads
-  const int64_t rest = block / w.groups;
+  const int64_t rest = quotient(block, w.groups);
+  s.group = (int)(block - rest * w.groups);  // neighbours on the card's eight parts take different heads
   // The last shares come first, and the first, which all tiles have, at the end: blocks that
   // have nothing to do stand together.  (Between the others they cost twice the time: blocks go
   // to the card's parts in turn, whatever there is to do.)
-  const int from_end = (int)(rest / w.units);
+  const int from_end = (int)quotient(rest, w.units);
   s.split = splits - 1 - from_end;
   const int64_t unit = rest - from_end * w.units;
-  s.at = find_tile(a, kRows / w.heads, unit);
+  s.at = find_tile(a, w.shift, unit);
   s.record = (unit * w.groups + s.group) * w.splits;
   return s;
 }
@@ -151,16 +153,30 @@ struct Prefill {
   int lane, wave, half, lim;  // lim: the last key that the lane's query sees
 
   // Tile `first` of the keys or values: a wave's load fills 1024 bytes, whole rows.  Rows
-  // behind the last key repeat it; they are masked.
+  // behind the last key repeat it; they are masked.  FIRST: before the loop, whose places the
+  // widest heads would else keep in memory and wait for (1021 queries over 8191 keys 148 us, 153).
+  template <bool FIRST = false>
   __device__ __forceinline__ void stage(const uint16_t* base, int64_t stride, int first, int lk, uint8_t* dst) const {
     constexpr int PER = kRow / 16, ROWS = 64 / PER;  // pieces of a row, rows of a load
     const __amdgpu_buffer_rsrc_t src = rows_from(base + first * stride);
     const int last = lk - 1 - first;
+    const int lane = FIRST && D == 256 ? opaque(this->lane) : this->lane;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int row = (wave + 4 * i) * ROWS + lane / PER, piece = (lane % PER) ^ swizzle<D>(row);
       copy_to_lds(src, (uint32_t)min(row, last) * (uint32_t)(2 * stride) + 16 * piece, dst + (wave + 4 * i) * 1024);
     }
+  }
+
+  __device__ __forceinline__ void load_queries(const uint16_t* from) {
+#pragma unroll
+    for (int k = 0; k < KS; ++k) q[k] = *(const u32x4*)(from + 16 * k);
+  }
+  // The queries are waited for here, and not where the compiler would wait for what was
+  // asked for after them too.
+  __device__ __forceinline__ void hold_queries() {
+#pragma unroll
+    for (int k = 0; k < KS; ++k) asm volatile("" : "+v"(q[k]));
   }
 
   // The softmax of the tile whose scores are in s: its weights in p.  masked: some query
@@ -183,7 +199,7 @@ struct Prefill {
     top = fmaxf(tops.x, tops.y) * c;
     // The maximum that is subtracted may lag 2^8 behind the true one: the sums stay far
     // inside fp32, and y is scaled anew only when a query's maximum really moves (1 x 16384
-    // 1076 us, 1122 where it follows at once; 1 x 8192 of 256 channels 570 us, 625).
+    // 1012 us, 1061 where it follows at once; 1 x 8192 of 256 channels 506 us, 573).
     if (__any(top > m + 8.f)) {
       const float now = fmaxf(m, top), f = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
       m = now;
@@ -214,12 +230,11 @@ struct Prefill {
   // y^T += V^T P^T from the values at vs, then S^T = K Q^T from the keys at ks; without VALUES
   // the scores alone.  The operands are read from LDS kAhead products ahead, in an order that
   // the compiler is held to: a wave has one neighbour on its SIMD, which does not hide a read
-  // that is waited for where it is used (1 x 16384, 32 heads of 128: 1023 us, 1051 without the
-  // order; 1031 at 6 ahead, 1033 at 8, 1044 at 12).  At 256 channels, where registers are short, the
-  // order holds for groups of four (1 x 8192: 548 us, 594 for single products, 579 without).
+  // that is waited for where it is used (1 x 16384, 32 heads of 128: 1012 us, 1040 in the
+  // compiler's order, 1023 with 8 ahead; 1 x 8192, 16 heads of 256: 503 us, 540).
   template <bool VALUES>
   __device__ __forceinline__ void products(const uint8_t* vs, const uint8_t* ks) {
-    constexpr int NV = VALUES ? 2 * KT * DT : 0, N = NV + KS * KT, kAhead = 4, kHeld = D == 256 ? 4 : 1;
+    constexpr int NV = VALUES ? 2 * KT * DT : 0, N = NV + KS * KT, kAhead = 4;
     const int i16 = lane & 15, g = lane >> 4, krow = lane & 31;
     int vat[2], kat = krow * kRow + ((half ^ swizzle<D>(krow)) << 4);
 #pragma unroll
@@ -245,7 +260,7 @@ struct Prefill {
     for (int j = 0; j < kAhead; ++j) read(j);
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (j % kHeld == 0) __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_sched_barrier(0);
       if (j < NV) {
         o[j % DT] = H::mfma32(f[j % kAhead], p[j / DT / 2][j / DT % 2], o[j % DT]);
       } else {
@@ -324,14 +339,18 @@ __global__ __launch_bounds__(256, 2) void attention_prefill_kernel(PrefillArgs a
   w.lane = threadIdx.x & 63;
   w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   w.half = w.lane >> 5;
-  const int queries = kRows / work.heads, first_query = at.tile * queries;
-  const int head = share.group * work.heads + w.wave % work.heads, first_row = first_query + 32 * (w.wave / work.heads);
+  const int queries = kRows >> work.shift, first_query = at.tile * queries;
+  const int head = (share.group << work.shift) + (w.wave & ((1 << work.shift) - 1));
+  const int first_row = first_query + 32 * (w.wave >> work.shift);
   const int row = first_row + (w.lane & 31);
   w.lim = a.causal ? min(row + at.lk - at.lq, at.lk - 1) : at.lk - 1;
   const int64_t token = at.q0 + min(row, at.lq - 1);
   const uint16_t* qp = a.q.p + token * a.q.token + head * a.q.head + 8 * w.half;
-#pragma unroll
-  for (int k = 0; k < W::KS; ++k) w.q[k] = *(const u32x4*)(qp + 16 * k);
+  // The widest heads' queries are asked for behind the first keys and waited for with them:
+  // they have no registers to wait in (1 x 8192 506 us, 532 with the queries first; of 64 and 128
+  // channels these go first, 1 x 4096 86 us and 91, 1 x 2048 54 and 60).
+  constexpr bool kQueriesFirst = D < 256;
+  if (kQueriesFirst) w.load_queries(qp);
   const int kv = head / (a.heads / a.kv_heads);
   const uint16_t* kp = a.k.p + at.k0 * a.k.token + kv * a.k.head;
   const uint16_t* vp = a.v.p + at.k0 * a.v.token + kv * a.v.head;
@@ -358,13 +377,20 @@ __global__ __launch_bounds__(256, 2) void attention_prefill_kernel(PrefillArgs a
       if (t + 2 < to) w.stage(kp, a.k.token, (t + 2) * W::BN, at.lk, kbuf + now * W::kTile);
     };
     if (from < to) {
-      w.stage(kp, a.k.token, from * W::BN, at.lk, kbuf);
-      w.stage(vp, a.v.token, from * W::BN, at.lk, vbuf);
+      w.template stage<true>(kp, a.k.token, from * W::BN, at.lk, kbuf);
+      if (!kQueriesFirst) {
+        __builtin_amdgcn_sched_barrier(0);
+        w.load_queries(qp);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      w.template stage<true>(vp, a.v.token, from * W::BN, at.lk, vbuf);
       if (from + 1 < to) {
-        w.stage(kp, a.k.token, (from + 1) * W::BN, at.lk, kbuf + W::kTile);
+        w.template stage<true>(kp, a.k.token, (from + 1) * W::BN, at.lk, kbuf + W::kTile);
         arrived<2 * W::kLoads>();
+        if (!kQueriesFirst) w.hold_queries();
       } else {
         arrived<W::kLoads>();
+        if (!kQueriesFirst) w.hold_queries();
       }
       meet();
       if (from * W::BN < wave_end) w.template products<false>(nullptr, kbuf);
@@ -430,10 +456,10 @@ __global__ __launch_bounds__(64) void attention_prefill_join_kernel(PrefillArgs 
   const Place& at = share.at;
   if (!at.found) return;
   const int lane = threadIdx.x, half = lane >> 5;
-  const int queries = kRows / work.heads, first_query = at.tile * queries;
+  const int queries = kRows >> work.shift, first_query = at.tile * queries;
   const int tiles = (keys_seen(a, at, first_query + queries - 1) + W::BN - 1) / W::BN, n = shares(work, tiles);
   if (n == 1) return;
-  const int row = first_query + 32 * (wave / work.heads) + (lane & 31);
+  const int row = first_query + 32 * (wave >> work.shift) + (lane & 31);
   const float* base = work.parts + share.record * RECORD;
   const float* ml = base + kRows * D + 64 * wave + (lane & 31);
   float m[kMaxSplits], l[kMaxSplits], top = -INFINITY, sum = 0.f;
@@ -458,7 +484,7 @@ __global__ __launch_bounds__(64) void attention_prefill_join_kernel(PrefillArgs 
   }
   if (row >= at.lq) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t out = (at.q0 + row) * (int64_t)a.heads + share.group * work.heads + wave % work.heads;
+  const int64_t out = (at.q0 + row) * (int64_t)a.heads + (share.group << work.shift) + (wave & ((1 << work.shift) - 1));
   uint16_t* y = a.y + out * D + 32 * d0 + 4 * half;
 #pragma unroll
   for (int e = 0; e < 8; ++e)
@@ -469,14 +495,14 @@ __global__ __launch_bounds__(64) void attention_prefill_join_kernel(PrefillArgs 
 PrefillWork work_of(const PrefillArgs& a) {
   PrefillWork w{};
   const int shared = a.heads / a.kv_heads;
-  w.heads = shared % 4 == 0 ? 4 : shared % 2 == 0 ? 2 : 1;
-  w.groups = a.heads / w.heads;
-  w.units = a.Tq / (kRows / w.heads) + std::min(a.n, a.Tq);
+  w.shift = shared % 4 == 0 ? 2 : shared % 2 == 0 ? 1 : 0;
+  w.groups = a.heads >> w.shift;
+  w.units = (a.Tq >> (kRowBits - w.shift)) + std::min(a.n, a.Tq);
   // Where there are fewer blocks than fill the card, several share the keys of one, if there
-  // are enough of these (1021 queries over 8191 keys, 16 heads of 256: 167 us, 389 without;
-  // shares of four tiles instead of eight: 1 x 1000, 33 us, 28 with eight).
+  // are enough of these (1021 queries over 8191 keys, 16 heads of 256: 148 us, 363 without;
+  // shares of four tiles instead of eight: 1 x 1000, 32 us, 28 with eight).
   // Not to even out ragged sequences: blocks that turn out to have nothing to do, and the
-  // joining, cost more than that gains (1809 of 4099 tokens in one of 11 sequences: 72 us, 55
+  // joining, cost more than that gains (1809 of 4099 tokens in one of 11 sequences: 67 us, 52
   // without).
   const int64_t blocks = w.units * w.groups, tiles = a.Tk / (kTileKeysOf(a.D) * kSplitTiles);
   w.splits = (int)std::max<int64_t>(1, std::min<int64_t>({kMaxSplits, (kFill + blocks / 2) / blocks, tiles}));

@@ -25,7 +25,6 @@
 
 #include "attention_device.h"
 #include "attention_internal.h"
-#include "wave_ops.h"
 
 namespace moe {
 
@@ -101,11 +100,6 @@ __device__ __forceinline__ void copy4_to_lds(const void* src, uint8_t* dst) {
 }
 #pragma clang diagnostic pop
 
-// a / b, in 32 bits where these do.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
 // Four e4m3 codes -> four 16-bit values (exact).
 template <bool F16>
 __device__ __forceinline__ u32x2 widen4(uint32_t v) {
@@ -130,20 +124,6 @@ __device__ __forceinline__ float over_column(float v, F f) {
 __device__ __forceinline__ u32x2 read_transposed8(const uint8_t* p) {
   typedef int i32x2_t __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2_t*)(p)));
-}
-
-// Sums over the lanes up to each.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t shifted(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, true);
-}
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
-  v += shifted<kDppShr1, 0xF>(v);
-  v += shifted<kDppShr2, 0xF>(v);
-  v += shifted<kDppShr4, 0xF>(v);
-  v += shifted<kDppShr8, 0xF>(v);
-  v += shifted<kDppBcast15, 0xA>(v);
-  return v + shifted<kDppBcast31, 0xC>(v);
 }
 
 template <bool F16, bool F8, int D>
