@@ -14,17 +14,20 @@ namespace moe {
 namespace {
 
 // ------------------------------------------------------------------ append
-// One token a block, or where there are few tokens several blocks.  Of a rotated head, channels i and i + R / 2 (or 2 i and 2 i + 1)
-// are one pair, turned by the angle position * inv_freq[i]:
+// Of a rotated head, channels i and i + R / 2 (or 2 i and 2 i + 1) are one pair, turned by
+// the angle position * inv_freq[i]:
 //   (a, b) -> (a cos - b sin, b cos + a sin).
 // The angle is formed and reduced to a fraction of a turn in fp64 (far positions keep
 // their bits), its sine and cosine in fp32, once a token and for all its heads.
-// A lane has two pieces of 16 bytes of a head row, a pair that is turned together where
-// there is one, and a row's lanes are neighbours, so a row's largest magnitude, for e4m3, is
-// a reduction among these; a row is read whole before any of it is written, so q and k may
-// be written in place.  The first rows are asked for before the angles and the page are known.
+// A block has one token, or where there are few tokens a part of its heads.  A lane has two
+// pieces of 16 bytes of a head row, a pair that is turned together where there is one, and a
+// row's lanes are neighbours, so a row's largest magnitude, for e4m3, is a reduction among
+// these; a row is read whole before any of it is written, so q and k may be written in place.
+// The first rows are asked for before the angles and the page are known.
+// HBM bounds long calls: 16381 tokens of 32 + 2 x 8 heads of 128, half of them turned, 84 us
+// (5.2 TB/s; 92 us with two rows in a lane's hand, 105 with four); a step of 64 tokens into
+// e4m3 is a launch, a trip to memory and the sines: 4.3 us.
 constexpr int kAppendThreads = 256;
-constexpr int kAppendDeep = 2;  // rows a lane has in hand
 
 template <int LANES>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
@@ -36,7 +39,7 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
 template <bool F16, bool F8, int D>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a, int blocks) {
   using H = Half<F16>;
-  constexpr int PER = D / 8, LANES = PER / 2, ROWS = kAppendThreads / LANES, DEEP = kAppendDeep;
+  constexpr int PER = D / 8, LANES = PER / 2, ROWS = kAppendThreads / LANES;
   __shared__ __attribute__((aligned(16))) float turn[2][D / 2];
   const int64_t unit = (int64_t)blockIdx.y * gridDim.x + blockIdx.x, t = unit / blocks;
   const int part = (int)(unit - t * blocks);
@@ -50,21 +53,16 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a,
   const bool turned = lane < pairs;
   const int piece = turned ? lane : pairs + lane, other = turned ? lane + pairs : piece + LANES - pairs;
 
-  u32x4 own[DEEP][2];
-  auto load = [&](int r0) {
-#pragma unroll
-    for (int u = 0; u < DEEP; ++u) {
-      const int r = r0 + u * ROWS;
-      if (r >= rows) continue;
-      const bool is_q = r < nq, is_k = !is_q && r < nq + kvh;
-      const HeadRows& from = is_q ? a.q : is_k ? a.k : a.v;
-      const uint16_t* x = from.p + t * from.token + (is_q ? r : is_k ? r - nq : r - nq - kvh) * from.head;
-      own[u][0] = *(const u32x4*)(x + 8 * piece);
-      own[u][1] = *(const u32x4*)(x + 8 * other);
-    }
+  u32x4 own[2];
+  auto load = [&](int r) {
+    const bool is_q = r < nq, is_k = !is_q && r < nq + kvh;
+    const HeadRows& from = is_q ? a.q : is_k ? a.k : a.v;
+    const uint16_t* x = from.p + t * from.token + (is_q ? r : is_k ? r - nq : r - nq - kvh) * from.head;
+    own[0] = *(const u32x4*)(x + 8 * piece);
+    own[1] = *(const u32x4*)(x + 8 * other);
   };
-  const int step = ROWS * blocks * DEEP, first = part * ROWS * DEEP + threadIdx.x / LANES;
-  if (row >= 0) load(first);
+  int r = part * ROWS + threadIdx.x / LANES;
+  if (row >= 0 && r < rows) load(r);
 
   int64_t page = -1;
   if (row >= 0 && row < a.c.rows && position >= 0 && (position >> a.c.shift) < a.c.width) {
@@ -81,59 +79,55 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a,
   }
   __syncthreads();
   if (row < 0) return;  // padding: everything stays as it was
-  for (int r0 = first;;) {
+  while (r < rows) {
+    const bool is_q = r < nq, is_k = !is_q && r < nq + kvh;
+    const HeadRows& to = is_q ? a.q_out : a.k_out;
+    const int h = is_q ? r : is_k ? r - nq : r - nq - kvh;
+    float f[2][8];
+    const bool turn_it = (is_q || is_k) && turned;
+    u32x4 bits[2] = {own[0], own[1]};
+    if (turn_it || F8) {
 #pragma unroll
-    for (int u = 0; u < DEEP; ++u) {
-      const int r = r0 + u * ROWS;
-      if (r >= rows) continue;
-      const bool is_q = r < nq, is_k = !is_q && r < nq + kvh;
-      const HeadRows& to = is_q ? a.q_out : a.k_out;
-      const int h = is_q ? r : is_k ? r - nq : r - nq - kvh;
-      float f[2][8];
-      const bool turn_it = (is_q || is_k) && turned;
-      u32x4 bits[2] = {own[u][0], own[u][1]};
-      if (turn_it || F8) {
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int e = 0; e < 8; ++e) f[i][e] = H::widen(own[i][e / 2] >> (16 * (e & 1)));
+    }
+    if (turn_it) {
+      if (a.interleaved) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[i][e] = H::widen(own[u][i][e / 2] >> (16 * (e & 1)));
-      }
-      if (turn_it) {
-        if (a.interleaved) {
+        for (int i = 0; i < 2; ++i) {
+          const int at = 4 * (i ? other : piece);
+          const f32x4 c = *(const f32x4*)(turn[0] + at), s = *(const f32x4*)(turn[1] + at);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int at = 4 * (i ? other : piece);
-            const f32x4 c = *(const f32x4*)(turn[0] + at), s = *(const f32x4*)(turn[1] + at);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float lo = f[i][2 * e], hi = f[i][2 * e + 1];
-              f[i][2 * e] = lo * c[e] - hi * s[e];
-              f[i][2 * e + 1] = hi * c[e] + lo * s[e];
-            }
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const f32x4 c = *(const f32x4*)(turn[0] + 8 * piece + 4 * x), s = *(const f32x4*)(turn[1] + 8 * piece + 4 * x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float lo = f[0][4 * x + e], hi = f[1][4 * x + e];
-              f[0][4 * x + e] = lo * c[e] - hi * s[e];
-              f[1][4 * x + e] = hi * c[e] + lo * s[e];
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float lo = f[i][2 * e], hi = f[i][2 * e + 1];
+            f[i][2 * e] = lo * c[e] - hi * s[e];
+            f[i][2 * e + 1] = hi * c[e] + lo * s[e];
           }
         }
+      } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          bits[i] = u32x4{H::pack(f[i][0], f[i][1]), H::pack(f[i][2], f[i][3]), H::pack(f[i][4], f[i][5]), H::pack(f[i][6], f[i][7])};
+        for (int x = 0; x < 2; ++x) {
+          const f32x4 c = *(const f32x4*)(turn[0] + 8 * piece + 4 * x), s = *(const f32x4*)(turn[1] + 8 * piece + 4 * x);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float lo = f[0][4 * x + e], hi = f[1][4 * x + e];
+            f[0][4 * x + e] = lo * c[e] - hi * s[e];
+            f[1][4 * x + e] = hi * c[e] + lo * s[e];
+          }
+        }
       }
-      if ((is_q || is_k) && to.p) {
-        uint16_t* y = (uint16_t*)to.p + t * to.token + h * to.head;
-        const uint32_t nan = 0x7FFF7FFFu;  // a NaN of either kind
-        *(u32x4*)(y + 8 * piece) = wrong ? u32x4{nan, nan, nan, nan} : bits[0];
-        *(u32x4*)(y + 8 * other) = wrong ? u32x4{nan, nan, nan, nan} : bits[1];
-      }
-      if (is_q || wrong) continue;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        bits[i] = u32x4{H::pack(f[i][0], f[i][1]), H::pack(f[i][2], f[i][3]), H::pack(f[i][4], f[i][5]), H::pack(f[i][6], f[i][7])};
+    }
+    if ((is_q || is_k) && to.p) {
+      uint16_t* y = (uint16_t*)to.p + t * to.token + h * to.head;
+      const uint32_t nan = 0x7FFF7FFFu;  // a NaN of either kind
+      *(u32x4*)(y + 8 * piece) = wrong ? u32x4{nan, nan, nan, nan} : bits[0];
+      *(u32x4*)(y + 8 * other) = wrong ? u32x4{nan, nan, nan, nan} : bits[1];
+    }
+    if (!is_q && !wrong) {
       const int64_t slot = (page * kvh + h) * a.c.P + (position & (a.c.P - 1));
       void* cache = (void*)(is_k ? a.c.k : a.c.v);
       if (F8) {
@@ -146,9 +140,8 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a,
         ((u32x4*)cache)[slot * PER + other] = bits[1];
       }
     }
-    r0 += step;
-    if (r0 - threadIdx.x / LANES >= rows) break;
-    load(r0);
+    r += ROWS * blocks;
+    if (r < rows) load(r);
   }
 }
 
@@ -494,8 +487,9 @@ int64_t blocks_of_plane(int64_t planes) { return planes ? std::max<int64_t>(1, 4
 int64_t pages_workspace_bytes(int64_t rows, int64_t n_pages) { return 256 + up256(8 * rows) + 3 * up256(4 * n_pages); }
 
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
-  constexpr int PIECES = 2 * kAppendThreads * kAppendDeep;
-  // 256 tokens fill the card with a block each
+  constexpr int PIECES = 2 * kAppendThreads;
+  // 256 tokens fill the card with a block each; of fewer, a block a pass over the token's rows
+  // (64 tokens of 32 + 2 x 8 heads of 128 into e4m3: 4.3 us, 5.3 with a block a token)
   const int pieces = ((a.q.p ? a.heads : 0) + 2 * a.c.kv_heads) * (a.c.D / 8);
   const int blocks = a.T < 256 ? std::max(1, std::min((pieces + PIECES - 1) / PIECES, 64)) : 1;
   const int64_t units = a.T * blocks, x = std::min<int64_t>(units, 1 << 20);
