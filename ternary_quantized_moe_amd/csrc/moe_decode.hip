@@ -9,15 +9,24 @@
 // a sequence that others share goes to the workspace as (m, l, sum), and a second launch
 // joins these in the order of the workers.
 //
-// A wave copies 32 tokens of keys and values into LDS of its own by loads that go there
+// A wave copies 32 or 64 tokens of keys and values into LDS of its own by loads that go there
 // directly, some tiles ahead, and needs no barrier until a sequence ends and the waves
-// join.  Scores are formed transposed, S^T = K Q^T, with the query heads on the matrix
+// join.  Every lane finds its token's row by itself, so pages may have any size (a second way
+// for tiles within a page, with one address for all lanes, won 0.5% there and lost 1.5%
+// elsewhere).  Scores are formed transposed, S^T = K Q^T, with the query heads on the matrix
 // core's columns (16 of them; fewer leave columns idle, which HBM hides); the softmax is
 // then within a lane and the four lanes of a column, and P stands as the second operand
 // of y^T = V^T P^T, whose first is read from LDS transposed.  P is rounded to 16 bits for
 // the matrix cores (half a step of itself, as y's own rounding).
 // e4m3 codes are widened exactly; a key's scale multiplies its scores, a value's scale
 // the weights before they are rounded.
+//
+// Of 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, it reads 974 MB in 176 us
+// (5.5 TB/s; some of that is in the Infinity Cache), of one of 131072 268 MB in 42 us and joins
+// in 6 (56 with the gap between the launches), of 256 of up to 3001 in e4m3 832 MB in 164 us
+// (5.1 TB/s).  One sequence of 77 tokens is a launch and a chain of latencies: 9 us, of which
+// finding the place takes 0.9, the page numbers 0.3, each of its two tiles 1.4 to ask for and
+// 0.9 to go through, the join of the waves and the store 1.5.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -30,14 +39,16 @@ namespace moe {
 
 namespace {
 
-constexpr int kBlocks = 256;   // one a CU: a block's tiles fill the LDS
+// One a CU: its tiles fill the LDS (512: 256 sequences in e4m3 177 us, 165 with 256).
+constexpr int kBlocks = 256;
 constexpr int kHeadTile = 16;  // query heads of a block
 
 template <int D>
-constexpr int kWaves = D == 256 ? 2 : 4;
+constexpr int kWaves = D == 256 ? 2 : 4;  // two tiles of each wave fit the LDS
 // Tokens of a wave's tile: what a wave does between a tile's arrival and its end is a chain
 // of latencies, so a tile has 64 tokens where these are short (64 channels, or 8 bits) and
-// 32 otherwise.
+// 32 otherwise (256 sequences of up to 3001 in e4m3 165 us, 178 with 32; 16 of up to 2000, 16
+// heads of 64, 20 us and 22).
 template <bool F8, int D>
 constexpr int kTileTokens = F8 || D == 64 ? 64 : 32;
 
@@ -72,22 +83,11 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // Loads that go to LDS, lane after lane from dst on (the same in the whole wave).  They are
 // written out, since the compiler waits for every such load of its own before any read of
 // LDS, the tiles in flight among them; they write no register, and what needs them waits for
-// them here.  Between a scalar that the vector unit wrote and its use as a descriptor stand
-// five wait states, one between m0 and its use.
+// them here.  Between m0 and its use stands one wait state.
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"  // m0 is set by every statement that uses it
 __device__ __forceinline__ uint32_t lds_address(uint8_t* p) {
   return (uint32_t)uniform((int)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)p);
-}
-// A buffer over the bytes from p on (p the same in the whole wave), and 16 bytes a lane of it, from lane_off + off on.
-__device__ __forceinline__ u32x4 buffer_from(const void* p) {
-  const uint64_t at = (uint64_t)(uintptr_t)p;
-  return u32x4{(uint32_t)uniform((int)at), (uint32_t)uniform((int)(at >> 32)), 0xFFFFFFFFu, 0x00027000u};
-}
-__device__ __forceinline__ void buffer_to_lds(u32x4 src, uint32_t lane_off, int off, uint8_t* dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds_address(dst)), "v"(lane_off),
-               "s"(src), "s"(off)
-               : "memory", "m0");
 }
 // 16 or 4 bytes a lane from the lane's address.
 __device__ __forceinline__ void copy16_to_lds(const void* src, uint8_t* dst) {
@@ -177,11 +177,7 @@ struct Decode {
   __device__ __forceinline__ int first_of(const Walk& w) const { return w.tile * kBlockKeys + wave * kKeys; }
   __device__ __forceinline__ const int32_t* table_of(const Walk& w) const { return a.c.tables + (int64_t)w.b * a.c.width; }
 
-  // Where a tile lies in one page, that page.
-  __device__ __forceinline__ int page_of(const Walk& w) const {
-    return a.c.width > 0 ? scalar_load(table_of(w) + (min(first_of(w), max(w.len - 1, 0)) >> a.c.shift)) : -1;
-  }
-  // Otherwise the page of every token goes to LDS, lane after lane, ahead of its tile.
+  // The page of every token goes to LDS, lane after lane, ahead of its tile.
   __device__ __forceinline__ void pages_to_lds(const Walk& w, uint8_t* dst) const {
     const int key = min(first_of(w) + (lane & (kKeys - 1)), max(w.len - 1, 0));
     copy4_to_lds(a.c.width > 0 ? table_of(w) + (key >> a.c.shift) : a.lengths, dst);
@@ -189,47 +185,22 @@ struct Decode {
 
   // The wave's tile into LDS.  Rows behind the last token repeat it; they are masked.  A
   // page that is none makes the sequence's results NaN and is read as page 0.
-  __device__ __forceinline__ bool stage(const Walk& w, int page, bool one_page, uint8_t* dst) const {
+  __device__ __forceinline__ bool stage(const Walk& w, int page, uint8_t* dst) const {
     const int first = first_of(w), last = max(w.len - 1, 0);
     const bool wrong = page < 0 || page >= a.c.n_pages || a.c.width == 0;
     if (wrong) page = 0;
     const int place = min(first + (lane & (kKeys - 1)), last) & (a.c.P - 1);  // of the lane's token in its page
-    if (one_page) {
-      const int from = min(first, last), end = last - from;
-      const int64_t at = (((int64_t)uniform(page) * a.c.kv_heads + kv) * a.c.P + (from & (a.c.P - 1))) * ROW;
-      const u32x4 from_k = buffer_from((const uint8_t*)a.c.k + at), from_v = buffer_from((const uint8_t*)a.c.v + at);
-      if (end >= kKeys - 1) {
-        // a lane's places in the loads differ by whole loads and in the swizzle
-        const uint32_t lane_off = lane / PER * ROW + 16 * ((lane % PER) ^ swizzle<ROW>(lane / PER));
+    const int64_t mine = ((int64_t)page * a.c.kv_heads + kv) * a.c.P + place;  // the lane's token's row of the cache
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const uint32_t off = lane_off ^ (16 * swizzle<ROW>(i * ROWS));
-          buffer_to_lds(from_k, off, i * 1024, dst + i * 1024);
-          buffer_to_lds(from_v, off, i * 1024, dst + kTile + i * 1024);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-          const int row = i * ROWS + lane / PER;
-          const uint32_t off = min(row, end) * ROW + 16 * ((lane % PER) ^ swizzle<ROW>(row));
-          buffer_to_lds(from_k, off, 0, dst + i * 1024);
-          buffer_to_lds(from_v, off, 0, dst + kTile + i * 1024);
-        }
-      }
-    } else {
-      const int64_t mine = ((int64_t)page * a.c.kv_heads + kv) * a.c.P + place;  // the lane's token's row of the cache
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) {
-        const int row = i * ROWS + lane / PER;
-        const int64_t at = __shfl(mine, row, 64) * ROW + 16 * ((lane % PER) ^ swizzle<ROW>(row));
-        copy16_to_lds((const uint8_t*)a.c.k + at, dst + i * 1024);
-        copy16_to_lds((const uint8_t*)a.c.v + at, dst + kTile + i * 1024);
-      }
+    for (int i = 0; i < kLoads; ++i) {
+      const int row = i * ROWS + lane / PER;
+      const int64_t at = __shfl(mine, row, 64) * ROW + 16 * ((lane % PER) ^ swizzle<ROW>(row));
+      copy16_to_lds((const uint8_t*)a.c.k + at, dst + i * 1024);
+      copy16_to_lds((const uint8_t*)a.c.v + at, dst + kTile + i * 1024);
     }
     if (F8) {  // the scales: the keys', then the values'
-      const int64_t at = ((int64_t)page * a.c.kv_heads + kv) * a.c.P + place;
-      copy4_to_lds(a.c.k_scales + at, dst + 2 * kTile);
-      copy4_to_lds(a.c.v_scales + at, dst + 2 * kTile + 256);
+      copy4_to_lds(a.c.k_scales + mine, dst + 2 * kTile);
+      copy4_to_lds(a.c.v_scales + mine, dst + 2 * kTile + 256);
     }
     return wrong && w.len > 0;
   }
@@ -471,32 +442,21 @@ __global__ __launch_bounds__(64 * kWaves<D>) void attention_decode_kernel(Decode
   const float c = a.scale * kLog2e;
   constexpr int AHEAD = W::kStages - 1;
   uint32_t wrong = 0;  // a bit for each buffer: its tile's page is none
-  // The page numbers are read a tile before they are needed: one as a scalar, or the
-  // tokens' into LDS.
-  const bool one_page = a.c.P >= W::kKeys;
+  // The page numbers are read a tile before they are needed.
   uint8_t* const ids = lds + W::W * W::kStages * W::kStage + w.wave * 512;
-  int page = 0, slot = 0, turn = 0;  // slot: the buffer of the next tile to load
-  if (one_page) {
-    page = w.page_of(ahead);
-  } else {
-    w.pages_to_lds(ahead, ids);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  }
+  int slot = 0, turn = 0;  // slot: the buffer of the next tile to load
+  w.pages_to_lds(ahead, ids);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   auto load_next = [&] {
     const typename W::Walk tile = ahead;
-    int of_tile = page;
     w.step(ahead);
-    if (one_page) {
-      if (ahead.left > 0) page = w.page_of(ahead);
-    } else {
-      // behind the numbers stand the loads of the tile before, and no others that were there
-      // when they were asked for
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(W::kPerStage) : "memory");
-      of_tile = *(const int*)(ids + 256 * turn + 4 * w.lane);
-      turn ^= 1;
-      w.pages_to_lds(ahead.left > 0 ? ahead : tile, ids + 256 * turn);
-    }
-    const bool bad = w.stage(tile, of_tile, one_page, w.mine + slot * W::kStage);
+    // behind the numbers stand the loads of the tile before, and no others that were there
+    // when they were asked for
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(W::kPerStage) : "memory");
+    const int page = *(const int*)(ids + 256 * turn + 4 * w.lane);
+    turn ^= 1;
+    w.pages_to_lds(ahead.left > 0 ? ahead : tile, ids + 256 * turn);
+    const bool bad = w.stage(tile, page, w.mine + slot * W::kStage);
     wrong = (wrong & ~(1u << slot)) | (uint32_t)bad << slot;
     slot = slot == AHEAD ? 0 : slot + 1;
   };
@@ -624,6 +584,7 @@ hipError_t launch(const DecodeArgs& a, DecodeWork w, hipStream_t stream) {
   constexpr int KEYS = Decode<F16, F8, D>::kBlockKeys;
   const int64_t most = a.B * std::max<int64_t>(1, (room + KEYS - 1) / KEYS);
   w.workers = (int)std::min<int64_t>(w.workers, most);
+  // Two tiles are gone through in less time than a second launch takes (77 tokens 11 us, 14).
   if (most <= 2) w.workers = 1;
   attention_decode_kernel<F16, F8, D><<<(unsigned)(w.groups * w.workers), 64 * kWaves<D>, 0, stream>>>(a, w);
   if (w.workers > 1)
