@@ -18,11 +18,11 @@
 // Where a launch has too few blocks for the card, several share the keys of a tile of
 // queries, and a second launch joins what they leave in the workspace.
 //
-// The matrix cores bound long prompts, and the power that they may draw: 1 x 16384, 32 heads of
+// The matrix cores bound long prompts, and the power that they may draw: 1 x 16384, 16 heads of
 // 128, causal, takes 1012 us (1.09 PFLOP/s; a loop of bare products reaches 1.27), 8 x 2048 of
 // 16 heads, not causal, 471 us (1.02), 1 x 8192, 16 heads of 256, 503 us (1.09), 1 x 4096, 32
 // heads of 64, 86 us (0.80: the exponentials weigh twice as much).  In the first the matrix
-// cores are busy 57% of the cycles, the vector units as long, and LDS has no bank conflicts.
+// cores are busy 56% of the cycles, the vector units 53%, and LDS has no bank conflicts.
 // Ragged prompts are bound by the longest row's walk over its keys (4099 tokens in 11 sequences
 // 52 us), and the smallest by a launch and three trips to memory (61 tokens 6.7 us).
 #include <hip/hip_runtime.h>
@@ -230,7 +230,7 @@ struct Prefill {
   // y^T += V^T P^T from the values at vs, then S^T = K Q^T from the keys at ks; without VALUES
   // the scores alone.  The operands are read from LDS kAhead products ahead, in an order that
   // the compiler is held to: a wave has one neighbour on its SIMD, which does not hide a read
-  // that is waited for where it is used (1 x 16384, 32 heads of 128: 1012 us, 1040 in the
+  // that is waited for where it is used (1 x 16384, 16 heads of 128: 1012 us, 1040 in the
   // compiler's order, 1023 with 8 ahead; 1 x 8192, 16 heads of 256: 503 us, 540).
   template <bool VALUES>
   __device__ __forceinline__ void products(const uint8_t* vs, const uint8_t* ks) {
@@ -495,6 +495,9 @@ __global__ __launch_bounds__(64) void attention_prefill_join_kernel(PrefillArgs 
 PrefillWork work_of(const PrefillArgs& a) {
   PrefillWork w{};
   const int shared = a.heads / a.kv_heads;
+  // As many heads to a block as share keys and divide it: fewer rows stay empty, and the waves
+  // walk over the same keys (4099 tokens in 11 sequences 52 us, 58 with a head a block; 1 x 1000
+  // 27.6 and 29.0).
   w.shift = shared % 4 == 0 ? 2 : shared % 2 == 0 ? 1 : 0;
   w.groups = a.heads >> w.shift;
   w.units = (a.Tq >> (kRowBits - w.shift)) + std::min(a.n, a.Tq);

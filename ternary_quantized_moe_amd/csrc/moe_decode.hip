@@ -22,8 +22,8 @@
 // the weights before they are rounded.
 //
 // Of 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, it reads 974 MB in 176 us
-// (5.5 TB/s; some of that is in the Infinity Cache), of one of 131072 268 MB in 42 us and joins
-// in 6 (56 with the gap between the launches), of 256 of up to 3001 in e4m3 832 MB in 164 us
+// (5.5 TB/s; some of that is in the Infinity Cache), of one of 131072 268 MB in 56 us, 6 of them
+// the join (48 where that cache holds more of it), of 256 of up to 3001 in e4m3 832 MB in 164 us
 // (5.1 TB/s).  One sequence of 77 tokens is a launch and a chain of latencies: 9 us, of which
 // finding the place takes 0.9, the page numbers 0.3, each of its two tiles 1.4 to ask for and
 // 0.9 to go through, the join of the waves and the store 1.5.

@@ -149,7 +149,10 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a,
 // The free pages are those with no references.  A call that needs pages takes the lowest
 // free ones, for the rows in rising order, so its result does not depend on how blocks
 // and waves run.  One block makes the plan (what every row needs, running sums, the list
-// of free pages); a second launch carries it out, rows and copies side by side.
+// of free pages); a second launch carries it out, rows and copies side by side.  The plan is a
+// chain of a few trips to memory (5.5 us for 64 forks), the copies are bound by
+// HBM (64 forks that copy 117 MB 24 us, with the pages in the Infinity Cache; 321 MB compacted
+// 131 us, 4.9 TB/s).
 constexpr int kPlanThreads = 1024, kPlanPer = 4;
 enum Kind { kReserve, kFork };
 
@@ -324,7 +327,8 @@ __device__ __forceinline__ void copy_pages(const PoolArgs& pools, const int32_t*
 }
 
 // The same in one launch, for up to a row a thread: each thread writes its row's new pages,
-// or the wave does where a row gets many.
+// or the wave does where a row gets many (a fork, a reserve and a free of 64 rows 39.5 us, 42.5
+// with two launches for the reserve).
 __global__ __launch_bounds__(kPlanThreads) void reserve_few_kernel(TableArgs t, const int32_t* grow, int32_t* status,
                                                                    Plan p) {
   __shared__ int64_t sums[kPlanThreads / 64];
@@ -479,7 +483,8 @@ int64_t planes_of(const PoolArgs& p) {
   for (int i = 0; i < p.n; ++i) n += p.pool[i].planes;
   return n;
 }
-// Blocks that copy one plane's pages: enough over all planes to fill the card some times over.
+// Blocks that copy one plane's pages: enough over all planes to fill the card some times over
+// (compacting 135 us, 138 with 1024 blocks and 132 with 16384; forks 39.5 us, 41 and 42).
 int64_t blocks_of_plane(int64_t planes) { return planes ? std::max<int64_t>(1, 4096 / planes) : 1; }
 
 }  // namespace
