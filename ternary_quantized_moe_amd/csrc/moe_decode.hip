@@ -22,8 +22,8 @@
 // the weights before they are rounded.
 //
 // Of 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, it reads 974 MB in 176 us
-// (5.5 TB/s; some of that is in the Infinity Cache), of one of 131072 268 MB in 56 us, 6 of them
-// the join (48 where that cache holds more of it), of 256 of up to 3001 in e4m3 832 MB in 164 us
+// (5.5 TB/s; some of that is in the Infinity Cache), of one of 131072 268 MB in 54 us, the
+// join with it (46 where that cache holds more of it), of 256 of up to 3001 in e4m3 832 MB in 164 us
 // (5.1 TB/s).  One sequence of 77 tokens is a launch and a chain of latencies: 9 us, of which
 // finding the place takes 0.9, the page numbers 0.3, each of its two tiles 1.4 to ask for and
 // 0.9 to go through, the join of the waves and the store 1.5.
@@ -548,19 +548,40 @@ __global__ __launch_bounds__(256) void attention_join_kernel(DecodeArgs a, Decod
   constexpr int64_t RECORD = kHeadTile * D + 2 * kHeadTile;
   const float* base = work.parts + ((int64_t)group * work.workers + w0) * 2 * RECORD;
   auto record = [&](int i) { return base + (2 * i + (i == 0 && who.x < 0 ? 1 : 0)) * RECORD; };
+  // A thread's first records are asked for ahead of the maximum, kDeep together (one sequence of
+  // 131072 54 us, 56 with one record after the other; batches, which have few, alike).
+  constexpr int kDeep = 8;
+  const int set = threadIdx.x / PER, d = threadIdx.x % PER;
+  float m[kDeep], w[kDeep];
+  f32x4 v[kDeep];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      if (i0 + u * SETS >= n) break;
+      const float* r = record(i0 + u * SETS);
+      m[u] = r[kHeadTile * D + row];
+      w[u] = r[kHeadTile * D + kHeadTile + row];
+      v[u] = *(const f32x4*)(r + row * D + 4 * d);
+    }
+  };
+  fetch(set);
   float top = -INFINITY;
   for (int i = threadIdx.x & 63; i < n; i += 64) top = fmaxf(top, record(i)[kHeadTile * D + row]);
 #pragma unroll
   for (int s = 32; s; s >>= 1) top = fmaxf(top, __shfl_xor(top, s, 64));
-  const int set = threadIdx.x / PER, d = threadIdx.x % PER;
   f32x4 sum = {0.f, 0.f, 0.f, 0.f};
   float l = 0.f;
-  for (int i = set; i < n; i += SETS) {
-    const float* r = record(i);
-    const float m = r[kHeadTile * D + row], lr = r[kHeadTile * D + kHeadTile + row];
-    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
-    l += lr == 0.f ? 0.f : lr * f;
-    sum += *(const f32x4*)(r + row * D + 4 * d) * f;
+  for (int i0 = set;;) {
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      if (i0 + u * SETS >= n) continue;
+      const float f = m[u] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[u] - top);
+      l += w[u] == 0.f ? 0.f : w[u] * f;
+      sum += v[u] * f;
+    }
+    i0 += kDeep * SETS;
+    if (i0 >= n) break;
+    fetch(i0);
   }
   sums[threadIdx.x] = sum;
   if (d == 0) weights[set] = l;
