@@ -124,6 +124,10 @@ __device__ __forceinline__ Share share_of(const PrefillArgs& a, const PrefillWor
   // to the card's parts in turn, whatever there is to do.)
   const int from_end = (int)quotient(rest, w.units);
   s.split = splits - 1 - from_end;
+  if (s.split < 0) {  // the last row of the grid may reach past the last block
+    s.at.found = false;
+    return s;
+  }
   const int64_t unit = rest - from_end * w.units;
   s.at = find_tile(a, w.shift, unit);
   s.record = (unit * w.groups + s.group) * w.splits;

@@ -604,7 +604,7 @@ int32_t moe_attention_prefill(int32_t type, const void* q, int64_t q_tokens, int
   if (!q_starts || !y) return fail(MOE_E_ARG, "NULL pointer (q_starts or y)");
   if ((uintptr_t)y % 16 || (uintptr_t)lse % 4 || (uintptr_t)q_starts % 4 || (uintptr_t)k_starts % 4)
     return fail(MOE_E_ARG, "y must be 16-byte, lse and the starts 4-byte aligned");
-  if (moe::prefill_blocks(a) > ((int64_t)1 << 36))
+  if (moe::prefill_blocks(a) > ((int64_t)65535 << 20))
     return fail(MOE_E_SHAPE, "%lld tokens of %d heads exceed one launch", (long long)q_tokens, (int)heads);
   const int64_t need = moe::prefill_workspace_bytes(a);
   if (need && !ws) return fail(MOE_E_ARG, "NULL workspace");

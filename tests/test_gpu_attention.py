@@ -210,6 +210,15 @@ def test_many_sequences(tq):
     check(y, None, oracle_of(q, k, v, lens, lens, True, 0.125), BF16, 64, 150, float(v.abs().max()))
 
 
+def test_more_blocks_than_one_dimension(tq):
+    """20000 sequences of one token and 64 heads of their own: 1.3 M blocks.  The one weight is off
+    from 1 by the score's roundings, far below half a step of bf16, so y is v."""
+    say("20000 sequences of one token")
+    q, k, v = inputs(21, [20000], [20000], 64, 64, 64, BF16)
+    y = tq.attention_prefill(q, k, v, torch.arange(20001, dtype=torch.int32, device="cuda"))
+    assert torch.equal(y, v)
+
+
 def test_packing_does_not_matter(tq):
     lens = [129, 64, 1, 300]
     say("packed against alone")
