@@ -141,6 +141,21 @@ def test_many_sequences(tq):
     again.check(again.run(), rows=rows)
 
 
+def test_the_largest_batch(tq):
+    """65535 sequences of one token or none; of one, y is the value (tests/test_gpu_attention.py)."""
+    say("decode 65535 sequences")
+    n = 65535
+    g = torch.Generator(device="cuda")
+    g.manual_seed(21)
+    q = torch.randn((n, 2, 64), generator=g, device="cuda").to(BF16)
+    k, v = (torch.randn((n, 1, 1, 64), generator=g, device="cuda").to(BF16) for _ in range(2))
+    tables = torch.randperm(n, generator=g, device="cuda").to(torch.int32)[:, None].contiguous()
+    lengths = (torch.arange(n, device="cuda") % 3 != 1).to(torch.int32)
+    y = tq.attention_decode(q, k, v, tables, lengths)
+    want = v[tables[:, 0].long(), :, 0].expand(n, 2, 64) * lengths[:, None, None].to(BF16)
+    assert torch.equal(y, want)
+
+
 def test_the_batch_changes_last_bits_only(tq):
     say("decode in other batches")
     c = Case(tq, 6, [900, 40, 1300, 7], 8, 2, 128, 32)

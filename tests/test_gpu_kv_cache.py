@@ -129,6 +129,24 @@ def test_append_without_rotation(tq):
         assert torch.equal(b.scales[name + "_scales"][page, :, off].flatten(), scales.flatten())
 
 
+def test_more_tokens_than_one_dimension(tq):
+    """2^20 + 3 tokens of 257 sequences, a block each."""
+    say("append 2^20 + 3 tokens")
+    n, P = (1 << 20) + 3, 4096
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    k, v = (torch.randn((n, 1, 64), generator=g, device="cuda").to(BF16) for _ in range(2))
+    k_cache, v_cache = (torch.zeros((257, 1, P, 64), dtype=BF16, device="cuda") for _ in range(2))
+    token = torch.arange(n, device="cuda")
+    tables = torch.randperm(257, generator=g, device="cuda").to(torch.int32)[:, None].contiguous()
+    rows, positions = (token // P).to(torch.int32), (token % P).to(torch.int32)
+    tq.kv_append(k, v, k_cache, v_cache, tables, rows, positions)
+    page = tables[rows.long(), 0].long()
+    assert torch.equal(k_cache[page, 0, positions.long()], k[:, 0])
+    assert torch.equal(v_cache[page, 0, positions.long()], v[:, 0])
+    assert not k_cache[tables[256, 0].long(), 0, 3:].any()
+
+
 def test_far_positions(tq):
     say("far positions")
     a = Append(4, [0, 0, 0], [1, (1 << 20) - 1, 999983], 2, 1, 64, 4096, 64, F16)
