@@ -152,7 +152,7 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a,
 // of free pages); a second launch carries it out, rows and copies side by side.  The plan is a
 // chain of a few trips to memory (5.5 us for 64 forks), the copies are bound by
 // HBM (64 forks that copy 117 MB 24 us, with the pages in the Infinity Cache; 321 MB compacted
-// 131 us, 4.9 TB/s).
+// 127 us, 5.0 TB/s).
 constexpr int kPlanThreads = 1024, kPlanPer = 4;
 enum Kind { kReserve, kFork };
 
@@ -290,6 +290,8 @@ __device__ __forceinline__ void carry_out(const TableArgs& t, const int32_t* ask
   if (lane == 0) t.lengths[r] = len;
 }
 
+constexpr int64_t kCopyStep = 16 * 256 * 4;  // bytes of a block's step
+constexpr int64_t kCopyBlocks = 16384;
 // One plane's share of the moves: block x of `blocks`, 16 bytes a lane where pages allow.
 __device__ __forceinline__ void copy_pages(const PoolArgs& pools, const int32_t* from, const int32_t* to, int64_t n,
                                            int64_t x, int64_t blocks, int64_t plane) {
@@ -299,7 +301,7 @@ __device__ __forceinline__ void copy_pages(const PoolArgs& pools, const int32_t*
   const int64_t bytes = pools.pool[which].page_bytes;
   char* base = pools.pool[which].base + plane * pools.n_pages * bytes;
   const bool wide = bytes % 16 == 0 && (uintptr_t)base % 16 == 0;
-  constexpr int64_t CHUNK = 16 * 256 * 4;  // bytes of a block's step
+  constexpr int64_t CHUNK = kCopyStep;
   const int64_t chunks = (bytes + CHUNK - 1) / CHUNK;
   for (int64_t item = x; item < n * chunks; item += blocks) {
     const int64_t k = item / chunks, c = (item - k * chunks) * CHUNK;
@@ -483,9 +485,17 @@ int64_t planes_of(const PoolArgs& p) {
   for (int i = 0; i < p.n; ++i) n += p.pool[i].planes;
   return n;
 }
-// Blocks that copy one plane's pages: enough over all planes to fill the card some times over
-// (compacting 135 us, 138 with 1024 blocks and 132 with 16384; forks 39.5 us, 41 and 42).
-int64_t blocks_of_plane(int64_t planes) { return planes ? std::max<int64_t>(1, 4096 / planes) : 1; }
+// Blocks that copy one plane's share of at most `moves` pages: a block for every two steps, up to
+// enough over all planes to fill the card many times over (compacting 321 MB 132 us, 135 with
+// 4096 blocks; 64 forks, a reserve and a free 39.5 us, 42 with 16384).
+int64_t blocks_of_plane(const PoolArgs& p, int64_t moves) {
+  const int64_t planes = planes_of(p);
+  if (!planes) return 1;
+  int64_t bytes = 0;
+  for (int i = 0; i < p.n; ++i) bytes = std::max(bytes, p.pool[i].page_bytes);
+  const int64_t steps = moves * ((bytes + kCopyStep - 1) / kCopyStep);
+  return std::max<int64_t>(1, std::min<int64_t>((steps + 1) / 2, kCopyBlocks / planes));
+}
 
 }  // namespace
 
@@ -527,7 +537,7 @@ hipError_t launch_kv_fork(const TableArgs& t, const int32_t* parents, const Pool
                           hipStream_t stream) {
   const Plan p = plan_in(ws, t.rows, t.n_pages);
   pages_plan_kernel<kFork><<<1, kPlanThreads, 0, stream>>>(t, parents, p);
-  const int64_t row_blocks = (t.rows + 3) / 4, planes = planes_of(pools), per = blocks_of_plane(planes);
+  const int64_t row_blocks = (t.rows + 3) / 4, planes = planes_of(pools), per = blocks_of_plane(pools, t.rows);
   pages_do_kernel<kFork><<<(unsigned)(row_blocks + planes * per), 256, 0, stream>>>(t, parents, p, status, pools, row_blocks,
                                                                                     per);
   return hipGetLastError();
@@ -542,14 +552,14 @@ hipError_t launch_kv_compact(const TableArgs& t, const PoolArgs& pools, int32_t*
                              int32_t* live, void* ws, hipStream_t stream) {
   const Plan p = plan_in(ws, t.rows, t.n_pages);
   compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(t, p, new_refs, live);
-  const int64_t row_blocks = (t.rows + 3) / 4, planes = planes_of(pools), per = blocks_of_plane(planes);
+  const int64_t row_blocks = (t.rows + 3) / 4, planes = planes_of(pools), per = blocks_of_plane(pools, t.n_pages / 2);
   compact_do_kernel<<<(unsigned)(row_blocks + planes * per), 256, 0, stream>>>(t, p, new_tables, pools, row_blocks, per);
   return hipGetLastError();
 }
 
 hipError_t launch_kv_copy_pages(const PoolArgs& pools, const int32_t* src, const int32_t* dst, int64_t n,
                                 hipStream_t stream) {
-  const int64_t planes = planes_of(pools), per = blocks_of_plane(planes);
+  const int64_t planes = planes_of(pools), per = blocks_of_plane(pools, n);
   copy_pages_kernel<<<(unsigned)(planes * per), 256, 0, stream>>>(pools, src, dst, n, per);
   return hipGetLastError();
 }
