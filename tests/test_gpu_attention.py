@@ -210,6 +210,15 @@ def test_many_sequences(tq):
     check(y, None, oracle_of(q, k, v, lens, lens, True, 0.125), BF16, 64, 150, float(v.abs().max()))
 
 
+@pytest.mark.parametrize("H,Hk", [(4096, 1), (4096, 4096)])
+def test_most_heads(tq, H, Hk):
+    say(f"{H} heads of {Hk}")
+    lens = [40, 1, 3]
+    q, k, v = inputs(22, lens, lens, H, Hk, 64, BF16)
+    check(tq.attention_prefill(q, k, v, starts_of(lens)), None, oracle_of(q, k, v, lens, lens, True, 0.125), BF16, 64, 40,
+          float(v.abs().max()))
+
+
 def test_more_blocks_than_one_dimension(tq):
     """20000 sequences of one token and 64 heads of their own: 1.3 M blocks.  The one weight is off
     from 1 by the score's roundings, far below half a step of bf16, so y is v."""

@@ -112,6 +112,15 @@ def test_head_layouts(tq, H, Hk, e4m3):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("H,Hk", [(256, 256), (4096, 1), (4096, 4096)])
+def test_as_many_groups_as_workers(tq, H, Hk):
+    """One worker for each group of heads: no shares, no workspace."""
+    say(f"decode heads {H} of {Hk}")
+    assert tq.lib().moe_attention_decode_workspace_bytes(3, H, Hk, 64) == 0
+    c = Case(tq, 22, [130, 0, 77], H, Hk, 64, 32, BF16)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("P", [1, 2, 8, 64, 512, 4096])
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_pages_of_any_size(tq, P, e4m3):
