@@ -23,8 +23,8 @@
 //
 // Of 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, it reads 974 MB in 176 us
 // (5.5 TB/s; some of that is in the Infinity Cache), of one of 131072 268 MB in 54 us, the
-// join with it (46 where that cache holds more of it), of 256 of up to 3001 in e4m3 832 MB in 164 us
-// (5.1 TB/s).  One sequence of 77 tokens is a launch and a chain of latencies: 9 us, of which
+// join with it (46 where that cache holds more of it), of 256 of up to 3001 in e4m3 832 MB in
+// 162 us (5.1 TB/s).  One sequence of 77 tokens is a launch and a chain of latencies: 9 us, of which
 // finding the place takes 0.9, the page numbers 0.3, each of its two tiles 1.4 to ask for and
 // 0.9 to go through, the join of the waves and the store 1.5.
 #include <hip/hip_runtime.h>
@@ -185,8 +185,8 @@ struct Decode {
 
   // The wave's tile into LDS.  Rows behind the last token repeat it; they are masked.  A
   // page that is none makes the sequence's results NaN and is read as page 0.
-  __device__ __forceinline__ bool stage(const Walk& w, int page, uint8_t* dst) const {
-    const int first = first_of(w), last = max(w.len - 1, 0);
+  __device__ __forceinline__ bool stage(int first, int len, int page, uint8_t* dst) const {
+    const int last = max(len - 1, 0);
     const bool wrong = page < 0 || page >= a.c.n_pages || a.c.width == 0;
     if (wrong) page = 0;
     const int place = min(first + (lane & (kKeys - 1)), last) & (a.c.P - 1);  // of the lane's token in its page
@@ -202,7 +202,7 @@ struct Decode {
       copy4_to_lds(a.c.k_scales + mine, dst + 2 * kTile);
       copy4_to_lds(a.c.v_scales + mine, dst + 2 * kTile + 256);
     }
-    return wrong && w.len > 0;
+    return wrong && len > 0;
   }
 
   // The queries of sequence b.
@@ -386,7 +386,7 @@ struct Decode {
 template <bool F16, bool F8, int D>
 __global__ __launch_bounds__(64 * kWaves<D>) void attention_decode_kernel(DecodeArgs a, DecodeWork work) {
   using W = Decode<F16, F8, D>;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[W::W * (W::kStages * W::kStage + 512)];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[W::W * W::kStages * (W::kStage + 256)];
   __shared__ __attribute__((aligned(16))) float room[W::W / 2 * W::kRecord];
   W w(a);
   w.lane = threadIdx.x & 63;
@@ -436,31 +436,44 @@ __global__ __launch_bounds__(64 * kWaves<D>) void attention_decode_kernel(Decode
     }
   }
   now.left = each + (worker < extra);
-  typename W::Walk ahead = now;  // the tile to load next
+  typename W::Walk far = now;  // the tile whose page numbers are asked for next
 
   w.mine = lds + w.wave * W::kStages * W::kStage;
   const float c = a.scale * kLog2e;
   constexpr int AHEAD = W::kStages - 1;
   uint32_t wrong = 0;  // a bit for each buffer: its tile's page is none
-  // The page numbers are read a tile before they are needed.
-  uint8_t* const ids = lds + W::W * W::kStages * W::kStage + w.wave * 512;
-  int slot = 0, turn = 0;  // slot: the buffer of the next tile to load
-  w.pages_to_lds(ahead, ids);
+  // A tile's page numbers are asked for behind the loads of the tile AHEAD + 1 before it, and so
+  // are there when the one AHEAD before it is: nothing waits for them alone (256 sequences in e4m3
+  // 162 us, 163.5 with the numbers asked for ahead of the loads of the tile before).
+  uint8_t* const ids = lds + W::W * W::kStages * W::kStage + w.wave * (W::kStages * 256);
+  int first_at[AHEAD + 1], len_at[AHEAD + 1];  // of the tiles to load next
+  int slot = 0;                                // the buffers of the next one
+  int64_t to_load = now.left;
+#pragma unroll
+  for (int i = 0; i <= AHEAD; ++i) {
+    first_at[i] = w.first_of(far);
+    len_at[i] = far.len;
+    w.pages_to_lds(far, ids + 256 * i);
+    w.step(far);
+  }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   auto load_next = [&] {
-    const typename W::Walk tile = ahead;
-    w.step(ahead);
-    // behind the numbers stand the loads of the tile before, and no others that were there
-    // when they were asked for
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(W::kPerStage) : "memory");
-    const int page = *(const int*)(ids + 256 * turn + 4 * w.lane);
-    turn ^= 1;
-    w.pages_to_lds(ahead.left > 0 ? ahead : tile, ids + 256 * turn);
-    const bool bad = w.stage(tile, page, w.mine + slot * W::kStage);
+    --to_load;
+    const int page = *(const int*)(ids + 256 * slot + 4 * w.lane);
+    const bool bad = w.stage(first_at[0], len_at[0], page, w.mine + slot * W::kStage);
     wrong = (wrong & ~(1u << slot)) | (uint32_t)bad << slot;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      first_at[i] = first_at[i + 1];
+      len_at[i] = len_at[i + 1];
+    }
+    first_at[AHEAD] = w.first_of(far);
+    len_at[AHEAD] = far.len;
+    w.pages_to_lds(far, ids + 256 * slot);
+    w.step(far);
     slot = slot == AHEAD ? 0 : slot + 1;
   };
-  for (int i = 0; i < AHEAD && ahead.left > 0; ++i) load_next();
+  for (int i = 0; i < AHEAD && to_load > 0; ++i) load_next();
   w.fetch(now.b, head0, heads, w.q);
   // the queries are waited for here: in the loop, waiting for them would wait for the tiles in flight
 #pragma unroll
@@ -472,9 +485,10 @@ __global__ __launch_bounds__(64 * kWaves<D>) void attention_decode_kernel(Decode
   int at = 0;           // the buffer of the present tile
   for (;;) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (ahead.left > 0) {
+    if (to_load > 0) {
       load_next();
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(AHEAD * W::kPerStage) : "memory");
+      // what came before the last AHEAD tiles and their page numbers is there
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"(AHEAD * (W::kPerStage + 1)) : "memory");
     } else {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
