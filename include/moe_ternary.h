@@ -378,7 +378,9 @@ int32_t moe_attention_prefill(int32_t type, const void* q, int64_t q_tokens, int
  *             is 0); it carries nothing from one call to the next
  * A sequence of length 0 gets y = 0 and lse = -inf; cache places behind a sequence's last
  * token may hold anything.  A page number outside [0, n_pages) reads nothing there and makes the
- * sequence's results NaN.  Numerics are moe_attention_prefill's; e4m3 values enter exactly, their scales in fp32.
+ * sequence's results NaN.  Numerics are moe_attention_prefill's; e4m3 codes enter exactly, a key's scale multiplies
+ * the score in fp32, and a weight times its value's scale is what is rounded to `type`: by half a step of itself,
+ * in fp16 by 2^-32 of the largest such product where that is more, whatever the scales are.
  * Limits are moe_attention_prefill's; batch at most 65535, n_pages in [1, 2^31).  How a
  * sequence is shared among workers, and so the last bits of y, depends on the batch's
  * lengths.  batch = 0 is a no-op.  y, lse and the workspace overlap neither each other nor

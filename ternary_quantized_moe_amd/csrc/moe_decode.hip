@@ -19,7 +19,7 @@
 // of y^T = V^T P^T, whose first is read from LDS transposed.  P is rounded to 16 bits for
 // the matrix cores (half a step of itself, as y's own rounding).
 // e4m3 codes are widened exactly; a key's scale multiplies its scores, a value's scale
-// the weights before they are rounded.
+// the weights before they are rounded, in fp16 relative to the largest such product.
 //
 // Of 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, it reads 974 MB in 176 us
 // (5.5 TB/s; some of that is in the Infinity Cache), of one of 131072 268 MB in 54 us, the
@@ -137,13 +137,19 @@ struct Decode {
   static constexpr int kBlockKeys = W * kKeys;
   static constexpr int kRecord = 64 * (D / 4 + 2);  // floats of a wave's state
   static constexpr int QS = D / 32, DT = D / 16;
+  // What is rounded to 16 bits is a weight times its value's scale, which may lie anywhere in
+  // fp32, while fp16 has 30 exponents.  So there the sums of the values have a reference n of
+  // their own beside m: they are formed of p scale 2^(m - n), the largest of which so far
+  // lies between 2^7 and 2^15 (256 sequences of up to 3001 in fp16 over e4m3 167 us; the products as
+  // they are, which small scales make zeros of, 162 us).
+  static constexpr bool kOwnRange = F16 && F8;
 
   const DecodeArgs& a;
   int lane, wave, col, quad, kv;
   uint8_t* mine;
   u32x4 q[QS];
   f32x4 o[DT];
-  float m, l;
+  float m, l, n;
   bool bad;
 
   __device__ __forceinline__ Decode(const DecodeArgs& args) : a(args) {}
@@ -213,7 +219,7 @@ struct Decode {
       to[k] = *(const u32x4*)(p + (F8 ? 64 * (k / 2) + 16 * quad + 8 * (k & 1) : 32 * k + 8 * quad));
   }
   __device__ __forceinline__ void begin() {
-    m = -INFINITY;
+    m = n = -INFINITY;
     l = 0.f;
     bad = false;
 #pragma unroll
@@ -302,8 +308,7 @@ struct Decode {
       const float now = fmaxf(m, top), f = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
       m = now;
       l *= f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) o[d] *= f;
+      if (!kOwnRange) scale_sums(f);
     }
     const float off = m == -INFINITY ? 0.f : m;
 #pragma unroll
@@ -318,6 +323,24 @@ struct Decode {
       for (int t = 0; t < ST; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[t][i] *= whole || 16 * t + 4 * quad + i < there ? v_scale[t][i] : 0.f;
+    }
+    if (kOwnRange) {
+      // Products below 2^-33 count as that: their sums stay far below what fp16 holds.
+      float big = 0x1p-33f;
+#pragma unroll
+      for (int t = 0; t < ST; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) big = fmaxf(big, __builtin_fabsf(s[t][i]));
+      big = over_column(big, [](float x, float y) { return fmaxf(x, y); });
+      const float at = __builtin_amdgcn_logf(big) + m;  // base 2
+      if (__any(at > n + 15.f)) {
+        const float now = fmaxf(n, at - 7.f);
+        scale_sums(now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(n - now));
+        n = now;
+      }
+      const float f = n == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - n);
+#pragma unroll
+      for (int t = 0; t < ST; ++t) s[t] *= f;
     }
     // k slot 8 quad + e of a product over 32 tokens is token 16 (e / 4) + 4 quad + e % 4.
     // Values behind the last token become zeros: they may hold anything.
@@ -352,9 +375,15 @@ struct Decode {
     }
   }
 
+  __device__ __forceinline__ void scale_sums(float f) {
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] *= f;
+  }
+
   // The waves' shares of a sequence, joined in wave 0: half of them hand theirs over, and
   // so on.
   __device__ __forceinline__ void join(float* room) {
+    if (kOwnRange) scale_sums(n == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(n - m));
     l = over_column(l, [](float x, float y) { return x + y; });
     if (__any(bad)) l = NAN;
 #pragma unroll
