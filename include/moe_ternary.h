@@ -334,8 +334,10 @@ int32_t moe_sample(int32_t type, const void* logits, int64_t batch, int32_t voca
  * taken as the nearer end, and a sequence that ends before it starts has no tokens; where
  * falling starts give a token to two sequences, either's result or none stands there.
  * Numerics: scores, the softmax's maximum and sum and y's sums are fp32; the weights
- * are rounded to `type` for the matrix cores (each off by half a step of itself), y is
- * rounded once.  A score beyond fp32 is infinite, and what exp underflows has no weight.
+ * are rounded to `type` for the matrix cores: each is off by half a step of itself, in fp16 by
+ * 2^-32 of the row's largest weight where that is more (one below 2^-21 of it); y is rounded
+ * once.  A score beyond fp32 is infinite, and what exp underflows has no weight.  Weights
+ * stand at up to 2^8 in the sums (fp16 2^15), so values above 2^88 may make these infinite.
  * head_dim is 64, 128 or 256; heads is a multiple of kv_heads, at most 4096; strides are
  * multiples of 8 from head_dim up to 2^24; q, k, v and y 16-byte aligned; tokens at most
  * 2^31 - 256, n_seqs at most 65535; scale finite and positive.  q_tokens = 0 or n_seqs = 0

@@ -17,11 +17,21 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
-// 16-bit values of one kind: their products, their rounding (nearest even), their ones
-// and the bits that all are set in an infinity or a NaN.
+// 16-bit values of one kind: their products, their rounding (nearest even) and the bits
+// that all are set in an infinity or a NaN.
 template <bool F16>
 struct Half {
-  static constexpr uint32_t kOne = F16 ? 0x3C00 : 0x3F80, kExponent = F16 ? 0x7C00 : 0x7F80;
+  static constexpr uint32_t kExponent = F16 ? 0x7C00 : 0x7F80;
+  // The weights of a softmax are formed as 2^(s - m), m = the largest s so far - kLift, and that
+  // may lag kLag behind: the largest is 2^kLift to 2^(kLift + kLag).  fp16 holds up to 2^16 and
+  // loses bits below 2^-14, so its weights stand high in that range: those below 2^-21 of the
+  // largest are off by 2^-32 of it at most (without the lift, 2^-14 and 2^-25: 16384 keys of
+  // 2^-25 each beside one of 1 were lost, 2^-11 of the sum).
+  static constexpr float kLift = F16 ? 7.f : 0.f, kLag = 8.f;
+  // The logarithm of the sum of the weights 2^(s - m), base e.
+  static __device__ __forceinline__ float log_of_sum(float m, float sum) {
+    return sum == 0.f ? -INFINITY : (m + kLift) * kLn2 + logf(sum * (F16 ? 0x1p-7f : 1.f));
+  }
   // D = A(32 x 16) B(16 x 32) + C.  Lane l supplies row l % 32 of A and column l % 32 of
   // B, k 8 (l / 32) .. + 7; it holds column l % 32 of D, row 8 (i / 4) + 4 (l / 32) + i % 4 in element i.
   static __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {

@@ -13,7 +13,8 @@
 // transposing reads of V follow the order in which the scores lie.  Two blocks share a CU,
 // and one's products run beside the other's softmax.  P is rounded to the values' type
 // (nearest even) for the matrix cores; each p is off by half a step of itself, as y is by its
-// own rounding, and l is summed before the rounding.
+// own rounding (in fp16 by 2^-32 of the largest where that is more), and l is summed before
+// the rounding.
 //
 // Where a launch has too few blocks for the card, several share the keys of a tile of
 // queries, and a second launch joins what they leave in the workspace.
@@ -204,8 +205,8 @@ struct Prefill {
     // The maximum that is subtracted may lag 2^8 behind the true one: the sums stay far
     // inside fp32, and y is scaled anew only when a query's maximum really moves (1 x 16384
     // 1012 us, 1061 where it follows at once; 1 x 8192 of 256 channels 506 us, 573).
-    if (__any(top > m + 8.f)) {
-      const float now = fmaxf(m, top), f = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
+    if (__any(top > m + (H::kLift + H::kLag))) {
+      const float now = fmaxf(m, top - H::kLift), f = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
       m = now;
       l *= f;
 #pragma unroll
@@ -319,7 +320,7 @@ struct Prefill {
       for (int e = 0; e < 4; ++e)
         *(u32x2*)(y + 32 * d + 8 * e) = u32x2{H::pack(o[d][4 * e] * inv, o[d][4 * e + 1] * inv),
                                               H::pack(o[d][4 * e + 2] * inv, o[d][4 * e + 3] * inv)};
-    if (a.lse && !half) a.lse[token * a.heads + head] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum);
+    if (a.lse && !half) a.lse[token * a.heads + head] = H::log_of_sum(m, sum);
   }
 };
 
@@ -493,7 +494,7 @@ __global__ __launch_bounds__(64) void attention_prefill_join_kernel(PrefillArgs 
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     *(u32x2*)(y + 8 * e) = u32x2{W::H::pack(o[e].x * inv, o[e].y * inv), W::H::pack(o[e].z * inv, o[e].w * inv)};
-  if (a.lse && part < 4 && !half) a.lse[out] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+  if (a.lse && part < 4 && !half) a.lse[out] = W::H::log_of_sum(top, sum);
 }
 
 PrefillWork work_of(const PrefillArgs& a) {

@@ -17,7 +17,8 @@
 // core's columns (16 of them; fewer leave columns idle, which HBM hides); the softmax is
 // then within a lane and the four lanes of a column, and P stands as the second operand
 // of y^T = V^T P^T, whose first is read from LDS transposed.  P is rounded to 16 bits for
-// the matrix cores (half a step of itself, as y's own rounding).
+// the matrix cores (half a step of itself, as y's own rounding; in fp16 2^-32 of the largest
+// where that is more).
 // e4m3 codes are widened exactly; a key's scale multiplies its scores, a value's scale
 // the weights before they are rounded, in fp16 relative to the largest such product.
 //
@@ -304,8 +305,8 @@ struct Decode {
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, s[t][i]);
     top = over_column(top, [](float x, float y) { return fmaxf(x, y); }) * c;
-    if (__any(top > m + 8.f)) {  // the maximum that is subtracted may lag 2^8 behind
-      const float now = fmaxf(m, top), f = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
+    if (__any(top > m + (H::kLift + H::kLag))) {  // the maximum that is subtracted may lag behind
+      const float now = fmaxf(m, top - H::kLift), f = now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - now);
       m = now;
       l *= f;
       if (!kOwnRange) scale_sums(f);
@@ -333,8 +334,8 @@ struct Decode {
         for (int i = 0; i < 4; ++i) big = fmaxf(big, __builtin_fabsf(s[t][i]));
       big = over_column(big, [](float x, float y) { return fmaxf(x, y); });
       const float at = __builtin_amdgcn_logf(big) + m;  // base 2
-      if (__any(at > n + 15.f)) {
-        const float now = fmaxf(n, at - 7.f);
+      if (__any(at > n + (H::kLift + H::kLag))) {
+        const float now = fmaxf(n, at - H::kLift);
         scale_sums(now == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(n - now));
         n = now;
       }
@@ -541,7 +542,7 @@ __global__ __launch_bounds__(64 * kWaves<D>) void attention_decode_kernel(Decode
             for (int d = 0; d < W::DT; ++d)
               *(u32x2*)(y + 16 * d) = u32x2{W::H::pack(w.o[d].x * inv, w.o[d].y * inv),
                                             W::H::pack(w.o[d].z * inv, w.o[d].w * inv)};
-            if (a.lse && w.quad == 0) a.lse[row] = w.l == 0.f ? -INFINITY : w.m * kLn2 + logf(w.l);
+            if (a.lse && w.quad == 0) a.lse[row] = W::H::log_of_sum(w.m, w.l);
           }
         } else {
           float* part = work.parts + (((int64_t)group * work.workers + worker) * 2 + (first_part ? 0 : 1)) *
@@ -638,7 +639,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(DecodeArgs a, Decod
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t out = b * a.heads + head;
   *(u32x2*)(a.y + out * D + 4 * d) = u32x2{Half<F16>::pack(sum.x * inv, sum.y * inv), Half<F16>::pack(sum.z * inv, sum.w * inv)};
-  if (a.lse && d == 0) a.lse[out] = l == 0.f ? -INFINITY : top * kLn2 + logf(l);
+  if (a.lse && d == 0) a.lse[out] = Half<F16>::log_of_sum(top, l);
 }
 
 template <bool F16, bool F8, int D>
