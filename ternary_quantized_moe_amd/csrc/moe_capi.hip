@@ -391,7 +391,7 @@ int32_t moe_rms_norm(const uint16_t* x, const uint16_t* residual, int64_t T, int
                      uint16_t* sum, uint16_t* y, uint8_t* q, float* scales, void* stream) {
   if (d <= 0 || d % 128 || d > moe::kNormMaxD)
     return fail(MOE_E_SHAPE, "d %d is not a positive multiple of 128 up to %d", (int)d, moe::kNormMaxD);
-  if (T < 0 || T > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "token count %lld outside [0, 2^31 - 256]", (long long)T);
+  if (T < 0 || T > 0x7FFFFFFFll) return fail(MOE_E_SHAPE, "token count %lld outside [0, 2^31)", (long long)T);
   if (!(eps >= 0.f) || std::isinf(eps)) return fail(MOE_E_ARG, "eps must be finite and not negative");
   if (T == 0) return ok();
   if (!y && !q) return fail(MOE_E_ARG, "give y, q or both");
