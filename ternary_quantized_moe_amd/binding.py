@@ -8,6 +8,7 @@ PyTorch provides device memory and the current stream.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -871,7 +872,8 @@ def _pools(pools, device, n_pages):
         if not p.is_contiguous():
             raise MoeError(-1, f"pool {i} is not contiguous")
         c[i].base, c[i].planes = p.data_ptr(), p.shape[0]
-        c[i].page_bytes = p.stride(1) * p.element_size()
+        # (not the stride of the pages, which means nothing where there is one page)
+        c[i].page_bytes = math.prod(p.shape[2:]) * p.element_size()
     return c, len(pools)
 
 
