@@ -711,6 +711,11 @@ def _cache(k, v, k_scales, v_scales, device, dtype, T):
             *shape)
 
 
+def _scale(dim, scale):
+    """The scale of the scores; heads without channels, which the call refuses, have none."""
+    return scale if scale is not None else dim ** -0.5 if dim else 1.0
+
+
 def attention_prefill(q, k, v, starts, k_starts=None, causal: bool = True, scale: Optional[float] = None, y=None,
                       lse=None, workspace=None, stream=None):
     """Attention of packed sequences: q [tokens, heads, dim], k and v [k tokens, kv heads,
@@ -751,7 +756,7 @@ def attention_prefill(q, k, v, starts, k_starts=None, causal: bool = True, scale
     if workspace is not None:
         ws, wn = _aligned(workspace)
     rc = L.moe_attention_prefill(kind, qp, n, H, q_token, q_head, kp, vp, m, Hk, k_token, k_head, v_token, v_head, D, sp,
-                                 ksp, size[0] - 1, causal, D ** -0.5 if scale is None else scale, yp, lp, ws, wn,
+                                 ksp, size[0] - 1, causal, _scale(D, scale), yp, lp, ws, wn,
                                  T["stream"](dev) if stream is None else _on(stream, dev, y, workspace))
     if rc:
         _check(rc)
@@ -794,7 +799,7 @@ def attention_decode(q, k_cache, v_cache, tables, lengths, k_scales=None, v_scal
         raise MoeError(-1, f"the workspace is on {workspace.device}, not on the current device cuda:{dev}")
     ws, wn = _aligned(workspace)
     rc = L.moe_attention_decode(kind, qp, B, H, q_row, q_head, ck, kp, vp, ksp, vsp, pages, Hk, P, D, tp, width, lenp,
-                                D ** -0.5 if scale is None else scale, yp, lp, ws, wn,
+                                _scale(D, scale), yp, lp, ws, wn,
                                 T["stream"](dev) if stream is None else _on(stream, dev, y, workspace))
     if rc:
         _check(rc)
