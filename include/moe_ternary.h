@@ -476,7 +476,8 @@ int32_t moe_kv_free(const int32_t* tables, int64_t n_rows, int32_t width, int32_
 /* The pages in use become pages 0 .. n - 1: those from n on move to the free ones below, both
  * in rising order, in every pool.  new_tables [n_rows x width] and new_refs [n_pages] take
  * the tables and counts after that (they may be tables and refs); entries behind a row's
- * last page are copied.  live: device int32 [1], n.  The pages moved from keep their content. */
+ * last page are copied.  live: device int32 [1], n.  The pages moved from keep their content.
+ * n_rows = 0, a no-op here too, leaves new_refs and live unwritten. */
 int32_t moe_kv_compact(const int32_t* tables, int64_t n_rows, int32_t width, const int32_t* lengths,
                        const int32_t* refs, int64_t n_pages, int32_t page_size, const moe_kv_pool* pools,
                        int32_t n_pools, int32_t* new_tables, int32_t* new_refs, int32_t* live, void* workspace,

@@ -961,7 +961,8 @@ def kv_compact(tables, lengths, refs, page_size: int, pools, new_tables=None, ne
                stream=None):
     """The n pages in use become pages 0 .. n - 1 of every pool (cache tensors [layers, pages,
     ...]); those above move to the free ones below.  -> (new_tables, new_refs, live), live
-    int32 [1] = n; new_tables and new_refs may be tables and refs themselves."""
+    int32 [1] = n; new_tables and new_refs may be tables and refs themselves.  Without rows the
+    pages in use move all the same."""
     T = _types()
     dev, R, n, head = _pages(tables, lengths, refs, T)
     if new_tables is None:
@@ -974,10 +975,16 @@ def kv_compact(tables, lengths, refs, page_size: int, pools, new_tables=None, ne
     rp = _operand("new_refs", new_refs, dev, T["i32s"], (n,))
     lp = _operand("live", live, dev, T["i32s"], (1,))
     c, count = _pools(pools, dev, n)
-    workspace, ws, wn = _pages_space(workspace, tables, R, n, T)
+    row = None
+    if R == 0:  # without rows the call does nothing: one whose content does not matter stands in
+        W = tables.shape[1]
+        row = refs.new_empty((W + 1,))
+        tp = row.data_ptr()
+        head = (tp, 1, W, tp + 4 * W, *head[4:])
+    workspace, ws, wn = _pages_space(workspace, tables, max(R, 1), n, T)
     rc = lib().moe_kv_compact(*head, page_size, c, count, tp, rp, lp, ws, wn,
                               T["stream"](dev) if stream is None else _on(stream, dev, new_tables, new_refs, live,
-                                                                          workspace))
+                                                                          workspace, row))
     if rc:
         _check(rc)
     return new_tables, new_refs, live
