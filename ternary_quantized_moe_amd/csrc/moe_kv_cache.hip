@@ -499,7 +499,10 @@ int64_t blocks_of_plane(const PoolArgs& p, int64_t moves) {
 
 }  // namespace
 
-int64_t pages_workspace_bytes(int64_t rows, int64_t n_pages) { return 256 + up256(8 * rows) + 3 * up256(4 * n_pages); }
+// (No rows take the space of one, which may stand in for them.)
+int64_t pages_workspace_bytes(int64_t rows, int64_t n_pages) {
+  return 256 + up256(8 * std::max<int64_t>(rows, 1)) + 3 * up256(4 * n_pages);
+}
 
 hipError_t launch_kv_append(const AppendArgs& a, hipStream_t stream) {
   constexpr int PIECES = 2 * kAppendThreads;

@@ -24,7 +24,10 @@ def test_compact_without_rows(tq):
         assert new_tables.shape == (0, 5)
         assert live.tolist() == [3] and new_refs.tolist() == [1, 2, 1, 0, 0, 0, 0] and torch.equal(x, want)
     x = pool.clone()
-    tq.kv_compact(tables, lengths, refs, 4, [x], new_tables=tables, new_refs=refs, live=live)
+    need = tq.lib().moe_kv_pages_workspace_bytes(0, 7)
+    space = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
+    space = space[-space.data_ptr() % 256:][:need]
+    tq.kv_compact(tables, lengths, refs, 4, [x], new_tables=tables, new_refs=refs, live=live, workspace=space)
     assert live.tolist() == [3] and refs.tolist() == [1, 2, 1, 0, 0, 0, 0] and torch.equal(x, want)
     with pytest.raises(tq.MoeError):
         tq.kv_compact(tables[:, :0], lengths, refs, 4, [x])
