@@ -19,13 +19,16 @@
 // Where a launch has too few blocks for the card, several share the keys of a tile of
 // queries, and a second launch joins what they leave in the workspace.
 //
-// The matrix cores bound long prompts, and the power that they may draw: 1 x 16384, 16 heads of
-// 128, causal, takes 1012 us (1.09 PFLOP/s; a loop of bare products reaches 1.27), 8 x 2048 of
-// 16 heads, not causal, 471 us (1.02), 1 x 8192, 16 heads of 256, 503 us (1.09), 1 x 4096, 32
-// heads of 64, 86 us (0.80: the exponentials weigh twice as much).  In the first the matrix
-// cores are busy 56% of the cycles, the vector units 53%, and LDS has no bank conflicts.
+// The matrix cores bound long prompts, and the power that they may draw, which differs from card
+// to card: 1 x 16384, 16 heads of 128, causal, takes 1012 to 1071 us (1.03 to 1.09 PFLOP/s; the
+// library's largest products 1.35 to 1.39), 8 x 2048 of 16 heads, not causal, 471 to 490 us (0.98
+// to 1.02), 1 x 8192, 16 heads of 256, 503 to 526 us (1.05 to 1.09), 1 x 4096, 32 heads of 64, 86
+// to 98 us (0.70 to 0.80: the exponentials weigh twice as much, the vector units are busy 60% of
+// the cycles and the matrix cores 35%).  In the first the matrix cores are busy 56% of the
+// cycles, the vector units 54%, and LDS has no bank conflicts.  Times that stand for two choices
+// below were taken in turn on one card.
 // Ragged prompts are bound by the longest row's walk over its keys (4099 tokens in 11 sequences
-// 52 us), and the smallest by a launch and three trips to memory (61 tokens 6.7 us).
+// 52 us), and the smallest by a launch and three trips to memory (61 tokens 6.2 us).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -508,7 +511,11 @@ PrefillWork work_of(const PrefillArgs& a) {
   w.units = (a.Tq >> (kRowBits - w.shift)) + std::min(a.n, a.Tq);
   // Where there are fewer blocks than fill the card, several share the keys of one, if there
   // are enough of these (1021 queries over 8191 keys, 16 heads of 256: 148 us, 363 without;
-  // shares of four tiles instead of eight: 1 x 1000, 32 us, 28 with eight).
+  // shares of four tiles instead of eight: 1 x 1000, 32 us, 28 with eight).  The number is the
+  // nearest, which starts up to a third more blocks than two a CU: rounded down it is slower
+  // where a CU holds three (64 channels, 1100 queries over 8100 keys, 32 heads: 131 us, 111 so)
+  // and faster where it holds two (128 channels, 700 over 8192: 121 us, 143 so; 1100 over 8192:
+  // 185 and 196).
   // Not to even out ragged sequences: blocks that turn out to have nothing to do, and the
   // joining, cost more than that gains (1809 of 4099 tokens in one of 11 sequences: 67 us, 52
   // without).

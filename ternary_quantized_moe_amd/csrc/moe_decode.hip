@@ -1,7 +1,8 @@
 // Attention of one new token of every sequence over a paged cache, for gfx950:
 //   y_h = sum_j p_hj v_j,   p_hj = exp(s_hj - m_h) / sum_j exp(s_hj - m_h),   s_hj = scale q_h k_j
-// over the lengths[b] cached tokens j of sequence b.  Every key and value is read once
-// for all query heads that share it, so HBM bounds it.
+// over the lengths[b] cached tokens j of sequence b.  Every key and value is read once for
+// each 16 query heads that share it, so HBM bounds it (with up to 16 heads a key head; of 64, a
+// token of 131072, whose keys and values are 67 MB, takes 48 us, 13 of them for that much).
 //
 // The tiles (a few dozen tokens for each wave of a block) of all sequences stand in one
 // row, which the workers of a kv head share equally, however ragged the lengths are; a
@@ -25,9 +26,9 @@
 // Of 64 sequences of up to 8192 tokens, 32 heads over 8 of 128, it reads 974 MB in 176 us
 // (5.5 TB/s; some of that is in the Infinity Cache), of one of 131072 268 MB in 54 us, the
 // join with it (46 where that cache holds more of it), of 256 of up to 3001 in e4m3 832 MB in
-// 162 us (5.1 TB/s).  One sequence of 77 tokens is a launch and a chain of latencies: 9 us, of which
-// finding the place takes 0.9, the page numbers 0.3, each of its two tiles 1.4 to ask for and
-// 0.9 to go through, the join of the waves and the store 1.5.
+// 162 us (5.1 TB/s), in fp16 over e4m3 in 167.  One sequence of 77 tokens is a launch and a
+// chain of latencies: 9 us, of which finding the place takes 0.9, the page numbers 0.3, each of
+// its two tiles 1.4 to ask for and 0.9 to go through, the join of the waves and the store 1.5.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -40,7 +41,8 @@ namespace moe {
 
 namespace {
 
-// One a CU: its tiles fill the LDS (512: 256 sequences in e4m3 177 us, 165 with 256).
+// One a CU: its tiles fill the LDS (512: 256 sequences in e4m3 177 us, 165 with 256).  Groups of
+// heads share them equally, so numbers that do not divide it leave some CUs idle.
 constexpr int kBlocks = 256;
 constexpr int kHeadTile = 16;  // query heads of a block
 
